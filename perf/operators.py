@@ -9,11 +9,12 @@ Each case is one call, or one run of calls, that a serving step makes:
   report   logprobs_top: log-probability of the chosen token, entropy, top alternatives
 
 The format of the cache: a group of 32 consecutive dims of one token and kv-head is held as 4-bit
-codes n + 8, n in -7 .. 7, and a scale s, a bf16 number of 5 significant bits, and stands for n * s.
-A (page, kv-head) block of K or V has 1152 bytes: 16 rows of 64 bytes of codes, then 16 rows of 4
-scales.  A row's codes are 16 little-endian 32-bit words of 8 codes each; code i of a word has its
-lowest bit at bit (4i + 3) mod 32.  Dim d = 32j + 8p + 2t + e (p, t < 4, e < 2) of K is code p + 4e of
-word 4t + j; dim d = 64w + 32h + 8p + g (g < 8) of V is code 4h + p of word 2g + w.
+codes n + 8, n in -7 .. 7, and a scale s, a bf16 number of 4 significant bits, and stands for n * s.
+A (page, kv-head) block of K or V has 1152 bytes: the codes of its 16 tokens, 64 bytes each, then 16
+rows of 4 scales.  Codes lie in little-endian 32-bit words of 8, code i at bits 4i .. 4i + 3.  Dim
+d = 32j + 8p + 2t + e (p, t < 4, e < 2) of token r of K is code p + 4e of word 16r + 4t + j; dim
+d = 64w + 32h + 8p + g (g < 8) of token r = 8a + 2b + c (c < 2) of V is code 4h + p of word
+128a + 16g + 4b + 2c + w.
 """
 import math
 
@@ -106,19 +107,20 @@ def work(c):
 
 # ----------------------------------------------------------- the 4-bit format ----
 def _places(device):
-    """(word, lowest bit before the rotation) of every dim of a K row and of a V row."""
-    d = torch.arange(D, device=device)
+    """(word, lowest bit) of token r's dim d, [16, 128] each, in a K block and in a V block."""
+    r, d = torch.arange(PAGE, device=device)[:, None], torch.arange(D, device=device)
     p, t, e = (d % 32) // 8, (d % 8) // 2, d % 2
     h = (d // 32) % 2
-    return (4 * t + d // 32, 4 * (p + 4 * e)), (2 * (d % 8) + d // 64, 4 * (4 * h + p))
+    return ((16 * r + 4 * t + d // 32, (4 * (p + 4 * e)).expand(PAGE, -1)),
+            (128 * (r // 8) + 16 * (d % 8) + 4 * ((r % 8) // 2) + 2 * (r % 2) + d // 64, (4 * (4 * h + p)).expand(PAGE, -1)))
 
 
 def _quantise(x):
     """Codes n (float) and scales [..., 4] of rows x [..., 128]."""
     g = x.float().unflatten(-1, (4, GROUP))
     amax = g.abs().amax(-1)
-    b = (amax / 7).view(torch.int32)
-    s = ((b + 0x3FFFF + ((b >> 19) & 1)) & ~0x7FFFF).view(torch.float32)  # 5 significant bits, nearest even
+    b = (amax / torch.full_like(amax, 7.0)).view(torch.int32)  # a quotient, where a product with 1/7 would miss ties
+    s = ((b + 0x7FFFF + ((b >> 20) & 1)) & ~0xFFFFF).view(torch.float32)  # 4 significant bits, nearest even
     s = torch.where(amax < 2.0 ** 126, s, math.nan)
     n = torch.round(g / s[..., None]).clamp(-7, 7)
     n = torch.where((s > 0)[..., None], n, 0.0)
@@ -134,21 +136,18 @@ def _pack(x, place):
     """Rows x [pages, Hkv, 16, 128] -> blocks [pages, Hkv, 1152] uint8."""
     n, s = _quantise(x)
     word, bit = place
-    order = torch.argsort(word * 32 + bit)  # dims by word, then by code
-    c = (n.to(torch.int32) + 8).index_select(-1, order).unflatten(-1, (16, 8))
+    order = torch.argsort((word * 32 + bit).flatten())  # (token, dim) by word, then by code
+    c = (n.to(torch.int32) + 8).flatten(-2).index_select(-1, order).unflatten(-1, (256, 8))
     w = (c << (4 * torch.arange(8, device=x.device, dtype=torch.int32))).sum(-1).to(torch.int32)
-    w = (w << 3) | ((w >> 29) & 7)
-    return torch.cat([w.contiguous().view(torch.uint8).flatten(-2),
-                      s.to(torch.bfloat16).contiguous().view(torch.uint8).flatten(-2)], -1)
+    return torch.cat([w.view(torch.uint8), s.to(torch.bfloat16).contiguous().view(torch.uint8).flatten(-2)], -1)
 
 
 def _unpack(blocks, place):
     """Blocks [..., 1152] uint8 -> rows [..., 16, 128] fp32."""
     word, bit = place
-    w = blocks[..., :1024].view(torch.int32).unflatten(-1, (16, 16))
-    s = blocks[..., 1024:].view(torch.bfloat16).unflatten(-1, (16, 4))
-    w = ((w >> 3) & 0x1FFFFFFF) | (w << 29)
-    n = ((w.index_select(-1, word) >> bit.to(torch.int32)) & 15) - 8
+    w = blocks[..., :1024].view(torch.int32).index_select(-1, word.flatten()).unflatten(-1, (PAGE, D))
+    s = blocks[..., 1024:].view(torch.bfloat16).unflatten(-1, (PAGE, 4))
+    n = ((w >> bit.to(torch.int32)) & 15) - 8
     return _values(n.float(), s.float())
 
 
@@ -360,26 +359,26 @@ def _run_own(st):
 def _read64(blocks, is_v):
     """Blocks [n, Hkv, 1152] -> [Hkv, n * 16, 128], from the bytes by the format's formula."""
     b = blocks.to(torch.int64)
-    d = torch.arange(D, device=b.device)
-    word = 2 * (d % 8) + d // 64 if is_v else 4 * ((d % 8) // 2) + d // 32
-    code = 4 * ((d // 32) % 2) + (d % 32) // 8 if is_v else (d % 32) // 8 + 4 * (d % 2)
-    rows = b[..., :1024].reshape(*b.shape[:2], PAGE, 16, 4)
-    w = rows[..., 0] + (rows[..., 1] << 8) + (rows[..., 2] << 16) + (rows[..., 3] << 24)
-    wd = w[..., word]
-    low = (4 * code + 3) % 32
-    n = ((wd >> low) | torch.where(low > 28, wd << (32 - low), 0)) & 15
+    r, d = torch.arange(PAGE, device=b.device)[:, None], torch.arange(D, device=b.device)
+    if is_v:
+        code = 4 * ((d // 32) % 2) + (d % 32) // 8
+        byte = 512 * (r // 8) + 64 * (d % 8) + 16 * ((r % 8) // 2) + 8 * (r % 2) + 4 * (d // 64) + code // 2
+    else:
+        code = (d % 32) // 8 + 4 * (d % 2)
+        byte = 64 * r + 16 * ((d % 8) // 2) + 4 * (d // 32) + code // 2
+    n = torch.where(code % 2 == 1, b[..., byte] // 16, b[..., byte] % 16) - 8
     sb = b[..., 1024:].reshape(*b.shape[:2], PAGE, 4, 2)
     s = ((sb[..., 0] + (sb[..., 1] << 8)) << 16).to(torch.int32).view(torch.float32).double()
-    x = (n - 8).double() * s[..., d // GROUP]
+    x = n.double() * s[..., d // GROUP]
     return x.permute(1, 0, 2, 3).reshape(b.shape[1], -1, D)
 
 
 def _four64(x):
     """What rows x [..., 128] are held as in 4 bits, in 64 bits: the scale from exact quotients and powers of two."""
     g = x.double().reshape(*x.shape[:-1], 4, GROUP)
-    raw = g.abs().amax(-1) / 7
-    m, e = torch.frexp(raw)
-    s = (torch.round(m * 32) * ((e.long() + 1018) << 52).view(torch.float64))[..., None]  # times 2^(e - 5), from its bits
+    amax = g.abs().amax(-1)
+    m, e = torch.frexp(amax / torch.full_like(amax, 7.0))
+    s = (torch.round(m * 16) * ((e.long() + 1019) << 52).view(torch.float64))[..., None]  # times 2^(e - 4), from its bits
     n = torch.where(s > 0, torch.round(g / torch.where(s > 0, s, 1.0)), 0.0).clamp(-7, 7)
     return (n * s).reshape(x.shape)
 
