@@ -121,7 +121,7 @@ def _quantise(x):
     amax = g.abs().amax(-1)
     b = (amax / torch.full_like(amax, 7.0)).view(torch.int32)  # a quotient, where a product with 1/7 would miss ties
     s = ((b + 0x7FFFF + ((b >> 20) & 1)) & ~0xFFFFF).view(torch.float32)  # 4 significant bits, nearest even
-    s = torch.where(amax < 2.0 ** 126, s, math.nan)
+    s = torch.where(amax < 2.0 ** 123, torch.where(amax < 2.0 ** -120, 0.0, s), math.nan)
     n = torch.round(g / s[..., None]).clamp(-7, 7)
     n = torch.where((s > 0)[..., None], n, 0.0)
     return n.flatten(-2), s
