@@ -23,7 +23,8 @@
  *
  * Data types: all activations, weights, caches and outputs are bf16
  * (IEEE binary32 truncated to its top 16 bits); arithmetic is fp32; every
- * output is rounded once, to nearest-even, to bf16.
+ * output is rounded once, to nearest-even, to bf16.  Log-probabilities are
+ * fp32, and a KV cache can also be held in 4 bits (bi_kv4_append).
  */
 #ifndef BI_H_
 #define BI_H_
@@ -45,6 +46,10 @@ extern "C" {
 #define BI_DECODE_CHUNK 256
 /* Bytes of arrival counters at the start of a decode-attention workspace. */
 #define BI_DECODE_COUNTER_BYTES 262144
+/* Bytes of one (page, kv-head) block of K or of V in a 4-bit cache. */
+#define BI_KV4_BLOCK_BYTES 1152
+/* The most alternatives bi_logprobs_top gives for a row. */
+#define BI_MAX_TOP_LOGPROBS 32
 
 typedef enum {
     BI_OK = 0,
@@ -380,6 +385,130 @@ bi_status bi_silu_mul(const void* gate_up, int64_t ld_gate_up, int32_t T, int32_
 bi_status bi_logprobs(const void* logits, int64_t rows, int32_t vocab, int64_t ld,
                       const int32_t* targets, float* logprob_out, float* lse_out,
                       cudaStream_t stream);
+
+/*
+ * The 4-bit cache.  k_cache and v_cache are uint8 [num_pages][Hkv]
+ * [BI_KV4_BLOCK_BYTES], 16-byte aligned: 1152 bytes where a bf16 page block
+ * has 4096.  A group of 32 consecutive dims of one token and kv-head is held
+ * as codes n + 8 and one scale s:
+ *     s = max|x| / 7 rounded to 4 significant bits, nearest even (kept as bf16)
+ *     n = x / s rounded to nearest even, -7 .. 7
+ * and stands for n * s, which is a bf16 number, at most s / 2 away from x.  A
+ * group that holds a NaN, an infinity or a magnitude of 2^123 or more stands
+ * for NaN throughout, one with every magnitude below 2^-120 for zeros.  A block holds the codes of its 16 tokens (64 bytes
+ * each), then bf16 scales [16 tokens][4 groups].  Codes lie in little-endian
+ * 32-bit words of 8, code i in bits 4i .. 4i + 3:
+ *     K: dim 32j + 8p + 2t + e (j, p, t < 4; e < 2) of token r is code p + 4e
+ *        of word 16r + 4t + j;
+ *     V: dim 64w + 32h + 8p + g (w, h < 2; p < 4; g < 8) of token 8a + 2b + c
+ *        (c < 2) is code 4h + p of word 128a + 16g + 4b + 2c + w.
+ * Bytes that no token was written to are never part of a result, whatever
+ * they hold.  Two tokens of one call must not share a slot: which bytes of
+ * either are kept is not defined.
+ *
+ * bi_kv4_append -- quantise the K and V rows of T tokens into their slots, for
+ * keys and values computed elsewhere (a bf16 cache takes those by any copy).
+ * The rule of "3. Batch-Invariant Attention" of "Defeating Nondeterminism in
+ * LLM Inference: The Core Role of Batch Invariance" that new tokens join the
+ * one cache layout before attention reads it; a row's codes depend on its own
+ * 128 values only.
+ *
+ *   k, v       device, bf16 [T][ld_k], [T][ld_v]: per token Hkv heads of 128
+ *              values; ld_k, ld_v >= Hkv * 128, multiples of 8 (so that rows
+ *              of a qkv projection can be given where they lie).
+ *   slots      device, int32 [T]: each token's cache slot, page * 16 + offset.
+ *   num_pages * Hkv * 16 < 2^31.  D = 128, page_size = 16.
+ * A slot out of range is reported on the device (BI_ERR_DEVICE_BAD_INPUT) and
+ * that token is skipped.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED,
+ * CUDA.
+ */
+bi_status bi_kv4_append(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int32_t T,
+                        int32_t Hkv, int32_t D, const int32_t* slots, void* k_cache, void* v_cache,
+                        int32_t num_pages, int32_t page_size, cudaStream_t stream);
+
+/*
+ * bi_qk_norm_rope_append_kv4 -- bi_qk_norm_rope_append with a 4-bit cache: the
+ * bf16 K and V rows that it would write into a bf16 cache are quantised as
+ * bi_kv4_append does, in the same launch.  q_out has bi_qk_norm_rope_append's
+ * bits and the caches those of bi_kv4_append over its rows.  Arguments, checks
+ * and errors as bi_qk_norm_rope_append; num_pages * Hkv * 16 < 2^31.
+ */
+bi_status bi_qk_norm_rope_append_kv4(const void* qkv, int64_t ld_qkv, int32_t T, int32_t Hq,
+                                     int32_t Hkv, int32_t D, const int32_t* positions,
+                                     const int32_t* slots, const float* rope_table, int32_t max_pos,
+                                     const void* q_norm_w, const void* k_norm_w, float eps,
+                                     void* q_out, void* k_cache, void* v_cache, int32_t num_pages,
+                                     int32_t page_size, cudaStream_t stream);
+
+/*
+ * bi_kv4_read -- read the tokens of S sequences back from a 4-bit cache into a
+ * bf16 cache of the same page numbering: for every sequence s and token t <
+ * seq_lens[s], the rows of all kv-heads in page block_table[s][t / 16] of
+ * k_out and v_out.  Nothing is rounded (n * s is a bf16 number) and no other
+ * row is written.  bi_prefill_attention reads the result with the same block
+ * table: that is how many query rows attend over a 4-bit cache, one bf16 cache
+ * serving every layer in turn.
+ *
+ *   block_table  device, int32 [S][max_pages_per_seq], as bi_decode_attention;
+ *                sequences may share pages.
+ *   seq_lens     device, int32 [S]: 0 .. max_seq_len tokens.
+ *   k_out, v_out device, bf16 [num_pages][Hkv][16][128], 16-byte aligned; no
+ *                overlap with the 4-bit caches.
+ *   S            0 .. 65535;  max_seq_len >= 1, <= max_pages_per_seq * 16.
+ *   num_pages * Hkv * 16 < 2^31.  D = 128, page_size = 16.
+ * A length or a page out of range is reported on the device
+ * (BI_ERR_DEVICE_BAD_INPUT) and that sequence, or page, is skipped.  Errors:
+ * INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA.
+ */
+bi_status bi_kv4_read(const void* k_cache, const void* v_cache, const int32_t* block_table,
+                      int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t S, int32_t Hkv,
+                      int32_t D, int32_t page_size, int32_t num_pages, int32_t max_seq_len,
+                      void* k_out, void* v_out, cudaStream_t stream);
+
+/*
+ * bi_decode_attention_kv4 -- bi_decode_attention over a 4-bit cache: the bits
+ * of bi_decode_attention over the bf16 cache that bi_kv4_read makes of it,
+ * without making it.  Operation, arguments, workspace
+ * (bi_decode_attention_workspace_size bytes, counters zero at first use),
+ * checks and errors as bi_decode_attention; k_cache and v_cache are 4-bit
+ * caches, Hkv <= 65535.  One kernel launch (two only when B * Hkv >
+ * BI_DECODE_COUNTER_BYTES / 4 and some sequence spans several CTAs).
+ */
+bi_status bi_decode_attention_kv4(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_table, int32_t max_pages_per_seq,
+                                  const int32_t* seq_lens, int32_t B, int32_t Hq, int32_t Hkv,
+                                  int32_t D, int32_t page_size, int32_t num_pages,
+                                  int32_t max_seq_len, float scale, void* out, void* workspace,
+                                  size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * bi_logprobs_top -- what a sampler reports of a row of logits: bi_logprobs'
+ * log-sum-exp and target log-probability (the same bits for logits that are
+ * -inf or within +-1024), the entropy of the row's softmax in nats, and the k
+ * largest logits as token ids and log-probabilities, largest first, equal
+ * logits by ascending id:
+ *     entropy[r] = -sum_j p_j log p_j,   p_j = exp(x[r][j] - lse[r])      (fp32)
+ *     top_logprobs[r][i] = x[r][top_ids[r][i]] - lse[r]                   (fp32)
+ *
+ * Operation: as bi_logprobs, "Experimental Validation and Future Prospects" of
+ * "Defeating Nondeterminism in LLM Inference: The Core Role of Batch
+ * Invariance": one row per CTA, reductions in an order that depends only on
+ * `vocab`.  -inf logits (a masked vocabulary) add nothing and come last among
+ * the k; a row of nothing else has lse -inf, entropy and log-probabilities
+ * NaN.  NaN logits make the row's numbers NaN and rank below every number. 
+ * Masks of finite values (-1e9, bf16's lowest) do as well as -inf.
+ *   logits       device, bf16 [rows][ld], ld >= vocab, both multiples of 8.
+ *   targets      device, int32 [rows], with logprob_out fp32 [rows]; or both null.
+ *   lse_out, entropy_out   device, fp32 [rows], each or null.
+ *   k            1 .. BI_MAX_TOP_LOGPROBS, <= vocab <= 2^30.
+ *   top_ids      device, int32 [rows][k];  top_logprobs  device, fp32 [rows][k].
+ * A target outside 0 .. vocab-1 gives NaN and BI_ERR_DEVICE_BAD_INPUT.  Errors:
+ * INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA.
+ */
+bi_status bi_logprobs_top(const void* logits, int64_t rows, int32_t vocab, int64_t ld,
+                          const int32_t* targets, float* logprob_out, float* lse_out,
+                          float* entropy_out, int32_t k, int32_t* top_ids, float* top_logprobs,
+                          cudaStream_t stream);
 
 /*
  * bi_decode_attention_fixed_splits -- the same attention with a fixed split

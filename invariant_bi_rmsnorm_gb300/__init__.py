@@ -15,6 +15,12 @@ tensors must live on a CUDA device, and a missing library raises.
     prefill_attention(...)                causal attention for many rows per sequence,
                                           bit-identical per row to decode_attention
     qk_norm_rope_append(...), silu_mul(gate_up), logprobs(logits, targets)
+    kv4_cache(num_pages, Hkv)             a pair of empty 4-bit caches, and what uses them:
+    kv4_append(k, v, slots, ...), qk_norm_rope_append_kv4(...)
+                                          quantise new tokens' K/V into their slots
+    kv4_read(...)                         read sequences back into a bf16 cache (prefill's)
+    decode_attention_kv4(...)             decode attention over the 4-bit cache
+    logprobs_top(logits, targets, k)      log-probability, lse, entropy, k best tokens
 
 Every output row's bits depend only on that row's own inputs (batch
 invariance); see include/bi.h for the exact contract of each call.
@@ -26,7 +32,8 @@ import math
 import torch
 
 from . import _lib
-from ._lib import DECODE_CHUNK, DECODE_COUNTER_BYTES, PAGE_SIZE
+from ._lib import (DECODE_CHUNK, DECODE_COUNTER_BYTES, KV4_BLOCK_BYTES, MAX_TOP_LOGPROBS,
+                   PAGE_SIZE)
 
 __all__ = ["BiError", "rmsnorm", "gemm", "gemm_swiglu", "interleave_gate_up",
            "decode_attention", "decode_attention_fixed_splits",
@@ -34,7 +41,9 @@ __all__ = ["BiError", "rmsnorm", "gemm", "gemm_swiglu", "interleave_gate_up",
            "qk_norm_rope_append", "silu_mul", "logprobs",
            "decode_attention_workspace_size", "selftest_wait_timeout",
            "decode_num_chunks", "decode_chunk_len", "get_device_error", "abi_version",
-           "status_string", "PAGE_SIZE", "DECODE_CHUNK"]
+           "status_string", "PAGE_SIZE", "DECODE_CHUNK", "kv4_cache", "kv4_append",
+           "qk_norm_rope_append_kv4", "kv4_read", "decode_attention_kv4", "logprobs_top",
+           "KV4_BLOCK_BYTES", "MAX_TOP_LOGPROBS"]
 
 
 class BiError(RuntimeError):
@@ -401,3 +410,197 @@ def decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
         int(max_seq_len), float(scale), out.data_ptr(), ws_ptr, ws_bytes, _stream(stream)),
         "bi_decode_attention")
     return out
+
+
+# --------------------------------------------------------- 4-bit KV cache ----
+def _cuda_i32(t: torch.Tensor, name: str, shape: tuple) -> None:
+    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _one_device(where: str, *tensors) -> None:
+    """Every tensor on the current device, whose stream and error word the call uses."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: every tensor must be on the current CUDA device ({dev})")
+
+
+def _kv4_caches(k_cache: torch.Tensor, v_cache: torch.Tensor, where: str) -> tuple[int, int]:
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not t.is_cuda or t.dtype != torch.uint8 or not t.is_contiguous():
+            raise ValueError(f"{where}: {n} must be a contiguous uint8 CUDA tensor")
+    shape = k_cache.shape
+    if len(shape) != 3 or shape[2] != KV4_BLOCK_BYTES or v_cache.shape != shape:
+        raise ValueError(f"{where}: 4-bit caches [num_pages, Hkv, {KV4_BLOCK_BYTES}] expected")
+    return shape[0], shape[1]
+
+
+def kv4_cache(num_pages: int, Hkv: int, device="cuda") -> tuple[torch.Tensor, torch.Tensor]:
+    """A pair of empty 4-bit K and V caches, uint8 [num_pages, Hkv, 1152]: pages
+    of 16 tokens, heads of 128 dims (include/bi.h gives the layout)."""
+    k = torch.zeros((num_pages, Hkv, KV4_BLOCK_BYTES), dtype=torch.uint8, device=device)
+    return k, torch.zeros_like(k)
+
+
+def _kv4_rows(t: torch.Tensor, name: str) -> int:
+    """Token stride (elements) of k or v [T, Hkv, 128] with whole heads side by side."""
+    _cuda_bf16(t, name)
+    if t.dim() != 3 or t.shape[2] != 128:
+        raise ValueError(f"{name} must be [T, Hkv, 128]")
+    T, Hkv, _ = t.shape
+    if t.numel() and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != 128)):
+        raise ValueError(f"{name}: the heads of a token must lie side by side")
+    return int(t.stride(0)) if T > 1 else Hkv * 128
+
+
+def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+               v_cache: torch.Tensor, stream=None) -> None:
+    """Quantise k, v [T, Hkv, 128] (any token stride: views of a qkv projection
+    will do) to 4 bits in the slots (page * 16 + offset, int32 [T]) of the caches."""
+    num_pages, Hkv = _kv4_caches(k_cache, v_cache, "kv4_append")
+    ld_k, ld_v = _kv4_rows(k, "k"), _kv4_rows(v, "v")
+    T = k.shape[0]
+    if k.shape != v.shape or k.shape[1] != Hkv:
+        raise ValueError("kv4_append: k and v [T, Hkv, 128] of the caches' Hkv expected")
+    _cuda_i32(slots, "slots", (T,))
+    _one_device("kv4_append", k, v, slots, k_cache, v_cache)
+    _check(_lib.load().bi_kv4_append(
+        k.data_ptr(), ld_k, v.data_ptr(), ld_v, T, Hkv, 128, slots.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), num_pages, PAGE_SIZE, _stream(stream)), "bi_kv4_append")
+
+
+def qk_norm_rope_append_kv4(qkv: torch.Tensor, Hq: int, Hkv: int, positions: torch.Tensor,
+                            slots: torch.Tensor, rope: torch.Tensor, q_norm_w, k_norm_w,
+                            k_cache: torch.Tensor, v_cache: torch.Tensor, eps: float = 1e-6,
+                            q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """qk_norm_rope_append into 4-bit caches: q -> q_out [T, Hq, 128]; the k and
+    v rows, quantised -> their slots."""
+    num_pages, Hkv2 = _kv4_caches(k_cache, v_cache, "qk_norm_rope_append_kv4")
+    _cuda_bf16(qkv, "qkv")
+    ld = _row_major_2d(qkv, "qkv")
+    T = qkv.shape[0]
+    if Hkv2 != Hkv or qkv.shape[1] < (Hq + 2 * Hkv) * 128:
+        raise ValueError("qk_norm_rope_append_kv4: qkv [T, (Hq + 2 Hkv) * 128] and caches of Hkv "
+                         "heads expected")
+    _cuda_i32(positions, "positions", (T,))
+    _cuda_i32(slots, "slots", (T,))
+    if (not rope.is_cuda or rope.dtype != torch.float32 or not rope.is_contiguous()
+            or rope.dim() != 2 or rope.shape[1] != 128):
+        raise ValueError("rope must be a contiguous float32 CUDA tensor [max_pos, 128]")
+    for t, n in ((q_norm_w, "q_norm_w"), (k_norm_w, "k_norm_w")):
+        if t is not None:
+            _cuda_bf16(t, n)
+            if t.shape != (128,) or not t.is_contiguous():
+                raise ValueError(f"{n} must be a contiguous [128] tensor")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, 128), dtype=torch.bfloat16, device=qkv.device)
+    else:
+        _cuda_bf16(q_out, "q_out")
+        if q_out.shape != (T, Hq, 128) or not q_out.is_contiguous():
+            raise ValueError("q_out must be a contiguous [T, Hq, 128] tensor")
+    _one_device("qk_norm_rope_append_kv4", qkv, positions, slots, rope, q_norm_w, k_norm_w,
+                k_cache, v_cache, q_out)
+    _check(_lib.load().bi_qk_norm_rope_append_kv4(
+        qkv.data_ptr(), ld, T, Hq, Hkv, 128, positions.data_ptr(), slots.data_ptr(),
+        rope.data_ptr(), rope.shape[0], q_norm_w.data_ptr() if q_norm_w is not None else None,
+        k_norm_w.data_ptr() if k_norm_w is not None else None, eps, q_out.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), num_pages, PAGE_SIZE, _stream(stream)),
+        "bi_qk_norm_rope_append_kv4")
+    return q_out
+
+
+def kv4_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+             seq_lens: torch.Tensor, max_seq_len: int, k_out: torch.Tensor, v_out: torch.Tensor,
+             stream=None) -> None:
+    """Read the tokens of sequences back from 4-bit caches into bf16 caches
+    k_out, v_out [num_pages, Hkv, 16, 128] of the same page numbering (other
+    rows stay as they are): the caches prefill_attention takes, with the same
+    block_table [S, max_pages_per_seq] and seq_lens [S]."""
+    num_pages, Hkv = _kv4_caches(k_cache, v_cache, "kv4_read")
+    shape = (num_pages, Hkv, PAGE_SIZE, 128)
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        _cuda_bf16(t, n)
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"kv4_read: {n} must be a contiguous {shape} tensor")
+    if block_table.dim() != 2:
+        raise ValueError("kv4_read: block_table [S, max_pages_per_seq] expected")
+    S, width = block_table.shape
+    _cuda_i32(block_table, "block_table", (S, width))
+    _cuda_i32(seq_lens, "seq_lens", (S,))
+    _one_device("kv4_read", k_cache, v_cache, block_table, seq_lens, k_out, v_out)
+    _check(_lib.load().bi_kv4_read(
+        k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), width, seq_lens.data_ptr(),
+        S, Hkv, 128, PAGE_SIZE, num_pages, int(max_seq_len), k_out.data_ptr(), v_out.data_ptr(),
+        _stream(stream)), "bi_kv4_read")
+
+
+def decode_attention_kv4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         block_table: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                         scale: float | None = None, out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """decode_attention over 4-bit caches [num_pages, Hkv, 1152]: the bits of
+    decode_attention over what kv4_read gives of them.  Other arguments, and
+    the workspace, as decode_attention."""
+    num_pages, Hkv = _kv4_caches(k_cache, v_cache, "decode_attention_kv4")
+    _cuda_bf16(q, "q")
+    if q.dim() != 3 or not q.is_contiguous() or block_table.dim() != 2:
+        raise ValueError("decode_attention_kv4: contiguous q [B, Hq, D] and block_table "
+                         "[B, max_pages_per_seq] expected")
+    B, Hq, D = q.shape
+    width = block_table.shape[1]
+    _cuda_i32(block_table, "block_table", (B, width))
+    _cuda_i32(seq_lens, "seq_lens", (B,))
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _cuda_bf16(out, "out")
+        if out.shape != q.shape or not out.is_contiguous():
+            raise ValueError("decode_attention_kv4: out must be a contiguous [B, Hq, D] tensor")
+    if workspace is None:
+        need = decode_attention_workspace_size(B, Hq, D, max_seq_len)
+        if need > 0:
+            # the leading arrival counters must start at zero (every call leaves
+            # them zero, so a caller-kept workspace is cleared only once)
+            workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("decode_attention_kv4: workspace must be a contiguous CUDA tensor")
+    _one_device("decode_attention_kv4", q, k_cache, v_cache, block_table, seq_lens, out, workspace)
+    _check(_lib.load().bi_decode_attention_kv4(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), width,
+        seq_lens.data_ptr(), B, Hq, Hkv, D, PAGE_SIZE, num_pages, int(max_seq_len), scale,
+        out.data_ptr(), workspace.data_ptr() if workspace is not None else None,
+        workspace.nbytes if workspace is not None else 0, _stream(stream)),
+        "bi_decode_attention_kv4")
+    return out
+
+
+# ---------------------------------------------------- per-token log-probs ----
+def logprobs_top(logits: torch.Tensor, targets: torch.Tensor | None, k: int, stream=None):
+    """(logprob of targets [rows] or None, lse [rows], entropy [rows], top_ids
+    [rows, k] int32, top_logprobs [rows, k]) of bf16 logits [rows, vocab]: the
+    bits of logprobs(logits, targets), the softmax's entropy in nats, and the k
+    (1 .. 32) largest logits' tokens, largest first, equal ones by ascending id."""
+    _cuda_bf16(logits, "logits")
+    ld = _row_major_2d(logits, "logits")
+    rows, vocab = logits.shape
+    k = int(k)
+    if k < 1:
+        raise ValueError("logprobs_top: k must be at least 1")
+    if targets is not None:
+        _cuda_i32(targets, "targets", (rows,))
+    _one_device("logprobs_top", logits, targets)
+    dev = logits.device
+    f = torch.empty((3, rows), dtype=torch.float32, device=dev)
+    lp, lse, entropy = f.unbind(0)
+    ids = torch.empty((rows, k), dtype=torch.int32, device=dev)
+    top = torch.empty((rows, k), dtype=torch.float32, device=dev)
+    _check(_lib.load().bi_logprobs_top(
+        logits.data_ptr(), rows, vocab, ld, targets.data_ptr() if targets is not None else None,
+        lp.data_ptr() if targets is not None else None, lse.data_ptr(), entropy.data_ptr(), k,
+        ids.data_ptr(), top.data_ptr(), _stream(stream)), "bi_logprobs_top")
+    return (lp if targets is not None else None), lse, entropy, ids, top

@@ -23,6 +23,8 @@ BI_ERR_DEVICE_BAD_INPUT = 7
 PAGE_SIZE = 16
 DECODE_CHUNK = 256
 DECODE_COUNTER_BYTES = 262144  # arrival counters at the start of an attention workspace
+KV4_BLOCK_BYTES = 1152  # one (page, kv-head) block of K or of V in a 4-bit cache
+MAX_TOP_LOGPROBS = 32
 
 # every entry point include/bi.h declares
 EXPORTS = (
@@ -34,6 +36,8 @@ EXPORTS = (
     "bi_add_rmsnorm",
     "bi_qk_norm_rope_append", "bi_silu_mul", "bi_decode_attention_launches", "bi_logprobs",
     "bi_gemm_swiglu",
+    "bi_kv4_append", "bi_qk_norm_rope_append_kv4", "bi_kv4_read", "bi_decode_attention_kv4",
+    "bi_logprobs_top",
 )
 
 _lib = None
@@ -103,6 +107,18 @@ def load() -> ctypes.CDLL:
     lib.bi_decode_attention_launches.restype = _i32
     lib.bi_logprobs.argtypes = [_vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp]
     lib.bi_logprobs.restype = ctypes.c_int
+    lib.bi_kv4_append.argtypes = [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _i32,
+                                  _i32, _vp]
+    lib.bi_kv4_append.restype = ctypes.c_int
+    lib.bi_qk_norm_rope_append_kv4.argtypes = lib.bi_qk_norm_rope_append.argtypes
+    lib.bi_qk_norm_rope_append_kv4.restype = ctypes.c_int
+    lib.bi_kv4_read.argtypes = [_vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp,
+                                _vp, _vp]
+    lib.bi_kv4_read.restype = ctypes.c_int
+    lib.bi_decode_attention_kv4.argtypes = lib.bi_decode_attention.argtypes
+    lib.bi_decode_attention_kv4.restype = ctypes.c_int
+    lib.bi_logprobs_top.argtypes = [_vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp]
+    lib.bi_logprobs_top.restype = ctypes.c_int
     lib.bi_selftest_wait_timeout.argtypes = [_i32, _vp]
     lib.bi_selftest_wait_timeout.restype = ctypes.c_int
     _lib = lib

@@ -15,6 +15,7 @@
 
 #include "bi_internal.h"
 #include "bi_ptx.cuh"
+#include "kv4.cuh"
 
 namespace {
 
@@ -35,8 +36,8 @@ struct RopeArgs {
     const __nv_bfloat16* k_norm_w;  // [128] or null
     float eps;
     __nv_bfloat16* q_out;  // [T][Hq][128]
-    __nv_bfloat16* k_cache;
-    __nv_bfloat16* v_cache;  // [num_pages][Hkv][16][128]
+    void* k_cache;
+    void* v_cache;  // bf16 [num_pages][Hkv][16][128], or 4-bit blocks [num_pages][Hkv][1152]
     int64_t num_slots;       // num_pages * 16
     int page_size;
     uint32_t* err;
@@ -54,7 +55,8 @@ struct RopeArgs {
 //                -> rotate-half RoPE in fp32: y_i = x_i c_i - x_{64+i} s_i,
 //                   y_{64+i} = x_{64+i} c_i + x_i s_i, rounded once to bf16
 //   v heads:     copied.
-// q goes to q_out; k and v to their token's cache slot.  Each head's
+// q goes to q_out; k and v to their token's cache slot, in bf16 or (kKv4)
+// quantised from those bf16 values to 4 bits (kv4.cuh).  Each head's
 // arithmetic depends only on its own 128 values, the position and the weights.
 constexpr int kRopeWarps = 8;
 constexpr int kPairsPerPass = 3;
@@ -83,6 +85,7 @@ __device__ __forceinline__ void unpack4(uint2 v, float* x) {
     x[3] = __uint_as_float(v.y & 0xffff0000u);
 }
 
+template <bool kKv4>
 __global__ void __launch_bounds__(kRopeWarps * 32, 4) qk_norm_rope_append_kernel(const RopeArgs a) {
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
@@ -139,15 +142,16 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) qk_norm_rope_append_kernel
             for (int e = 0; e < 8; ++e) ss = __fmaf_rn(x[e], x[e], ss);
 #pragma unroll
             for (int o = 8; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (!live) continue;
-            if (is_v) {  // v: copy into the cache
+            if (!kKv4 && !live) continue;
+            if (!kKv4 && is_v) {  // v: copy into the cache
                 const int hv = h - a.Hq - a.Hkv;
-                __nv_bfloat16* dst = a.v_cache + kv_slot + hv * (BI_PAGE_SIZE * kD);
+                __nv_bfloat16* dst =
+                    static_cast<__nv_bfloat16*>(a.v_cache) + kv_slot + hv * (BI_PAGE_SIZE * kD);
                 *reinterpret_cast<uint2*>(dst + i0) = lo[j];
                 *reinterpret_cast<uint2*>(dst + kHalf + i0) = hi[j];
                 continue;
             }
-            if (norm) {
+            if (norm && !(kKv4 && is_v)) {
                 // ss / 128 computed as ss * 2^-7: the same correctly rounded value
                 const float r = rsqrtf(__fmul_rn(ss, 1.f / kD) + a.eps);
                 float w[8];
@@ -163,16 +167,40 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) qk_norm_rope_append_kernel
                 y[e] = __fsub_rn(__fmul_rn(x[e], c[e]), __fmul_rn(x[4 + e], sn[e]));
                 y[4 + e] = __fadd_rn(__fmul_rn(x[4 + e], c[e]), __fmul_rn(x[e], sn[e]));
             }
-            __nv_bfloat16* dst;
-            if (is_q) {
-                dst = a.q_out + (static_cast<int64_t>(t) * a.Hq + h) * kD;
-            } else {
-                dst = a.k_cache + kv_slot + (h - a.Hq) * (BI_PAGE_SIZE * kD);
+            const uint2 y_lo = make_uint2(bi::pack_bf16x2(y[0], y[1]), bi::pack_bf16x2(y[2], y[3]));
+            const uint2 y_hi = make_uint2(bi::pack_bf16x2(y[4], y[5]), bi::pack_bf16x2(y[6], y[7]));
+            if (is_q || !kKv4) {
+                __nv_bfloat16* dst;
+                if (is_q) {
+                    dst = a.q_out + (static_cast<int64_t>(t) * a.Hq + h) * kD;
+                } else {
+                    dst = static_cast<__nv_bfloat16*>(a.k_cache) + kv_slot + (h - a.Hq) * (BI_PAGE_SIZE * kD);
+                }
+                *reinterpret_cast<uint2*>(dst + i0) = y_lo;
+                *reinterpret_cast<uint2*>(dst + kHalf + i0) = y_hi;
             }
-            *reinterpret_cast<uint2*>(dst + i0) =
-                make_uint2(bi::pack_bf16x2(y[0], y[1]), bi::pack_bf16x2(y[2], y[3]));
-            *reinterpret_cast<uint2*>(dst + kHalf + i0) =
-                make_uint2(bi::pack_bf16x2(y[4], y[5]), bi::pack_bf16x2(y[6], y[7]));
+            if constexpr (kKv4) {
+                // whether either head of the pair is a k or a v head is the same for
+                // every lane; the other half's lanes only take part in the exchanges
+                const int l = lane & 15;
+                const int first_v = a.Hq + a.Hkv;
+                const int64_t blk = page * a.Hkv;
+                if (2 * pr < first_v && 2 * pr + 1 >= a.Hq) {
+                    float k[8];
+                    unpack4(y_lo, k);
+                    unpack4(y_hi, k + 4);
+                    const bool is_k = !is_q && !is_v;
+                    bi_kv4::write_row<false>(
+                        k, static_cast<uint8_t*>(a.k_cache) + (blk + (is_k ? h - a.Hq : 0)) * bi_kv4::kBlockBytes,
+                        static_cast<int>(off), l, is_k);
+                }
+                if (2 * pr + 1 >= first_v) {
+                    const bool v_live = is_v && live;
+                    bi_kv4::write_row<true>(
+                        x, static_cast<uint8_t*>(a.v_cache) + (blk + (v_live ? h - first_v : 0)) * bi_kv4::kBlockBytes,
+                        static_cast<int>(off), l, v_live);
+                }
+            }
         }
     }
 }
@@ -204,15 +232,18 @@ __global__ void silu_mul_kernel(const __nv_bfloat16* __restrict__ gu, int64_t ld
 
 }  // namespace
 
-extern "C" bi_status bi_qk_norm_rope_append(const void* qkv, int64_t ld_qkv, int32_t T, int32_t Hq,
-                                            int32_t Hkv, int32_t D, const int32_t* positions,
-                                            const int32_t* slots, const float* rope_table,
-                                            int32_t max_pos, const void* q_norm_w,
-                                            const void* k_norm_w, float eps, void* q_out,
-                                            void* k_cache, void* v_cache, int32_t num_pages,
-                                            int32_t page_size, cudaStream_t stream) {
+namespace {
+
+bi_status launch_qk_norm_rope_append(bool kv4, const void* qkv, int64_t ld_qkv, int32_t T,
+                                     int32_t Hq, int32_t Hkv, int32_t D, const int32_t* positions,
+                                     const int32_t* slots, const float* rope_table, int32_t max_pos,
+                                     const void* q_norm_w, const void* k_norm_w, float eps,
+                                     void* q_out, void* k_cache, void* v_cache, int32_t num_pages,
+                                     int32_t page_size, cudaStream_t stream) {
     if (T < 0 || Hq <= 0 || Hkv <= 0 || max_pos < 1 || num_pages < 1) return BI_ERR_INVALID_ARG;
     if (D != kD || page_size != BI_PAGE_SIZE) return BI_ERR_UNSUPPORTED_SHAPE;
+    if (kv4 && static_cast<int64_t>(num_pages) * Hkv * BI_PAGE_SIZE >= (int64_t{1} << 31))
+        return BI_ERR_UNSUPPORTED_SHAPE;
     if (ld_qkv < static_cast<int64_t>(Hq + 2 * Hkv) * kD) return BI_ERR_INVALID_ARG;
     if (ld_qkv & 7) return BI_ERR_MISALIGNED;
     if (!(eps >= 0.f) || !std::isfinite(eps)) return BI_ERR_INVALID_ARG;
@@ -237,15 +268,41 @@ extern "C" bi_status bi_qk_norm_rope_append(const void* qkv, int64_t ld_qkv, int
     a.k_norm_w = static_cast<const __nv_bfloat16*>(k_norm_w);
     a.eps = eps;
     a.q_out = static_cast<__nv_bfloat16*>(q_out);
-    a.k_cache = static_cast<__nv_bfloat16*>(k_cache);
-    a.v_cache = static_cast<__nv_bfloat16*>(v_cache);
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
     a.num_slots = static_cast<int64_t>(num_pages) * page_size;
     a.page_size = page_size;
     a.err = bi::device_error_word();
-    return bi::launch_pdl(qk_norm_rope_append_kernel, dim3(static_cast<unsigned>(T)),
-                          dim3(kRopeWarps * 32), 0, stream, a) == cudaSuccess
+    return bi::launch_pdl(kv4 ? qk_norm_rope_append_kernel<true> : qk_norm_rope_append_kernel<false>,
+                          dim3(static_cast<unsigned>(T)), dim3(kRopeWarps * 32), 0, stream, a) == cudaSuccess
                ? BI_OK
                : BI_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" bi_status bi_qk_norm_rope_append(const void* qkv, int64_t ld_qkv, int32_t T, int32_t Hq,
+                                            int32_t Hkv, int32_t D, const int32_t* positions,
+                                            const int32_t* slots, const float* rope_table,
+                                            int32_t max_pos, const void* q_norm_w,
+                                            const void* k_norm_w, float eps, void* q_out,
+                                            void* k_cache, void* v_cache, int32_t num_pages,
+                                            int32_t page_size, cudaStream_t stream) {
+    return launch_qk_norm_rope_append(false, qkv, ld_qkv, T, Hq, Hkv, D, positions, slots,
+                                      rope_table, max_pos, q_norm_w, k_norm_w, eps, q_out, k_cache,
+                                      v_cache, num_pages, page_size, stream);
+}
+
+extern "C" bi_status bi_qk_norm_rope_append_kv4(const void* qkv, int64_t ld_qkv, int32_t T, int32_t Hq,
+                                            int32_t Hkv, int32_t D, const int32_t* positions,
+                                            const int32_t* slots, const float* rope_table,
+                                            int32_t max_pos, const void* q_norm_w,
+                                            const void* k_norm_w, float eps, void* q_out,
+                                            void* k_cache, void* v_cache, int32_t num_pages,
+                                            int32_t page_size, cudaStream_t stream) {
+    return launch_qk_norm_rope_append(true, qkv, ld_qkv, T, Hq, Hkv, D, positions, slots,
+                                      rope_table, max_pos, q_norm_w, k_norm_w, eps, q_out, k_cache,
+                                      v_cache, num_pages, page_size, stream);
 }
 
 extern "C" bi_status bi_silu_mul(const void* gate_up, int64_t ld_gate_up, int32_t T, int32_t F,

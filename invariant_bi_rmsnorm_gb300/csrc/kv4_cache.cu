@@ -1,0 +1,211 @@
+// bi_kv4_append and bi_kv4_read: writing rows of K and V into a 4-bit paged
+// cache, and reading the pages of sequences back into a bf16 one (kv4.cuh has
+// the format and its arithmetic).
+//
+// Both are per row: "Defeating Nondeterminism in LLM Inference: The Core Role
+// of Batch Invariance", section "3. Batch-Invariant Attention", asks that a
+// token's K/V be the same whichever step and batch it was written in, and here
+// a row's codes depend on its own 128 values only.
+#include <cuda_bf16.h>
+
+#include "bi_internal.h"
+#include "bi_ptx.cuh"
+#include "kv4.cuh"
+
+namespace {
+
+constexpr int kD = 128;
+constexpr int kThreads = 256;
+constexpr int kHalfWarps = kThreads / 16;
+
+struct AppendArgs {
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    int64_t ld_k, ld_v;
+    int64_t rows;  // T * Hkv
+    int Hkv;
+    const int32_t* slots;
+    uint8_t* k_cache;
+    uint8_t* v_cache;
+    int64_t num_slots;
+    uint32_t* err;
+};
+
+__device__ __forceinline__ void load_row(const __nv_bfloat16* p, int l, float (&x)[8]) {
+    const uint2 lo = *reinterpret_cast<const uint2*>(p + 4 * l);
+    const uint2 hi = *reinterpret_cast<const uint2*>(p + kD / 2 + 4 * l);
+    x[0] = __uint_as_float(lo.x << 16);
+    x[1] = __uint_as_float(lo.x & 0xffff0000u);
+    x[2] = __uint_as_float(lo.y << 16);
+    x[3] = __uint_as_float(lo.y & 0xffff0000u);
+    x[4] = __uint_as_float(hi.x << 16);
+    x[5] = __uint_as_float(hi.x & 0xffff0000u);
+    x[6] = __uint_as_float(hi.y << 16);
+    x[7] = __uint_as_float(hi.y & 0xffff0000u);
+}
+
+// One half-warp per (token, kv-head): its K row and its V row.
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {
+    bi::launch_dependents();
+    bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
+    const int l = threadIdx.x & 15;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kHalfWarps + (threadIdx.x >> 4);
+    bool live = row < a.rows;
+    const int64_t t = live ? row / a.Hkv : 0;
+    const int h = live ? static_cast<int>(row - t * a.Hkv) : 0;
+    const int64_t slot = a.slots[t];
+    if (slot < 0 || slot >= a.num_slots) {
+        if (live && l == 0 && h == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
+        live = false;
+    }
+    float xk[8], xv[8];
+    load_row(a.k + t * a.ld_k + h * kD, l, xk);
+    load_row(a.v + t * a.ld_v + h * kD, l, xv);
+    const int off = live ? static_cast<int>(slot % BI_PAGE_SIZE) : 0;
+    const int64_t block = live ? (slot / BI_PAGE_SIZE) * a.Hkv + h : 0;
+    bi_kv4::write_row<false>(xk, a.k_cache + block * bi_kv4::kBlockBytes, off, l, live);
+    bi_kv4::write_row<true>(xv, a.v_cache + block * bi_kv4::kBlockBytes, off, l, live);
+}
+
+struct ReadArgs {
+    const uint8_t* k_cache;
+    const uint8_t* v_cache;
+    const int32_t* block_table;
+    int max_pages_per_seq;
+    const int32_t* seq_lens;
+    int Hkv, num_pages, max_seq_len;
+    __nv_bfloat16* k_out;
+    __nv_bfloat16* v_out;
+    uint32_t* err;
+};
+
+// One CTA per (sequence, page): thread (r, c) writes dims 8c .. 8c + 7 of
+// token r, for every kv-head in turn.
+__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
+    bi::launch_dependents();
+    bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
+    const int s = blockIdx.y, p = blockIdx.x;
+    const int L = a.seq_lens[s];
+    if (L < 0 || L > a.max_seq_len) {
+        if (threadIdx.x == 0 && p == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
+        return;
+    }
+    if (p * BI_PAGE_SIZE >= L) return;
+    const int pg = a.block_table[static_cast<int64_t>(s) * a.max_pages_per_seq + p];
+    if (pg < 0 || pg >= a.num_pages) {
+        if (threadIdx.x == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
+        return;
+    }
+    const int r = threadIdx.x >> 4, c = threadIdx.x & 15;
+    if (r >= L - p * BI_PAGE_SIZE) return;  // rows behind the sequence stay as they were
+    for (int h = 0; h < a.Hkv; ++h) {
+        const int64_t blk = static_cast<int64_t>(pg) * a.Hkv + h;
+        const int64_t out = (blk * BI_PAGE_SIZE + r) * kD + 8 * c;
+        const int sb = bi_kv4::kScaleOffset + bi_kv4::kScaleRowBytes * r + 2 * (c >> 2);
+        {
+            const uint8_t* b = a.k_cache + blk * bi_kv4::kBlockBytes;
+            const uint32_t sc = *reinterpret_cast<const uint16_t*>(b + sb);
+            const bi_kv4::ScalePair sp = bi_kv4::scale_pair(sc | (sc << 16));
+            uint32_t o[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                o[t] = bi_kv4::kv4_pair(
+                    *reinterpret_cast<const uint32_t*>(b + 64 * r + 16 * t + 4 * (c >> 2)), c & 3, sp);
+            *reinterpret_cast<uint4*>(a.k_out + out) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        {
+            const uint8_t* b = a.v_cache + blk * bi_kv4::kBlockBytes;
+            const uint32_t sc = *reinterpret_cast<const uint16_t*>(b + sb);
+            const bi_kv4::ScalePair sp = bi_kv4::scale_pair(sc | (sc << 16));
+            uint32_t o[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                // dims 8c + 2t and 8c + 2t + 1: code c % 8 of words g = 2t, 2t + 1
+                const uint8_t* q = b + 512 * (r >> 3) + 128 * t + 8 * (r & 7) + 4 * (c >> 3);
+                const uint32_t w0 = *reinterpret_cast<const uint32_t*>(q) >> (4 * (c & 7));
+                const uint32_t w1 = *reinterpret_cast<const uint32_t*>(q + 64) >> (4 * (c & 7));
+                o[t] = bi_kv4::kv4_pair((w0 & 15u) | (w1 << 16), 0, sp);
+            }
+            *reinterpret_cast<uint4*>(a.v_out + out) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+}  // namespace
+
+extern "C" bi_status bi_kv4_append(const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                                   int32_t T, int32_t Hkv, int32_t D, const int32_t* slots,
+                                   void* k_cache, void* v_cache, int32_t num_pages,
+                                   int32_t page_size, cudaStream_t stream) {
+    if (T < 0 || Hkv <= 0 || num_pages < 1) return BI_ERR_INVALID_ARG;
+    if (D != kD || page_size != BI_PAGE_SIZE) return BI_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<int64_t>(num_pages) * Hkv * BI_PAGE_SIZE >= (int64_t{1} << 31))
+        return BI_ERR_UNSUPPORTED_SHAPE;
+    const int64_t width = static_cast<int64_t>(Hkv) * kD;
+    if (ld_k < width || ld_v < width) return BI_ERR_INVALID_ARG;
+    if ((ld_k & 7) || (ld_v & 7)) return BI_ERR_MISALIGNED;
+    const int64_t rows = static_cast<int64_t>(T) * Hkv;
+    const int64_t ctas = (rows + kHalfWarps - 1) / kHalfWarps;
+    if (ctas > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return BI_OK;
+    if (!k || !v || !slots || !k_cache || !v_cache) return BI_ERR_INVALID_ARG;
+    if (!bi::aligned16(k) || !bi::aligned16(v) || !bi::aligned16(k_cache) ||
+        !bi::aligned16(v_cache) || misaligned4(slots))
+        return BI_ERR_MISALIGNED;
+    AppendArgs a;
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.ld_k = ld_k;
+    a.ld_v = ld_v;
+    a.rows = rows;
+    a.Hkv = Hkv;
+    a.slots = slots;
+    a.k_cache = static_cast<uint8_t*>(k_cache);
+    a.v_cache = static_cast<uint8_t*>(v_cache);
+    a.num_slots = static_cast<int64_t>(num_pages) * BI_PAGE_SIZE;
+    a.err = bi::device_error_word();
+    return bi::launch_pdl(kv4_append_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0,
+                          stream, a) == cudaSuccess
+               ? BI_OK
+               : BI_ERR_CUDA;
+}
+
+extern "C" bi_status bi_kv4_read(const void* k_cache, const void* v_cache,
+                                 const int32_t* block_table, int32_t max_pages_per_seq,
+                                 const int32_t* seq_lens, int32_t S, int32_t Hkv, int32_t D,
+                                 int32_t page_size, int32_t num_pages, int32_t max_seq_len,
+                                 void* k_out, void* v_out, cudaStream_t stream) {
+    if (S < 0 || Hkv <= 0 || max_pages_per_seq < 1 || num_pages < 1 || max_seq_len < 1)
+        return BI_ERR_INVALID_ARG;
+    if (D != kD || page_size != BI_PAGE_SIZE) return BI_ERR_UNSUPPORTED_SHAPE;
+    if (S > 65535) return BI_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<int64_t>(num_pages) * Hkv * BI_PAGE_SIZE >= (int64_t{1} << 31))
+        return BI_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<int64_t>(max_seq_len) > static_cast<int64_t>(max_pages_per_seq) * BI_PAGE_SIZE)
+        return BI_ERR_INVALID_ARG;
+    if (S == 0) return BI_OK;
+    if (!k_cache || !v_cache || !block_table || !seq_lens || !k_out || !v_out)
+        return BI_ERR_INVALID_ARG;
+    if (!bi::aligned16(k_cache) || !bi::aligned16(v_cache) || !bi::aligned16(k_out) ||
+        !bi::aligned16(v_out) || misaligned4(block_table) || misaligned4(seq_lens))
+        return BI_ERR_MISALIGNED;
+    ReadArgs a;
+    a.k_cache = static_cast<const uint8_t*>(k_cache);
+    a.v_cache = static_cast<const uint8_t*>(v_cache);
+    a.block_table = block_table;
+    a.max_pages_per_seq = max_pages_per_seq;
+    a.seq_lens = seq_lens;
+    a.Hkv = Hkv;
+    a.num_pages = num_pages;
+    a.max_seq_len = max_seq_len;
+    a.k_out = static_cast<__nv_bfloat16*>(k_out);
+    a.v_out = static_cast<__nv_bfloat16*>(v_out);
+    a.err = bi::device_error_word();
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(max_seq_len) + BI_PAGE_SIZE - 1) / BI_PAGE_SIZE),
+                    static_cast<unsigned>(S));
+    return bi::launch_pdl(kv4_read_kernel, grid, dim3(kThreads), 0, stream, a) == cudaSuccess
+               ? BI_OK
+               : BI_ERR_CUDA;
+}

@@ -1,0 +1,370 @@
+// bi_logprobs_top: the log-sum-exp and target log-probability of a logits row
+// (bi_logprobs' bits for logits within +-1024), the entropy of its softmax, and
+// its k largest logits as token ids and log-probabilities (equal logits: the
+// lower id first).
+//
+// "Defeating Nondeterminism in LLM Inference: The Core Role of Batch
+// Invariance", section "Experimental Validation and Future Prospects" (true
+// on-policy RL): what a sampler reports of a token must not depend on the
+// batch.  One row per CTA; every reduction's order is fixed by the vocabulary
+// size, and which logits are the k largest does not depend on any order.
+//
+// One pass over the row (HBM), as bi_logprobs: thread t folds its vectors t,
+// t + 256, ... into (m, s) with the same operations, and beside them
+//     T = sum_j 2^(d_j) d_j,   d_j = (x_j - m) log2(e)          (fp32)
+// (m' = m + D moves d by -D log2(e): T' = (T + (m - m') log2(e) s) 2^(..)), so
+//     entropy = -sum p ln p = ln S - ln 2 * T / S,
+// in which nothing cancels: ln S >= 0 and T <= 0.
+//
+// The k largest: the pass also keeps the maximum of every segment (a few
+// consecutive vectors of one thread) in shared memory.  The k-th largest of
+// the 256 threads' maxima is at most the k-th largest logit, and few logits
+// reach it (a little over k for a row without order): only segments whose
+// maximum reaches it are read again (L2) and their logits at or above it
+// become candidates, ranked by counting.  Rows with too many candidates
+// (thousands of equal logits, as in a masked vocabulary) find the k-th largest
+// value itself by bisection over the 16-bit values, then the lowest ids among
+// its equals by a scan in id order.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "bi_internal.h"
+#include "bi_ptx.cuh"
+#include "logprobs.cuh"
+
+namespace {
+
+using bi_lp::kLog2e;
+using bi_lp::kThreads;
+
+constexpr int kUnroll = 4;     // vectors in flight per thread
+constexpr int kSegs = 32;      // segments per thread, at most
+constexpr int kMaxTop = 32;
+constexpr int kMaxCand = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNear = 1024.f;  // maxima up to here: d by one fma
+constexpr uint32_t kNegInf2 = 0xFF80FF80u;  // two bf16 -inf
+
+// A bf16 value as a 16-bit number of the same order; both zeros alike, NaN
+// below every number.
+__device__ __forceinline__ uint32_t key_of(uint32_t bits) {
+    if ((bits & 0x7FFFu) > 0x7F80u) return 0u;
+    if (bits == 0x8000u) bits = 0u;
+    return bits & 0x8000u ? 0xFFFFu & ~bits : bits | 0x8000u;
+}
+
+__device__ __forceinline__ float value_of(uint32_t key) {
+    if (key == 0u) return __uint_as_float(0x7FFFFFFFu);
+    return __uint_as_float((key & 0x8000u ? key & 0x7FFFu : 0xFFFFu & ~key) << 16);
+}
+
+struct Run {
+    float m, mc, s, t;
+};
+
+__device__ __forceinline__ void add_term(Run& r, float d) {
+    const float p = bi_lp::ex2_term(d);
+    r.s = __fadd_rn(r.s, p);
+    // p is 0 from d = -127 down; the bound keeps 0 * -inf (a masked logit) out
+    r.t = __fmaf_rn(p, fmaxf(d, -127.f), r.t);
+}
+
+// (a - b) log2(e) for a <= b, by which d falls as the maximum goes from a to
+// b; bounded where 2^.. is 0 anyway, so that 0 times it stays 0
+__device__ __forceinline__ float moved(float a, float b) {
+    return fmaxf(__fmul_rn(__fsub_rn(a, b), kLog2e), -1024.f);
+}
+
+// fold_vec of logprobs.cu with T beside s.  Returns the vector's maximum.  One
+// fma for d leaves it off by the rounding of m log2(e), the same for every term
+// of that maximum (so it cancels in the entropy) and below 2^-14 for |m| <=
+// 1024.  Past that -- logits no model gives, but a thread may see nothing else
+// than a mask's -1e9 or bf16's lowest value, whose m log2(e) is not even finite
+// -- d is taken from the difference, which is exact where it counts.
+__device__ __forceinline__ float fold_vec_t(Run& r, const uint4& u) {
+    const float x[8] = {bi_lp::lo16(u.x), bi_lp::hi16(u.x), bi_lp::lo16(u.y), bi_lp::hi16(u.y),
+                        bi_lp::lo16(u.z), bi_lp::hi16(u.z), bi_lp::lo16(u.w), bi_lp::hi16(u.w)};
+    float vm = x[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) vm = fmaxf(vm, x[e]);
+    if (vm == -INFINITY) return vm;  // nothing visible in this vector
+    if (vm > r.m) {
+        const float f = bi_lp::rescale(r.m, vm);
+        r.t = __fmul_rn(__fmaf_rn(moved(r.m, vm), r.s, r.t), f);
+        r.s = __fmul_rn(r.s, f);  // m = -inf: s is 0 and stays 0
+        r.m = vm;
+        r.mc = __fmul_rn(vm, kLog2e);
+    }
+    if (fabsf(r.m) <= kNear) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) add_term(r, __fmaf_rn(x[e], kLog2e, -r.mc));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) add_term(r, __fmul_rn(__fsub_rn(x[e], r.m), kLog2e));
+    }
+    return vm;
+}
+
+// combine of logprobs.cu with T beside s.
+__device__ __forceinline__ void combine_t(Run& a, float m2, float s2, float t2) {
+    const float M = fmaxf(a.m, m2);
+    if (M == -INFINITY) return;  // both empty
+    const float f1 = bi_lp::rescale(a.m, M), f2 = bi_lp::rescale(m2, M);
+    a.t = __fadd_rn(__fmul_rn(__fmaf_rn(moved(a.m, M), a.s, a.t), f1),
+                    __fmul_rn(__fmaf_rn(moved(m2, M), s2, t2), f2));
+    a.s = __fadd_rn(__fmul_rn(a.s, f1), __fmul_rn(s2, f2));
+    a.m = M;
+}
+
+struct TopArgs {
+    const __nv_bfloat16* logits;
+    int64_t ld;
+    int vocab;
+    const int32_t* targets;
+    float* logprob_out;
+    float* lse_out;
+    float* entropy_out;
+    int k;
+    int seg_vecs;  // vectors of one thread in one segment (a multiple of kUnroll)
+    int32_t* top_ids;
+    float* top_logprobs;
+    uint32_t* err;
+};
+
+// Sum of one int over the CTA, in every thread.
+__device__ __forceinline__ int block_sum(int v, int* red) {
+    v = __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) n += red[w];
+    return n;
+}
+
+// f(id, key) for the logits of this thread's segments whose maximum reaches
+// `least` and that reach it themselves.
+template <typename F>
+__device__ __forceinline__ void each_reaching(const uint4* xv, int nvec, int seg_vecs,
+                                              const uint16_t* seg_max, uint32_t least, F f) {
+    const int tid = threadIdx.x;
+    for (int sg = 0; sg * seg_vecs * kThreads < nvec; ++sg) {
+        if (seg_max[sg * kThreads + tid] < least) continue;
+        for (int i = 0; i < seg_vecs; ++i) {
+            const int v = (sg * seg_vecs + i) * kThreads + tid;
+            if (v >= nvec) break;
+            const uint4 u = xv[v];
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t key = key_of((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+                if (key >= least) f(8 * v + e, key);
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) logprobs_top_kernel(const TopArgs a) {
+    bi::launch_dependents();
+    bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
+    __shared__ uint16_t seg_max[kSegs * kThreads];
+    __shared__ uint16_t thread_max[kThreads];
+    __shared__ unsigned long long cand[kMaxCand];  // key above, ~id below: larger is better
+    __shared__ float red_m[kWarps], red_s[kWarps], red_t[kWarps];
+    __shared__ int red[kWarps];
+    __shared__ float lse_s;
+    __shared__ uint32_t thr_s;
+    __shared__ int ncand;
+    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x;
+    const int lane = tid & 31, warp = tid >> 5;
+    const __nv_bfloat16* x = a.logits + row * a.ld;
+    const uint4* xv = reinterpret_cast<const uint4*>(x);
+    const int nvec = a.vocab / 8;
+
+    // ---- one pass: (m, s, T) and the segments' maxima ----
+    Run r = {-INFINITY, -INFINITY, 0.f, 0.f};
+    uint32_t best = 0;
+    for (int sg = 0; sg * a.seg_vecs * kThreads < nvec; ++sg) {
+        float sm = -INFINITY;
+        for (int i0 = 0; i0 < a.seg_vecs; i0 += kUnroll) {
+            uint4 u[kUnroll];
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                const int v = (sg * a.seg_vecs + i0 + i) * kThreads + tid;
+                u[i] = v < nvec ? xv[v] : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
+            }
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) sm = fmaxf(sm, fold_vec_t(r, u[i]));
+        }
+        const uint32_t key = key_of(__float_as_uint(sm) >> 16);
+        seg_max[sg * kThreads + tid] = static_cast<uint16_t>(key);
+        best = max(best, key);
+    }
+    thread_max[tid] = static_cast<uint16_t>(best);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, r.m, o);
+        const float s2 = __shfl_xor_sync(0xffffffffu, r.s, o);
+        const float t2 = __shfl_xor_sync(0xffffffffu, r.t, o);
+        combine_t(r, m2, s2, t2);
+    }
+    if (lane == 0) {
+        red_m[warp] = r.m;
+        red_s[warp] = r.s;
+        red_t[warp] = r.t;
+    }
+    if (tid == 0) ncand = 0;
+    __syncthreads();
+    if (tid == 0) {
+        Run c = {red_m[0], 0.f, red_s[0], red_t[0]};
+        for (int i = 1; i < kWarps; ++i) combine_t(c, red_m[i], red_s[i], red_t[i]);
+        const float ls = logf(c.s);
+        const float lse = __fadd_rn(c.m, ls);
+        lse_s = lse;
+        if (a.lse_out) a.lse_out[row] = lse;
+        if (a.entropy_out) a.entropy_out[row] = __fsub_rn(ls, __fmul_rn(kLn2, __fdiv_rn(c.t, c.s)));
+        if (a.targets && a.logprob_out) {
+            const int t = a.targets[row];
+            if (t < 0 || t >= a.vocab) {
+                bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
+                a.logprob_out[row] = NAN;
+            } else {
+                a.logprob_out[row] = __fsub_rn(__bfloat162float(x[t]), lse);
+            }
+        }
+    }
+
+    // ---- the k-th largest of the threads' maxima ----
+    {
+        int rank = 0;
+        for (int i = 0; i < kThreads; ++i) {
+            const uint32_t o = thread_max[i];
+            rank += o > best || (o == best && i < tid);
+        }
+        if (rank == a.k - 1) thr_s = best;
+    }
+    __syncthreads();
+    // a maximum of -inf may be that of a thread without logits, or with NaN only:
+    // then every logit is a candidate
+    const uint32_t thr = thr_s <= 0x007Fu ? 0u : thr_s;
+
+    // ---- candidates: every logit at or above it ----
+    each_reaching(xv, nvec, a.seg_vecs, seg_max, thr, [&](int id, uint32_t key) {
+        const int at = atomicAdd(&ncand, 1);
+        if (at < kMaxCand)
+            cand[at] = (static_cast<unsigned long long>(key) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id));
+    });
+    __syncthreads();
+    int n = ncand;
+    if (n > kMaxCand) {
+        // the k-th largest value: the largest key that k logits reach
+        uint32_t lo = thr, hi = 0x10000u;  // reached by k and more; by fewer
+        while (hi - lo > 1) {
+            const uint32_t mid = (lo + hi) / 2;
+            int mine = 0;
+            each_reaching(xv, nvec, a.seg_vecs, seg_max, mid, [&](int, uint32_t) { ++mine; });
+            if (block_sum(mine, red) >= a.k) lo = mid;
+            else hi = mid;
+        }
+        __syncthreads();
+        if (tid == 0) ncand = 0;
+        __syncthreads();
+        // fewer than k lie above it ...
+        each_reaching(xv, nvec, a.seg_vecs, seg_max, lo + 1, [&](int id, uint32_t key) {
+            cand[atomicAdd(&ncand, 1)] =
+                (static_cast<unsigned long long>(key) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id));
+        });
+        __syncthreads();
+        n = ncand;
+        // ... and the lowest ids among its equals fill the rest
+        for (int v0 = 0; v0 < nvec && n < a.k; v0 += kThreads) {
+            const int v = v0 + tid;
+            const bool may = v < nvec && seg_max[(v0 / kThreads / a.seg_vecs) * kThreads + tid] >= lo;
+            if (!__syncthreads_or(may)) continue;
+            uint32_t eq = 0;
+            if (may) {
+                const uint4 u = xv[v];
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    eq |= (key_of((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) == lo ? 1u : 0u) << e;
+            }
+            const int mine = __popc(eq);
+            int before = mine;  // inclusive prefix over the warp
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, before, o);
+                if (lane >= o) before += y;
+            }
+            if (lane == 31) red[warp] = before;
+            __syncthreads();
+            int at = n + before - mine, total = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) at += red[w];
+                total += red[w];
+            }
+            for (uint32_t left = eq; left && at < a.k; left &= left - 1, ++at)
+                cand[at] = (static_cast<unsigned long long>(lo) << 32) |
+                           (0xFFFFFFFFu - static_cast<uint32_t>(8 * v + __ffs(left) - 1));
+            n = min(a.k, n + total);
+            __syncthreads();  // red is written again
+        }
+        __syncthreads();
+    }
+
+    // ---- rank the candidates: no two compare equal ----
+    const float lse = lse_s;
+    for (int i = tid; i < n; i += kThreads) {
+        const unsigned long long c = cand[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += cand[j] > c;
+        if (rank < a.k) {
+            a.top_ids[row * a.k + rank] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(c));
+            a.top_logprobs[row * a.k + rank] = __fsub_rn(value_of(static_cast<uint32_t>(c >> 32)), lse);
+        }
+    }
+}
+
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+}  // namespace
+
+extern "C" bi_status bi_logprobs_top(const void* logits, int64_t rows, int32_t vocab, int64_t ld,
+                                     const int32_t* targets, float* logprob_out, float* lse_out,
+                                     float* entropy_out, int32_t k, int32_t* top_ids,
+                                     float* top_logprobs, cudaStream_t stream) {
+    if (rows < 0 || rows > 0x7fffffffLL || k < 1) return BI_ERR_INVALID_ARG;
+    if (vocab < 8 || (vocab & 7) || vocab > (1 << 30) || k > kMaxTop || k > vocab)
+        return BI_ERR_UNSUPPORTED_SHAPE;
+    if (ld < vocab) return BI_ERR_INVALID_ARG;
+    if (ld & 7) return BI_ERR_MISALIGNED;
+    if (rows == 0) return BI_OK;
+    if (!logits || !top_ids || !top_logprobs || (targets != nullptr) != (logprob_out != nullptr))
+        return BI_ERR_INVALID_ARG;
+    if (!bi::aligned16(logits) || misaligned4(targets) || misaligned4(logprob_out) ||
+        misaligned4(lse_out) || misaligned4(entropy_out) || misaligned4(top_ids) ||
+        misaligned4(top_logprobs))
+        return BI_ERR_MISALIGNED;
+    const int64_t per_thread = (vocab / 8 + kThreads - 1) / kThreads;
+    TopArgs a;
+    a.logits = static_cast<const __nv_bfloat16*>(logits);
+    a.ld = ld;
+    a.vocab = vocab;
+    a.targets = targets;
+    a.logprob_out = logprob_out;
+    a.lse_out = lse_out;
+    a.entropy_out = entropy_out;
+    a.k = k;
+    a.seg_vecs = static_cast<int>(kUnroll * ((per_thread + kUnroll * kSegs - 1) / (kUnroll * kSegs)));
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.err = bi::device_error_word();
+    return bi::launch_pdl(logprobs_top_kernel, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0,
+                          stream, a) == cudaSuccess
+               ? BI_OK
+               : BI_ERR_CUDA;
+}
