@@ -90,6 +90,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 __device__ __forceinline__ uint32_t lo_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 
+// The values of the codes at bits 4p .. 4p + 3 of both halves of w, p = 0 .. 3.
+__device__ __forceinline__ void four_pairs(uint32_t (&v)[4], uint32_t w, const ScalePair& sp) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) v[p] = bi_kv4::kv4_pair(w, p, sp);
+}
+
 // bi_attn::page_scores over a 4-bit K block.
 __device__ __forceinline__ void page_scores_kv4(float (&sc)[4], const uint8_t* kb,
                                                 const uint32_t (&qb0)[8], const uint32_t (&qb1)[8],
@@ -105,52 +111,80 @@ __device__ __forceinline__ void page_scores_kv4(float (&sc)[4], const uint8_t* k
 #pragma unroll
     for (int j = 0; j < 4; ++j) {  // the group of dims 32j .. 32j + 31: two 16-deep steps
         const uint32_t da = j < 2 ? sa.x : sa.y, db = j < 2 ? sb.x : sb.y;
-        const ScalePair pa = bi_kv4::scale_pair(j & 1 ? hi_halves(da, da) : lo_halves(da, da));
-        const ScalePair pb = bi_kv4::scale_pair(j & 1 ? hi_halves(db, db) : lo_halves(db, db));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int ks = 2 * j + e;
-            bi::mma_bf16_16816(sc, bi_kv4::kv4_pair(wa[j], 2 * e, pa), bi_kv4::kv4_pair(wb[j], 2 * e, pb),
-                               bi_kv4::kv4_pair(wa[j], 2 * e + 1, pa),
-                               bi_kv4::kv4_pair(wb[j], 2 * e + 1, pb), qb0[ks], qb1[ks]);
-        }
+        uint32_t va[4], vb[4];
+        four_pairs(va, wa[j], bi_kv4::scale_pair(j & 1 ? hi_halves(da, da) : lo_halves(da, da)));
+        four_pairs(vb, wb[j], bi_kv4::scale_pair(j & 1 ? hi_halves(db, db) : lo_halves(db, db)));
+        bi::mma_bf16_16816(sc, va[0], vb[0], va[1], vb[1], qb0[2 * j], qb1[2 * j]);
+        bi::mma_bf16_16816(sc, va[2], vb[2], va[3], vb[3], qb0[2 * j + 1], qb1[2 * j + 1]);
     }
 }
 
-// The values of the 32 dims of group `gr` of a V block, as the A operands of
-// their two 16-dim tiles: a[i][0..3].  Tokens from `valid` on stand for zeros,
-// whatever the block holds there.
-__device__ __forceinline__ void v_operands(uint32_t (&a)[2][4], const uint8_t* vb, int gr, int valid,
-                                           int lane) {
-    // this lane's tokens 2(l%4), 2(l%4) + 1 and the two 8 further on
-    const uint4 ca = *reinterpret_cast<const uint4*>(vb + 16 * lane);
-    const uint4 cb = *reinterpret_cast<const uint4*>(vb + 512 + 16 * lane);
-    const uint8_t* sp = vb + kScaleOffset + 2 * kScaleRowBytes * (lane & 3) + 4 * (gr >> 1);
-    uint32_t s0 = *reinterpret_cast<const uint32_t*>(sp);
-    uint32_t s1 = *reinterpret_cast<const uint32_t*>(sp + kScaleRowBytes);
-    uint32_t s8 = *reinterpret_cast<const uint32_t*>(sp + 8 * kScaleRowBytes);
-    uint32_t s9 = *reinterpret_cast<const uint32_t*>(sp + 9 * kScaleRowBytes);
+// A page's scores in log2 units (bi_attn::softmax_step's x); tokens from
+// `valid` on are not there.
+__device__ __forceinline__ void page_logs(float (&x)[4], const uint8_t* kb, const uint32_t (&qb0)[8],
+                                          const uint32_t (&qb1)[8], int valid, float scale_log2,
+                                          int lane) {
+    page_scores_kv4(x, kb, qb0, qb1, lane);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __fmul_rn(x[e], scale_log2);
+    if (valid < kPage) {
+        if ((lane >> 2) >= valid) x[0] = x[1] = -INFINITY;
+        if ((lane >> 2) + 8 >= valid) x[2] = x[3] = -INFINITY;
+    }
+}
+
+// A page's weights p (tokens l/4, l/4 + 8; two columns each), split into bf16
+// high part and remainder and transposed into mma B fragments.
+__device__ __forceinline__ void split_weights(const float (&p)[4], bi_attn::PFrags& pf) {
+    const uint32_t pA = bi::pack_bf16x2(p[0], p[1]);
+    const uint32_t pB = bi::pack_bf16x2(p[2], p[3]);
+    const uint32_t rA = bi::pack_bf16x2(__fsub_rn(p[0], __uint_as_float(pA << 16)),
+                                        __fsub_rn(p[1], __uint_as_float(pA & 0xffff0000u)));
+    const uint32_t rB = bi::pack_bf16x2(__fsub_rn(p[2], __uint_as_float(pB << 16)),
+                                        __fsub_rn(p[3], __uint_as_float(pB & 0xffff0000u)));
+    pf.hi0 = bi::movmatrix_trans(pA);
+    pf.hi1 = bi::movmatrix_trans(pB);
+    pf.lo0 = bi::movmatrix_trans(rA);
+    pf.lo1 = bi::movmatrix_trans(rB);
+}
+
+// A lane's part of a V block: codes and scales of tokens 2(l%4) and the next
+// (a), and of the two tokens 8 further on (b).  Tokens from `valid` on stand
+// for zeros, whatever the block holds there.
+struct VFrags {
+    uint4 ca, cb, sa, sb;
+};
+
+__device__ __forceinline__ void load_v(VFrags& f, const uint8_t* vb, int valid, int lane) {
+    f.ca = *reinterpret_cast<const uint4*>(vb + 16 * lane);
+    f.cb = *reinterpret_cast<const uint4*>(vb + 512 + 16 * lane);
+    const uint8_t* sp = vb + kScaleOffset + 2 * kScaleRowBytes * (lane & 3);
+    f.sa = *reinterpret_cast<const uint4*>(sp);
+    f.sb = *reinterpret_cast<const uint4*>(sp + 8 * kScaleRowBytes);
     if (valid < kPage) {
         const int t = 2 * (lane & 3);
-        if (t >= valid) s0 = 0u;
-        if (t + 1 >= valid) s1 = 0u;
-        if (t + 8 >= valid) s8 = 0u;
-        if (t + 9 >= valid) s9 = 0u;
+        if (t >= valid) f.sa.x = f.sa.y = 0u;
+        if (t + 1 >= valid) f.sa.z = f.sa.w = 0u;
+        if (t + 8 >= valid) f.sb.x = f.sb.y = 0u;
+        if (t + 9 >= valid) f.sb.z = f.sb.w = 0u;
     }
+}
+
+// bi_attn::pv_step for the 32 dims of group `gr`: two 16-dim tiles of O^T.
+__device__ __forceinline__ void pv_group(float (&acc0)[4], float (&acc1)[4], const VFrags& f, int gr,
+                                         const bi_attn::PFrags& pf) {
     // codes of (even token, odd token) side by side; their scales likewise
-    const uint32_t e0 = gr & 2 ? ca.y : ca.x, o0 = gr & 2 ? ca.w : ca.z;
-    const uint32_t e1 = gr & 2 ? cb.y : cb.x, o1 = gr & 2 ? cb.w : cb.z;
-    const uint32_t sel = gr & 1 ? 0x7632u : 0x5410u;
-    const uint32_t wa = __byte_perm(e0, o0, sel), wb = __byte_perm(e1, o1, sel);
-    const ScalePair pa = bi_kv4::scale_pair(__byte_perm(s0, s1, sel));
-    const ScalePair pb = bi_kv4::scale_pair(__byte_perm(s8, s9, sel));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        a[i][0] = bi_kv4::kv4_pair(wa, 2 * i, pa);
-        a[i][1] = bi_kv4::kv4_pair(wa, 2 * i + 1, pa);
-        a[i][2] = bi_kv4::kv4_pair(wb, 2 * i, pb);
-        a[i][3] = bi_kv4::kv4_pair(wb, 2 * i + 1, pb);
-    }
+    const uint32_t half = gr & 1 ? 0x7632u : 0x5410u;
+    const bool up = gr & 2;
+    const uint32_t wa = __byte_perm(up ? f.ca.y : f.ca.x, up ? f.ca.w : f.ca.z, half);
+    const uint32_t wb = __byte_perm(up ? f.cb.y : f.cb.x, up ? f.cb.w : f.cb.z, half);
+    uint32_t va[4], vb[4];
+    four_pairs(va, wa, bi_kv4::scale_pair(__byte_perm(up ? f.sa.y : f.sa.x, up ? f.sa.w : f.sa.z, half)));
+    four_pairs(vb, wb, bi_kv4::scale_pair(__byte_perm(up ? f.sb.y : f.sb.x, up ? f.sb.w : f.sb.z, half)));
+    bi::mma_bf16_16816(acc0, va[0], va[1], vb[0], vb[1], pf.hi0, pf.hi1);
+    bi::mma_bf16_16816(acc0, va[0], va[1], vb[0], vb[1], pf.lo0, pf.lo1);
+    bi::mma_bf16_16816(acc1, va[2], va[3], vb[2], vb[3], pf.hi0, pf.hi1);
+    bi::mma_bf16_16816(acc1, va[2], va[3], vb[2], vb[3], pf.lo0, pf.lo1);
 }
 
 // One butterfly for the two columns of every lane over the 8 lanes that share
@@ -245,14 +279,7 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
         for (int i = 0; i < kPagesPerWarp; ++i) {
             const int p = warp + kWarps * i;
             if (p >= np) break;
-            page_scores_kv4(x[i], ks + p * kBlockBytes, qb0, qb1, lane);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[i][e] = __fmul_rn(x[i][e], a.scale_log2);
-            const int valid = tokens - p * kPage;
-            if (valid < kPage) {
-                if ((lane >> 2) >= valid) x[i][0] = x[i][1] = -INFINITY;
-                if ((lane >> 2) + 8 >= valid) x[i][2] = x[i][3] = -INFINITY;
-            }
+            page_logs(x[i], ks + p * kBlockBytes, qb0, qb1, tokens - p * kPage, a.scale_log2, lane);
             const float mx = reduce_columns(fmaxf(x[i][0], x[i][2]), fmaxf(x[i][1], x[i][3]), lane,
                                             [](float u, float v) { return fmaxf(u, v); });
             if (lane < 8) tb.pmax[p][2 * (lane & 3) + (lane >> 2)] = mx;
@@ -300,19 +327,12 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
         const int p = warp + kWarps * i;
         if (p >= np) break;
         const float2 m = *reinterpret_cast<const float2*>(&tb.ref[p][2 * (lane & 3)]);
-        const float p0 = bi_attn::exp2_ftz(__fsub_rn(x[i][0], m.x));
-        const float p1 = bi_attn::exp2_ftz(__fsub_rn(x[i][1], m.y));
-        const float p2 = bi_attn::exp2_ftz(__fsub_rn(x[i][2], m.x));
-        const float p3 = bi_attn::exp2_ftz(__fsub_rn(x[i][3], m.y));
-        const uint32_t pA = bi::pack_bf16x2(p0, p1);
-        const uint32_t pB = bi::pack_bf16x2(p2, p3);
-        const uint32_t rA = bi::pack_bf16x2(__fsub_rn(p0, __uint_as_float(pA << 16)),
-                                            __fsub_rn(p1, __uint_as_float(pA & 0xffff0000u)));
-        const uint32_t rB = bi::pack_bf16x2(__fsub_rn(p2, __uint_as_float(pB << 16)),
-                                            __fsub_rn(p3, __uint_as_float(pB & 0xffff0000u)));
-        weights[p * 32 + lane] = make_uint4(bi::movmatrix_trans(pA), bi::movmatrix_trans(pB),
-                                            bi::movmatrix_trans(rA), bi::movmatrix_trans(rB));
-        const float ps = reduce_columns(__fadd_rn(p0, p2), __fadd_rn(p1, p3), lane,
+        const float w[4] = {bi_attn::exp2_ftz(__fsub_rn(x[i][0], m.x)), bi_attn::exp2_ftz(__fsub_rn(x[i][1], m.y)),
+                            bi_attn::exp2_ftz(__fsub_rn(x[i][2], m.x)), bi_attn::exp2_ftz(__fsub_rn(x[i][3], m.y))};
+        bi_attn::PFrags pf;
+        split_weights(w, pf);
+        weights[p * 32 + lane] = make_uint4(pf.hi0, pf.hi1, pf.lo0, pf.lo1);
+        const float ps = reduce_columns(__fadd_rn(w[0], w[2]), __fadd_rn(w[1], w[3]), lane,
                                         [](float u, float v) { return __fadd_rn(u, v); });
         if (lane < 8) tb.psum[p][2 * (lane & 3) + (lane >> 2)] = ps;
     }
@@ -330,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
     for (int i = 0; i < 2; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll 2
     for (int p = 0; p < np; ++p) {
-        uint32_t va[2][4];
-        v_operands(va, vs + p * kBlockBytes, warp, tokens - p * kPage, lane);
+        VFrags f;
+        load_v(f, vs + p * kBlockBytes, tokens - p * kPage, lane);
         const uint4 w = weights[p * 32 + lane];
         if (moved >> p & 1u) {
             const float2 al = *reinterpret_cast<const float2*>(&tb.alpha[p][2 * (lane & 3)]);
@@ -343,11 +363,7 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
                 acc[i][3] = __fmul_rn(acc[i][3], al.y);
             }
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            bi::mma_bf16_16816(acc[i], va[i][0], va[i][1], va[i][2], va[i][3], w.x, w.y);
-            bi::mma_bf16_16816(acc[i], va[i][0], va[i][1], va[i][2], va[i][3], w.z, w.w);
-        }
+        pv_group(acc[0], acc[1], f, warp, bi_attn::PFrags{w.x, w.y, w.z, w.w});
     }
     __syncthreads();  // l is there
 
@@ -382,6 +398,329 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
     // the last CTA of this (sequence, kv-head) to arrive folds it
     bi_attn::arrive_and_fold<kStagingBytes>(a, ctr, nch, s, g, nch, smem, small, tid);
 }
+
+// ---------------------------------------------------------------------------
+// The many-chunk form: one warp, alone in its CTA, per (sequence, kv-head,
+// chunk), so that nothing ever waits for another warp and a finished chunk's
+// place on the SM is taken at once.  Pages come through a ring of kRing
+// stages; while a page's weights and output products are under way the next
+// page's scores are formed (they depend on nothing before them).
+
+constexpr int kRing = 4;  // pages in flight
+constexpr int kLoadBytes = 2 * kBlockBytes;
+constexpr int kStageBytes = kLoadBytes + 16;  // K, V, the stage's barrier
+constexpr uint32_t kAll = 0xffffffffu;
+
+// bi_attn::ColState of two columns, as the fast path of weights_step wants it.
+struct WarpState {
+    float th[2];   // reference maximum + slack
+    float ref[2];  // reference maximum; 0 while it is -inf (then every score is
+                   // -inf so far, and so is its difference from 0)
+    float l;       // reduce_columns' column of this lane
+    float acc[8][4];
+};
+
+// The page's weights from its scores in log2 units: bi_attn::softmax_step,
+// operation by operation, without what changes nothing.  The reference maximum
+// moves on few pages only; one vote finds the others, and there neither the
+// page's maximum is formed nor O rescaled (by 1).
+__device__ __forceinline__ void weights_step(WarpState& st, const float (&x)[4], int lane,
+                                             bi_attn::PFrags& pf) {
+    float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+    float al = 1.f;
+    if (__any_sync(kAll, mx0 > st.th[0] || mx1 > st.th[1])) {
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(kAll, mx0, off));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(kAll, mx1, off));
+        }
+        const float m0 = st.th[0] == -INFINITY ? -INFINITY : st.ref[0];
+        const float m1 = st.th[1] == -INFINITY ? -INFINITY : st.ref[1];
+        const float mn0 = mx0 > st.th[0] ? mx0 : m0;
+        const float mn1 = mx1 > st.th[1] ? mx1 : m1;
+        const float al0 = mn0 == m0 ? 1.f : bi_attn::exp2_ftz(__fsub_rn(m0, mn0));
+        const float al1 = mn1 == m1 ? 1.f : bi_attn::exp2_ftz(__fsub_rn(m1, mn1));
+        al = lane & 4 ? al1 : al0;
+        st.th[0] = __fadd_rn(mn0, bi_attn::kRescaleSlack);
+        st.th[1] = __fadd_rn(mn1, bi_attn::kRescaleSlack);
+        st.ref[0] = mn0 == -INFINITY ? 0.f : mn0;
+        st.ref[1] = mn1 == -INFINITY ? 0.f : mn1;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+            st.acc[mt][0] = __fmul_rn(st.acc[mt][0], al0);
+            st.acc[mt][1] = __fmul_rn(st.acc[mt][1], al1);
+            st.acc[mt][2] = __fmul_rn(st.acc[mt][2], al0);
+            st.acc[mt][3] = __fmul_rn(st.acc[mt][3], al1);
+        }
+    }
+    const float p[4] = {bi_attn::exp2_ftz(__fsub_rn(x[0], st.ref[0])), bi_attn::exp2_ftz(__fsub_rn(x[1], st.ref[1])),
+                        bi_attn::exp2_ftz(__fsub_rn(x[2], st.ref[0])), bi_attn::exp2_ftz(__fsub_rn(x[3], st.ref[1]))};
+    split_weights(p, pf);
+    st.l = __fmaf_rn(st.l, al,
+                     reduce_columns(__fadd_rn(p[0], p[2]), __fadd_rn(p[1], p[3]), lane,
+                                    [](float u, float v) { return __fadd_rn(u, v); }));
+}
+
+// A chunk's partial as the warp kernel writes and reads it: O's dims of a row
+// in the order of the accumulators, position 16mt + 2g + i for dim 16mt + g +
+// 8i.
+__device__ __forceinline__ float* partial_o(const SplitArgs& a, int64_t row, int c) {
+    return a.ws_acc + (row * a.max_chunks + c) * kD;
+}
+
+__device__ __forceinline__ float2* partial_ml(const SplitArgs& a, int64_t row, int c) {
+    return reinterpret_cast<float2*>(a.ws_ml) + row * a.max_chunks + c;
+}
+
+// The fold of one (sequence, kv-head) by the warp that arrived last, in
+// ascending chunk order with bi_attn::attn_merge_kernel's operations.  Lane l
+// has positions 4l .. 4l + 3 of every row.  As in bi_attn::fold_sequence the
+// running maxima are a prefix maximum, taken for 32 chunks at once (lane =
+// chunk), and all factors with them; the partials of kAhead chunks are loaded
+// before the first of them is folded.
+template <int G>
+__device__ __forceinline__ void fold_warp(const SplitArgs& a, int64_t row0, int nch, float4* factors,
+                                          int lane) {
+    constexpr int kAhead = G <= 3 ? 8 : 24 / G;
+    float4 o[G];
+    float l[G], m[G];
+    for (int cb = 0; cb < nch; cb += 32) {
+        const int nb = min(32, nch - cb);
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+            const float2 ml = lane < nb ? __ldcg(partial_ml(a, row0 + h, cb + lane)) : make_float2(-INFINITY, 0.f);
+            float v = ml.x;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float u = __shfl_up_sync(kAll, v, off);
+                if (lane >= off) v = fmaxf(v, u);
+            }
+            if (cb > 0) v = fmaxf(m[h], v);  // running maximum after chunk cb + lane
+            float before = __shfl_up_sync(kAll, v, 1);
+            if (lane == 0) before = cb > 0 ? m[h] : 0.f;
+            m[h] = __shfl_sync(kAll, v, 31);
+            if (lane < nb)
+                factors[lane * G + h] = make_float4(bi_attn::exp2_ftz(before - v),
+                                                    bi_attn::exp2_ftz(ml.x - v), ml.y, 0.f);
+        }
+        __syncwarp();
+        for (int i0 = 0; i0 < nb; i0 += kAhead) {
+            float4 part[kAhead][G];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                for (int h = 0; h < G; ++h)
+                    if (i0 + u < nb)
+                        part[u][h] = __ldcg(reinterpret_cast<const float4*>(partial_o(a, row0 + h, cb + i0 + u)) + lane);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (i0 + u >= nb) break;
+#pragma unroll
+                for (int h = 0; h < G; ++h) {
+                    const float4 f = factors[(i0 + u) * G + h];
+                    if (cb + i0 + u == 0) {
+                        o[h] = part[u][h];
+                        l[h] = f.z;
+                    } else {
+                        o[h].x = bi_attn::fold_value(o[h].x, f.x, part[u][h].x, f.y);
+                        o[h].y = bi_attn::fold_value(o[h].y, f.x, part[u][h].y, f.y);
+                        o[h].z = bi_attn::fold_value(o[h].z, f.x, part[u][h].z, f.y);
+                        o[h].w = bi_attn::fold_value(o[h].w, f.x, part[u][h].w, f.y);
+                        l[h] = bi_attn::fold_value(l[h], f.x, f.z, f.y);
+                    }
+                }
+            }
+        }
+    }
+    // positions 4l .. 4l + 3: dims d, d + 8, d + 1, d + 9
+    const int d = 16 * (lane >> 2) + 2 * (lane & 3);
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+        const float il = bi_attn::inv_weight(l[h]);
+        uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (row0 + h) * kD + d);
+        out[0] = bi::pack_bf16x2(bi_attn::normalise(o[h].x, il), bi_attn::normalise(o[h].z, il));
+        out[4] = bi::pack_bf16x2(bi_attn::normalise(o[h].y, il), bi_attn::normalise(o[h].w, il));
+    }
+}
+
+__global__ void __launch_bounds__(32, 16) attn_warp_kv4_kernel(const Kv4Args ka) {
+    bi::launch_dependents();
+    bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
+    const SplitArgs& a = ka.s;
+    const int c = blockIdx.x;  // chunk
+    const int g = blockIdx.y;
+    const int s = blockIdx.z;
+    const int lane = threadIdx.x;
+
+    const int L = a.seq_lens[s];
+    if (L < 1 || L > a.max_seq_len) {
+        if (lane == 0 && c == 0 && g == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
+        return;
+    }
+    const int nch = (L + kChunk - 1) / kChunk;
+    if (c >= nch) return;
+    const int tokens = min(kChunk, L - c * kChunk);
+    const int np = (tokens + kPage - 1) / kPage;
+    // several CTAs share a longer sequence and the last one to arrive folds it
+    uint32_t* const ctr = nch > 1 ? a.counters + static_cast<int64_t>(s) * a.Hkv + g : nullptr;
+
+    __shared__ __align__(16) uint8_t ring[kRing * kStageBytes];
+    auto bar_of = [](uint8_t* stage) { return reinterpret_cast<uint64_t*>(stage + kLoadBytes); };
+
+    // lane p keeps where page p lies, and copies it when its stage is free
+    int pg = 0;
+    if (lane < np)
+        pg = a.block_table[static_cast<int64_t>(s) * a.max_pages_per_seq + c * kPagesPerChunk + lane];
+    if (__any_sync(kAll, pg < 0 || pg >= a.num_pages)) {
+        if (lane == 0) {
+            bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
+            if (nch > 1) bi_attn::arrive_bad(ctr, nch);
+        }
+        return;
+    }
+    const int64_t at = (static_cast<int64_t>(pg) * a.Hkv + g) * kBlockBytes;
+    const uint8_t* const k_src = ka.k_cache + at;
+    const uint8_t* const v_src = ka.v_cache + at;
+    if (lane < kRing) bi::mbar_init(bar_of(ring + lane * kStageBytes), 1);
+    bi::fence_mbar_init();
+    __syncwarp();
+    auto copy_page = [&](uint8_t* stage) {
+        bi::mbar_arrive_expect_tx(bar_of(stage), kLoadBytes);
+        bulk_load(stage, k_src, kBlockBytes, bar_of(stage));
+        bulk_load(stage + kBlockBytes, v_src, kBlockBytes, bar_of(stage));
+    };
+    if (lane < min(np, kRing)) copy_page(ring + lane * kStageBytes);
+
+    // column n of the mma tile = query head g*group + n (n < group)
+    const int64_t row0 = static_cast<int64_t>(s) * a.Hq + g * a.group;
+    uint32_t qb0[8], qb1[8];
+    bi_attn::load_q_frags((lane >> 2) < a.group ? a.q + (row0 + (lane >> 2)) * kD : nullptr, lane, qb0, qb1);
+
+    WarpState st;
+    st.th[0] = st.th[1] = -INFINITY;
+    st.ref[0] = st.ref[1] = 0.f;
+    st.l = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) st.acc[mt][0] = st.acc[mt][1] = st.acc[mt][2] = st.acc[mt][3] = 0.f;
+
+    uint8_t* cur = ring;  // the stage of page p
+    uint32_t parity = 0;  // of the phase its copies complete
+    bool ok = __all_sync(kAll, bi::mbar_wait(bar_of(cur), 0));
+    int p = 0;
+    float x[4];
+    if (ok) page_logs(x, cur, qb0, qb1, tokens, a.scale_log2, lane);
+    // full pages with a page behind them
+    for (; ok && p < np - 1; ++p) {
+        uint8_t* next = cur + kStageBytes;
+        if (next == ring + kRing * kStageBytes) {
+            next = ring;
+            parity ^= 1;
+        }
+        ok = __all_sync(kAll, bi::mbar_wait(bar_of(next), parity));
+        if (!ok) break;
+        bi_attn::PFrags pf;
+        weights_step(st, x, lane, pf);
+        VFrags f;
+        load_v(f, cur + kBlockBytes, kPage, lane);
+        __syncwarp();  // every lane is done with the stage
+        if (lane == p + kRing && lane < np) copy_page(cur);
+        page_logs(x, next, qb0, qb1, kPage, a.scale_log2, lane);
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr) pv_group(st.acc[2 * gr], st.acc[2 * gr + 1], f, gr, pf);
+        cur = next;
+    }
+    if (!ok) {
+        if (lane == 0) {
+            bi::report_error(a.err, bi::kErrTimeout | bi::kWhereAttnSplit);
+            // copies may still write to this CTA's shared memory: one more bounded
+            // wait each (page p + 1, or 0, is the first that was not seen to land)
+            for (int i = 0; i < kRing; ++i) {
+                const int late = p + i;
+                if (late < np) bi::mbar_wait_for(bar_of(ring + (late % kRing) * kStageBytes), (late / kRing) & 1, bi::kDrainNs);
+            }
+            if (nch > 1) bi_attn::arrive_bad(ctr, nch);
+        }
+        return;
+    }
+    {  // the last page, whose last tokens may not be there
+        const int valid = tokens - (np - 1) * kPage;
+        if (valid < kPage) {
+            if ((lane >> 2) >= valid) x[0] = x[1] = -INFINITY;
+            if ((lane >> 2) + 8 >= valid) x[2] = x[3] = -INFINITY;
+        }
+        bi_attn::PFrags pf;
+        weights_step(st, x, lane, pf);
+        VFrags f;
+        load_v(f, cur + kBlockBytes, valid, lane);
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr) pv_group(st.acc[2 * gr], st.acc[2 * gr + 1], f, gr, pf);
+    }
+
+    const int h0 = 2 * (lane & 3);
+    // both columns' sums: lane l holds one of them, lane l ^ 4 the other
+    const float other = __shfl_xor_sync(kAll, st.l, 4);
+    const float l[2] = {lane & 4 ? other : st.l, lane & 4 ? st.l : other};
+    if (nch == 1) {  // the whole sequence: bf16(O / l)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (h0 + e >= a.group) continue;
+            const float il = bi_attn::inv_weight(l[e]);
+            __nv_bfloat16* o = a.out + (row0 + h0 + e) * kD + (lane >> 2);
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+                o[16 * mt] = __float2bfloat16_rn(bi_attn::normalise(st.acc[mt][e], il));
+                o[16 * mt + 8] = __float2bfloat16_rn(bi_attn::normalise(st.acc[mt][2 + e], il));
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (h0 + e >= a.group) continue;
+        float2* o = reinterpret_cast<float2*>(partial_o(a, row0 + h0 + e, c)) + (lane >> 2);
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) o[8 * mt] = make_float2(st.acc[mt][e], st.acc[mt][2 + e]);
+        if (lane < 4)
+            *partial_ml(a, row0 + h0 + e, c) =
+                make_float2(st.th[e] == -INFINITY ? -INFINITY : st.ref[e], l[e]);
+    }
+    __syncwarp();
+    uint32_t now = 0;
+    if (lane == 0) {
+        // release: this warp's partial is visible before its arrival counts;
+        // acquire: the last arrival sees every other warp's partial
+        now = bi::atomic_add_acq_rel_gpu(ctr, bi_attn::kArrive) + bi_attn::kArrive;
+        if ((now & 0xffffu) == static_cast<uint32_t>(nch)) {
+            atomicExch(ctr, 0u);  // ready for the next call
+            if (now >> 16) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
+        }
+    }
+    now = __shfl_sync(kAll, now, 0);
+    if ((now & 0xffffu) != static_cast<uint32_t>(nch) || now >> 16) return;
+    float4* factors = reinterpret_cast<float4*>(ring);
+    static_assert(32 * kMaxGroup * 16 <= kRing * kStageBytes, "the factors fit in the ring");
+    switch (a.group) {
+        case 1: fold_warp<1>(a, row0, nch, factors, lane); break;
+        case 2: fold_warp<2>(a, row0, nch, factors, lane); break;
+        case 3: fold_warp<3>(a, row0, nch, factors, lane); break;
+        case 4: fold_warp<4>(a, row0, nch, factors, lane); break;
+        case 5: fold_warp<5>(a, row0, nch, factors, lane); break;
+        case 6: fold_warp<6>(a, row0, nch, factors, lane); break;
+        case 7: fold_warp<7>(a, row0, nch, factors, lane); break;
+        default: fold_warp<8>(a, row0, nch, factors, lane); break;
+    }
+}
+
+// Chunks per SM (at the launch's bound on the lengths; lengths spread up to the
+// bound fill about half of them) from which on the warp kernel is taken.
+// Measured on GB300 with 8 kv-heads, chunk kernel against warp kernel: 14 per
+// SM (B = 8 up to 8192 tokens) 21 against 35 us, 27 (B = 16) 35 against 40, 40
+// (B = 24) 50 against 51, 54 (B = 32) 64 against 60, 108 (B = 64) 117 against
+// 101, 431 (B = 256) 440 against 341 us.  The chunk kernel's four warps finish
+// a chunk several times sooner, the warp kernel issues a quarter fewer
+// instructions and has no barriers.
+constexpr int64_t kManyChunks = 44;
 
 // set once per device; any thread may race to set it, the attribute is idempotent
 std::atomic<bool> g_attr_set[64] = {};
@@ -455,8 +794,10 @@ extern "C" bi_status bi_decode_attention_kv4(const void* q, const void* k_cache,
     args.num_splits = 0;
     args.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     args.chunks_per_cta = 1;
-    return bi::launch_pdl(attn_chunk_kv4_kernel, dim3(max_chunks, Hkv, B), dim3(kThreads), kSmemBytes,
-                          stream, ka) == cudaSuccess
-               ? BI_OK
-               : BI_ERR_CUDA;
+    const dim3 grid(max_chunks, Hkv, B);
+    const cudaError_t e =
+        static_cast<int64_t>(max_chunks) * Hkv * B >= kManyChunks * static_cast<int64_t>(bi::sm_count())
+            ? bi::launch_pdl(attn_warp_kv4_kernel, grid, dim3(32), 0, stream, ka)
+            : bi::launch_pdl(attn_chunk_kv4_kernel, grid, dim3(kThreads), kSmemBytes, stream, ka);
+    return e == cudaSuccess ? BI_OK : BI_ERR_CUDA;
 }
