@@ -46,6 +46,16 @@ __all__ = ["BiError", "rmsnorm", "gemm", "gemm_swiglu", "interleave_gate_up",
            "KV4_BLOCK_BYTES", "MAX_TOP_LOGPROBS"]
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _current_device() -> int:
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2  # no device: no tensor is there
+
+
 class BiError(RuntimeError):
     """A libbi.so call returned a status other than BI_OK."""
 
@@ -69,7 +79,8 @@ def _check(status: int, where: str) -> None:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building a torch.cuda.Stream object takes 3 us
+        return _raw_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -413,29 +424,33 @@ def decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
 
 
 # --------------------------------------------------------- 4-bit KV cache ----
-def _cuda_i32(t: torch.Tensor, name: str, shape: tuple) -> None:
-    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+# A decode step makes these calls once a layer, so each tests all it has to in
+# one condition and sorts out what was wrong only when something was.
+_BF16, _I32, _U8, _F32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
 
 
-def _one_device(where: str, *tensors) -> None:
-    """Every tensor on the current device, whose stream and error word the call uses."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{where}: every tensor must be on the current CUDA device ({dev})")
-
-
-def _kv4_caches(k_cache: torch.Tensor, v_cache: torch.Tensor, where: str) -> tuple[int, int]:
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not t.is_cuda or t.dtype != torch.uint8 or not t.is_contiguous():
-            raise ValueError(f"{where}: {n} must be a contiguous uint8 CUDA tensor")
-    shape = k_cache.shape
-    if len(shape) != 3 or shape[2] != KV4_BLOCK_BYTES or v_cache.shape != shape:
-        raise ValueError(f"{where}: 4-bit caches [num_pages, Hkv, {KV4_BLOCK_BYTES}] expected")
-    return shape[0], shape[1]
+def _refuse(where: str, *wanted):
+    """Raise for the first of (tensor, name, dtype, shape) that is not a
+    contiguous tensor of that type and shape (None: any) on the current CUDA
+    device."""
+    for t, name, dtype, shape in wanted:
+        if t is None:
+            continue
+        kind = str(dtype).split(".")[-1]
+        if not t.is_cuda:
+            raise ValueError(f"{where}: {name} must be a CUDA tensor (no CPU path exists)")
+        if t.dtype != dtype:
+            raise ValueError(f"{where}: {name} must be {kind}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+        if shape is not None and (t.dim() != len(shape)
+                                  or any(w is not None and w != n for w, n in zip(shape, t.shape))):
+            want = ", ".join("any" if w is None else str(w) for w in shape)
+            raise ValueError(f"{where}: {name} must have shape [{want}], got {tuple(t.shape)}")
+    for t, name, _, _ in wanted:
+        if t is not None and t.get_device() != _current_device():
+            raise ValueError(f"{where}: {name} must be on the current CUDA device ({_current_device()})")
+    raise ValueError(f"{where}: arguments do not fit together")
 
 
 def kv4_cache(num_pages: int, Hkv: int, device="cuda") -> tuple[torch.Tensor, torch.Tensor]:
@@ -445,31 +460,42 @@ def kv4_cache(num_pages: int, Hkv: int, device="cuda") -> tuple[torch.Tensor, to
     return k, torch.zeros_like(k)
 
 
-def _kv4_rows(t: torch.Tensor, name: str) -> int:
-    """Token stride (elements) of k or v [T, Hkv, 128] with whole heads side by side."""
-    _cuda_bf16(t, name)
+def _side_by_side(t: torch.Tensor) -> bool:
+    """Whether t [T, Hkv, 128] has the values of a token in one run."""
     if t.dim() != 3 or t.shape[2] != 128:
-        raise ValueError(f"{name} must be [T, Hkv, 128]")
-    T, Hkv, _ = t.shape
-    if t.numel() and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != 128)):
-        raise ValueError(f"{name}: the heads of a token must lie side by side")
-    return int(t.stride(0)) if T > 1 else Hkv * 128
+        return False
+    st = t.stride()
+    return t.numel() == 0 or (st[2] == 1 and (t.shape[1] == 1 or st[1] == 128))
 
 
 def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
                v_cache: torch.Tensor, stream=None) -> None:
     """Quantise k, v [T, Hkv, 128] (any token stride: views of a qkv projection
     will do) to 4 bits in the slots (page * 16 + offset, int32 [T]) of the caches."""
-    num_pages, Hkv = _kv4_caches(k_cache, v_cache, "kv4_append")
-    ld_k, ld_v = _kv4_rows(k, "k"), _kv4_rows(v, "v")
-    T = k.shape[0]
-    if k.shape != v.shape or k.shape[1] != Hkv:
-        raise ValueError("kv4_append: k and v [T, Hkv, 128] of the caches' Hkv expected")
-    _cuda_i32(slots, "slots", (T,))
-    _one_device("kv4_append", k, v, slots, k_cache, v_cache)
+    dev = _current_device()
+    shape, cs = k.shape, k_cache.shape
+    if not (k.dtype is v.dtype is _BF16 and _side_by_side(k) and _side_by_side(v) and v.shape == shape
+            and slots.dtype is _I32 and slots.shape == shape[:1] and slots.is_contiguous()
+            and k_cache.dtype is v_cache.dtype is _U8 and len(cs) == 3 and cs[1] == shape[1]
+            and cs[2] == KV4_BLOCK_BYTES and v_cache.shape == cs and k_cache.is_contiguous()
+            and v_cache.is_contiguous()
+            and dev == k.get_device() == v.get_device() == slots.get_device()
+            == k_cache.get_device() == v_cache.get_device()):
+        for t, n in ((k, "k"), (v, "v")):
+            _cuda_bf16(t, n)
+            if not _side_by_side(t):
+                raise ValueError(f"kv4_append: {n} must be [T, Hkv, 128], the heads of a token side by side")
+        if v.shape != shape:
+            raise ValueError("kv4_append: k and v must have the same shape")
+        cache = (None, shape[1], KV4_BLOCK_BYTES)
+        _refuse("kv4_append", (k_cache, "k_cache", _U8, cache), (v_cache, "v_cache", _U8, cache),
+                (slots, "slots", _I32, shape[:1]))
+    T, Hkv, _ = shape
     _check(_lib.load().bi_kv4_append(
-        k.data_ptr(), ld_k, v.data_ptr(), ld_v, T, Hkv, 128, slots.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), num_pages, PAGE_SIZE, _stream(stream)), "bi_kv4_append")
+        k.data_ptr(), k.stride(0) if T > 1 else Hkv * 128, v.data_ptr(),
+        v.stride(0) if T > 1 else Hkv * 128, T, Hkv, 128, slots.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), cs[0], PAGE_SIZE, _raw_stream(dev) if stream is None else _stream(stream)),
+        "bi_kv4_append")
 
 
 def qk_norm_rope_append_kv4(qkv: torch.Tensor, Hq: int, Hkv: int, positions: torch.Tensor,
@@ -478,36 +504,38 @@ def qk_norm_rope_append_kv4(qkv: torch.Tensor, Hq: int, Hkv: int, positions: tor
                             q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """qk_norm_rope_append into 4-bit caches: q -> q_out [T, Hq, 128]; the k and
     v rows, quantised -> their slots."""
-    num_pages, Hkv2 = _kv4_caches(k_cache, v_cache, "qk_norm_rope_append_kv4")
-    _cuda_bf16(qkv, "qkv")
-    ld = _row_major_2d(qkv, "qkv")
-    T = qkv.shape[0]
-    if Hkv2 != Hkv or qkv.shape[1] < (Hq + 2 * Hkv) * 128:
-        raise ValueError("qk_norm_rope_append_kv4: qkv [T, (Hq + 2 Hkv) * 128] and caches of Hkv "
-                         "heads expected")
-    _cuda_i32(positions, "positions", (T,))
-    _cuda_i32(slots, "slots", (T,))
-    if (not rope.is_cuda or rope.dtype != torch.float32 or not rope.is_contiguous()
-            or rope.dim() != 2 or rope.shape[1] != 128):
-        raise ValueError("rope must be a contiguous float32 CUDA tensor [max_pos, 128]")
-    for t, n in ((q_norm_w, "q_norm_w"), (k_norm_w, "k_norm_w")):
-        if t is not None:
-            _cuda_bf16(t, n)
-            if t.shape != (128,) or not t.is_contiguous():
-                raise ValueError(f"{n} must be a contiguous [128] tensor")
+    dev = _current_device()
     if q_out is None:
-        q_out = torch.empty((T, Hq, 128), dtype=torch.bfloat16, device=qkv.device)
-    else:
-        _cuda_bf16(q_out, "q_out")
-        if q_out.shape != (T, Hq, 128) or not q_out.is_contiguous():
-            raise ValueError("q_out must be a contiguous [T, Hq, 128] tensor")
-    _one_device("qk_norm_rope_append_kv4", qkv, positions, slots, rope, q_norm_w, k_norm_w,
-                k_cache, v_cache, q_out)
+        q_out = torch.empty((qkv.shape[0], Hq, 128), dtype=_BF16, device=qkv.device)
+    shape, cs, rs = qkv.shape, k_cache.shape, rope.shape
+    if not (len(shape) == 2 and qkv.dtype is _BF16 and shape[1] >= (Hq + 2 * Hkv) * 128
+            and qkv.stride(1) == 1 and positions.dtype is slots.dtype is _I32
+            and positions.shape == slots.shape == shape[:1] and positions.is_contiguous()
+            and slots.is_contiguous() and rope.dtype is _F32 and len(rs) == 2 and rs[1] == 128
+            and rope.is_contiguous() and k_cache.dtype is v_cache.dtype is _U8 and len(cs) == 3
+            and cs[1] == Hkv and cs[2] == KV4_BLOCK_BYTES and v_cache.shape == cs
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and q_out.dtype is _BF16
+            and q_out.shape == (shape[0], Hq, 128) and q_out.is_contiguous()
+            and dev == qkv.get_device() == positions.get_device() == slots.get_device()
+            == rope.get_device() == k_cache.get_device() == v_cache.get_device() == q_out.get_device()):
+        where = "qk_norm_rope_append_kv4"
+        _cuda_bf16(qkv, "qkv")
+        if qkv.dim() != 2 or shape[1] < (Hq + 2 * Hkv) * 128 or qkv.stride(1) != 1:
+            raise ValueError(f"{where}: qkv [T, (Hq + 2 Hkv) * 128] with whole rows expected")
+        cache = (None, Hkv, KV4_BLOCK_BYTES)
+        _refuse(where, (k_cache, "k_cache", _U8, cache), (v_cache, "v_cache", _U8, cache),
+                (positions, "positions", _I32, shape[:1]), (slots, "slots", _I32, shape[:1]),
+                (rope, "rope", _F32, (None, 128)), (q_out, "q_out", _BF16, (shape[0], Hq, 128)))
+    for t, n in ((q_norm_w, "q_norm_w"), (k_norm_w, "k_norm_w")):
+        if t is not None and not (t.dtype is _BF16 and t.shape == (128,) and t.is_contiguous()
+                                  and t.get_device() == dev):
+            _refuse("qk_norm_rope_append_kv4", (t, n, _BF16, (128,)))
+    T = shape[0]
     _check(_lib.load().bi_qk_norm_rope_append_kv4(
-        qkv.data_ptr(), ld, T, Hq, Hkv, 128, positions.data_ptr(), slots.data_ptr(),
-        rope.data_ptr(), rope.shape[0], q_norm_w.data_ptr() if q_norm_w is not None else None,
-        k_norm_w.data_ptr() if k_norm_w is not None else None, eps, q_out.data_ptr(),
-        k_cache.data_ptr(), v_cache.data_ptr(), num_pages, PAGE_SIZE, _stream(stream)),
+        qkv.data_ptr(), qkv.stride(0) if T > 1 else shape[1], T, Hq, Hkv, 128, positions.data_ptr(),
+        slots.data_ptr(), rope.data_ptr(), rs[0], None if q_norm_w is None else q_norm_w.data_ptr(),
+        None if k_norm_w is None else k_norm_w.data_ptr(), eps, q_out.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), cs[0], PAGE_SIZE, _raw_stream(dev) if stream is None else _stream(stream)),
         "bi_qk_norm_rope_append_kv4")
     return q_out
 
@@ -519,22 +547,25 @@ def kv4_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Te
     k_out, v_out [num_pages, Hkv, 16, 128] of the same page numbering (other
     rows stay as they are): the caches prefill_attention takes, with the same
     block_table [S, max_pages_per_seq] and seq_lens [S]."""
-    num_pages, Hkv = _kv4_caches(k_cache, v_cache, "kv4_read")
-    shape = (num_pages, Hkv, PAGE_SIZE, 128)
-    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        _cuda_bf16(t, n)
-        if t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"kv4_read: {n} must be a contiguous {shape} tensor")
-    if block_table.dim() != 2:
-        raise ValueError("kv4_read: block_table [S, max_pages_per_seq] expected")
-    S, width = block_table.shape
-    _cuda_i32(block_table, "block_table", (S, width))
-    _cuda_i32(seq_lens, "seq_lens", (S,))
-    _one_device("kv4_read", k_cache, v_cache, block_table, seq_lens, k_out, v_out)
+    dev = _current_device()
+    cs, bs, ls = k_cache.shape, block_table.shape, seq_lens.shape
+    if not (k_cache.dtype is v_cache.dtype is _U8 and len(cs) == 3 and cs[2] == KV4_BLOCK_BYTES
+            and v_cache.shape == cs and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_table.dtype is seq_lens.dtype is _I32 and len(bs) == 2 and len(ls) == 1
+            and ls[0] == bs[0] and block_table.is_contiguous() and seq_lens.is_contiguous()
+            and k_out.dtype is v_out.dtype is _BF16
+            and k_out.shape == v_out.shape == (cs[0], cs[1], PAGE_SIZE, 128)
+            and k_out.is_contiguous() and v_out.is_contiguous()
+            and dev == k_cache.get_device() == v_cache.get_device() == block_table.get_device()
+            == seq_lens.get_device() == k_out.get_device() == v_out.get_device()):
+        cache = (None, None, KV4_BLOCK_BYTES)
+        _refuse("kv4_read", (k_cache, "k_cache", _U8, cache), (v_cache, "v_cache", _U8, cs),
+                (block_table, "block_table", _I32, (None, None)), (seq_lens, "seq_lens", _I32, bs[:1]),
+                *((t, n, _BF16, (cs[0], cs[1], PAGE_SIZE, 128)) for t, n in ((k_out, "k_out"), (v_out, "v_out"))))
     _check(_lib.load().bi_kv4_read(
-        k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), width, seq_lens.data_ptr(),
-        S, Hkv, 128, PAGE_SIZE, num_pages, int(max_seq_len), k_out.data_ptr(), v_out.data_ptr(),
-        _stream(stream)), "bi_kv4_read")
+        k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), bs[1], seq_lens.data_ptr(),
+        bs[0], cs[1], 128, PAGE_SIZE, cs[0], max_seq_len, k_out.data_ptr(), v_out.data_ptr(),
+        _raw_stream(dev) if stream is None else _stream(stream)), "bi_kv4_read")
 
 
 def decode_attention_kv4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -544,38 +575,40 @@ def decode_attention_kv4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     """decode_attention over 4-bit caches [num_pages, Hkv, 1152]: the bits of
     decode_attention over what kv4_read gives of them.  Other arguments, and
     the workspace, as decode_attention."""
-    num_pages, Hkv = _kv4_caches(k_cache, v_cache, "decode_attention_kv4")
-    _cuda_bf16(q, "q")
-    if q.dim() != 3 or not q.is_contiguous() or block_table.dim() != 2:
-        raise ValueError("decode_attention_kv4: contiguous q [B, Hq, D] and block_table "
-                         "[B, max_pages_per_seq] expected")
-    B, Hq, D = q.shape
-    width = block_table.shape[1]
-    _cuda_i32(block_table, "block_table", (B, width))
-    _cuda_i32(seq_lens, "seq_lens", (B,))
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    dev = _current_device()
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _cuda_bf16(out, "out")
-        if out.shape != q.shape or not out.is_contiguous():
-            raise ValueError("decode_attention_kv4: out must be a contiguous [B, Hq, D] tensor")
+    qs, cs, bs = q.shape, k_cache.shape, block_table.shape
+    if not (q.dtype is out.dtype is _BF16 and len(qs) == 3 and out.shape == qs and q.is_contiguous()
+            and out.is_contiguous() and k_cache.dtype is v_cache.dtype is _U8 and len(cs) == 3
+            and cs[2] == KV4_BLOCK_BYTES and v_cache.shape == cs and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and block_table.dtype is seq_lens.dtype is _I32
+            and len(bs) == 2 and bs[0] == qs[0] and seq_lens.shape == qs[:1]
+            and block_table.is_contiguous() and seq_lens.is_contiguous()
+            and dev == q.get_device() == out.get_device() == k_cache.get_device()
+            == v_cache.get_device() == block_table.get_device() == seq_lens.get_device()):
+        where = "decode_attention_kv4"
+        _refuse(where, (q, "q", _BF16, (None, None, None)),
+                (k_cache, "k_cache", _U8, (None, None, KV4_BLOCK_BYTES)), (v_cache, "v_cache", _U8, cs),
+                (block_table, "block_table", _I32, (qs[0], None)), (seq_lens, "seq_lens", _I32, qs[:1]),
+                (out, "out", _BF16, qs))
+    B, Hq, D = qs
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
     if workspace is None:
         need = decode_attention_workspace_size(B, Hq, D, max_seq_len)
         if need > 0:
             # the leading arrival counters must start at zero (every call leaves
             # them zero, so a caller-kept workspace is cleared only once)
             workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("decode_attention_kv4: workspace must be a contiguous CUDA tensor")
-    _one_device("decode_attention_kv4", q, k_cache, v_cache, block_table, seq_lens, out, workspace)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse("decode_attention_kv4", (workspace, "workspace", workspace.dtype, None))
+    ws = workspace is not None
     _check(_lib.load().bi_decode_attention_kv4(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), width,
-        seq_lens.data_ptr(), B, Hq, Hkv, D, PAGE_SIZE, num_pages, int(max_seq_len), scale,
-        out.data_ptr(), workspace.data_ptr() if workspace is not None else None,
-        workspace.nbytes if workspace is not None else 0, _stream(stream)),
-        "bi_decode_attention_kv4")
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), bs[1],
+        seq_lens.data_ptr(), B, Hq, cs[1], D, PAGE_SIZE, cs[0], max_seq_len, scale, out.data_ptr(),
+        workspace.data_ptr() if ws else None, workspace.nbytes if ws else 0,
+        _raw_stream(dev) if stream is None else _stream(stream)), "bi_decode_attention_kv4")
     return out
 
 
@@ -585,22 +618,29 @@ def logprobs_top(logits: torch.Tensor, targets: torch.Tensor | None, k: int, str
     [rows, k] int32, top_logprobs [rows, k]) of bf16 logits [rows, vocab]: the
     bits of logprobs(logits, targets), the softmax's entropy in nats, and the k
     (1 .. 32) largest logits' tokens, largest first, equal ones by ascending id."""
-    _cuda_bf16(logits, "logits")
-    ld = _row_major_2d(logits, "logits")
-    rows, vocab = logits.shape
-    k = int(k)
+    dev = _current_device()
+    shape = logits.shape
+    if not (logits.dtype is _BF16 and len(shape) == 2 and logits.stride(1) == 1
+            and logits.get_device() == dev):
+        _cuda_bf16(logits, "logits")
+        _row_major_2d(logits, "logits")
+        if logits.get_device() != dev:
+            _refuse("logprobs_top", (logits.contiguous(), "logits", _BF16, None))
+    rows, vocab = shape
     if k < 1:
         raise ValueError("logprobs_top: k must be at least 1")
-    if targets is not None:
-        _cuda_i32(targets, "targets", (rows,))
-    _one_device("logprobs_top", logits, targets)
-    dev = logits.device
-    f = torch.empty((3, rows), dtype=torch.float32, device=dev)
-    lp, lse, entropy = f.unbind(0)
-    ids = torch.empty((rows, k), dtype=torch.int32, device=dev)
-    top = torch.empty((rows, k), dtype=torch.float32, device=dev)
+    if targets is not None and not (targets.dtype is _I32 and targets.shape == shape[:1]
+                                    and targets.is_contiguous() and targets.get_device() == dev):
+        _refuse("logprobs_top", (targets, "targets", _I32, shape[:1]))
+    on = logits.device
+    lse = torch.empty(rows, dtype=_F32, device=on)
+    entropy = torch.empty_like(lse)
+    lp = torch.empty_like(lse) if targets is not None else None
+    top = torch.empty((rows, k), dtype=_F32, device=on)
+    ids = torch.empty((rows, k), dtype=_I32, device=on)
     _check(_lib.load().bi_logprobs_top(
-        logits.data_ptr(), rows, vocab, ld, targets.data_ptr() if targets is not None else None,
-        lp.data_ptr() if targets is not None else None, lse.data_ptr(), entropy.data_ptr(), k,
-        ids.data_ptr(), top.data_ptr(), _stream(stream)), "bi_logprobs_top")
-    return (lp if targets is not None else None), lse, entropy, ids, top
+        logits.data_ptr(), rows, vocab, logits.stride(0) if rows > 1 else vocab,
+        None if targets is None else targets.data_ptr(), None if lp is None else lp.data_ptr(),
+        lse.data_ptr(), entropy.data_ptr(), k, ids.data_ptr(), top.data_ptr(),
+        _raw_stream(dev) if stream is None else _stream(stream)), "bi_logprobs_top")
+    return lp, lse, entropy, ids, top

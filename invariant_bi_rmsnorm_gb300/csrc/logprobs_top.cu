@@ -38,13 +38,17 @@ namespace {
 using bi_lp::kLog2e;
 using bi_lp::kThreads;
 
-constexpr int kUnroll = 4;     // vectors in flight per thread
+// Vectors a thread loads while it folds as many.  At six CTAs per SM (40
+// registers) 2 is best at 1024 rows (78 us; 1 takes 97, 4 spills), and one row
+// takes 17.5 us with 2, 4 or 8.
+constexpr int kUnroll = 2;
 constexpr int kSegs = 32;      // segments per thread, at most
 constexpr int kMaxTop = 32;
 constexpr int kMaxCand = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNear = 1024.f;  // maxima up to here: d by one fma
+constexpr float kLowest = -3.3895313892515355e38f;  // bf16's lowest finite value
 constexpr uint32_t kNegInf2 = 0xFF80FF80u;  // two bf16 -inf
 
 // A bf16 value as a 16-bit number of the same order; both zeros alike, NaN
@@ -60,16 +64,14 @@ __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float((key & 0x8000u ? key & 0x7FFFu : 0xFFFFu & ~key) << 16);
 }
 
+// Running reduction of one thread.  m starts at the lowest finite value instead
+// of -inf, so that no difference with it is undefined: s is 0 until a logit
+// reaches m, and what multiplies a zero s changes no bit.
 struct Run {
-    float m, mc, s, t;
+    float m, mc, s;
+    float2 t;   // T, in two halves (elements 0, 2, .. and 1, 3, .. of the vectors)
+    bool far;   // |m| > kNear in some lane of the warp
 };
-
-__device__ __forceinline__ void add_term(Run& r, float d) {
-    const float p = bi_lp::ex2_term(d);
-    r.s = __fadd_rn(r.s, p);
-    // p is 0 from d = -127 down; the bound keeps 0 * -inf (a masked logit) out
-    r.t = __fmaf_rn(p, fmaxf(d, -127.f), r.t);
-}
 
 // (a - b) log2(e) for a <= b, by which d falls as the maximum goes from a to
 // b; bounded where 2^.. is 0 anyway, so that 0 times it stays 0
@@ -77,40 +79,80 @@ __device__ __forceinline__ float moved(float a, float b) {
     return fmaxf(__fmul_rn(__fsub_rn(a, b), kLog2e), -1024.f);
 }
 
-// fold_vec of logprobs.cu with T beside s.  Returns the vector's maximum.  One
-// fma for d leaves it off by the rounding of m log2(e), the same for every term
-// of that maximum (so it cancels in the entropy) and below 2^-14 for |m| <=
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+// fold_vec of logprobs.cu with T beside s: the same s, operation by operation
+// (a maximum that stays multiplies s by 1, a vector without a visible logit adds
+// zeros to it).  Returns the vector's maximum.  The maximum of some lane moves
+// in most vectors of a row's first half; the whole warp takes that branch or
+// none of it does.
+//
+// One fma for d leaves it off by the rounding of m log2(e), the same for every
+// term of that maximum (so it cancels in the entropy) and below 2^-14 for |m| <=
 // 1024.  Past that -- logits no model gives, but a thread may see nothing else
 // than a mask's -1e9 or bf16's lowest value, whose m log2(e) is not even finite
 // -- d is taken from the difference, which is exact where it counts.
 __device__ __forceinline__ float fold_vec_t(Run& r, const uint4& u) {
-    const float x[8] = {bi_lp::lo16(u.x), bi_lp::hi16(u.x), bi_lp::lo16(u.y), bi_lp::hi16(u.y),
-                        bi_lp::lo16(u.z), bi_lp::hi16(u.z), bi_lp::lo16(u.w), bi_lp::hi16(u.w)};
-    float vm = x[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) vm = fmaxf(vm, x[e]);
-    if (vm == -INFINITY) return vm;  // nothing visible in this vector
-    if (vm > r.m) {
-        const float f = bi_lp::rescale(r.m, vm);
-        r.t = __fmul_rn(__fmaf_rn(moved(r.m, vm), r.s, r.t), f);
-        r.s = __fmul_rn(r.s, f);  // m = -inf: s is 0 and stays 0
-        r.m = vm;
-        r.mc = __fmul_rn(vm, kLog2e);
+    const uint32_t h = max_bf16x2(max_bf16x2(u.x, u.y), max_bf16x2(u.z, u.w));
+    const float vm = fmaxf(bi_lp::lo16(h), bi_lp::hi16(h));
+    if (__any_sync(0xffffffffu, vm > r.m)) {
+        const float m = fmaxf(r.m, vm);
+        const float by = __fmul_rn(__fsub_rn(r.m, m), kLog2e);
+        const float f = exp2f(by);  // bi_lp::rescale(r.m, m)
+        r.t.x = __fmul_rn(__fmaf_rn(fmaxf(by, -1024.f), r.s, r.t.x), f);
+        r.t.y = __fmul_rn(r.t.y, f);
+        r.s = __fmul_rn(r.s, f);
+        r.m = m;
+        r.mc = __fmul_rn(m, kLog2e);
+        r.far = __any_sync(0xffffffffu, fabsf(m) > kNear);
     }
-    if (fabsf(r.m) <= kNear) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if (!r.far) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) add_term(r, __fmaf_rn(x[e], kLog2e, -r.mc));
+        for (int i = 0; i < 4; ++i) {
+            const float2 d = fma2(make_float2(bi_lp::lo16(w[i]), bi_lp::hi16(w[i])),
+                                  make_float2(kLog2e, kLog2e), make_float2(-r.mc, -r.mc));
+            const float2 p = make_float2(bi_lp::ex2_term(d.x), bi_lp::ex2_term(d.y));
+            r.s = __fadd_rn(r.s, p.x);
+            r.s = __fadd_rn(r.s, p.y);
+            // p is 0 from d = -127 down; the bound keeps 0 * -inf (a masked logit) out
+            r.t = fma2(p, make_float2(fmaxf(d.x, -127.f), fmaxf(d.y, -127.f)), r.t);
+        }
     } else {
+        const bool far = fabsf(r.m) > kNear;  // this lane
 #pragma unroll
-        for (int e = 0; e < 8; ++e) add_term(r, __fmul_rn(__fsub_rn(x[e], r.m), kLog2e));
+        for (int e = 0; e < 8; ++e) {
+            const float x = e & 1 ? bi_lp::hi16(w[e >> 1]) : bi_lp::lo16(w[e >> 1]);
+            const float d = far ? __fmul_rn(__fsub_rn(x, r.m), kLog2e) : __fmaf_rn(x, kLog2e, -r.mc);
+            const float p = bi_lp::ex2_term(d);
+            r.s = __fadd_rn(r.s, p);
+            r.t.x = __fmaf_rn(p, fmaxf(d, -127.f), r.t.x);
+        }
     }
     return vm;
 }
 
-// combine of logprobs.cu with T beside s.
-__device__ __forceinline__ void combine_t(Run& a, float m2, float s2, float t2) {
+// A thread's part of the row, reduced: combine of logprobs.cu with T beside s.
+struct Part {
+    float m, s, t;
+};
+
+__device__ __forceinline__ void combine_t(Part& a, float m2, float s2, float t2) {
     const float M = fmaxf(a.m, m2);
-    if (M == -INFINITY) return;  // both empty
     const float f1 = bi_lp::rescale(a.m, M), f2 = bi_lp::rescale(m2, M);
     a.t = __fadd_rn(__fmul_rn(__fmaf_rn(moved(a.m, M), a.s, a.t), f1),
                     __fmul_rn(__fmaf_rn(moved(m2, M), s2, t2), f2));
@@ -145,66 +187,77 @@ __device__ __forceinline__ int block_sum(int v, int* red) {
     return n;
 }
 
-// f(id, key) for the logits of this thread's segments whose maximum reaches
-// `least` and that reach it themselves.
+// f(id, key) for the logits at or above `least`: of the segments whose maximum
+// reaches it, one after the other, a lane per logit.
 template <typename F>
-__device__ __forceinline__ void each_reaching(const uint4* xv, int nvec, int seg_vecs,
+__device__ __forceinline__ void each_reaching(const uint16_t* x, int vocab, int seg_vecs,
                                               const uint16_t* seg_max, uint32_t least, F f) {
-    const int tid = threadIdx.x;
-    for (int sg = 0; sg * seg_vecs * kThreads < nvec; ++sg) {
-        if (seg_max[sg * kThreads + tid] < least) continue;
-        for (int i = 0; i < seg_vecs; ++i) {
-            const int v = (sg * seg_vecs + i) * kThreads + tid;
-            if (v >= nvec) break;
-            const uint4 u = xv[v];
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t key = key_of((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-                if (key >= least) f(8 * v + e, key);
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int sg = 0; sg * seg_vecs * kThreads * 8 < vocab; ++sg) {
+        uint32_t reach = __ballot_sync(0xffffffffu, seg_max[sg * kThreads + tid] >= least);
+        for (; reach; reach &= reach - 1) {
+            const int owner = tid - lane + __ffs(reach) - 1;  // the thread whose segment it is
+            for (int j = lane; j < 8 * seg_vecs; j += 32) {
+                const int id = 8 * ((sg * seg_vecs + (j >> 3)) * kThreads + owner) + (j & 7);
+                const uint32_t key = id < vocab ? key_of(x[id]) : 0u;
+                if (id < vocab && key >= least) f(id, key);
             }
         }
     }
 }
 
-__global__ void __launch_bounds__(kThreads) logprobs_top_kernel(const TopArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) logprobs_top_kernel(const TopArgs a) {
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
     __shared__ uint16_t seg_max[kSegs * kThreads];
-    __shared__ uint16_t thread_max[kThreads];
     __shared__ unsigned long long cand[kMaxCand];  // key above, ~id below: larger is better
+    __shared__ __align__(16) uint16_t thread_max[kThreads];
+    __shared__ uint32_t kth_s;
     __shared__ float red_m[kWarps], red_s[kWarps], red_t[kWarps];
     __shared__ int red[kWarps];
     __shared__ float lse_s;
-    __shared__ uint32_t thr_s;
     __shared__ int ncand;
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x;
     const int lane = tid & 31, warp = tid >> 5;
     const __nv_bfloat16* x = a.logits + row * a.ld;
     const uint4* xv = reinterpret_cast<const uint4*>(x);
+    const uint16_t* xb = reinterpret_cast<const uint16_t*>(x);
     const int nvec = a.vocab / 8;
 
-    // ---- one pass: (m, s, T) and the segments' maxima ----
-    Run r = {-INFINITY, -INFINITY, 0.f, 0.f};
+    // ---- one pass: (m, s, T) and the segments' maxima; kUnroll vectors of a
+    // thread are on their way while the kUnroll before them are folded ----
+    Run run = {kLowest, 0.f, 0.f, make_float2(0.f, 0.f), true};
     uint32_t best = 0;
-    for (int sg = 0; sg * a.seg_vecs * kThreads < nvec; ++sg) {
-        float sm = -INFINITY;
-        for (int i0 = 0; i0 < a.seg_vecs; i0 += kUnroll) {
-            uint4 u[kUnroll];
+    {
+        uint4 next[kUnroll];
+        auto load = [&](int v0) {
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
-                const int v = (sg * a.seg_vecs + i0 + i) * kThreads + tid;
-                u[i] = v < nvec ? xv[v] : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
+                const int v = v0 + i * kThreads;
+                next[i] = v < nvec ? __ldcs(xv + v) : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
             }
+        };
+        int v0 = tid;
+        load(v0);
+        for (int sg = 0; sg * a.seg_vecs * kThreads < nvec; ++sg) {
+            float sm = -INFINITY;
+            for (int i0 = 0; i0 < a.seg_vecs; i0 += kUnroll) {
+                uint4 u[kUnroll];
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i) sm = fmaxf(sm, fold_vec_t(r, u[i]));
+                for (int i = 0; i < kUnroll; ++i) u[i] = next[i];
+                v0 += kUnroll * kThreads;
+                load(v0);
+#pragma unroll
+                for (int i = 0; i < kUnroll; ++i) sm = fmaxf(sm, fold_vec_t(run, u[i]));
+            }
+            const uint32_t key = key_of(__float_as_uint(sm) >> 16);
+            seg_max[sg * kThreads + tid] = static_cast<uint16_t>(key);
+            best = max(best, key);
         }
-        const uint32_t key = key_of(__float_as_uint(sm) >> 16);
-        seg_max[sg * kThreads + tid] = static_cast<uint16_t>(key);
-        best = max(best, key);
     }
     thread_max[tid] = static_cast<uint16_t>(best);
+    Part r = {run.m, run.s, __fadd_rn(run.t.x, run.t.y)};
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, r.m, o);
@@ -220,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_top_kernel(const TopArgs a)
     if (tid == 0) ncand = 0;
     __syncthreads();
     if (tid == 0) {
-        Run c = {red_m[0], 0.f, red_s[0], red_t[0]};
+        Part c = {red_m[0], red_s[0], red_t[0]};
         for (int i = 1; i < kWarps; ++i) combine_t(c, red_m[i], red_s[i], red_t[i]);
         const float ls = logf(c.s);
         const float lse = __fadd_rn(c.m, ls);
@@ -237,23 +290,30 @@ __global__ void __launch_bounds__(kThreads) logprobs_top_kernel(const TopArgs a)
             }
         }
     }
-
-    // ---- the k-th largest of the threads' maxima ----
-    {
-        int rank = 0;
-        for (int i = 0; i < kThreads; ++i) {
-            const uint32_t o = thread_max[i];
-            rank += o > best || (o == best && i < tid);
+    if (warp == 1) {
+        // the k-th largest of the threads' maxima: the largest key that k of them
+        // reach, bit by bit (8 keys a lane)
+        const uint4 t8 = reinterpret_cast<const uint4*>(thread_max)[lane];
+        const uint32_t w[4] = {t8.x, t8.y, t8.z, t8.w};
+        uint32_t kth = 0;
+#pragma unroll 1
+        for (uint32_t bit = 0x8000u; bit; bit >>= 1) {
+            const uint32_t mid = kth | bit;
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) n += ((w[i] & 0xFFFFu) >= mid) + ((w[i] >> 16) >= mid);
+            if (__reduce_add_sync(0xffffffffu, n) >= a.k) kth = mid;
         }
-        if (rank == a.k - 1) thr_s = best;
+        if (lane == 0) kth_s = kth;
     }
     __syncthreads();
+
     // a maximum of -inf may be that of a thread without logits, or with NaN only:
     // then every logit is a candidate
-    const uint32_t thr = thr_s <= 0x007Fu ? 0u : thr_s;
+    const uint32_t thr = kth_s <= 0x007Fu ? 0u : kth_s;
 
     // ---- candidates: every logit at or above it ----
-    each_reaching(xv, nvec, a.seg_vecs, seg_max, thr, [&](int id, uint32_t key) {
+    each_reaching(xb, a.vocab, a.seg_vecs, seg_max, thr, [&](int id, uint32_t key) {
         const int at = atomicAdd(&ncand, 1);
         if (at < kMaxCand)
             cand[at] = (static_cast<unsigned long long>(key) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id));
@@ -266,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_top_kernel(const TopArgs a)
         while (hi - lo > 1) {
             const uint32_t mid = (lo + hi) / 2;
             int mine = 0;
-            each_reaching(xv, nvec, a.seg_vecs, seg_max, mid, [&](int, uint32_t) { ++mine; });
+            each_reaching(xb, a.vocab, a.seg_vecs, seg_max, mid, [&](int, uint32_t) { ++mine; });
             if (block_sum(mine, red) >= a.k) lo = mid;
             else hi = mid;
         }
@@ -274,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_top_kernel(const TopArgs a)
         if (tid == 0) ncand = 0;
         __syncthreads();
         // fewer than k lie above it ...
-        each_reaching(xv, nvec, a.seg_vecs, seg_max, lo + 1, [&](int id, uint32_t key) {
+        each_reaching(xb, a.vocab, a.seg_vecs, seg_max, lo + 1, [&](int id, uint32_t key) {
             cand[atomicAdd(&ncand, 1)] =
                 (static_cast<unsigned long long>(key) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id));
         });

@@ -455,25 +455,38 @@ def test_binding_refusals():
     kc, vc = bi.kv4_cache(4, 2)
     rows = torch.zeros(3, 2, 128, dtype=torch.bfloat16, device="cuda")
     idx = torch.zeros(3, dtype=torch.int32, device="cuda")
-    with pytest.raises(ValueError, match="side by side"):
-        bi.kv4_append(rows.transpose(0, 1).contiguous().transpose(0, 1), rows, idx, kc, vc)
-    with pytest.raises(ValueError, match="of the caches' Hkv"):
-        bi.kv4_append(rows[:, :1], rows[:, :1], idx, kc, vc)
-    with pytest.raises(ValueError, match="slots"):
-        bi.kv4_append(rows, rows, idx[:2], kc, vc)
-    with pytest.raises(ValueError, match="int32"):
-        bi.kv4_append(rows, rows, idx.long(), kc, vc)
-    with pytest.raises(ValueError, match="4-bit caches"):
-        bi.kv4_append(rows, rows, idx, kc[..., :1024].contiguous(), vc[..., :1024].contiguous())
-    with pytest.raises(ValueError, match="uint8"):
-        bi.decode_attention_kv4(rows, kc.float(), vc, idx[:, None], idx, 16)
-    with pytest.raises(ValueError, match="seq_lens"):
-        bi.decode_attention_kv4(rows, kc, vc, idx[:, None], idx[:2], 16)
-    with pytest.raises(bi.BiError, match="TOO_SMALL"):
-        bi.decode_attention_kv4(rows, kc, vc, torch.zeros(3, 32, dtype=torch.int32, device="cuda"), idx, 512,
-                                workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
-    with pytest.raises(ValueError, match="k_out"):
-        bi.kv4_read(kc, vc, idx[:, None], idx, 16, rows, rows)
-    with pytest.raises(ValueError, match="caches of Hkv"):
-        bi.qk_norm_rope_append_kv4(rows.view(3, 256), 2, 2, idx, idx,
-                                   torch.zeros(4, 128, device="cuda"), None, None, kc, vc)
+    rope = torch.zeros(4, 128, device="cuda")
+    w = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    qkv = torch.zeros(3, 768, dtype=torch.bfloat16, device="cuda")
+    bt = idx[:, None].contiguous()
+
+    def refused(match, f, *a, kind=ValueError, **kw):
+        with pytest.raises(kind, match=match):
+            f(*a, **kw)
+    refused("side by side", bi.kv4_append, rows.transpose(0, 1).contiguous().transpose(0, 1), rows, idx, kc, vc)
+    refused("k_cache", bi.kv4_append, rows[:, :1], rows[:, :1], idx, kc, vc)
+    refused("same shape", bi.kv4_append, rows, rows[:2], idx, kc, vc)
+    refused("slots", bi.kv4_append, rows, rows, idx[:2], kc, vc)
+    refused("int32", bi.kv4_append, rows, rows, idx.long(), kc, vc)
+    refused("bfloat16", bi.kv4_append, rows.float(), rows, idx, kc, vc)
+    refused("1152", bi.kv4_append, rows, rows, idx, kc[..., :1024].contiguous(), vc[..., :1024].contiguous())
+    refused("contiguous", bi.kv4_append, rows, rows, idx, kc, vc.expand(4, 2, 1152).transpose(0, 1).contiguous().transpose(0, 1))
+    refused("CUDA", bi.kv4_append, rows, rows, idx.cpu(), kc, vc)
+    refused("uint8", bi.decode_attention_kv4, rows, kc.float(), vc, bt, idx, 16)
+    refused("v_cache", bi.decode_attention_kv4, rows, kc, vc[:3], bt, idx, 16)
+    refused("seq_lens", bi.decode_attention_kv4, rows, kc, vc, bt, idx[:2], 16)
+    refused("block_table", bi.decode_attention_kv4, rows, kc, vc, bt[:2], idx, 16)
+    refused("out", bi.decode_attention_kv4, rows, kc, vc, bt, idx, 16, out=rows[:2].clone())
+    refused("q must be contiguous", bi.decode_attention_kv4, rows.transpose(0, 1), kc, vc, bt, idx, 16)
+    refused("CUDA", bi.decode_attention_kv4, rows, kc, vc, bt, idx, 16, workspace=torch.zeros(64))
+    refused("TOO_SMALL", bi.decode_attention_kv4, rows, kc, vc, torch.zeros(3, 32, dtype=torch.int32, device="cuda"),
+            idx, 512, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"), kind=bi.BiError)
+    refused("k_out", bi.kv4_read, kc, vc, bt, idx, 16, rows, rows)
+    refused("seq_lens", bi.kv4_read, kc, vc, bt, idx[:1], 16, rows, rows)
+    fused = bi.qk_norm_rope_append_kv4
+    refused("k_cache", fused, qkv, 2, 1, idx, idx, rope, None, None, kc, vc)
+    refused("whole rows", fused, qkv[:, :700], 2, 2, idx, idx, rope, None, None, kc, vc)
+    refused("rope", fused, qkv, 2, 2, idx, idx, rope.double(), None, None, kc, vc)
+    refused("positions", fused, qkv, 2, 2, idx[:1], idx, rope, None, None, kc, vc)
+    refused("k_norm_w", fused, qkv, 2, 2, idx, idx, rope, w, w[:64], kc, vc)
+    refused("q_out", fused, qkv, 2, 2, idx, idx, rope, w, w, kc, vc, q_out=qkv)
