@@ -186,18 +186,15 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) qk_norm_rope_append_kernel
                 const int first_v = a.Hq + a.Hkv;
                 const int64_t blk = page * a.Hkv;
                 if (2 * pr < first_v && 2 * pr + 1 >= a.Hq) {
-                    float k[8];
-                    unpack4(y_lo, k);
-                    unpack4(y_hi, k + 4);
                     const bool is_k = !is_q && !is_v;
                     bi_kv4::write_row<false>(
-                        k, static_cast<uint8_t*>(a.k_cache) + (blk + (is_k ? h - a.Hq : 0)) * bi_kv4::kBlockBytes,
+                        bi_kv4::RowPart{y_lo, y_hi}, static_cast<uint8_t*>(a.k_cache) + (blk + (is_k ? h - a.Hq : 0)) * bi_kv4::kBlockBytes,
                         static_cast<int>(off), l, is_k);
                 }
                 if (2 * pr + 1 >= first_v) {
                     const bool v_live = is_v && live;
                     bi_kv4::write_row<true>(
-                        x, static_cast<uint8_t*>(a.v_cache) + (blk + (v_live ? h - first_v : 0)) * bi_kv4::kBlockBytes,
+                        bi_kv4::RowPart{lo[j], hi[j]}, static_cast<uint8_t*>(a.v_cache) + (blk + (v_live ? h - first_v : 0)) * bi_kv4::kBlockBytes,
                         static_cast<int>(off), l, v_live);
                 }
             }

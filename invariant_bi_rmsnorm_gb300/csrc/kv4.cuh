@@ -32,6 +32,7 @@
 #include <cstdint>
 
 #include "bi_internal.h"
+#include "bi_ptx.cuh"
 
 namespace bi_kv4 {
 
@@ -80,91 +81,93 @@ __device__ __forceinline__ uint32_t kv4_pair(uint32_t w, int p, const ScalePair&
 }
 
 // ---------------------------------------------------------------- writing ----
-// s from the largest magnitude of the group (bits of |x| as an unsigned
-// number, so that a NaN is largest of all)
+// A row of 128 bf16 values as a half-warp holds it: lane l of 16 has dims
+// 4l .. 4l + 3 (lo) and 64 + 4l .. 64 + 4l + 3 (hi), two values a register.
+struct RowPart {
+    uint2 lo, hi;
+};
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// s from the bf16 bits of the largest magnitude of the group (as a whole number,
+// so that a NaN is largest of all).  amax * (1/7) is off by 2^-24 and would miss
+// the ties of the rounding to 4 bits; those are 5-bit numbers and everything
+// else is 2^-9 away from them, so rounding to 21 bits first puts them back.
 __device__ __forceinline__ float group_scale(uint32_t amax_bits) {
-    if (amax_bits >= 0x7D000000u) return __uint_as_float(0x7FFFFFFFu);  // 2^123 and more, inf, NaN
-    if (amax_bits < 0x03800000u) return 0.f;                            // below 2^-120
-    const uint32_t b = __float_as_uint(__fdiv_rn(__uint_as_float(amax_bits), 7.f));
-    return __uint_as_float((b + 0x7FFFFu + ((b >> 20) & 1u)) & 0xFFF00000u);
+    uint32_t b = __float_as_uint(__fmul_rn(__uint_as_float(amax_bits << 16), 1.f / 7.f));
+    b = (b + 4u) & ~7u;
+    b = (b + 0x7FFFFu + ((b >> 20) & 1u)) & 0xFFF00000u;
+    if (amax_bits >= 0x7D00u) b = 0x7FFF0000u;  // 2^123 and more, inf, NaN
+    if (amax_bits < 0x0380u) b = 0u;            // below 2^-120
+    return __uint_as_float(b);
 }
 
-// code = rne(x / s) + 8.  With inv = 1 / s correctly rounded, y = x * inv is
-// within 2^-20 of x / s.  x / s (8 bits over 4) is a tie k + 1/2 exactly or at
-// least 2^-9 away from one, so y rounded to multiples of 2^-11 (by adding and
-// taking away 6144) lands on every tie and on the right side of the others,
-// and the last addition rounds it to nearest even.  inv = 0 for s = 0 (n = 0),
-// NaN for s = NaN (any code will do).
+// 0x4B400000 + n + 8, n = rne(x / s).  inv is 1 / s to 1 ulp, so x * inv is
+// within 2^-20 of x / s, which (8 bits over 4) is a tie k + 1/2 exactly or at
+// least 2^-9 away from one: rounded to multiples of 2^-11 (the fma adds 6144)
+// it lies on every tie and on the right side of the others.  The addition
+// rounds that to nearest even.  |x| / s < 7.5 keeps n within -7 .. 7.
 __device__ __forceinline__ uint32_t code_of(float x, float inv) {
-    float y = __fmul_rn(x, inv);
-    y = fminf(fmaxf(y, -7.f), 7.f);  // also takes a NaN away
-    y = __fsub_rn(__fadd_rn(y, 6144.f), 6144.f);
-    return __float_as_uint(__fadd_rn(y, 12582912.f + 8.f)) & 15u;
+    return __float_as_uint(__fadd_rn(__fmaf_rn(x, inv, 6144.f), 12582912.f + 8.f - 6144.f));
 }
 
-__device__ __forceinline__ uint32_t amax4(const float* x) {
-    const uint32_t m = 0x7FFFFFFFu;
-    return max(max(__float_as_uint(x[0]) & m, __float_as_uint(x[1]) & m),
-               max(__float_as_uint(x[2]) & m, __float_as_uint(x[3]) & m));
+// The codes of four values (two registers of bf16 pairs), one a byte.
+__device__ __forceinline__ uint32_t four_codes(uint2 v, float inv) {
+    const uint32_t c0 = code_of(__uint_as_float(v.x << 16), inv);
+    const uint32_t c1 = code_of(__uint_as_float(v.x & 0xffff0000u), inv);
+    const uint32_t c2 = code_of(__uint_as_float(v.y << 16), inv);
+    const uint32_t c3 = code_of(__uint_as_float(v.y & 0xffff0000u), inv);
+    // a code's own byte, and a zero byte above it
+    return __byte_perm(__byte_perm(c0, c1, 0x0040), __byte_perm(c2, c3, 0x0040), 0x5410);
 }
 
-// Quantise one row of 128 values held by a half-warp (lane l of 16: dims
-// 4l .. 4l + 3 in x[0..3], dims 64 + 4l .. in x[4..7]; every lane of the warp
-// takes part) and write it as token `off` of `block` where `live`.
+// Quantise one row and write it as token `off` of `block` where `live`; every
+// lane of the warp takes part.
 template <bool kIsV>
-__device__ __forceinline__ void write_row(const float (&x)[8], uint8_t* block, int off, int l,
-                                          bool live) {
-    constexpr uint32_t kAll = 0xffffffffu;
-    uint32_t alo = amax4(x), ahi = amax4(x + 4);
+__device__ __forceinline__ void write_row(const RowPart& r, uint8_t* block, int off, int l, bool live) {
+    constexpr uint32_t kAll = 0xffffffffu, kAbs = 0x7FFF7FFFu;
+    // largest magnitudes of the lo and the hi group side by side, over the 8
+    // lanes of a group
+    const uint32_t alo = max_u16x2(r.lo.x & kAbs, r.lo.y & kAbs);
+    const uint32_t ahi = max_u16x2(r.hi.x & kAbs, r.hi.y & kAbs);
+    uint32_t am = max_u16x2(__byte_perm(alo, ahi, 0x5410), __byte_perm(alo, ahi, 0x7632));
 #pragma unroll
-    for (int o = 1; o <= 4; o <<= 1) {  // the 8 lanes of a group
-        alo = max(alo, __shfl_xor_sync(kAll, alo, o));
-        ahi = max(ahi, __shfl_xor_sync(kAll, ahi, o));
-    }
-    const float slo = group_scale(alo), shi = group_scale(ahi);
-    const float ilo = slo == 0.f ? 0.f : __frcp_rn(slo), ihi = shi == 0.f ? 0.f : __frcp_rn(shi);
-    uint32_t c[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        c[e] = code_of(x[e], ilo);
-        c[4 + e] = code_of(x[4 + e], ihi);
-    }
-    // every lane adds its codes to several words; a reduce-scatter over the
-    // lanes that share them leaves one whole word per lane
-    uint32_t word;
-    int at;  // its byte
+    for (int o = 1; o <= 4; o <<= 1) am = max_u16x2(am, __shfl_xor_sync(kAll, am, o));
+    const float slo = group_scale(am & 0xffffu), shi = group_scale(am >> 16);
+    const float ilo = slo == 0.f ? 0.f : bi::rcp_approx(slo);
+    const float ihi = shi == 0.f ? 0.f : bi::rcp_approx(shi);
+    const uint32_t clo = four_codes(r.lo, ilo), chi = four_codes(r.hi, ihi);
+    // A lane's eight codes belong to eight words (V) or four (K).  Three
+    // exchanges with the lanes 2, 4 and (V) 8 away, whose codes go into the same
+    // words, leave every lane with one whole word: lanes keep the lo or the hi
+    // codes, nibbles becoming bytes, then two of the four bytes, then a half.
     const bool b1 = l & 2, b2 = l & 4, b3 = l & 8;
+    const uint32_t got = __shfl_xor_sync(kAll, b1 ? clo : chi, 2);
+    const uint32_t even = b1 ? got : clo, odd = b1 ? chi : got;
+    uint32_t word = even + 16u * odd;
+    word = __byte_perm(word, __shfl_xor_sync(kAll, word, 4), b2 ? 0x3726 : 0x5140);
+    int at;  // its byte
     if (!kIsV) {
-        const int sh = 4 * ((l & 7) >> 1);
-        // words (t, j): t = 2 (l & 1) and the next, j = l / 8 and 2 more
-        const uint32_t a0 = (c[0] | (c[1] << 16)) << sh, b0 = (c[2] | (c[3] << 16)) << sh;
-        const uint32_t a1 = (c[4] | (c[5] << 16)) << sh, b1w = (c[6] | (c[7] << 16)) << sh;
-        const uint32_t a = (b1 ? a1 : a0) | __shfl_xor_sync(kAll, b1 ? a0 : a1, 2);
-        const uint32_t b = (b1 ? b1w : b0) | __shfl_xor_sync(kAll, b1 ? b0 : b1w, 2);
-        word = (b2 ? b : a) | __shfl_xor_sync(kAll, b2 ? a : b, 4);
+        // word (t, j): t = 2 (l % 2) + b2, j = l / 8 + 2 b1
         at = kRowBytes * off + 16 * (2 * (l & 1) + (b2 ? 1 : 0)) + 4 * ((l >> 3) + (b1 ? 2 : 0));
     } else {
-        const int sh = 4 * (l >> 1);
-        // words (g, w): g = 4 (l & 1) + i, w = 0 for x[i], 1 for x[4 + i]
-        uint32_t u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            u[i] = ((b1 ? c[4 + i] : c[i]) << sh) |
-                   __shfl_xor_sync(kAll, (b1 ? c[i] : c[4 + i]) << sh, 2);
-        const uint32_t u0 = (b2 ? u[2] : u[0]) | __shfl_xor_sync(kAll, b2 ? u[0] : u[2], 4);
-        const uint32_t u1 = (b2 ? u[3] : u[1]) | __shfl_xor_sync(kAll, b2 ? u[1] : u[3], 4);
-        word = (b3 ? u1 : u0) | __shfl_xor_sync(kAll, b3 ? u0 : u1, 8);
+        word = __byte_perm(word, __shfl_xor_sync(kAll, word, 8), b3 ? 0x3276 : 0x5410);
+        // word (g, w): g = 4 (l % 2) + 2 b2 + b3, w = b1
         const int g = 4 * (l & 1) + (b2 ? 2 : 0) + (b3 ? 1 : 0);
         at = 512 * (off >> 3) + 64 * g + 8 * (off & 7) + (b1 ? 4 : 0);
     }
     // lane 0 holds the scales of groups 0 and 2, lane 8 those of 1 and 3
-    const uint32_t mine = (__float_as_uint(slo) >> 16) | (__float_as_uint(shi) & 0xffff0000u);
+    const uint32_t mine = __byte_perm(__float_as_uint(slo), __float_as_uint(shi), 0x7632);
     const uint32_t other = __shfl_xor_sync(kAll, mine, 8);
     if (!live) return;
     *reinterpret_cast<uint32_t*>(block + at) = word;
     if (l == 0)
         *reinterpret_cast<uint2*>(block + kScaleOffset + kScaleRowBytes * off) =
-            make_uint2((mine & 0xffffu) | (other << 16), (mine >> 16) | (other & 0xffff0000u));
+            make_uint2(__byte_perm(mine, other, 0x5410), __byte_perm(mine, other, 0x7632));
 }
 
 }  // namespace bi_kv4

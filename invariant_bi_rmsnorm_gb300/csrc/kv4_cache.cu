@@ -31,17 +31,8 @@ struct AppendArgs {
     uint32_t* err;
 };
 
-__device__ __forceinline__ void load_row(const __nv_bfloat16* p, int l, float (&x)[8]) {
-    const uint2 lo = *reinterpret_cast<const uint2*>(p + 4 * l);
-    const uint2 hi = *reinterpret_cast<const uint2*>(p + kD / 2 + 4 * l);
-    x[0] = __uint_as_float(lo.x << 16);
-    x[1] = __uint_as_float(lo.x & 0xffff0000u);
-    x[2] = __uint_as_float(lo.y << 16);
-    x[3] = __uint_as_float(lo.y & 0xffff0000u);
-    x[4] = __uint_as_float(hi.x << 16);
-    x[5] = __uint_as_float(hi.x & 0xffff0000u);
-    x[6] = __uint_as_float(hi.y << 16);
-    x[7] = __uint_as_float(hi.y & 0xffff0000u);
+__device__ __forceinline__ bi_kv4::RowPart load_row(const __nv_bfloat16* p, int l) {
+    return {*reinterpret_cast<const uint2*>(p + 4 * l), *reinterpret_cast<const uint2*>(p + kD / 2 + 4 * l)};
 }
 
 // One half-warp per (token, kv-head): its K row and its V row.
@@ -58,9 +49,8 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
         if (live && l == 0 && h == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
         live = false;
     }
-    float xk[8], xv[8];
-    load_row(a.k + t * a.ld_k + h * kD, l, xk);
-    load_row(a.v + t * a.ld_v + h * kD, l, xv);
+    const bi_kv4::RowPart xk = load_row(a.k + t * a.ld_k + h * kD, l);
+    const bi_kv4::RowPart xv = load_row(a.v + t * a.ld_v + h * kD, l);
     const int off = live ? static_cast<int>(slot % BI_PAGE_SIZE) : 0;
     const int64_t block = live ? (slot / BI_PAGE_SIZE) * a.Hkv + h : 0;
     bi_kv4::write_row<false>(xk, a.k_cache + block * bi_kv4::kBlockBytes, off, l, live);
