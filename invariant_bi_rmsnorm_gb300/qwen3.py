@@ -15,6 +15,12 @@ fills the rest of a per-step token budget with prompt tokens of waiting
 sequences -- a prompt that does not fit is split across steps (chunked
 prefill).  Decode rows use bi_decode_attention; prompt rows use
 bi_prefill_attention; both give a token the same bits.
+
+With kv_bits=4 the cache is held in 4 bits: new tokens are quantised as they
+are appended, decode attends over the codes, and prompt rows attend over the
+step's sequences read back into one bf16 cache that every layer uses in turn.
+Decode and prefill still give a token the same bits, and a request's logits
+still do not depend on the batch.
 """
 from __future__ import annotations
 
@@ -24,9 +30,11 @@ from dataclasses import dataclass, field
 import numpy as np
 import torch
 
-from . import (add_rmsnorm, decode_attention, decode_attention_workspace_size, gemm,
-               gemm_swiglu, interleave_gate_up, logprobs, prefill_attention,
-               prefill_attention_workspace_size, qk_norm_rope_append, rmsnorm, silu_mul)
+from . import (add_rmsnorm, decode_attention, decode_attention_kv4,
+               decode_attention_workspace_size, gemm, gemm_swiglu, interleave_gate_up, kv4_cache,
+               kv4_read, logprobs, logprobs_top, prefill_attention,
+               prefill_attention_workspace_size, qk_norm_rope_append, qk_norm_rope_append_kv4,
+               rmsnorm, silu_mul)
 from . import inputs
 from ._lib import PAGE_SIZE
 
@@ -120,7 +128,7 @@ class Engine:
 
     def __init__(self, weights: Qwen3Weights, num_pages: int, max_tokens_per_step: int = 8192,
                  n_layers: int | None = None, device="cuda", ops: str = "bi",
-                 cuda_graphs: bool = False):
+                 cuda_graphs: bool = False, kv_bits: int = 16):
         """ops="bi": every GEMM and RMSNorm through this library (batch-invariant).
         ops="torch": GEMMs through torch.matmul (cuBLAS) and RMSNorms through
         torch.nn.functional.rms_norm instead -- the non-invariant comparison.
@@ -129,9 +137,14 @@ class Engine:
         with rows that read and write one reserved page.  The kernels are the
         same, and no row's arithmetic depends on the others, so the logits are
         the same bits as without graphs; what goes away is the per-launch host
-        work of about 300 launches a step."""
+        work of about 300 launches a step.
+        kv_bits: 16, a bf16 cache, or 4, a cache of 4-bit codes (1152 bytes a
+        page and head where bf16 takes 4096) and one layer's worth of bf16
+        cache for prompts to attend over."""
         if ops not in ("bi", "torch"):
             raise ValueError("ops must be 'bi' or 'torch'")
+        if kv_bits not in (4, 16):
+            raise ValueError("kv_bits must be 4 or 16")
         self.ops = ops
         self.w = weights
         cfg = self.cfg = weights.cfg
@@ -140,9 +153,16 @@ class Engine:
         self.num_pages = num_pages
         self.budget = max_tokens_per_step
         D, Hkv = cfg.head_dim, cfg.kv_heads
-        self.k_cache = [torch.empty(num_pages, Hkv, PAGE_SIZE, D, dtype=torch.bfloat16,
-                                    device=self.device) for _ in range(self.n_layers)]
-        self.v_cache = [torch.empty_like(k) for k in self.k_cache]
+        self.kv_bits = kv_bits
+        page_cache = lambda: torch.empty(num_pages, Hkv, PAGE_SIZE, D, dtype=torch.bfloat16,  # noqa: E731
+                                         device=self.device)
+        if kv_bits == 4:
+            caches = [kv4_cache(num_pages, Hkv, self.device) for _ in range(self.n_layers)]
+            self.k_cache, self.v_cache = [k for k, _ in caches], [v for _, v in caches]
+            self.read_back = (page_cache(), page_cache())
+        else:
+            self.k_cache = [page_cache() for _ in range(self.n_layers)]
+            self.v_cache = [torch.empty_like(k) for k in self.k_cache]
         self.cuda_graphs = cuda_graphs
         if cuda_graphs and num_pages < 2:
             raise ValueError("cuda_graphs needs a spare page for padding rows")
@@ -272,6 +292,7 @@ class Engine:
         gemm, rmsnorm, add_rmsnorm = self._ops()
         torch.index_select(self.w.embed, 0, tok_d, out=res)
         Hq, Hkv = cfg.heads, cfg.kv_heads
+        append = qk_norm_rope_append_kv4 if self.kv_bits == 4 else qk_norm_rope_append
         for l in range(self.n_layers):
             L = self.w.layers[l]
             if l == 0:
@@ -279,9 +300,8 @@ class Engine:
             else:
                 add_rmsnorm(b["d"], res, L["in_norm"], cfg.eps, out=b["n"])
             gemm(b["n"], L["qkv"], out=b["qkv"])
-            qk_norm_rope_append(b["qkv"], Hq, Hkv, pos_d, slot_d, self.rope, L["q_norm"],
-                                L["k_norm"], self.k_cache[l], self.v_cache[l], cfg.eps,
-                                q_out=b["q"])
+            append(b["qkv"], Hq, Hkv, pos_d, slot_d, self.rope, L["q_norm"], L["k_norm"],
+                   self.k_cache[l], self.v_cache[l], cfg.eps, q_out=b["q"])
             self._attention(l, b, meta)
             gemm(b["attn"].view(T, Hq * cfg.head_dim), L["o"], out=b["o"])
             add_rmsnorm(b["o"], res, L["post_norm"], cfg.eps, out=b["n"])
@@ -427,6 +447,7 @@ class Engine:
 
     def _attention(self, l, b, meta):
         kc, vc = self.k_cache[l], self.v_cache[l]
+        attend = decode_attention_kv4 if self.kv_bits == 4 else decode_attention
         for kind in ("dec", "pre"):
             if kind not in meta:
                 continue
@@ -437,21 +458,27 @@ class Engine:
                 q, out = torch.index_select(b["q"], 0, rows), None
             if kind == "dec":
                 _, bt, lens, mx, _ = meta[kind]
-                out = decode_attention(q, kc, vc, bt, lens, max_seq_len=mx, out=out,
-                                       workspace=meta.get("ws"))
+                out = attend(q, kc, vc, bt, lens, max_seq_len=mx, out=out,
+                             workspace=meta.get("ws"))
             else:
                 _, bt, lens, indptr, mq, mx = meta[kind]
+                if self.kv_bits == 4:
+                    kv4_read(kc, vc, bt, lens, mx, *self.read_back)
+                    kc, vc = self.read_back
                 out = prefill_attention(q, kc, vc, bt, lens, indptr, max_q_len=mq,
                                         max_seq_len=mx, out=out, workspace=meta.get("pws"))
             if not isinstance(rows, slice):
                 b["attn"].index_copy_(0, rows, out)
 
     # ------------------------------------------------------- scheduling ----
-    def generate(self, seqs: list[Sequence], record: set | None = None):
+    def generate(self, seqs: list[Sequence], record: set | None = None, top: int = 0):
         """Run every sequence to max_new generated tokens.  Returns
         {sid: [logits row per generated token]} (CPU bf16) for sids in `record`;
         the log-probability of each generated token (bi_logprobs, fp32) goes to
-        self.logprobs[sid] for the same sids.
+        self.logprobs[sid] for the same sids.  With top > 0 (up to 32) so do,
+        per generated token, the entropy of its distribution to
+        self.entropies[sid] and the `top` likeliest tokens' ids and
+        log-probabilities to self.top[sid] (bi_logprobs_top).
 
         The host runs one step ahead of the device: step i+1 is planned and
         queued while step i computes (no request ends early, so the schedule
@@ -501,9 +528,13 @@ class Engine:
                 if rec:
                     rj = self._up([j for j, _ in rec])
                     lg = torch.index_select(logits, 0, rj)
-                    lps, _ = logprobs(lg, picks[rj].to(torch.int32))
+                    chosen = picks[rj].to(torch.int32)
+                    if top > 0:
+                        lps, _, *report = logprobs_top(lg, chosen, top)
+                    else:
+                        (lps, _), report = logprobs(lg, chosen), None
                     for i, (_, sid) in enumerate(rec):
-                        rec_rows[sid].append((lg, lps, i))
+                        rec_rows[sid].append((lg, lps, report, i))
                 host = torch.empty(picks.shape, dtype=picks.dtype, pin_memory=True)
                 host.copy_(picks, non_blocking=True)
                 ev = torch.cuda.Event()
@@ -519,12 +550,16 @@ class Engine:
                     self._release(s)
         if prev is not None:
             self._resolve(prev)
-        logs, self.logprobs = {}, {}
+        def rows_of(picked):
+            return list(torch.stack(picked).cpu().unbind(0)) if picked else []
+        logs, self.logprobs, self.entropies, self.top = {}, {}, {}, {}
         for sid, rows in rec_rows.items():
-            lg = torch.stack([t[i] for t, _, i in rows]).cpu() if rows else None
-            lp = torch.stack([t[i] for _, t, i in rows]).cpu() if rows else None
-            logs[sid] = list(lg.unbind(0)) if rows else []
-            self.logprobs[sid] = list(lp.unbind(0)) if rows else []
+            logs[sid] = rows_of([lg[i] for lg, _, _, i in rows])
+            self.logprobs[sid] = rows_of([lps[i] for _, lps, _, i in rows])
+            if top > 0:
+                self.entropies[sid] = rows_of([r[0][i] for _, _, r, i in rows])
+                self.top[sid] = list(zip(rows_of([r[1][i] for _, _, r, i in rows]),
+                                         rows_of([r[2][i] for _, _, r, i in rows])))
         return logs
 
     def _up(self, values):
