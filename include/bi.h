@@ -454,7 +454,7 @@ bi_status bi_qk_norm_rope_append_kv4(const void* qkv, int64_t ld_qkv, int32_t T,
  *   seq_lens     device, int32 [S]: 0 .. max_seq_len tokens.
  *   k_out, v_out device, bf16 [num_pages][Hkv][16][128], 16-byte aligned; no
  *                overlap with the 4-bit caches.
- *   S            0 .. 65535;  max_seq_len >= 1, <= max_pages_per_seq * 16.
+ *   S, Hkv       0 .. 65535;  max_seq_len >= 1, <= max_pages_per_seq * 16.
  *   num_pages * Hkv * 16 < 2^31.  D = 128, page_size = 16.
  * A length or a page out of range is reported on the device
  * (BI_ERR_DEVICE_BAD_INPUT) and that sequence, or page, is skipped.  Errors:

@@ -22,12 +22,12 @@ struct AppendArgs {
     const __nv_bfloat16* k;
     const __nv_bfloat16* v;
     int64_t ld_k, ld_v;
-    int64_t rows;  // T * Hkv
-    int Hkv;
+    uint32_t rows;  // T * Hkv
+    uint32_t Hkv;
     const int32_t* slots;
     uint8_t* k_cache;
     uint8_t* v_cache;
-    int64_t num_slots;
+    int32_t num_slots;
     uint32_t* err;
 };
 
@@ -40,19 +40,19 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
     const int l = threadIdx.x & 15;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kHalfWarps + (threadIdx.x >> 4);
+    const uint32_t row = blockIdx.x * kHalfWarps + (threadIdx.x >> 4);
     bool live = row < a.rows;
-    const int64_t t = live ? row / a.Hkv : 0;
-    const int h = live ? static_cast<int>(row - t * a.Hkv) : 0;
-    const int64_t slot = a.slots[t];
+    const uint32_t t = live ? row / a.Hkv : 0;
+    const uint32_t h = live ? row - t * a.Hkv : 0;
+    const bi_kv4::RowPart xk = load_row(a.k + t * a.ld_k + h * kD, l);
+    const bi_kv4::RowPart xv = load_row(a.v + t * a.ld_v + h * kD, l);
+    const int32_t slot = a.slots[t];
     if (slot < 0 || slot >= a.num_slots) {
         if (live && l == 0 && h == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
         live = false;
     }
-    const bi_kv4::RowPart xk = load_row(a.k + t * a.ld_k + h * kD, l);
-    const bi_kv4::RowPart xv = load_row(a.v + t * a.ld_v + h * kD, l);
-    const int off = live ? static_cast<int>(slot % BI_PAGE_SIZE) : 0;
-    const int64_t block = live ? (slot / BI_PAGE_SIZE) * a.Hkv + h : 0;
+    const int off = slot & (BI_PAGE_SIZE - 1);
+    const int64_t block = live ? static_cast<int64_t>(slot / BI_PAGE_SIZE) * a.Hkv + h : 0;
     bi_kv4::write_row<false>(xk, a.k_cache + block * bi_kv4::kBlockBytes, off, l, live);
     bi_kv4::write_row<true>(xv, a.v_cache + block * bi_kv4::kBlockBytes, off, l, live);
 }
@@ -69,55 +69,62 @@ struct ReadArgs {
     uint32_t* err;
 };
 
-// One CTA per (sequence, page): thread (r, c) writes dims 8c .. 8c + 7 of
-// token r, for every kv-head in turn.
+// One CTA per (sequence, page, kHeads kv-heads): thread (r, c) writes dims 8c ..
+// 8c + 7 of token r of every head, all loads before any store.
+constexpr int kHeads = 2;
+
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
     const int s = blockIdx.y, p = blockIdx.x;
+    const int h0 = blockIdx.z * kHeads;
     const int L = a.seq_lens[s];
     if (L < 0 || L > a.max_seq_len) {
-        if (threadIdx.x == 0 && p == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
+        if (threadIdx.x == 0 && p == 0 && h0 == 0)
+            bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
         return;
     }
     if (p * BI_PAGE_SIZE >= L) return;
     const int pg = a.block_table[static_cast<int64_t>(s) * a.max_pages_per_seq + p];
     if (pg < 0 || pg >= a.num_pages) {
-        if (threadIdx.x == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
+        if (threadIdx.x == 0 && h0 == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
         return;
     }
     const int r = threadIdx.x >> 4, c = threadIdx.x & 15;
     if (r >= L - p * BI_PAGE_SIZE) return;  // rows behind the sequence stay as they were
-    for (int h = 0; h < a.Hkv; ++h) {
-        const int64_t blk = static_cast<int64_t>(pg) * a.Hkv + h;
-        const int64_t out = (blk * BI_PAGE_SIZE + r) * kD + 8 * c;
-        const int sb = bi_kv4::kScaleOffset + bi_kv4::kScaleRowBytes * r + 2 * (c >> 2);
-        {
-            const uint8_t* b = a.k_cache + blk * bi_kv4::kBlockBytes;
-            const uint32_t sc = *reinterpret_cast<const uint16_t*>(b + sb);
-            const bi_kv4::ScalePair sp = bi_kv4::scale_pair(sc | (sc << 16));
-            uint32_t o[4];
+    const int k_at = 64 * r + 4 * (c >> 2);                                  // word (t = 0, j = c / 4)
+    const int v_at = 512 * (r >> 3) + 8 * (r & 7) + 4 * (c >> 3);            // word (g = 0, w = c / 8)
+    const int s_at = bi_kv4::kScaleOffset + bi_kv4::kScaleRowBytes * r + 2 * (c >> 2);
+    const int64_t blk0 = static_cast<int64_t>(pg) * a.Hkv + h0;
+    uint32_t kw[kHeads][4], vw[kHeads][8], ks[kHeads], vs[kHeads];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-                o[t] = bi_kv4::kv4_pair(
-                    *reinterpret_cast<const uint32_t*>(b + 64 * r + 16 * t + 4 * (c >> 2)), c & 3, sp);
-            *reinterpret_cast<uint4*>(a.k_out + out) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        {
-            const uint8_t* b = a.v_cache + blk * bi_kv4::kBlockBytes;
-            const uint32_t sc = *reinterpret_cast<const uint16_t*>(b + sb);
-            const bi_kv4::ScalePair sp = bi_kv4::scale_pair(sc | (sc << 16));
-            uint32_t o[4];
+    for (int i = 0; i < kHeads; ++i) {
+        if (h0 + i >= a.Hkv) break;
+        const uint8_t* kb = a.k_cache + (blk0 + i) * bi_kv4::kBlockBytes;
+        const uint8_t* vb = a.v_cache + (blk0 + i) * bi_kv4::kBlockBytes;
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                // dims 8c + 2t and 8c + 2t + 1: code c % 8 of words g = 2t, 2t + 1
-                const uint8_t* q = b + 512 * (r >> 3) + 128 * t + 8 * (r & 7) + 4 * (c >> 3);
-                const uint32_t w0 = *reinterpret_cast<const uint32_t*>(q) >> (4 * (c & 7));
-                const uint32_t w1 = *reinterpret_cast<const uint32_t*>(q + 64) >> (4 * (c & 7));
-                o[t] = bi_kv4::kv4_pair((w0 & 15u) | (w1 << 16), 0, sp);
-            }
-            *reinterpret_cast<uint4*>(a.v_out + out) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int t = 0; t < 4; ++t) kw[i][t] = *reinterpret_cast<const uint32_t*>(kb + k_at + 16 * t);
+#pragma unroll
+        for (int g = 0; g < 8; ++g) vw[i][g] = *reinterpret_cast<const uint32_t*>(vb + v_at + 64 * g);
+        ks[i] = *reinterpret_cast<const uint16_t*>(kb + s_at);
+        vs[i] = *reinterpret_cast<const uint16_t*>(vb + s_at);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        if (h0 + i >= a.Hkv) break;
+        const int64_t out = ((blk0 + i) * BI_PAGE_SIZE + r) * kD + 8 * c;
+        uint32_t ko[4], vo[4];
+        const bi_kv4::ScalePair kp = bi_kv4::scale_pair(ks[i] * 0x10001u);
+        const bi_kv4::ScalePair vp = bi_kv4::scale_pair(vs[i] * 0x10001u);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            ko[t] = bi_kv4::kv4_pair(kw[i][t], c & 3, kp);
+            // dims 8c + 2t, 8c + 2t + 1: code c % 8 of words g = 2t, 2t + 1
+            const uint32_t lo = vw[i][2 * t] >> (4 * (c & 7)), hi = vw[i][2 * t + 1] >> (4 * (c & 7));
+            vo[t] = bi_kv4::kv4_pair(__byte_perm(lo, hi, 0x5410), 0, vp);
         }
+        *reinterpret_cast<uint4*>(a.k_out + out) = make_uint4(ko[0], ko[1], ko[2], ko[3]);
+        *reinterpret_cast<uint4*>(a.v_out + out) = make_uint4(vo[0], vo[1], vo[2], vo[3]);
     }
 }
 
@@ -138,7 +145,7 @@ extern "C" bi_status bi_kv4_append(const void* k, int64_t ld_k, const void* v, i
     if ((ld_k & 7) || (ld_v & 7)) return BI_ERR_MISALIGNED;
     const int64_t rows = static_cast<int64_t>(T) * Hkv;
     const int64_t ctas = (rows + kHalfWarps - 1) / kHalfWarps;
-    if (ctas > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
+    if (rows > 0x7fffff00LL) return BI_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return BI_OK;
     if (!k || !v || !slots || !k_cache || !v_cache) return BI_ERR_INVALID_ARG;
     if (!bi::aligned16(k) || !bi::aligned16(v) || !bi::aligned16(k_cache) ||
@@ -149,12 +156,12 @@ extern "C" bi_status bi_kv4_append(const void* k, int64_t ld_k, const void* v, i
     a.v = static_cast<const __nv_bfloat16*>(v);
     a.ld_k = ld_k;
     a.ld_v = ld_v;
-    a.rows = rows;
-    a.Hkv = Hkv;
+    a.rows = static_cast<uint32_t>(rows);
+    a.Hkv = static_cast<uint32_t>(Hkv);
     a.slots = slots;
     a.k_cache = static_cast<uint8_t*>(k_cache);
     a.v_cache = static_cast<uint8_t*>(v_cache);
-    a.num_slots = static_cast<int64_t>(num_pages) * BI_PAGE_SIZE;
+    a.num_slots = num_pages * BI_PAGE_SIZE;
     a.err = bi::device_error_word();
     return bi::launch_pdl(kv4_append_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0,
                           stream, a) == cudaSuccess
@@ -170,7 +177,7 @@ extern "C" bi_status bi_kv4_read(const void* k_cache, const void* v_cache,
     if (S < 0 || Hkv <= 0 || max_pages_per_seq < 1 || num_pages < 1 || max_seq_len < 1)
         return BI_ERR_INVALID_ARG;
     if (D != kD || page_size != BI_PAGE_SIZE) return BI_ERR_UNSUPPORTED_SHAPE;
-    if (S > 65535) return BI_ERR_UNSUPPORTED_SHAPE;
+    if (S > 65535 || Hkv > 65535) return BI_ERR_UNSUPPORTED_SHAPE;
     if (static_cast<int64_t>(num_pages) * Hkv * BI_PAGE_SIZE >= (int64_t{1} << 31))
         return BI_ERR_UNSUPPORTED_SHAPE;
     if (static_cast<int64_t>(max_seq_len) > static_cast<int64_t>(max_pages_per_seq) * BI_PAGE_SIZE)
@@ -194,7 +201,7 @@ extern "C" bi_status bi_kv4_read(const void* k_cache, const void* v_cache,
     a.v_out = static_cast<__nv_bfloat16*>(v_out);
     a.err = bi::device_error_word();
     const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(max_seq_len) + BI_PAGE_SIZE - 1) / BI_PAGE_SIZE),
-                    static_cast<unsigned>(S));
+                    static_cast<unsigned>(S), static_cast<unsigned>((Hkv + kHeads - 1) / kHeads));
     return bi::launch_pdl(kv4_read_kernel, grid, dim3(kThreads), 0, stream, a) == cudaSuccess
                ? BI_OK
                : BI_ERR_CUDA;
