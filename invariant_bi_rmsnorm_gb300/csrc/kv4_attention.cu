@@ -67,8 +67,10 @@ struct Tables {
     float alpha[kPagesPerChunk][kMaxGroup];  // the factor O and l are rescaled by before it
     float psum[kPagesPerChunk][kMaxGroup];   // the page's weight sum
     float m[kMaxGroup], l[kMaxGroup];        // the chunk's reference and weight sum
-    uint32_t moved;                          // pages with an alpha other than 1
+    uint32_t moved;                          // pages with an alpha other than 1; kRefPerPage
 };
+constexpr uint32_t kRefPerPage = 1u << 31;  // else ref[0] is every page's and alpha is not set
+static_assert(kPagesPerChunk < 31, "a bit per page");
 static_assert(sizeof(Tables) <= kFoldFloats * 4, "the tables fit where the fold works");
 
 struct Kv4Args {
@@ -170,21 +172,29 @@ __device__ __forceinline__ void load_v(VFrags& f, const uint8_t* vb, int valid, 
     }
 }
 
-// bi_attn::pv_step for the 32 dims of group `gr`: two 16-dim tiles of O^T.
-__device__ __forceinline__ void pv_group(float (&acc0)[4], float (&acc1)[4], const VFrags& f, int gr,
-                                         const bi_attn::PFrags& pf) {
-    // codes of (even token, odd token) side by side; their scales likewise
-    const uint32_t half = gr & 1 ? 0x7632u : 0x5410u;
-    const bool up = gr & 2;
-    const uint32_t wa = __byte_perm(up ? f.ca.y : f.ca.x, up ? f.ca.w : f.ca.z, half);
-    const uint32_t wb = __byte_perm(up ? f.cb.y : f.cb.x, up ? f.cb.w : f.cb.z, half);
+// bi_attn::pv_step for a group of 32 dims, two 16-dim tiles of O^T.  wa, wb:
+// codes of the even and the odd token side by side (tokens 2(l%4) and the next;
+// 8 further on); sa, sb: their scales likewise.
+__device__ __forceinline__ void pv_tiles(float (&acc0)[4], float (&acc1)[4], uint32_t wa, uint32_t wb,
+                                         uint32_t sa, uint32_t sb, const bi_attn::PFrags& pf) {
     uint32_t va[4], vb[4];
-    four_pairs(va, wa, bi_kv4::scale_pair(__byte_perm(up ? f.sa.y : f.sa.x, up ? f.sa.w : f.sa.z, half)));
-    four_pairs(vb, wb, bi_kv4::scale_pair(__byte_perm(up ? f.sb.y : f.sb.x, up ? f.sb.w : f.sb.z, half)));
+    four_pairs(va, wa, bi_kv4::scale_pair(sa));
+    four_pairs(vb, wb, bi_kv4::scale_pair(sb));
     bi::mma_bf16_16816(acc0, va[0], va[1], vb[0], vb[1], pf.hi0, pf.hi1);
     bi::mma_bf16_16816(acc0, va[0], va[1], vb[0], vb[1], pf.lo0, pf.lo1);
     bi::mma_bf16_16816(acc1, va[2], va[3], vb[2], vb[3], pf.hi0, pf.hi1);
     bi::mma_bf16_16816(acc1, va[2], va[3], vb[2], vb[3], pf.lo0, pf.lo1);
+}
+
+// pv_tiles for group `gr` (a constant) of a loaded V block.
+__device__ __forceinline__ void pv_group(float (&acc0)[4], float (&acc1)[4], const VFrags& f, int gr,
+                                         const bi_attn::PFrags& pf) {
+    const uint32_t half = gr & 1 ? 0x7632u : 0x5410u;
+    const bool up = gr & 2;
+    pv_tiles(acc0, acc1, __byte_perm(up ? f.ca.y : f.ca.x, up ? f.ca.w : f.ca.z, half),
+             __byte_perm(up ? f.cb.y : f.cb.x, up ? f.cb.w : f.cb.z, half),
+             __byte_perm(up ? f.sa.y : f.sa.x, up ? f.sa.w : f.sa.z, half),
+             __byte_perm(up ? f.sb.y : f.sb.x, up ? f.sb.w : f.sb.z, half), pf);
 }
 
 // One butterfly for the two columns of every lane over the 8 lanes that share
@@ -300,25 +310,37 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
     // ---- 2: the online softmax's reference maxima (bi_attn::softmax_step) ----
     if (warp == 0) {
         const int n = lane & 7;
-        float m = -INFINITY;
-        uint32_t moved = 0;
-        for (int p = 0; p < np; ++p) {
-            const float mx = tb.pmax[p][n];
-            const float mn = mx > __fadd_rn(m, bi_attn::kRescaleSlack) ? mx : m;
-            const float al = mn == m ? 1.f : bi_attn::exp2_ftz(__fsub_rn(m, mn));
-            if (__any_sync(0xffffffffu, mn != m)) moved |= 1u << p;
-            m = mn;
-            if (lane < 8) {
-                // no visible score so far: every score is -inf, and so is its
-                // difference from 0
-                tb.ref[p][n] = m == -INFINITY ? 0.f : m;
-                tb.alpha[p][n] = al;
+        const float m0 = tb.pmax[0][n];  // the first page's maximum is its reference
+        float top = m0;
+        for (int p = lane >> 3; p < np; p += 4) top = fmaxf(top, tb.pmax[p][n]);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        // no page moves it further (as a rule): one reference, no rescaling
+        if (__all_sync(0xffffffffu, m0 > -INFINITY && !(top > __fadd_rn(m0, bi_attn::kRescaleSlack)))) {
+            if (lane < 8) tb.ref[0][n] = tb.m[n] = m0;
+            if (lane == 0) tb.moved = 0u;
+        } else {
+            float m = -INFINITY;
+            uint32_t moved = kRefPerPage;
+            for (int p = 0; p < np; ++p) {
+                const float mx = tb.pmax[p][n];
+                const float mn = mx > __fadd_rn(m, bi_attn::kRescaleSlack) ? mx : m;
+                const float al = mn == m ? 1.f : bi_attn::exp2_ftz(__fsub_rn(m, mn));
+                if (__any_sync(0xffffffffu, mn != m)) moved |= 1u << p;
+                m = mn;
+                if (lane < 8) {
+                    // no visible score so far: every score is -inf, and so is its
+                    // difference from 0
+                    tb.ref[p][n] = m == -INFINITY ? 0.f : m;
+                    tb.alpha[p][n] = al;
+                }
             }
+            if (lane < 8) tb.m[n] = m;
+            if (lane == 0) tb.moved = moved & ~1u;  // before page 0 there is nothing to rescale
         }
-        if (lane < 8) tb.m[n] = m;
-        if (lane == 0) tb.moved = moved & ~1u;  // before page 0 there is nothing to rescale
     }
     __syncthreads();
+    const uint32_t moved = tb.moved;
 
     // ---- 3: weights p = 2^(x - m) of this warp's pages, split into bf16 high
     // part and remainder, transposed into mma B fragments ----
@@ -326,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
     for (int i = 0; i < kPagesPerWarp; ++i) {
         const int p = warp + kWarps * i;
         if (p >= np) break;
-        const float2 m = *reinterpret_cast<const float2*>(&tb.ref[p][2 * (lane & 3)]);
+        const float2 m = *reinterpret_cast<const float2*>(&tb.ref[moved & kRefPerPage ? p : 0][2 * (lane & 3)]);
         const float w[4] = {bi_attn::exp2_ftz(__fsub_rn(x[i][0], m.x)), bi_attn::exp2_ftz(__fsub_rn(x[i][1], m.y)),
                             bi_attn::exp2_ftz(__fsub_rn(x[i][2], m.x)), bi_attn::exp2_ftz(__fsub_rn(x[i][3], m.y))};
         bi_attn::PFrags pf;
@@ -339,19 +361,33 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
     __syncthreads();
 
     // ---- 4: O^T of this warp's 32 dims, page after page; l beside it ----
-    const uint32_t moved = tb.moved;
     if (warp == kWarps - 1 && lane < 8) {
         float l = 0.f;
-        for (int p = 0; p < np; ++p) l = __fmaf_rn(l, tb.alpha[p][lane], tb.psum[p][lane]);
+        for (int p = 0; p < np; ++p)
+            l = __fmaf_rn(l, moved >> p & 1u ? tb.alpha[p][lane] : 1.f, tb.psum[p][lane]);
         tb.l[lane] = l;
     }
     float acc[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-#pragma unroll 2
-    for (int p = 0; p < np; ++p) {
-        VFrags f;
-        load_v(f, vs + p * kBlockBytes, tokens - p * kPage, lane);
+    const bool up = warp & 2;  // which words and halves hold this warp's group
+    const uint32_t half = warp & 1 ? 0x7632u : 0x5410u;
+    auto output_page = [&](int p, int valid) {
+        const uint8_t* vb = vs + p * kBlockBytes;
+        const uint4 ca = *reinterpret_cast<const uint4*>(vb + 16 * lane);
+        const uint4 cb = *reinterpret_cast<const uint4*>(vb + 512 + 16 * lane);
+        const uint8_t* sp = vb + kScaleOffset + 2 * kScaleRowBytes * (lane & 3) + 4 * (warp >> 1);
+        uint32_t s0 = *reinterpret_cast<const uint32_t*>(sp);
+        uint32_t s1 = *reinterpret_cast<const uint32_t*>(sp + kScaleRowBytes);
+        uint32_t s8 = *reinterpret_cast<const uint32_t*>(sp + 8 * kScaleRowBytes);
+        uint32_t s9 = *reinterpret_cast<const uint32_t*>(sp + 9 * kScaleRowBytes);
+        if (valid < kPage) {  // as load_v
+            const int t = 2 * (lane & 3);
+            if (t >= valid) s0 = 0u;
+            if (t + 1 >= valid) s1 = 0u;
+            if (t + 8 >= valid) s8 = 0u;
+            if (t + 9 >= valid) s9 = 0u;
+        }
         const uint4 w = weights[p * 32 + lane];
         if (moved >> p & 1u) {
             const float2 al = *reinterpret_cast<const float2*>(&tb.alpha[p][2 * (lane & 3)]);
@@ -363,8 +399,13 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
                 acc[i][3] = __fmul_rn(acc[i][3], al.y);
             }
         }
-        pv_group(acc[0], acc[1], f, warp, bi_attn::PFrags{w.x, w.y, w.z, w.w});
-    }
+        pv_tiles(acc[0], acc[1], __byte_perm(up ? ca.y : ca.x, up ? ca.w : ca.z, half),
+                 __byte_perm(up ? cb.y : cb.x, up ? cb.w : cb.z, half), __byte_perm(s0, s1, half),
+                 __byte_perm(s8, s9, half), bi_attn::PFrags{w.x, w.y, w.z, w.w});
+    };
+#pragma unroll 4
+    for (int p = 0; p < np - 1; ++p) output_page(p, kPage);
+    output_page(np - 1, tokens - (np - 1) * kPage);  // whose last tokens may not be there
     __syncthreads();  // l is there
 
     const int h0 = 2 * (lane & 3);

@@ -35,26 +35,40 @@ __device__ __forceinline__ bi_kv4::RowPart load_row(const __nv_bfloat16* p, int 
     return {*reinterpret_cast<const uint2*>(p + 4 * l), *reinterpret_cast<const uint2*>(p + kD / 2 + 4 * l)};
 }
 
-// One half-warp per (token, kv-head): its K row and its V row.
+// A half-warp takes kRows (token, kv-head) pairs, the K row and the V row of
+// each, all loads before any arithmetic.
+constexpr int kRows = 2;
+
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
     const int l = threadIdx.x & 15;
-    const uint32_t row = blockIdx.x * kHalfWarps + (threadIdx.x >> 4);
-    bool live = row < a.rows;
-    const uint32_t t = live ? row / a.Hkv : 0;
-    const uint32_t h = live ? row - t * a.Hkv : 0;
-    const bi_kv4::RowPart xk = load_row(a.k + t * a.ld_k + h * kD, l);
-    const bi_kv4::RowPart xv = load_row(a.v + t * a.ld_v + h * kD, l);
-    const int32_t slot = a.slots[t];
-    if (slot < 0 || slot >= a.num_slots) {
-        if (live && l == 0 && h == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
-        live = false;
+    bi_kv4::RowPart xk[kRows], xv[kRows];
+    int32_t slot[kRows];
+    uint32_t head[kRows];
+    bool live[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const uint32_t row = (blockIdx.x * kRows + i) * kHalfWarps + (threadIdx.x >> 4);
+        live[i] = row < a.rows;
+        const uint32_t t = live[i] ? row / a.Hkv : 0;
+        head[i] = live[i] ? row - t * a.Hkv : 0;
+        xk[i] = load_row(a.k + t * a.ld_k + head[i] * kD, l);
+        xv[i] = load_row(a.v + t * a.ld_v + head[i] * kD, l);
+        slot[i] = a.slots[t];
     }
-    const int off = slot & (BI_PAGE_SIZE - 1);
-    const int64_t block = live ? static_cast<int64_t>(slot / BI_PAGE_SIZE) * a.Hkv + h : 0;
-    bi_kv4::write_row<false>(xk, a.k_cache + block * bi_kv4::kBlockBytes, off, l, live);
-    bi_kv4::write_row<true>(xv, a.v_cache + block * bi_kv4::kBlockBytes, off, l, live);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (slot[i] < 0 || slot[i] >= a.num_slots) {
+            if (live[i] && l == 0 && head[i] == 0)
+                bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
+            live[i] = false;
+        }
+        const int off = slot[i] & (BI_PAGE_SIZE - 1);
+        const int64_t block = live[i] ? static_cast<int64_t>(slot[i] / BI_PAGE_SIZE) * a.Hkv + head[i] : 0;
+        bi_kv4::write_row<false>(xk[i], a.k_cache + block * bi_kv4::kBlockBytes, off, l, live[i]);
+        bi_kv4::write_row<true>(xv[i], a.v_cache + block * bi_kv4::kBlockBytes, off, l, live[i]);
+    }
 }
 
 struct ReadArgs {
@@ -144,7 +158,7 @@ extern "C" bi_status bi_kv4_append(const void* k, int64_t ld_k, const void* v, i
     if (ld_k < width || ld_v < width) return BI_ERR_INVALID_ARG;
     if ((ld_k & 7) || (ld_v & 7)) return BI_ERR_MISALIGNED;
     const int64_t rows = static_cast<int64_t>(T) * Hkv;
-    const int64_t ctas = (rows + kHalfWarps - 1) / kHalfWarps;
+    const int64_t ctas = (rows + kRows * kHalfWarps - 1) / (kRows * kHalfWarps);
     if (rows > 0x7fffff00LL) return BI_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return BI_OK;
     if (!k || !v || !slots || !k_cache || !v_cache) return BI_ERR_INVALID_ARG;

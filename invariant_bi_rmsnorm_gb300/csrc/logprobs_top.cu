@@ -38,10 +38,9 @@ namespace {
 using bi_lp::kLog2e;
 using bi_lp::kThreads;
 
-// Vectors a thread loads while it folds as many.  At six CTAs per SM (40
-// registers) 2 is best at 1024 rows (78 us; 1 takes 97, 4 spills), and one row
-// takes 17.5 us with 2, 4 or 8.
-constexpr int kUnroll = 2;
+// Vectors a thread has on their way at a time.  1024 rows of 151936 logits took
+// 70 us with 4 (five CTAs per SM), 83 with 2 (six), 71 with 8 (four).
+constexpr int kUnroll = 4;
 constexpr int kSegs = 32;      // segments per thread, at most
 constexpr int kMaxTop = 32;
 constexpr int kMaxCand = 512;
@@ -206,7 +205,7 @@ __device__ __forceinline__ void each_reaching(const uint16_t* x, int vocab, int 
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 6) logprobs_top_kernel(const TopArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) logprobs_top_kernel(const TopArgs a) {
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
     __shared__ uint16_t seg_max[kSegs * kThreads];
@@ -225,36 +224,24 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_top_kernel(const TopArgs
     const uint16_t* xb = reinterpret_cast<const uint16_t*>(x);
     const int nvec = a.vocab / 8;
 
-    // ---- one pass: (m, s, T) and the segments' maxima; kUnroll vectors of a
-    // thread are on their way while the kUnroll before them are folded ----
+    // ---- one pass: (m, s, T) and the segments' maxima ----
     Run run = {kLowest, 0.f, 0.f, make_float2(0.f, 0.f), true};
     uint32_t best = 0;
-    {
-        uint4 next[kUnroll];
-        auto load = [&](int v0) {
+    for (int sg = 0, v0 = tid; sg * a.seg_vecs * kThreads < nvec; ++sg) {
+        float sm = -INFINITY;
+        for (int i0 = 0; i0 < a.seg_vecs; i0 += kUnroll, v0 += kUnroll * kThreads) {
+            uint4 u[kUnroll];
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
                 const int v = v0 + i * kThreads;
-                next[i] = v < nvec ? __ldcs(xv + v) : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
+                u[i] = v < nvec ? __ldcs(xv + v) : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
             }
-        };
-        int v0 = tid;
-        load(v0);
-        for (int sg = 0; sg * a.seg_vecs * kThreads < nvec; ++sg) {
-            float sm = -INFINITY;
-            for (int i0 = 0; i0 < a.seg_vecs; i0 += kUnroll) {
-                uint4 u[kUnroll];
 #pragma unroll
-                for (int i = 0; i < kUnroll; ++i) u[i] = next[i];
-                v0 += kUnroll * kThreads;
-                load(v0);
-#pragma unroll
-                for (int i = 0; i < kUnroll; ++i) sm = fmaxf(sm, fold_vec_t(run, u[i]));
-            }
-            const uint32_t key = key_of(__float_as_uint(sm) >> 16);
-            seg_max[sg * kThreads + tid] = static_cast<uint16_t>(key);
-            best = max(best, key);
+            for (int i = 0; i < kUnroll; ++i) sm = fmaxf(sm, fold_vec_t(run, u[i]));
         }
+        const uint32_t key = key_of(__float_as_uint(sm) >> 16);
+        seg_max[sg * kThreads + tid] = static_cast<uint16_t>(key);
+        best = max(best, key);
     }
     thread_max[tid] = static_cast<uint16_t>(best);
     Part r = {run.m, run.s, __fadd_rn(run.t.x, run.t.y)};
