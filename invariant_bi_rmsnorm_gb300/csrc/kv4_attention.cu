@@ -756,12 +756,12 @@ __global__ void __launch_bounds__(32, 16) attn_warp_kv4_kernel(const Kv4Args ka)
 // Chunks per SM (at the launch's bound on the lengths; lengths spread up to the
 // bound fill about half of them) from which on the warp kernel is taken.
 // Measured on GB300 with 8 kv-heads, chunk kernel against warp kernel: 14 per
-// SM (B = 8 up to 8192 tokens) 21 against 35 us, 27 (B = 16) 35 against 40, 40
-// (B = 24) 50 against 51, 54 (B = 32) 64 against 60, 108 (B = 64) 117 against
-// 101, 431 (B = 256) 440 against 341 us.  The chunk kernel's four warps finish
-// a chunk several times sooner, the warp kernel issues a quarter fewer
-// instructions and has no barriers.
-constexpr int64_t kManyChunks = 44;
+// SM (B = 8 up to 8192 tokens) 20 against 35 us, 27 (B = 16) 32 against 40, 40
+// (B = 24) 47 against 51, 54 (B = 32) 59 against 60, 81 (B = 48) 85 against 80,
+// 108 (B = 64) 112 against 101.  The chunk kernel's four warps finish a chunk
+// several times sooner; the warp kernel issues a quarter fewer instructions and
+// has no barriers.
+constexpr int64_t kManyChunks = 60;
 
 // set once per device; any thread may race to set it, the attribute is idempotent
 std::atomic<bool> g_attr_set[64] = {};
