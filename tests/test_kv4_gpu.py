@@ -219,6 +219,20 @@ def _problem(lens, Hq, Hkv, seed, spare=3):
     return (p["q"].cuda(), kc, vc, p["block_table"].cuda(), p["seq_lens"].cuda())
 
 
+# Launches of many chunks run a kernel of their own; a bound on the lengths far
+# above them makes one of any batch.
+BOTH_KERNELS = pytest.mark.parametrize("many", [False, True], ids=["few-chunks", "many-chunks"])
+
+
+def _bound(many, bt, msl, Hkv):
+    """(block table, max_seq_len) of a launch of few or of many chunks."""
+    if many:
+        msl = 256 * -(-60 * 160 // (bt.shape[0] * Hkv))
+    wide = torch.full((bt.shape[0], max(bt.shape[1], -(-msl // 16))), -1, dtype=torch.int32, device="cuda")
+    wide[:, :bt.shape[1]] = bt
+    return wide, msl
+
+
 def _both(q, kc, vc, bt, lens, msl, **kw):
     got = bi.decode_attention_kv4(q, kc, vc, bt, lens, msl, **kw)
     ko, vo = _read_all(kc, vc)
@@ -227,10 +241,12 @@ def _both(q, kc, vc, bt, lens, msl, **kw):
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(32, 8), (8, 1), (5, 5), (14, 2), (3, 1), (28, 4), (6, 3), (20, 4), (6, 1)])
-def test_attention_has_the_bits_of_the_read_back_cache(Hq, Hkv):
+@BOTH_KERNELS
+def test_attention_has_the_bits_of_the_read_back_cache(Hq, Hkv, many):
     lens = [1, 2, 15, 16, 17, 255, 256, 257, 1000, 1025, 40, 2049]
     q, kc, vc, bt, sl = _problem(lens, Hq, Hkv, 940 + Hq)
-    got, want, ko, vo = _both(q, kc, vc, bt, sl, max(lens))
+    bt, msl = _bound(many, bt, max(lens), Hkv)
+    got, want, ko, vo = _both(q, kc, vc, bt, sl, msl)
     assert np.array_equal(bits(got), bits(want))
     ref = oracle.decode_attention(q.cpu(), ko.cpu(), vo.cpu(), bt.cpu(), sl.cpu())
     tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -13 * float(vo.abs().max())
@@ -283,66 +299,100 @@ def test_row_alone_and_in_a_batch():
 
 
 @pytest.mark.parametrize("scale", [1e-6, 0.5, 30.0])
-def test_peaked_and_flat_scores(scale):
+@BOTH_KERNELS
+def test_peaked_and_flat_scores(scale, many):
     lens = [3, 290, 1030]
     q, kc, vc, bt, sl = _problem(lens, 16, 4, 985)
-    got, want, _, _ = _both(q, kc, vc, bt, sl, max(lens), scale=scale)
+    bt, msl = _bound(many, bt, max(lens), 4)
+    got, want, _, _ = _both(q, kc, vc, bt, sl, msl, scale=scale)
     assert np.array_equal(bits(got), bits(want)) and torch.isfinite(got).all()
 
 
-def test_what_lies_behind_a_sequence_never_counts():
+@BOTH_KERNELS
+def test_scores_that_climb_page_after_page(many):
+    """Keys that grow along the sequence move the reference maximum on every
+    page; keys that shrink leave it at the first; either way down to weights of
+    zero.  And queries of -inf and NaN, which show in their own head only."""
+    lens = [700, 256, 33]
+    q, kc, vc, bt, sl = _problem(lens, 8, 4, 987)
+    P = kc.shape[0]
+    k, v = _read_all(kc, vc)
+    for i, L in enumerate(lens):
+        for t in range(L):
+            k[int(bt[i, t // 16]), :, t % 16] = ((t + 1) if i == 0 else (L - t)) / 40 * q[i, ::2].sign()
+    kc, vc = _cache_of(k, v)
+    bt, msl = _bound(many, bt, 700, 4)
+    got, want, _, _ = _both(q, kc, vc, bt, sl, msl)
+    assert np.array_equal(bits(got), bits(want)) and torch.isfinite(got).all() and P
+    bad = q.clone()
+    bad[0, 3, 5], bad[1, 2, 7], bad[2, 6, 0] = float("inf"), float("nan"), float("-inf")
+    got2, want2, _, _ = _both(bad, kc, vc, bt, sl, msl)
+    assert torch.equal(got2.isnan(), want2.isnan())
+    assert torch.equal(got2.nan_to_num(0.0), want2.nan_to_num(0.0))
+    for i, h in ((0, 3), (1, 2), (2, 6)):
+        keep = [j for j in range(8) if j != h]
+        assert np.array_equal(bits(got2[i, keep]), bits(got[i, keep]))
+
+
+@BOTH_KERNELS
+def test_what_lies_behind_a_sequence_never_counts(many):
     """Codes and scales of tokens behind the end, NaN scales among them."""
     lens = [1, 9, 23, 511]
     q, kc, vc, bt, sl = _problem(lens, 8, 2, 990)
-    ref = bi.decode_attention_kv4(q, kc, vc, bt, sl, 511)
+    bt, msl = _bound(many, bt, 511, 2)
+    ref = bi.decode_attention_kv4(q, kc, vc, bt, sl, msl)
     for i, L in enumerate(lens):
         p, r = int(bt[i, (L - 1) // 16]), (L - 1) % 16 + 1
         for c in (kc, vc):
             c[p, :, 1024 + 8 * r:] = 0xFF
         kc[p, :, 64 * r:1024] = 0x99
-    assert np.array_equal(bits(bi.decode_attention_kv4(q, kc, vc, bt, sl, 511)), bits(ref))
+    assert np.array_equal(bits(bi.decode_attention_kv4(q, kc, vc, bt, sl, msl)), bits(ref))
     assert torch.isfinite(ref).all()
 
 
-def test_a_nan_group_shows_in_its_own_sequence_only():
+@BOTH_KERNELS
+def test_a_nan_group_shows_in_its_own_sequence_only(many):
     lens = [40, 40]
     q, kc, vc, bt, sl = _problem(lens, 4, 1, 992)
-    ref = bi.decode_attention_kv4(q, kc, vc, bt, sl, 40)
+    bt, msl = _bound(many, bt, 40, 1)
+    ref = bi.decode_attention_kv4(q, kc, vc, bt, sl, msl)
     bad = torch.zeros(1, 1, 128, dtype=torch.bfloat16, device="cuda")
     bad[0, 0, 100] = float("inf")
     zero = torch.zeros_like(bad)
     slot = (bt[0, 1] * 16 + 3).reshape(1).to(torch.int32)
     bi.kv4_append(zero, bad, slot, kc, vc)
-    got, want, _, _ = _both(q, kc, vc, bt, sl, 40)
+    got, want, _, _ = _both(q, kc, vc, bt, sl, msl)
     assert np.array_equal(bits(got[1]), bits(ref[1])) and np.array_equal(bits(got), bits(want))
     assert torch.isnan(got[0, :, 96:]).all() and torch.isfinite(got[0, :, :96]).all()
 
 
-def test_bad_pages_and_lengths_are_reported():
+@BOTH_KERNELS
+def test_bad_pages_and_lengths_are_reported(many):
     lens = [40, 600, 33, 20]
     q, kc, vc, bt, sl = _problem(lens, 8, 2, 995)
-    ws = torch.zeros(bi.decode_attention_workspace_size(4, 8, 128, 2048), dtype=torch.uint8, device="cuda")
-    wide = torch.full((4, 128), -1, dtype=torch.int32, device="cuda")
-    wide[:, :bt.shape[1]] = bt
-    ref = bi.decode_attention_kv4(q, kc, vc, wide, sl, 2048, workspace=ws)
+    bt, msl = _bound(many, bt, 2048, 2)
+    ws = torch.zeros(bi.decode_attention_workspace_size(4, 8, 128, msl), dtype=torch.uint8, device="cuda")
+    ref = bi.decode_attention_kv4(q, kc, vc, bt, sl, msl, workspace=ws)
     for row, col, bad in ((0, 1, kc.shape[0]), (1, 20, -1), (1, 37, 2 ** 31 - 1)):
-        t = wide.clone()
+        t = bt.clone()
         t[row, col] = bad
         out = torch.full_like(q, 9.0)
-        bi.decode_attention_kv4(q, kc, vc, t, sl, 2048, out=out, workspace=ws)
+        bi.decode_attention_kv4(q, kc, vc, t, sl, msl, out=out, workspace=ws)
         with pytest.raises(bi.BiError, match="BAD_INPUT"):
             bi.get_device_error()
         keep = [i for i in range(4) if i != row]
         assert (out[row] == 9).all() and np.array_equal(bits(out[keep]), bits(ref[keep]))
         assert not ws[:bi._lib.DECODE_COUNTER_BYTES].any()
-    for bad in (0, -5, 2049):
+    for bad in (0, -5, msl + 1):
         l2 = sl.clone()
         l2[2] = bad
         out = torch.full_like(q, 9.0)
-        bi.decode_attention_kv4(q, kc, vc, wide, l2, 2048, out=out, workspace=ws)
+        bi.decode_attention_kv4(q, kc, vc, bt, l2, msl, out=out, workspace=ws)
         with pytest.raises(bi.BiError, match="BAD_INPUT"):
             bi.get_device_error()
         assert (out[2] == 9).all() and np.array_equal(bits(out[:2]), bits(ref[:2]))
+    # and all is well afterwards
+    assert np.array_equal(bits(bi.decode_attention_kv4(q, kc, vc, bt, sl, msl, workspace=ws)), bits(ref))
 
 
 def test_offsets_past_32_bits():
