@@ -417,7 +417,7 @@ bi_status bi_logprobs(const void* logits, int64_t rows, int32_t vocab, int64_t l
  *              values; ld_k, ld_v >= Hkv * 128, multiples of 8 (so that rows
  *              of a qkv projection can be given where they lie).
  *   slots      device, int32 [T]: each token's cache slot, page * 16 + offset.
- *   num_pages * Hkv * 16 < 2^31.  D = 128, page_size = 16.
+ *   num_pages * Hkv * 16 < 2^31;  T * Hkv <= 2^31 - 256.  D = 128, page_size = 16.
  * A slot out of range is reported on the device (BI_ERR_DEVICE_BAD_INPUT) and
  * that token is skipped.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED,
  * CUDA.

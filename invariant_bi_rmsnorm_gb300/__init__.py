@@ -564,7 +564,7 @@ def kv4_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Te
                 *((t, n, _BF16, (cs[0], cs[1], PAGE_SIZE, 128)) for t, n in ((k_out, "k_out"), (v_out, "v_out"))))
     _check(_lib.load().bi_kv4_read(
         k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), bs[1], seq_lens.data_ptr(),
-        bs[0], cs[1], 128, PAGE_SIZE, cs[0], max_seq_len, k_out.data_ptr(), v_out.data_ptr(),
+        bs[0], cs[1], 128, PAGE_SIZE, cs[0], int(max_seq_len), k_out.data_ptr(), v_out.data_ptr(),
         _raw_stream(dev) if stream is None else _stream(stream)), "bi_kv4_read")
 
 
@@ -596,7 +596,7 @@ def decode_attention_kv4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if workspace is None:
-        need = decode_attention_workspace_size(B, Hq, D, max_seq_len)
+        need = decode_attention_workspace_size(B, Hq, D, int(max_seq_len))
         if need > 0:
             # the leading arrival counters must start at zero (every call leaves
             # them zero, so a caller-kept workspace is cleared only once)
@@ -606,7 +606,7 @@ def decode_attention_kv4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     ws = workspace is not None
     _check(_lib.load().bi_decode_attention_kv4(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), bs[1],
-        seq_lens.data_ptr(), B, Hq, cs[1], D, PAGE_SIZE, cs[0], max_seq_len, scale, out.data_ptr(),
+        seq_lens.data_ptr(), B, Hq, cs[1], D, PAGE_SIZE, cs[0], int(max_seq_len), scale, out.data_ptr(),
         workspace.data_ptr() if ws else None, workspace.nbytes if ws else 0,
         _raw_stream(dev) if stream is None else _stream(stream)), "bi_decode_attention_kv4")
     return out
@@ -627,6 +627,7 @@ def logprobs_top(logits: torch.Tensor, targets: torch.Tensor | None, k: int, str
         if logits.get_device() != dev:
             _refuse("logprobs_top", (logits.contiguous(), "logits", _BF16, None))
     rows, vocab = shape
+    k = int(k)
     if k < 1:
         raise ValueError("logprobs_top: k must be at least 1")
     if targets is not None and not (targets.dtype is _I32 and targets.shape == shape[:1]

@@ -29,6 +29,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "attn_fold.cuh"
@@ -89,8 +90,18 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
         : "memory");
 }
 
-__device__ __forceinline__ uint32_t lo_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
-__device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
+// The low (high) half twice, as moves: the compiler takes them into the operand
+// of the bf16 arithmetic, which it does not with a byte permutation.
+__device__ __forceinline__ uint32_t twice_lo(uint32_t a) {
+    uint32_t d;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(d) : "r"(a));
+    return d;
+}
+__device__ __forceinline__ uint32_t twice_hi(uint32_t a) {
+    uint32_t d;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(d) : "r"(a));
+    return d;
+}
 
 // The values of the codes at bits 4p .. 4p + 3 of both halves of w, p = 0 .. 3.
 __device__ __forceinline__ void four_pairs(uint32_t (&v)[4], uint32_t w, const ScalePair& sp) {
@@ -114,8 +125,8 @@ __device__ __forceinline__ void page_scores_kv4(float (&sc)[4], const uint8_t* k
     for (int j = 0; j < 4; ++j) {  // the group of dims 32j .. 32j + 31: two 16-deep steps
         const uint32_t da = j < 2 ? sa.x : sa.y, db = j < 2 ? sb.x : sb.y;
         uint32_t va[4], vb[4];
-        four_pairs(va, wa[j], bi_kv4::scale_pair(j & 1 ? hi_halves(da, da) : lo_halves(da, da)));
-        four_pairs(vb, wb[j], bi_kv4::scale_pair(j & 1 ? hi_halves(db, db) : lo_halves(db, db)));
+        four_pairs(va, wa[j], bi_kv4::scale_pair(j & 1 ? twice_hi(da) : twice_lo(da)));
+        four_pairs(vb, wb[j], bi_kv4::scale_pair(j & 1 ? twice_hi(db) : twice_lo(db)));
         bi::mma_bf16_16816(sc, va[0], vb[0], va[1], vb[1], qb0[2 * j], qb1[2 * j]);
         bi::mma_bf16_16816(sc, va[2], vb[2], va[3], vb[3], qb0[2 * j + 1], qb1[2 * j + 1]);
     }
@@ -448,8 +459,7 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
 // page's scores are formed (they depend on nothing before them).
 
 constexpr int kRing = 4;  // pages in flight
-constexpr int kLoadBytes = 2 * kBlockBytes;
-constexpr int kStageBytes = kLoadBytes + 16;  // K, V, the stage's barrier
+constexpr int kStageBytes = 2 * kBlockBytes;
 constexpr uint32_t kAll = 0xffffffffu;
 
 // bi_attn::ColState of two columns, as the fast path of weights_step wants it.
@@ -607,31 +617,50 @@ __global__ void __launch_bounds__(32, 16) attn_warp_kv4_kernel(const Kv4Args ka)
     uint32_t* const ctr = nch > 1 ? a.counters + static_cast<int64_t>(s) * a.Hkv + g : nullptr;
 
     __shared__ __align__(16) uint8_t ring[kRing * kStageBytes];
-    auto bar_of = [](uint8_t* stage) { return reinterpret_cast<uint64_t*>(stage + kLoadBytes); };
 
-    // lane p keeps where page p lies, and copies it when its stage is free
-    int pg = 0;
-    if (lane < np)
-        pg = a.block_table[static_cast<int64_t>(s) * a.max_pages_per_seq + c * kPagesPerChunk + lane];
-    if (__any_sync(kAll, pg < 0 || pg >= a.num_pages)) {
-        if (lane == 0) {
-            bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
-            if (nch > 1) bi_attn::arrive_bad(ctr, nch);
+    // lane p keeps which block page p is
+    int block = 0;
+    {
+        int pg = 0;
+        if (lane < np)
+            pg = a.block_table[static_cast<int64_t>(s) * a.max_pages_per_seq + c * kPagesPerChunk + lane];
+        if (__any_sync(kAll, pg < 0 || pg >= a.num_pages)) {
+            if (lane == 0) {
+                bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
+                if (nch > 1) bi_attn::arrive_bad(ctr, nch);
+            }
+            return;
         }
-        return;
+        block = pg * a.Hkv + g;
     }
-    const int64_t at = (static_cast<int64_t>(pg) * a.Hkv + g) * kBlockBytes;
-    const uint8_t* const k_src = ka.k_cache + at;
-    const uint8_t* const v_src = ka.v_cache + at;
-    if (lane < kRing) bi::mbar_init(bar_of(ring + lane * kStageBytes), 1);
-    bi::fence_mbar_init();
-    __syncwarp();
-    auto copy_page = [&](uint8_t* stage) {
-        bi::mbar_arrive_expect_tx(bar_of(stage), kLoadBytes);
-        bulk_load(stage, k_src, kBlockBytes, bar_of(stage));
-        bulk_load(stage + kBlockBytes, v_src, kBlockBytes, bar_of(stage));
+    // A page's two blocks are 72 16-byte units each: two asynchronous copies a
+    // lane for each block, and one for the 8 units that are left of either.
+    // (Bulk copies, one lane's work, take the warp twice as many instructions,
+    // and a barrier's on top.)  A page is a group, there or not.
+    static_assert(kBlockBytes == 72 * 16, "units of a block");
+    const uint8_t* const k_src = ka.k_cache + 16 * lane;
+    const uint8_t* const v_src = ka.v_cache + 16 * lane;
+    const uint8_t* const rest_src = 1024 + (lane < 8 ? k_src : v_src - 128);
+    const int rest_dst = 1024 + (lane < 8 ? 16 * lane : kBlockBytes + 16 * (lane - 8));
+    auto copy_page = [&](int p, uint8_t* stage) {
+        if (p < np) {
+            const int64_t at = static_cast<int64_t>(__shfl_sync(kAll, block, p)) * kBlockBytes;
+            uint8_t* dst = stage + 16 * lane;
+            bi::cp_async_16(dst, k_src + at);
+            bi::cp_async_16(dst + 512, k_src + at + 512);
+            bi::cp_async_16(dst + kBlockBytes, v_src + at);
+            bi::cp_async_16(dst + kBlockBytes + 512, v_src + at + 512);
+            if (lane < 16) bi::cp_async_16(stage + rest_dst, rest_src + at);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    if (lane < min(np, kRing)) copy_page(ring + lane * kStageBytes);
+    // until at most kPending of the latest groups are on their way
+    auto wait_pages = [](auto pending) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(decltype(pending)::value) : "memory");
+        __syncwarp();  // every lane's copies, for every lane
+    };
+#pragma unroll
+    for (int p = 0; p < kRing; ++p) copy_page(p, ring + p * kStageBytes);
 
     // column n of the mma tile = query head g*group + n (n < group)
     const int64_t row0 = static_cast<int64_t>(s) * a.Hq + g * a.group;
@@ -646,43 +675,24 @@ __global__ void __launch_bounds__(32, 16) attn_warp_kv4_kernel(const Kv4Args ka)
     for (int mt = 0; mt < 8; ++mt) st.acc[mt][0] = st.acc[mt][1] = st.acc[mt][2] = st.acc[mt][3] = 0.f;
 
     uint8_t* cur = ring;  // the stage of page p
-    uint32_t parity = 0;  // of the phase its copies complete
-    bool ok = __all_sync(kAll, bi::mbar_wait(bar_of(cur), 0));
-    int p = 0;
+    wait_pages(std::integral_constant<int, kRing - 1>());
     float x[4];
-    if (ok) page_logs(x, cur, qb0, qb1, tokens, a.scale_log2, lane);
+    page_logs(x, cur, qb0, qb1, tokens, a.scale_log2, lane);
     // full pages with a page behind them
-    for (; ok && p < np - 1; ++p) {
+    for (int p = 0; p < np - 1; ++p) {
         uint8_t* next = cur + kStageBytes;
-        if (next == ring + kRing * kStageBytes) {
-            next = ring;
-            parity ^= 1;
-        }
-        ok = __all_sync(kAll, bi::mbar_wait(bar_of(next), parity));
-        if (!ok) break;
+        if (next == ring + kRing * kStageBytes) next = ring;
+        wait_pages(std::integral_constant<int, kRing - 2>());  // page p + 1 is here
         bi_attn::PFrags pf;
         weights_step(st, x, lane, pf);
         VFrags f;
         load_v(f, cur + kBlockBytes, kPage, lane);
         __syncwarp();  // every lane is done with the stage
-        if (lane == p + kRing && lane < np) copy_page(cur);
+        copy_page(p + kRing, cur);
         page_logs(x, next, qb0, qb1, kPage, a.scale_log2, lane);
 #pragma unroll
         for (int gr = 0; gr < 4; ++gr) pv_group(st.acc[2 * gr], st.acc[2 * gr + 1], f, gr, pf);
         cur = next;
-    }
-    if (!ok) {
-        if (lane == 0) {
-            bi::report_error(a.err, bi::kErrTimeout | bi::kWhereAttnSplit);
-            // copies may still write to this CTA's shared memory: one more bounded
-            // wait each (page p + 1, or 0, is the first that was not seen to land)
-            for (int i = 0; i < kRing; ++i) {
-                const int late = p + i;
-                if (late < np) bi::mbar_wait_for(bar_of(ring + (late % kRing) * kStageBytes), (late / kRing) & 1, bi::kDrainNs);
-            }
-            if (nch > 1) bi_attn::arrive_bad(ctr, nch);
-        }
-        return;
     }
     {  // the last page, whose last tokens may not be there
         const int valid = tokens - (np - 1) * kPage;
