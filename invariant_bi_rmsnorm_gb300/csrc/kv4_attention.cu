@@ -109,6 +109,16 @@ __device__ __forceinline__ void four_pairs(uint32_t (&v)[4], uint32_t w, const S
     for (int p = 0; p < 4; ++p) v[p] = bi_kv4::kv4_pair(w, p, sp);
 }
 
+// bi::mma_bf16_16816 onto zeros.
+__device__ __forceinline__ void mma_onto_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // bi_attn::page_scores over a 4-bit K block.
 __device__ __forceinline__ void page_scores_kv4(float (&sc)[4], const uint8_t* kb,
                                                 const uint32_t (&qb0)[8], const uint32_t (&qb1)[8],
@@ -120,14 +130,13 @@ __device__ __forceinline__ void page_scores_kv4(float (&sc)[4], const uint8_t* k
     const uint2 sb = *reinterpret_cast<const uint2*>(sp + 8 * kScaleRowBytes);
     const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sc[i] = 0.f;
-#pragma unroll
     for (int j = 0; j < 4; ++j) {  // the group of dims 32j .. 32j + 31: two 16-deep steps
         const uint32_t da = j < 2 ? sa.x : sa.y, db = j < 2 ? sb.x : sb.y;
         uint32_t va[4], vb[4];
         four_pairs(va, wa[j], bi_kv4::scale_pair(j & 1 ? twice_hi(da) : twice_lo(da)));
         four_pairs(vb, wb[j], bi_kv4::scale_pair(j & 1 ? twice_hi(db) : twice_lo(db)));
-        bi::mma_bf16_16816(sc, va[0], vb[0], va[1], vb[1], qb0[2 * j], qb1[2 * j]);
+        if (j == 0) mma_onto_zero(sc, va[0], vb[0], va[1], vb[1], qb0[0], qb1[0]);
+        else bi::mma_bf16_16816(sc, va[0], vb[0], va[1], vb[1], qb0[2 * j], qb1[2 * j]);
         bi::mma_bf16_16816(sc, va[2], vb[2], va[3], vb[3], qb0[2 * j + 1], qb1[2 * j + 1]);
     }
 }
@@ -475,7 +484,7 @@ struct WarpState {
 // operation by operation, without what changes nothing.  The reference maximum
 // moves on few pages only; one vote finds the others, and there neither the
 // page's maximum is formed nor O rescaled (by 1).
-__device__ __forceinline__ void weights_step(WarpState& st, const float (&x)[4], int lane,
+__device__ __forceinline__ void weights_step(WarpState& st, const float (&x)[4], bool first, int lane,
                                              bi_attn::PFrags& pf) {
     float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
     float al = 1.f;
@@ -496,12 +505,14 @@ __device__ __forceinline__ void weights_step(WarpState& st, const float (&x)[4],
         st.th[1] = __fadd_rn(mn1, bi_attn::kRescaleSlack);
         st.ref[0] = mn0 == -INFINITY ? 0.f : mn0;
         st.ref[1] = mn1 == -INFINITY ? 0.f : mn1;
+        if (!first) {  // O is zero before the first page
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
-            st.acc[mt][0] = __fmul_rn(st.acc[mt][0], al0);
-            st.acc[mt][1] = __fmul_rn(st.acc[mt][1], al1);
-            st.acc[mt][2] = __fmul_rn(st.acc[mt][2], al0);
-            st.acc[mt][3] = __fmul_rn(st.acc[mt][3], al1);
+            for (int mt = 0; mt < 8; ++mt) {
+                st.acc[mt][0] = __fmul_rn(st.acc[mt][0], al0);
+                st.acc[mt][1] = __fmul_rn(st.acc[mt][1], al1);
+                st.acc[mt][2] = __fmul_rn(st.acc[mt][2], al0);
+                st.acc[mt][3] = __fmul_rn(st.acc[mt][3], al1);
+            }
         }
     }
     const float p[4] = {bi_attn::exp2_ftz(__fsub_rn(x[0], st.ref[0])), bi_attn::exp2_ftz(__fsub_rn(x[1], st.ref[1])),
@@ -684,7 +695,7 @@ __global__ void __launch_bounds__(32, 16) attn_warp_kv4_kernel(const Kv4Args ka)
         if (next == ring + kRing * kStageBytes) next = ring;
         wait_pages(std::integral_constant<int, kRing - 2>());  // page p + 1 is here
         bi_attn::PFrags pf;
-        weights_step(st, x, lane, pf);
+        weights_step(st, x, p == 0, lane, pf);
         VFrags f;
         load_v(f, cur + kBlockBytes, kPage, lane);
         __syncwarp();  // every lane is done with the stage
@@ -701,7 +712,7 @@ __global__ void __launch_bounds__(32, 16) attn_warp_kv4_kernel(const Kv4Args ka)
             if ((lane >> 2) + 8 >= valid) x[2] = x[3] = -INFINITY;
         }
         bi_attn::PFrags pf;
-        weights_step(st, x, lane, pf);
+        weights_step(st, x, np == 1, lane, pf);
         VFrags f;
         load_v(f, cur + kBlockBytes, valid, lane);
 #pragma unroll
@@ -766,12 +777,12 @@ __global__ void __launch_bounds__(32, 16) attn_warp_kv4_kernel(const Kv4Args ka)
 // Chunks per SM (at the launch's bound on the lengths; lengths spread up to the
 // bound fill about half of them) from which on the warp kernel is taken.
 // Measured on GB300 with 8 kv-heads, chunk kernel against warp kernel: 14 per
-// SM (B = 8 up to 8192 tokens) 20 against 35 us, 27 (B = 16) 32 against 40, 40
-// (B = 24) 47 against 51, 54 (B = 32) 59 against 60, 81 (B = 48) 85 against 80,
-// 108 (B = 64) 112 against 101.  The chunk kernel's four warps finish a chunk
-// several times sooner; the warp kernel issues a quarter fewer instructions and
+// SM (B = 8 up to 8192 tokens) 20 against 31 us, 27 (B = 16) 32 against 37, 40
+// (B = 24) 46 against 47, 54 (B = 32) 59 against 55, 81 (B = 48) 85 against 74,
+// 108 (B = 64) 112 against 94.  The chunk kernel's four warps finish a chunk
+// several times sooner; the warp kernel issues a third fewer instructions and
 // has no barriers.
-constexpr int64_t kManyChunks = 60;
+constexpr int64_t kManyChunks = 42;
 
 // set once per device; any thread may race to set it, the attribute is idempotent
 std::atomic<bool> g_attr_set[64] = {};

@@ -227,7 +227,7 @@ BOTH_KERNELS = pytest.mark.parametrize("many", [False, True], ids=["few-chunks",
 def _bound(many, bt, msl, Hkv):
     """(block table, max_seq_len) of a launch of few or of many chunks."""
     if many:
-        msl = 256 * -(-60 * 160 // (bt.shape[0] * Hkv))
+        msl = 256 * -(-42 * 160 // (bt.shape[0] * Hkv))
     wide = torch.full((bt.shape[0], max(bt.shape[1], -(-msl // 16))), -1, dtype=torch.int32, device="cuda")
     wide[:, :bt.shape[1]] = bt
     return wide, msl
