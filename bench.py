@@ -71,7 +71,9 @@ def parse_args():
     ap.add_argument("--case", choices=["gemm_gate_up", "gemm_qkv", "gemm_layers", "attention",
                                        "rmsnorm", "decoder", "prefill", "add_rmsnorm",
                                        "logprobs", "qk_norm_rope_append", "silu_mul",
-                                       "gemm_swiglu", "decode_latency"],
+                                       "gemm_swiglu", "decode_latency", "attention_kv4",
+                                       "kv4_append", "kv4_read", "qk_norm_rope_append_kv4",
+                                       "logprobs_top"],
                     help="time one kernel of the path alone (for profiling); prints its own line")
     ap.add_argument("--requests", type=int, default=1000, help="C5 decoder (--case decoder and the default line): requests")
     ap.add_argument("--layers", type=int, default=36, help="--case decoder: decoder layers")
@@ -81,7 +83,7 @@ def parse_args():
     ap.add_argument("--track", type=int, default=16,
                     help="--case decoder: requests re-run alone for the bitwise check")
     ap.add_argument("--batch", type=int, default=ATT_B,
-                    help="sequences for --case attention (a smaller case for ncu captures)")
+                    help="sequences for --case attention and attention_kv4 (a smaller case for ncu captures)")
     return ap.parse_args()
 
 
@@ -98,7 +100,9 @@ KERNEL_SOURCES = {"bi_gemm": "gemm.cu", "bi_decode_attention": "decode_attention
                   "bi_rmsnorm": "rmsnorm.cu", "bi_add_rmsnorm": "rmsnorm.cu",
                   "bi_prefill_attention": "prefill_attention.cu", "bi_logprobs": "logprobs.cu",
                   "bi_qk_norm_rope_append": "decoder_ops.cu", "bi_silu_mul": "decoder_ops.cu",
-                  "bi_gemm_swiglu": "gemm.cu"}
+                  "bi_gemm_swiglu": "gemm.cu", "bi_decode_attention_kv4": "kv4_attention.cu",
+                  "bi_kv4_append": "kv4_cache.cu", "bi_kv4_read": "kv4_cache.cu",
+                  "bi_qk_norm_rope_append_kv4": "decoder_ops.cu", "bi_logprobs_top": "logprobs_top.cu"}
 
 
 def kernel_source_sha(src: str) -> str:
@@ -939,6 +943,57 @@ def build_next_case(name: str, dev, bi, inputs):
     raise ValueError(name)
 
 
+KV4_CASES = ("attention_kv4", "kv4_append", "kv4_read", "qk_norm_rope_append_kv4", "logprobs_top")
+
+
+def build_kv4_case(name: str, batch: int, dev, bi, inputs):
+    """Input of one kernel of the 4-bit cache, or of the per-token report, as
+    (fn, algorithmic bytes of one launch) for `--case`."""
+    if name == "logprobs_top":
+        logits = inputs.normal_bf16((LOGPROB_ROWS, VOCAB), 620, std=2.0, device=dev)
+        tgt = torch.arange(LOGPROB_ROWS, dtype=torch.int32, device=dev)
+        return (lambda: bi.logprobs_top(logits, tgt, 20)), float(LOGPROB_ROWS * (2 * VOCAB + 16 + 160))
+    if name == "attention_kv4":
+        p = inputs.decode_problem(batch, max_len=MAX_LEN, seed=270, device=dev)
+        a = {k: v.to(dev) for k, v in p.items()}
+        P = a["k_cache"].shape[0]
+        kc, vc = bi.kv4_cache(P, HKV, dev)
+        rows = [a.pop(k).transpose(1, 2).reshape(P * 16, HKV, HD) for k in ("k_cache", "v_cache")]
+        bi.kv4_append(*rows, torch.arange(P * 16, dtype=torch.int32, device=dev), kc, vc)
+        out = torch.empty(batch, HQ, HD, dtype=torch.bfloat16, device=dev)
+        ws = torch.zeros(bi.decode_attention_workspace_size(batch, HQ, HD, MAX_LEN),
+                         dtype=torch.uint8, device=dev)
+        lens = p["seq_lens"].to(torch.int64)
+        work = float((lens * HKV * 144).sum() + batch * HQ * HD * 4 + 4 * ((lens + 15) // 16).sum())
+        return (lambda: bi.decode_attention_kv4(a["q"], kc, vc, a["block_table"], a["seq_lens"],
+                                                MAX_LEN, out=out, workspace=ws)), work
+    T = OPS_TOKENS
+    kc, vc = bi.kv4_cache(T // 16, HKV, dev)
+    qkv = inputs.normal_bf16((T, (HQ + 2 * HKV) * HD), 630, device=dev)
+    g = torch.Generator().manual_seed(631)
+    pos = torch.randint(0, 8192, (T,), generator=g, dtype=torch.int64).to(torch.int32).to(dev)
+    slots = torch.randperm(T, generator=g).to(torch.int32).to(dev)
+    heads = qkv.view(T, HQ + 2 * HKV, HD)
+    k, v = heads[:, HQ:HQ + HKV], heads[:, HQ + HKV:]
+    row16, row4 = HKV * HD * 4, HKV * 144
+    if name == "kv4_append":
+        return (lambda: bi.kv4_append(k, v, slots, kc, vc)), float(T * (row16 + row4 + 4))
+    if name == "kv4_read":
+        bi.kv4_append(k, v, slots, kc, vc)
+        ko = torch.empty(T // 16, HKV, 16, HD, dtype=torch.bfloat16, device=dev)
+        vo = torch.empty_like(ko)
+        table = torch.arange(T // 16, dtype=torch.int32, device=dev).view(16, -1)  # 16 sequences
+        lens = torch.full((16,), T // 16, dtype=torch.int32, device=dev)
+        return (lambda: bi.kv4_read(kc, vc, table, lens, T // 16, ko, vo)), float(T * (row16 + row4))
+    from invariant_bi_rmsnorm_gb300.qwen3 import rope_table
+    rope = rope_table(8192, 1e6, HD, device=dev)
+    ones = torch.ones(HD, dtype=torch.bfloat16, device=dev)
+    qo = torch.empty(T, HQ, HD, dtype=torch.bfloat16, device=dev)
+    per_tok = (HQ + 2 * HKV) * HD * 2 + HQ * HD * 2 + row4 + HD * 4 + 8
+    return (lambda: bi.qk_norm_rope_append_kv4(qkv, HQ, HKV, pos, slots, rope, ones, ones, kc, vc, EPS,
+                                               q_out=qo)), float(T * per_tok)
+
+
 NEXT_CASES = ("prefill", "add_rmsnorm", "logprobs", "qk_norm_rope_append", "silu_mul",
               "gemm_swiglu")
 
@@ -982,6 +1037,8 @@ def run_case(args):
         work, unit = sum(2.0 * GEMM_M * N * K for _, N, K in LAYERS), "TFLOP/s"
     elif args.case in NEXT_CASES:
         fn, work, unit, _ = build_next_case(args.case, dev, bi, inputs)
+    elif args.case in KV4_CASES:
+        (fn, work), unit = build_kv4_case(args.case, args.batch, dev, bi, inputs), "GB/s"
     elif args.case.startswith("gemm"):
         n, N, K = {"gemm_gate_up": LAYERS[2], "gemm_qkv": LAYERS[0]}[args.case]
         x = inputs.gemm_rows(GEMM_M, K, seed=50 + K, device=dev)

@@ -8,11 +8,23 @@
 // value n * s is a bf16 number, so a page's operands are exactly those that a
 // read-back bf16 cache would give, and so are the result's bits.
 //
-// One CTA (4 warps) per (sequence, kv-head, chunk).  The bytes of a chunk are
-// a quarter of a bf16 chunk's but its arithmetic is the same and the codes
-// have to be turned into numbers besides, so what bounds the kernel is the
-// instructions it issues; the work of a chunk is dealt out so that none is
-// done twice and every warp has a few pages' independent work at hand:
+// A lane takes its fragments of K and V from a block with 16-byte loads, in
+// the order of mma.sync's A operand (ldmatrix has no 4-bit form), and turns
+// them into bf16 pairs in registers: a shift, an and-or and one fma for two
+// values.
+//
+// The bytes of a chunk are little over a quarter of a bf16 chunk's but its
+// arithmetic is the same, and the codes have to be turned into numbers besides:
+// about 340 instructions a page and kv-head, 24 of them mma.sync, each of which
+// keeps a scheduler busy for 8 cycles (measured: 2.04 cycles per SM).  That is
+// about 130 cycles an SM where HBM would deliver the page in 98, so what bounds
+// both kernels below is the instructions they issue.  On GB300, cold, GQA 32/8,
+// lengths even over 1 .. 8192: B = 256 308 us (1.21 GB, 3.9 TB/s, 0.58 of the
+// copy rate; the bf16 cache's 4.3 GB take 599 us), B = 64 93 us.
+//
+// Few chunks: one CTA (4 warps) per (sequence, kv-head, chunk), which finishes
+// a chunk soonest (one sequence of 8192 tokens 11.4 us, of 300 7.5 us).  The
+// chunk's work is dealt out so that none is done twice:
 //   0  warp 0 copies the chunk's up to 16 pages into shared memory, two bulk
 //      copies (K, V) a lane;
 //   1  scores: warp w takes pages w, w + 4, ..., and their maxima;
@@ -21,10 +33,9 @@
 //   3  weights: warp w, its own pages; the split weights go to shared memory in
 //      the order of mma.sync's B operand, over the K blocks, which are done with;
 //   4  output: warp w takes dims 32w .. 32w + 31 (one group) over all pages.
-// A lane takes its fragments of K and V from a block with 16-byte loads, in
-// the order of mma.sync's A operand (ldmatrix has no 4-bit form), and turns
-// them into bf16 pairs in registers: a shift, an and-or and one fma for two
-// values.
+// Five CTAs share an SM (41 KB each); four were 12 % slower, seven (V copied
+// over K once the scores are there) 3 % faster in the middle and 28 % slower
+// for one sequence.  Many chunks: one warp per chunk, see below.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -465,7 +476,11 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
 // chunk), so that nothing ever waits for another warp and a finished chunk's
 // place on the SM is taken at once.  Pages come through a ring of kRing
 // stages; while a page's weights and output products are under way the next
-// page's scores are formed (they depend on nothing before them).
+// page's scores are formed (they depend on nothing before them).  366
+// instructions a page in all, the chunk's share included; 16 warps per SM (20
+// with fewer registers were no faster).  B = 256 up to 8192 tokens went from 341
+// to 312 us with per-lane copies in the place of bulk copies (see below) and
+// from 524 us with the four-warp CTA of the bf16 kernel.
 
 constexpr int kRing = 4;  // pages in flight
 constexpr int kStageBytes = 2 * kBlockBytes;
@@ -606,7 +621,7 @@ __device__ __forceinline__ void fold_warp(const SplitArgs& a, int64_t row0, int 
     }
 }
 
-__global__ void __launch_bounds__(32, 16) attn_warp_kv4_kernel(const Kv4Args ka) {
+__global__ void __launch_bounds__(32, 14) attn_warp_kv4_kernel(const Kv4Args ka) {
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
     const SplitArgs& a = ka.s;

@@ -36,7 +36,9 @@ __device__ __forceinline__ bi_kv4::RowPart load_row(const __nv_bfloat16* p, int 
 }
 
 // A half-warp takes kRows (token, kv-head) pairs, the K row and the V row of
-// each, all loads before any arithmetic.
+// each, all loads before any arithmetic.  8192 tokens of 8 heads (33.6 MB read,
+// 9.4 MB written) take 11.9 us cold, 3.6 TB/s: about 140 instructions for a
+// warp's two rows are what bounds it (1 pair 12.4 us, 4 pairs 12.3).
 constexpr int kRows = 2;
 
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {
@@ -84,7 +86,10 @@ struct ReadArgs {
 };
 
 // One CTA per (sequence, page, kHeads kv-heads): thread (r, c) writes dims 8c ..
-// 8c + 7 of token r of every head, all loads before any store.
+// 8c + 7 of token r of every head, all loads before any store.  Bound by HBM
+// and the latency of a CTA's three dependent loads (length, page, codes): 8192
+// tokens of 8 heads (9.4 MB read, 33.6 MB written) take 10.5 us cold, 4.1 TB/s
+// (16.3 us with a loop over the heads, 10.7 with one head or four a CTA).
 constexpr int kHeads = 2;
 
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {

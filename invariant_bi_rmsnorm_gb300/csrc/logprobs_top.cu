@@ -25,6 +25,12 @@
 // (thousands of equal logits, as in a masked vocabulary) find the k-th largest
 // value itself by bisection over the 16-bit values, then the lowest ids among
 // its equals by a scan in id order.
+//
+// What bounds it is the instructions of the pass: about 9.6 a logit, of which
+// the exponential, its sum in bi_logprobs' order and T take 5, and moving the
+// maximum (in most vectors of a row's first half some lane's does) 2.  1024
+// rows of 151936 logits, k = 20: 70 us, 4.4 TB/s, 0.65 of the copy rate
+// (bi_logprobs, without entropy and alternatives, 53 us); one row 19 us.
 #include <cuda_bf16.h>
 
 #include <cmath>
