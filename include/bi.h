@@ -392,12 +392,13 @@ bi_status bi_logprobs(const void* logits, int64_t rows, int32_t vocab, int64_t l
  * has 4096.  A group of 32 consecutive dims of one token and kv-head is held
  * as codes n + 8 and one scale s:
  *     s = max|x| / 7 rounded to 4 significant bits, nearest even (kept as bf16)
- *     n = x / s rounded to nearest even, -7 .. 7
+ *     n = x / s rounded to nearest even (-7 .. 7)
  * and stands for n * s, which is a bf16 number, at most s / 2 away from x.  A
  * group that holds a NaN, an infinity or a magnitude of 2^123 or more stands
- * for NaN throughout, one with every magnitude below 2^-120 for zeros.  A block holds the codes of its 16 tokens (64 bytes
- * each), then bf16 scales [16 tokens][4 groups].  Codes lie in little-endian
- * 32-bit words of 8, code i in bits 4i .. 4i + 3:
+ * for NaN throughout, one with every magnitude below 2^-120 for zeros.  A block
+ * holds the codes of its 16 tokens (64 bytes each), then bf16 scales
+ * [16 tokens][4 groups].  Codes lie in little-endian 32-bit words of 8, code i
+ * in bits 4i .. 4i + 3:
  *     K: dim 32j + 8p + 2t + e (j, p, t < 4; e < 2) of token r is code p + 4e
  *        of word 16r + 4t + j;
  *     V: dim 64w + 32h + 8p + g (w, h < 2; p < 4; g < 8) of token 8a + 2b + c

@@ -3,9 +3,9 @@
 //
 // A group is 32 consecutive dims of one token and kv-head (4 groups per row):
 //     s = RN4(max|x| / 7)                  4 significant bits, nearest even
-//     n = rne(x / s) clamped to -7 .. 7,   code = n + 8;   x^ = n * s
-// RN4 moves s by at most a factor 1 +- 1/17, so max|x| / s < 7.5: no value is
-// off by more than s / 2.  n has 3 significant bits and s 4, so n * s is a
+//     n = rne(x / s),   code = n + 8;      x^ = n * s
+// RN4 moves s by at most a factor 1 +- 1/17, so max|x| / s < 7.5: n is within
+// -7 .. 7 and no value is off by more than s / 2.  n has 3 significant bits and s 4, so n * s is a
 // bf16 number: reading back rounds nothing, and attention over the codes can
 // use the very operands that attention over a read-back bf16 cache would.  A
 // scale with all 8 bits of a bf16 would cost a rounding per element (and the
@@ -43,9 +43,8 @@ constexpr int kScaleRowBytes = 8;                // scales of one token
 static_assert(kBlockBytes == BI_PAGE_SIZE * (kRowBytes + kScaleRowBytes), "block size");
 
 // ---------------------------------------------------------------- reading ----
-// A group's scale twice over, and -136 s twice over (17 * 8 * s: 8 significant
-// bits, exact), from the scale's bf16 bits in the low half (kHigh: the high
-// half) of `two`.
+// The scales of two elements, and -136 s of both (17 * 8 * s: 8 significant
+// bits, exact).
 struct ScalePair {
     uint32_t s, off;
 };
@@ -64,7 +63,6 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
 
 constexpr uint32_t kMinus136x2 = 0xC308C308u;  // -136 as bf16, twice
 
-// scales of two elements (low, high half) -> the pair kv4_pair takes
 __device__ __forceinline__ ScalePair scale_pair(uint32_t s2) {
     return {s2, mul_bf16x2(s2, kMinus136x2)};
 }
@@ -110,7 +108,8 @@ __device__ __forceinline__ float group_scale(uint32_t amax_bits) {
 // within 2^-20 of x / s, which (8 bits over 4) is a tie k + 1/2 exactly or at
 // least 2^-9 away from one: rounded to multiples of 2^-11 (the fma adds 6144)
 // it lies on every tie and on the right side of the others.  The addition
-// rounds that to nearest even.  |x| / s < 7.5 keeps n within -7 .. 7.
+// rounds that to nearest even.  inv = 0 for s = 0 (n = 0); for s = NaN the byte is
+// 0xFF, which spoils codes of the same group only, and any code reads as NaN.
 __device__ __forceinline__ uint32_t code_of(float x, float inv) {
     return __float_as_uint(__fadd_rn(__fmaf_rn(x, inv, 6144.f), 12582912.f + 8.f - 6144.f));
 }

@@ -272,7 +272,10 @@ __global__ void __launch_bounds__(kThreads, 5) logprobs_top_kernel(const TopArgs
         const float lse = __fadd_rn(c.m, ls);
         lse_s = lse;
         if (a.lse_out) a.lse_out[row] = lse;
-        if (a.entropy_out) a.entropy_out[row] = __fsub_rn(ls, __fmul_rn(kLn2, __fdiv_rn(c.t, c.s)));
+        if (a.entropy_out) {
+            const float h = __fsub_rn(ls, __fmul_rn(kLn2, __fdiv_rn(c.t, c.s)));
+            a.entropy_out[row] = h < 0.f ? 0.f : h;  // the last bit of ln S may differ; NaN stays
+        }
         if (a.targets && a.logprob_out) {
             const int t = a.targets[row];
             if (t < 0 || t >= a.vocab) {

@@ -143,6 +143,19 @@ def test_rows_alone_batched_and_strided():
     assert few[0] is None and torch.equal(few[3], a[3][:, :3]) and torch.equal(few[4], a[4][:, :3])
 
 
+def test_many_rows_and_a_wide_vocabulary():
+    """More than 2^31 logits, whose last rows lie past 32-bit offsets; a
+    vocabulary with more than one round of vectors in every segment."""
+    rows = 2 ** 31 // V + 40
+    x = torch.empty(rows, V, dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(1145))
+    a = bi.logprobs_top(x, None, 4)
+    for r in (0, rows // 2, rows - 1):
+        assert all(torch.equal(p[r:r + 1], q) for p, q in zip(a[1:], bi.logprobs_top(x[r:r + 1].clone(), None, 4)[1:]))
+    del x
+    _check(inputs.normal_bf16((2, 1_310_728), seed=1146, std=2.0), 32)
+
+
 def test_a_captured_call_and_other_streams():
     x = inputs.normal_bf16((6, 8000), seed=1150).cuda()
     t = torch.arange(6, dtype=torch.int32, device="cuda")
