@@ -472,9 +472,8 @@ bi_status bi_kv4_read(const void* k_cache, const void* v_cache, const int32_t* b
  * without making it.  Operation, arguments, workspace
  * (bi_decode_attention_workspace_size bytes, counters zero at first use),
  * checks and errors as bi_decode_attention; k_cache and v_cache are 4-bit
- * caches, Hkv <= 65535, and with max_seq_len > 256 also B * Hkv <=
- * BI_DECODE_COUNTER_BYTES / 4 and max_seq_len <= 65535 * 256 (else
- * UNSUPPORTED_SHAPE).  One kernel launch.
+ * caches, Hkv <= 65535.  One kernel launch, or two (a second one folds the
+ * chunks of many long sequences).
  */
 bi_status bi_decode_attention_kv4(const void* q, const void* k_cache, const void* v_cache,
                                   const int32_t* block_table, int32_t max_pages_per_seq,

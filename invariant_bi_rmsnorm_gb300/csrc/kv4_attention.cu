@@ -19,8 +19,8 @@
 // keeps a scheduler busy for 8 cycles (measured: 2.04 cycles per SM).  That is
 // about 130 cycles an SM where HBM would deliver the page in 98, so what bounds
 // both kernels below is the instructions they issue.  On GB300, cold, GQA 32/8,
-// lengths even over 1 .. 8192: B = 256 308 us (1.21 GB, 3.9 TB/s, 0.58 of the
-// copy rate; the bf16 cache's 4.3 GB take 599 us), B = 64 93 us.
+// lengths even over 1 .. 8192: B = 256 289 us (1.21 GB, 4.2 TB/s, 0.62 of the
+// copy rate; the bf16 cache's 4.3 GB take 599 us), B = 64 83 us.
 //
 // Few chunks: one CTA (4 warps) per (sequence, kv-head, chunk), which finishes
 // a chunk soonest (one sequence of 8192 tokens 11.4 us, of 300 7.5 us).  The
@@ -54,7 +54,6 @@ using bi_attn::ceil_div;
 using bi_attn::kChunk;
 using bi_attn::kD;
 using bi_attn::kFoldFloats;
-using bi_attn::kMaxCounters;
 using bi_attn::kMaxGroup;
 using bi_attn::kPage;
 using bi_attn::kPagesPerChunk;
@@ -549,76 +548,89 @@ __device__ __forceinline__ float2* partial_ml(const SplitArgs& a, int64_t row, i
     return reinterpret_cast<float2*>(a.ws_ml) + row * a.max_chunks + c;
 }
 
-// The fold of one (sequence, kv-head) by the warp that arrived last, in
+// (m, l) of a chunk with a page index out of range: no weight sum is negative.
+constexpr float kNoChunk = -1.f;
+
+// The fold of the warp kernel's partials, a warp per (sequence, query head), in
 // ascending chunk order with bi_attn::attn_merge_kernel's operations.  Lane l
-// has positions 4l .. 4l + 3 of every row.  As in bi_attn::fold_sequence the
+// has positions 4l .. 4l + 3 of the row.  As in bi_attn::fold_sequence the
 // running maxima are a prefix maximum, taken for 32 chunks at once (lane =
-// chunk), and all factors with them; the partials of kAhead chunks are loaded
-// before the first of them is folded.
-template <int G>
-__device__ __forceinline__ void fold_warp(const SplitArgs& a, int64_t row0, int nch, float4* factors,
-                                          int lane) {
-    constexpr int kAhead = G <= 3 ? 8 : 24 / G;
-    float4 o[G];
-    float l[G], m[G];
+// chunk), and all factors with them; the partials of kAhead chunks are on their
+// way together.
+//
+// A launch of its own, because the rows are folded side by side here: the warp
+// that arrives last at its (sequence, kv-head) could fold its rows as well, but does
+// it alone while the SMs run dry (32 sequences of 8192 tokens 81 against 72 us,
+// B = 64 up to 8192 92.6 against 83.1, B = 256 308 against 289).  Sixteen
+// partials on their way instead of eight: 78, 89, 296 us.
+constexpr int kMergeWarps = 4;
+
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    merge_rows_kv4_kernel(const SplitArgs a, int64_t rows) {
+    bi::launch_dependents();
+    bi::grid_dependency_wait();  // the partials are there
+    constexpr int kAhead = 8;
+    __shared__ float4 all_factors[kMergeWarps][32];
+    float4* const factors = all_factors[threadIdx.x / 32];
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + threadIdx.x / 32;
+    if (row >= rows) return;
+    const int L = a.seq_lens[row / a.Hq];
+    if (L <= kChunk || L > a.max_seq_len) return;  // written, or reported, by the warp kernel
+    const int nch = (L + kChunk - 1) / kChunk;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f, m = 0.f;
     for (int cb = 0; cb < nch; cb += 32) {
         const int nb = min(32, nch - cb);
-        __syncwarp();
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-            const float2 ml = lane < nb ? __ldcg(partial_ml(a, row0 + h, cb + lane)) : make_float2(-INFINITY, 0.f);
-            float v = ml.x;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const float u = __shfl_up_sync(kAll, v, off);
-                if (lane >= off) v = fmaxf(v, u);
-            }
-            if (cb > 0) v = fmaxf(m[h], v);  // running maximum after chunk cb + lane
-            float before = __shfl_up_sync(kAll, v, 1);
-            if (lane == 0) before = cb > 0 ? m[h] : 0.f;
-            m[h] = __shfl_sync(kAll, v, 31);
-            if (lane < nb)
-                factors[lane * G + h] = make_float4(bi_attn::exp2_ftz(before - v),
-                                                    bi_attn::exp2_ftz(ml.x - v), ml.y, 0.f);
-        }
-        __syncwarp();
-        for (int i0 = 0; i0 < nb; i0 += kAhead) {
-            float4 part[kAhead][G];
+        float4 part[kAhead];
+        auto load = [&](int i0) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
+                if (i0 + u < nb)
+                    part[u] = __ldcg(reinterpret_cast<const float4*>(partial_o(a, row, cb + i0 + u)) + lane);
+        };
+        const float2 ml = lane < nb ? __ldcg(partial_ml(a, row, cb + lane)) : make_float2(-INFINITY, 0.f);
+        load(0);
+        if (__any_sync(kAll, ml.y == kNoChunk)) return;  // the output stays as it was
+        float v = ml.x;
 #pragma unroll
-                for (int h = 0; h < G; ++h)
-                    if (i0 + u < nb)
-                        part[u][h] = __ldcg(reinterpret_cast<const float4*>(partial_o(a, row0 + h, cb + i0 + u)) + lane);
+        for (int off = 1; off < 32; off <<= 1) {
+            const float u = __shfl_up_sync(kAll, v, off);
+            if (lane >= off) v = fmaxf(v, u);
+        }
+        if (cb > 0) v = fmaxf(m, v);  // running maximum after chunk cb + lane
+        float before = __shfl_up_sync(kAll, v, 1);
+        if (lane == 0) before = cb > 0 ? m : 0.f;
+        m = __shfl_sync(kAll, v, 31);
+        __syncwarp();  // every lane is done with the last factors
+        if (lane < nb)
+            factors[lane] = make_float4(bi_attn::exp2_ftz(before - v), bi_attn::exp2_ftz(ml.x - v), ml.y, 0.f);
+        __syncwarp();
+        for (int i0 = 0; i0 < nb; i0 += kAhead) {
+            if (i0 > 0) load(i0);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (i0 + u >= nb) break;
-#pragma unroll
-                for (int h = 0; h < G; ++h) {
-                    const float4 f = factors[(i0 + u) * G + h];
-                    if (cb + i0 + u == 0) {
-                        o[h] = part[u][h];
-                        l[h] = f.z;
-                    } else {
-                        o[h].x = bi_attn::fold_value(o[h].x, f.x, part[u][h].x, f.y);
-                        o[h].y = bi_attn::fold_value(o[h].y, f.x, part[u][h].y, f.y);
-                        o[h].z = bi_attn::fold_value(o[h].z, f.x, part[u][h].z, f.y);
-                        o[h].w = bi_attn::fold_value(o[h].w, f.x, part[u][h].w, f.y);
-                        l[h] = bi_attn::fold_value(l[h], f.x, f.z, f.y);
-                    }
+                const float4 f = factors[i0 + u];
+                if (cb + i0 + u == 0) {
+                    o = part[u];
+                    l = f.z;
+                } else {
+                    o.x = bi_attn::fold_value(o.x, f.x, part[u].x, f.y);
+                    o.y = bi_attn::fold_value(o.y, f.x, part[u].y, f.y);
+                    o.z = bi_attn::fold_value(o.z, f.x, part[u].z, f.y);
+                    o.w = bi_attn::fold_value(o.w, f.x, part[u].w, f.y);
+                    l = bi_attn::fold_value(l, f.x, f.z, f.y);
                 }
             }
         }
     }
     // positions 4l .. 4l + 3: dims d, d + 8, d + 1, d + 9
     const int d = 16 * (lane >> 2) + 2 * (lane & 3);
-#pragma unroll
-    for (int h = 0; h < G; ++h) {
-        const float il = bi_attn::inv_weight(l[h]);
-        uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (row0 + h) * kD + d);
-        out[0] = bi::pack_bf16x2(bi_attn::normalise(o[h].x, il), bi_attn::normalise(o[h].z, il));
-        out[4] = bi::pack_bf16x2(bi_attn::normalise(o[h].y, il), bi_attn::normalise(o[h].w, il));
-    }
+    const float il = bi_attn::inv_weight(l);
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * kD + d);
+    out[0] = bi::pack_bf16x2(bi_attn::normalise(o.x, il), bi_attn::normalise(o.z, il));
+    out[4] = bi::pack_bf16x2(bi_attn::normalise(o.y, il), bi_attn::normalise(o.w, il));
 }
 
 __global__ void __launch_bounds__(32, 14) attn_warp_kv4_kernel(const Kv4Args ka) {
@@ -639,8 +651,7 @@ __global__ void __launch_bounds__(32, 14) attn_warp_kv4_kernel(const Kv4Args ka)
     if (c >= nch) return;
     const int tokens = min(kChunk, L - c * kChunk);
     const int np = (tokens + kPage - 1) / kPage;
-    // several CTAs share a longer sequence and the last one to arrive folds it
-    uint32_t* const ctr = nch > 1 ? a.counters + static_cast<int64_t>(s) * a.Hkv + g : nullptr;
+    const int64_t row0 = static_cast<int64_t>(s) * a.Hq + g * a.group;
 
     __shared__ __align__(16) uint8_t ring[kRing * kStageBytes];
 
@@ -651,10 +662,9 @@ __global__ void __launch_bounds__(32, 14) attn_warp_kv4_kernel(const Kv4Args ka)
         if (lane < np)
             pg = a.block_table[static_cast<int64_t>(s) * a.max_pages_per_seq + c * kPagesPerChunk + lane];
         if (__any_sync(kAll, pg < 0 || pg >= a.num_pages)) {
-            if (lane == 0) {
-                bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
-                if (nch > 1) bi_attn::arrive_bad(ctr, nch);
-            }
+            if (lane == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
+            if (nch > 1 && lane < a.group)
+                *partial_ml(a, row0 + lane, c) = make_float2(-INFINITY, kNoChunk);
             return;
         }
         block = pg * a.Hkv + g;
@@ -689,7 +699,6 @@ __global__ void __launch_bounds__(32, 14) attn_warp_kv4_kernel(const Kv4Args ka)
     for (int p = 0; p < kRing; ++p) copy_page(p, ring + p * kStageBytes);
 
     // column n of the mma tile = query head g*group + n (n < group)
-    const int64_t row0 = static_cast<int64_t>(s) * a.Hq + g * a.group;
     uint32_t qb0[8], qb1[8];
     bi_attn::load_q_frags((lane >> 2) < a.group ? a.q + (row0 + (lane >> 2)) * kD : nullptr, lane, qb0, qb1);
 
@@ -762,42 +771,19 @@ __global__ void __launch_bounds__(32, 14) attn_warp_kv4_kernel(const Kv4Args ka)
             *partial_ml(a, row0 + h0 + e, c) =
                 make_float2(st.th[e] == -INFINITY ? -INFINITY : st.ref[e], l[e]);
     }
-    __syncwarp();
-    uint32_t now = 0;
-    if (lane == 0) {
-        // release: this warp's partial is visible before its arrival counts;
-        // acquire: the last arrival sees every other warp's partial
-        now = bi::atomic_add_acq_rel_gpu(ctr, bi_attn::kArrive) + bi_attn::kArrive;
-        if ((now & 0xffffu) == static_cast<uint32_t>(nch)) {
-            atomicExch(ctr, 0u);  // ready for the next call
-            if (now >> 16) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
-        }
-    }
-    now = __shfl_sync(kAll, now, 0);
-    if ((now & 0xffffu) != static_cast<uint32_t>(nch) || now >> 16) return;
-    float4* factors = reinterpret_cast<float4*>(ring);
-    static_assert(32 * kMaxGroup * 16 <= kRing * kStageBytes, "the factors fit in the ring");
-    switch (a.group) {
-        case 1: fold_warp<1>(a, row0, nch, factors, lane); break;
-        case 2: fold_warp<2>(a, row0, nch, factors, lane); break;
-        case 3: fold_warp<3>(a, row0, nch, factors, lane); break;
-        case 4: fold_warp<4>(a, row0, nch, factors, lane); break;
-        case 5: fold_warp<5>(a, row0, nch, factors, lane); break;
-        case 6: fold_warp<6>(a, row0, nch, factors, lane); break;
-        case 7: fold_warp<7>(a, row0, nch, factors, lane); break;
-        default: fold_warp<8>(a, row0, nch, factors, lane); break;
-    }
 }
 
 // Chunks per SM (at the launch's bound on the lengths; lengths spread up to the
 // bound fill about half of them) from which on the warp kernel is taken.
-// Measured on GB300 with 8 kv-heads, chunk kernel against warp kernel: 14 per
-// SM (B = 8 up to 8192 tokens) 20 against 31 us, 27 (B = 16) 32 against 37, 40
-// (B = 24) 46 against 47, 54 (B = 32) 59 against 55, 81 (B = 48) 85 against 74,
-// 108 (B = 64) 112 against 94.  The chunk kernel's four warps finish a chunk
-// several times sooner; the warp kernel issues a third fewer instructions and
-// has no barriers.
-constexpr int64_t kManyChunks = 42;
+// Measured on GB300 with 8 kv-heads, chunk kernel against warp kernel with its
+// fold: 7 per SM (B = 4 up to 8192 tokens) 14.0 against 20.2 us, 14 (B = 8) 19.6
+// against 23.5, (B = 128 up to 512) 20.5 against 22.1, 27 (B = 16 up to 8192)
+// 32.3 against 30.4, (B = 256 up to 512) 35.9 against 32.4, 40 (B = 24) 46.5
+// against 40.9, 108 (B = 64) 112 against 83.  The chunk kernel's four warps
+// finish a chunk several times sooner; the warp kernel issues a third fewer
+// instructions and has no barriers.  Below the rule there are far fewer chunks
+// than arrival counters, and than an arrival counter can count.
+constexpr int64_t kManyChunks = 22;
 
 // set once per device; any thread may race to set it, the attribute is idempotent
 std::atomic<bool> g_attr_set[64] = {};
@@ -829,9 +815,6 @@ extern "C" bi_status bi_decode_attention_kv4(const void* q, const void* k_cache,
         (reinterpret_cast<uintptr_t>(seq_lens) & 3))
         return BI_ERR_MISALIGNED;
     const int max_chunks = ceil_div(max_seq_len, kChunk);
-    // one arrival counter per (sequence, kv-head), of 16 bits
-    if (max_chunks > 1 && (static_cast<int64_t>(B) * Hkv > kMaxCounters || max_chunks > 65535))
-        return BI_ERR_UNSUPPORTED_SHAPE;
     const size_t need = bi_decode_attention_workspace_size(B, Hq, D, max_seq_len);
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return BI_ERR_WORKSPACE_TOO_SMALL;
@@ -872,9 +855,17 @@ extern "C" bi_status bi_decode_attention_kv4(const void* q, const void* k_cache,
     args.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     args.chunks_per_cta = 1;
     const dim3 grid(max_chunks, Hkv, B);
-    const cudaError_t e =
-        static_cast<int64_t>(max_chunks) * Hkv * B >= kManyChunks * static_cast<int64_t>(bi::sm_count())
-            ? bi::launch_pdl(attn_warp_kv4_kernel, grid, dim3(32), 0, stream, ka)
-            : bi::launch_pdl(attn_chunk_kv4_kernel, grid, dim3(kThreads), kSmemBytes, stream, ka);
-    return e == cudaSuccess ? BI_OK : BI_ERR_CUDA;
+    if (static_cast<int64_t>(max_chunks) * Hkv * B < kManyChunks * static_cast<int64_t>(bi::sm_count()))
+        return bi::launch_pdl(attn_chunk_kv4_kernel, grid, dim3(kThreads), kSmemBytes, stream, ka) ==
+                       cudaSuccess
+                   ? BI_OK
+                   : BI_ERR_CUDA;
+    if (bi::launch_pdl(attn_warp_kv4_kernel, grid, dim3(32), 0, stream, ka) != cudaSuccess)
+        return BI_ERR_CUDA;
+    if (max_chunks == 1) return BI_OK;
+    const int64_t rows = static_cast<int64_t>(B) * Hq;
+    return bi::launch_pdl(merge_rows_kv4_kernel, dim3(ceil_div(rows, kMergeWarps)),
+                          dim3(32 * kMergeWarps), 0, stream, args, rows) == cudaSuccess
+               ? BI_OK
+               : BI_ERR_CUDA;
 }

@@ -255,7 +255,8 @@ def test_attention_has_the_bits_of_the_read_back_cache(Hq, Hkv, many):
 
 @pytest.mark.parametrize("lens,msl", [([1], 1), ([300], 300), ([8192], 8192), ([9000, 3], 9001),
                                       ([256] * 40, 256), ([700] * 70, 4096), ([8192] * 9, 8192),
-                                      ([5000, 1] * 130, 8192), ([70000], 70000)])
+                                      ([5000, 1] * 130, 8192), ([70000], 70000),
+                                      ([20000, 3, 8193, 8192, 257], 131072)])
 def test_attention_over_launch_shapes(lens, msl):
     """Few and many sequences, one and many chunks a CTA, and a bound far above
     the lengths: always the read-back cache's bits."""
@@ -268,9 +269,9 @@ def test_attention_over_launch_shapes(lens, msl):
     assert np.array_equal(bits(got), bits(want))
 
 
-def test_as_many_pairs_as_counters():
-    """65536 (sequence, kv-head) pairs: every arrival counter in use."""
-    B, Hkv = 8192, 8
+def test_more_pairs_than_counters():
+    """65544 (sequence, kv-head) pairs, some of several chunks: the workspace has 65536 arrival counters."""
+    B, Hkv = 8193, 8
     lens = [1 + (i * 37) % 40 for i in range(B)]
     lens[5], lens[8000] = 1500, 1300
     table, P = inputs.paged_layout(torch.tensor(lens), seed=971)
