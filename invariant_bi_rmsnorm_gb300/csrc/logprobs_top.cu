@@ -29,8 +29,8 @@
 // What bounds it is the instructions of the pass: about 9.6 a logit, of which
 // the exponential, its sum in bi_logprobs' order and T take 5, and moving the
 // maximum (in most vectors of a row's first half some lane's does) 2.  1024
-// rows of 151936 logits, k = 20: 70 us, 4.4 TB/s, 0.65 of the copy rate
-// (bi_logprobs, without entropy and alternatives, 53 us); one row 19 us.
+// rows of 151936 logits, k = 20: 69 us, 4.5 TB/s, 0.67 of the copy rate
+// (bi_logprobs, without entropy and alternatives, 50 us); one row 18 us.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -44,8 +44,10 @@ namespace {
 using bi_lp::kLog2e;
 using bi_lp::kThreads;
 
-// Vectors a thread has on their way at a time.  1024 rows of 151936 logits took
-// 70 us with 4 (five CTAs per SM), 83 with 2 (six), 71 with 8 (four).
+// Vectors a thread loads at a time, while it folds as many before them.  1024,
+// 608 rows and one of 151936 logits, k = 20: 4 (four CTAs per SM) 68.8, 44.1 and
+// 17.9 us; nothing loaded ahead: 4 (five CTAs) 70.2, 50.2 and 19.0, 2 (six) 83
+// (1024 rows), 8 (three) 85, 57 and 17.7; 8 loaded ahead (three) 93, 63 and 20.4.
 constexpr int kUnroll = 4;
 constexpr int kSegs = 32;      // segments per thread, at most
 constexpr int kMaxTop = 32;
@@ -211,7 +213,7 @@ __device__ __forceinline__ void each_reaching(const uint16_t* x, int vocab, int 
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 5) logprobs_top_kernel(const TopArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) logprobs_top_kernel(const TopArgs a) {
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
     __shared__ uint16_t seg_max[kSegs * kThreads];
@@ -233,15 +235,22 @@ __global__ void __launch_bounds__(kThreads, 5) logprobs_top_kernel(const TopArgs
     // ---- one pass: (m, s, T) and the segments' maxima ----
     Run run = {kLowest, 0.f, 0.f, make_float2(0.f, 0.f), true};
     uint32_t best = 0;
+    auto load = [&](uint4 (&u)[kUnroll], int v0) {
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int v = v0 + i * kThreads;
+            u[i] = v < nvec ? __ldcs(xv + v) : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
+        }
+    };
+    uint4 next[kUnroll];
+    load(next, tid);
     for (int sg = 0, v0 = tid; sg * a.seg_vecs * kThreads < nvec; ++sg) {
         float sm = -INFINITY;
         for (int i0 = 0; i0 < a.seg_vecs; i0 += kUnroll, v0 += kUnroll * kThreads) {
             uint4 u[kUnroll];
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                const int v = v0 + i * kThreads;
-                u[i] = v < nvec ? __ldcs(xv + v) : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
-            }
+            for (int i = 0; i < kUnroll; ++i) u[i] = next[i];
+            load(next, v0 + kUnroll * kThreads);
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) sm = fmaxf(sm, fold_vec_t(run, u[i]));
         }
