@@ -38,6 +38,7 @@
 // for one sequence.  Many chunks: one warp per chunk, see below.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <type_traits>
@@ -633,144 +634,149 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     out[4] = bi::pack_bf16x2(bi_attn::normalise(o.y, il), bi_attn::normalise(o.w, il));
 }
 
+// kLoop: a warp takes chunks gridDim.x apart, else its one.
+template <bool kLoop>
 __global__ void __launch_bounds__(32, 14) attn_warp_kv4_kernel(const Kv4Args ka) {
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
     const SplitArgs& a = ka.s;
-    const int c = blockIdx.x;  // chunk
     const int g = blockIdx.y;
     const int s = blockIdx.z;
     const int lane = threadIdx.x;
 
     const int L = a.seq_lens[s];
     if (L < 1 || L > a.max_seq_len) {
-        if (lane == 0 && c == 0 && g == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
+        if (lane == 0 && blockIdx.x == 0 && g == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
         return;
     }
     const int nch = (L + kChunk - 1) / kChunk;
+    int c = blockIdx.x;  // chunk
     if (c >= nch) return;
-    const int tokens = min(kChunk, L - c * kChunk);
-    const int np = (tokens + kPage - 1) / kPage;
     const int64_t row0 = static_cast<int64_t>(s) * a.Hq + g * a.group;
 
     __shared__ __align__(16) uint8_t ring[kRing * kStageBytes];
 
-    // lane p keeps which block page p is
-    int block = 0;
-    {
-        int pg = 0;
-        if (lane < np)
-            pg = a.block_table[static_cast<int64_t>(s) * a.max_pages_per_seq + c * kPagesPerChunk + lane];
-        if (__any_sync(kAll, pg < 0 || pg >= a.num_pages)) {
-            if (lane == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
-            if (nch > 1 && lane < a.group)
-                *partial_ml(a, row0 + lane, c) = make_float2(-INFINITY, kNoChunk);
+    do {
+        const int tokens = min(kChunk, L - c * kChunk);
+        const int np = (tokens + kPage - 1) / kPage;
+        // lane p keeps which block page p is
+        int block = 0;
+        {
+            int pg = 0;
+            if (lane < np)
+                pg = a.block_table[static_cast<int64_t>(s) * a.max_pages_per_seq + c * kPagesPerChunk + lane];
+            if (__any_sync(kAll, pg < 0 || pg >= a.num_pages)) {
+                if (lane == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
+                if (nch > 1 && lane < a.group)
+                    *partial_ml(a, row0 + lane, c) = make_float2(-INFINITY, kNoChunk);
+                continue;
+            }
+            block = pg * a.Hkv + g;
+        }
+        // A page's two blocks are 72 16-byte units each: two asynchronous copies a
+        // lane for each block, and one for the 8 units that are left of either.
+        // (Bulk copies, one lane's work, take the warp twice as many instructions,
+        // and a barrier's on top.)  A page is a group, there or not.
+        static_assert(kBlockBytes == 72 * 16, "units of a block");
+        const uint8_t* const k_src = ka.k_cache + 16 * lane;
+        const uint8_t* const v_src = ka.v_cache + 16 * lane;
+        const uint8_t* const rest_src = 1024 + (lane < 8 ? k_src : v_src - 128);
+        const int rest_dst = 1024 + (lane < 8 ? 16 * lane : kBlockBytes + 16 * (lane - 8));
+        auto copy_page = [&](int p, uint8_t* stage) {
+            if (p < np) {
+                const int64_t at = static_cast<int64_t>(__shfl_sync(kAll, block, p)) * kBlockBytes;
+                uint8_t* dst = stage + 16 * lane;
+                bi::cp_async_16(dst, k_src + at);
+                bi::cp_async_16(dst + 512, k_src + at + 512);
+                bi::cp_async_16(dst + kBlockBytes, v_src + at);
+                bi::cp_async_16(dst + kBlockBytes + 512, v_src + at + 512);
+                if (lane < 16) bi::cp_async_16(stage + rest_dst, rest_src + at);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        // until at most kPending of the latest groups are on their way
+        auto wait_pages = [](auto pending) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(decltype(pending)::value) : "memory");
+            __syncwarp();  // every lane's copies, for every lane
+        };
+#pragma unroll
+        for (int p = 0; p < kRing; ++p) copy_page(p, ring + p * kStageBytes);
+
+        // column n of the mma tile = query head g*group + n (n < group)
+        uint32_t qb0[8], qb1[8];
+        bi_attn::load_q_frags((lane >> 2) < a.group ? a.q + (row0 + (lane >> 2)) * kD : nullptr, lane, qb0, qb1);
+
+        WarpState st;
+        st.th[0] = st.th[1] = -INFINITY;
+        st.ref[0] = st.ref[1] = 0.f;
+        st.l = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) st.acc[mt][0] = st.acc[mt][1] = st.acc[mt][2] = st.acc[mt][3] = 0.f;
+
+        uint8_t* cur = ring;  // the stage of page p
+        wait_pages(std::integral_constant<int, kRing - 1>());
+        float x[4];
+        page_logs(x, cur, qb0, qb1, tokens, a.scale_log2, lane);
+        // full pages with a page behind them
+        for (int p = 0; p < np - 1; ++p) {
+            uint8_t* next = cur + kStageBytes;
+            if (next == ring + kRing * kStageBytes) next = ring;
+            wait_pages(std::integral_constant<int, kRing - 2>());  // page p + 1 is here
+            bi_attn::PFrags pf;
+            weights_step(st, x, p == 0, lane, pf);
+            VFrags f;
+            load_v(f, cur + kBlockBytes, kPage, lane);
+            __syncwarp();  // every lane is done with the stage
+            copy_page(p + kRing, cur);
+            page_logs(x, next, qb0, qb1, kPage, a.scale_log2, lane);
+#pragma unroll
+            for (int gr = 0; gr < 4; ++gr) pv_group(st.acc[2 * gr], st.acc[2 * gr + 1], f, gr, pf);
+            cur = next;
+        }
+        {  // the last page, whose last tokens may not be there
+            const int valid = tokens - (np - 1) * kPage;
+            if (valid < kPage) {
+                if ((lane >> 2) >= valid) x[0] = x[1] = -INFINITY;
+                if ((lane >> 2) + 8 >= valid) x[2] = x[3] = -INFINITY;
+            }
+            bi_attn::PFrags pf;
+            weights_step(st, x, np == 1, lane, pf);
+            VFrags f;
+            load_v(f, cur + kBlockBytes, valid, lane);
+#pragma unroll
+            for (int gr = 0; gr < 4; ++gr) pv_group(st.acc[2 * gr], st.acc[2 * gr + 1], f, gr, pf);
+        }
+
+        const int h0 = 2 * (lane & 3);
+        // both columns' sums: lane l holds one of them, lane l ^ 4 the other
+        const float other = __shfl_xor_sync(kAll, st.l, 4);
+        const float l[2] = {lane & 4 ? other : st.l, lane & 4 ? st.l : other};
+        if (nch == 1) {  // the whole sequence: bf16(O / l)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (h0 + e >= a.group) continue;
+                const float il = bi_attn::inv_weight(l[e]);
+                __nv_bfloat16* o = a.out + (row0 + h0 + e) * kD + (lane >> 2);
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt) {
+                    o[16 * mt] = __float2bfloat16_rn(bi_attn::normalise(st.acc[mt][e], il));
+                    o[16 * mt + 8] = __float2bfloat16_rn(bi_attn::normalise(st.acc[mt][2 + e], il));
+                }
+            }
             return;
         }
-        block = pg * a.Hkv + g;
-    }
-    // A page's two blocks are 72 16-byte units each: two asynchronous copies a
-    // lane for each block, and one for the 8 units that are left of either.
-    // (Bulk copies, one lane's work, take the warp twice as many instructions,
-    // and a barrier's on top.)  A page is a group, there or not.
-    static_assert(kBlockBytes == 72 * 16, "units of a block");
-    const uint8_t* const k_src = ka.k_cache + 16 * lane;
-    const uint8_t* const v_src = ka.v_cache + 16 * lane;
-    const uint8_t* const rest_src = 1024 + (lane < 8 ? k_src : v_src - 128);
-    const int rest_dst = 1024 + (lane < 8 ? 16 * lane : kBlockBytes + 16 * (lane - 8));
-    auto copy_page = [&](int p, uint8_t* stage) {
-        if (p < np) {
-            const int64_t at = static_cast<int64_t>(__shfl_sync(kAll, block, p)) * kBlockBytes;
-            uint8_t* dst = stage + 16 * lane;
-            bi::cp_async_16(dst, k_src + at);
-            bi::cp_async_16(dst + 512, k_src + at + 512);
-            bi::cp_async_16(dst + kBlockBytes, v_src + at);
-            bi::cp_async_16(dst + kBlockBytes + 512, v_src + at + 512);
-            if (lane < 16) bi::cp_async_16(stage + rest_dst, rest_src + at);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    // until at most kPending of the latest groups are on their way
-    auto wait_pages = [](auto pending) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(decltype(pending)::value) : "memory");
-        __syncwarp();  // every lane's copies, for every lane
-    };
-#pragma unroll
-    for (int p = 0; p < kRing; ++p) copy_page(p, ring + p * kStageBytes);
-
-    // column n of the mma tile = query head g*group + n (n < group)
-    uint32_t qb0[8], qb1[8];
-    bi_attn::load_q_frags((lane >> 2) < a.group ? a.q + (row0 + (lane >> 2)) * kD : nullptr, lane, qb0, qb1);
-
-    WarpState st;
-    st.th[0] = st.th[1] = -INFINITY;
-    st.ref[0] = st.ref[1] = 0.f;
-    st.l = 0.f;
-#pragma unroll
-    for (int mt = 0; mt < 8; ++mt) st.acc[mt][0] = st.acc[mt][1] = st.acc[mt][2] = st.acc[mt][3] = 0.f;
-
-    uint8_t* cur = ring;  // the stage of page p
-    wait_pages(std::integral_constant<int, kRing - 1>());
-    float x[4];
-    page_logs(x, cur, qb0, qb1, tokens, a.scale_log2, lane);
-    // full pages with a page behind them
-    for (int p = 0; p < np - 1; ++p) {
-        uint8_t* next = cur + kStageBytes;
-        if (next == ring + kRing * kStageBytes) next = ring;
-        wait_pages(std::integral_constant<int, kRing - 2>());  // page p + 1 is here
-        bi_attn::PFrags pf;
-        weights_step(st, x, p == 0, lane, pf);
-        VFrags f;
-        load_v(f, cur + kBlockBytes, kPage, lane);
-        __syncwarp();  // every lane is done with the stage
-        copy_page(p + kRing, cur);
-        page_logs(x, next, qb0, qb1, kPage, a.scale_log2, lane);
-#pragma unroll
-        for (int gr = 0; gr < 4; ++gr) pv_group(st.acc[2 * gr], st.acc[2 * gr + 1], f, gr, pf);
-        cur = next;
-    }
-    {  // the last page, whose last tokens may not be there
-        const int valid = tokens - (np - 1) * kPage;
-        if (valid < kPage) {
-            if ((lane >> 2) >= valid) x[0] = x[1] = -INFINITY;
-            if ((lane >> 2) + 8 >= valid) x[2] = x[3] = -INFINITY;
-        }
-        bi_attn::PFrags pf;
-        weights_step(st, x, np == 1, lane, pf);
-        VFrags f;
-        load_v(f, cur + kBlockBytes, valid, lane);
-#pragma unroll
-        for (int gr = 0; gr < 4; ++gr) pv_group(st.acc[2 * gr], st.acc[2 * gr + 1], f, gr, pf);
-    }
-
-    const int h0 = 2 * (lane & 3);
-    // both columns' sums: lane l holds one of them, lane l ^ 4 the other
-    const float other = __shfl_xor_sync(kAll, st.l, 4);
-    const float l[2] = {lane & 4 ? other : st.l, lane & 4 ? st.l : other};
-    if (nch == 1) {  // the whole sequence: bf16(O / l)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if (h0 + e >= a.group) continue;
-            const float il = bi_attn::inv_weight(l[e]);
-            __nv_bfloat16* o = a.out + (row0 + h0 + e) * kD + (lane >> 2);
+            float2* o = reinterpret_cast<float2*>(partial_o(a, row0 + h0 + e, c)) + (lane >> 2);
 #pragma unroll
-            for (int mt = 0; mt < 8; ++mt) {
-                o[16 * mt] = __float2bfloat16_rn(bi_attn::normalise(st.acc[mt][e], il));
-                o[16 * mt + 8] = __float2bfloat16_rn(bi_attn::normalise(st.acc[mt][2 + e], il));
-            }
+            for (int mt = 0; mt < 8; ++mt) o[8 * mt] = make_float2(st.acc[mt][e], st.acc[mt][2 + e]);
+            if (lane < 4)
+                *partial_ml(a, row0 + h0 + e, c) =
+                    make_float2(st.th[e] == -INFINITY ? -INFINITY : st.ref[e], l[e]);
         }
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        if (h0 + e >= a.group) continue;
-        float2* o = reinterpret_cast<float2*>(partial_o(a, row0 + h0 + e, c)) + (lane >> 2);
-#pragma unroll
-        for (int mt = 0; mt < 8; ++mt) o[8 * mt] = make_float2(st.acc[mt][e], st.acc[mt][2 + e]);
-        if (lane < 4)
-            *partial_ml(a, row0 + h0 + e, c) =
-                make_float2(st.th[e] == -INFINITY ? -INFINITY : st.ref[e], l[e]);
-    }
+        if (kLoop) __syncwarp();  // every lane is done with the ring
+    } while (kLoop && (c += gridDim.x) < nch);
 }
 
 // Chunks per SM (at the launch's bound on the lengths; lengths spread up to the
@@ -784,6 +790,14 @@ __global__ void __launch_bounds__(32, 14) attn_warp_kv4_kernel(const Kv4Args ka)
 // instructions and has no barriers.  Below the rule there are far fewer chunks
 // than arrival counters, and than an arrival counter can count.
 constexpr int64_t kManyChunks = 22;
+
+// Warps of a launch with one chunk each; a launch whose bound on the lengths asks
+// for more has about as many, each with several chunks.  A warp without a chunk
+// costs 0.7 ns, and a bound may be far above the lengths (captured graphs): 256
+// sequences of 300 tokens under a bound of 131072 take 45 us, and 1060 with a
+// warp a chunk; lengths even over 1 .. 8192, which fill half of the bound,
+// B = 256, 296 against 289 (twice as many warps: 52 and 291).
+constexpr int64_t kMostWarps = 16384;
 
 // set once per device; any thread may race to set it, the attribute is idempotent
 std::atomic<bool> g_attr_set[64] = {};
@@ -860,8 +874,13 @@ extern "C" bi_status bi_decode_attention_kv4(const void* q, const void* k_cache,
                        cudaSuccess
                    ? BI_OK
                    : BI_ERR_CUDA;
-    if (bi::launch_pdl(attn_warp_kv4_kernel, grid, dim3(32), 0, stream, ka) != cudaSuccess)
-        return BI_ERR_CUDA;
+    const int64_t most = std::max<int64_t>(1, kMostWarps / (static_cast<int64_t>(Hkv) * B));
+    const cudaError_t e =
+        max_chunks <= most
+            ? bi::launch_pdl(attn_warp_kv4_kernel<false>, grid, dim3(32), 0, stream, ka)
+            : bi::launch_pdl(attn_warp_kv4_kernel<true>, dim3(static_cast<unsigned>(most), Hkv, B), dim3(32),
+                             0, stream, ka);
+    if (e != cudaSuccess) return BI_ERR_CUDA;
     if (max_chunks == 1) return BI_OK;
     const int64_t rows = static_cast<int64_t>(B) * Hq;
     return bi::launch_pdl(merge_rows_kv4_kernel, dim3(ceil_div(rows, kMergeWarps)),

@@ -8,6 +8,8 @@
 // a row's codes depend on its own 128 values only.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "bi_internal.h"
 #include "bi_ptx.cuh"
 #include "kv4.cuh"
@@ -85,65 +87,73 @@ struct ReadArgs {
     uint32_t* err;
 };
 
-// One CTA per (sequence, page, kHeads kv-heads): thread (r, c) writes dims 8c ..
-// 8c + 7 of token r of every head, all loads before any store.  Bound by HBM
-// and the latency of a CTA's three dependent loads (length, page, codes): 8192
-// tokens of 8 heads (9.4 MB read, 33.6 MB written) take 10.5 us cold, 4.1 TB/s
-// (16.3 us with a loop over the heads, 10.7 with one head or four a CTA).
+// One CTA per (sequence, page, kHeads kv-heads), pages gridDim.x apart: thread
+// (r, c) writes dims 8c .. 8c + 7 of token r of every head, all loads before any
+// store.  Bound by HBM and the latency of a CTA's three dependent loads (length,
+// page, codes): 8192 tokens of 8 heads (9.4 MB read, 33.6 MB written) take 10.5
+// us cold, 4.1 TB/s (16.3 us with a loop over the heads, 10.7 with one head or
+// four a CTA).
 constexpr int kHeads = 2;
+// CTAs of a launch: a bound far above the lengths would ask for very many that
+// find no page.  29 sequences of 32 .. 512 tokens under a bound of 131072 take
+// 7.8 us (958 with a CTA a page, 18 with 16384 CTAs), one of 131072 tokens 134
+// (138, 133).
+constexpr int64_t kMostCtas = 4096;
 
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
-    const int s = blockIdx.y, p = blockIdx.x;
+    const int s = blockIdx.y;
     const int h0 = blockIdx.z * kHeads;
     const int L = a.seq_lens[s];
     if (L < 0 || L > a.max_seq_len) {
-        if (threadIdx.x == 0 && p == 0 && h0 == 0)
+        if (threadIdx.x == 0 && blockIdx.x == 0 && h0 == 0)
             bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
         return;
     }
-    if (p * BI_PAGE_SIZE >= L) return;
-    const int pg = a.block_table[static_cast<int64_t>(s) * a.max_pages_per_seq + p];
-    if (pg < 0 || pg >= a.num_pages) {
-        if (threadIdx.x == 0 && h0 == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
-        return;
-    }
     const int r = threadIdx.x >> 4, c = threadIdx.x & 15;
-    if (r >= L - p * BI_PAGE_SIZE) return;  // rows behind the sequence stay as they were
-    const int k_at = 64 * r + 4 * (c >> 2);                                  // word (t = 0, j = c / 4)
-    const int v_at = 512 * (r >> 3) + 8 * (r & 7) + 4 * (c >> 3);            // word (g = 0, w = c / 8)
-    const int s_at = bi_kv4::kScaleOffset + bi_kv4::kScaleRowBytes * r + 2 * (c >> 2);
-    const int64_t blk0 = static_cast<int64_t>(pg) * a.Hkv + h0;
-    uint32_t kw[kHeads][4], vw[kHeads][8], ks[kHeads], vs[kHeads];
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        if (h0 + i >= a.Hkv) break;
-        const uint8_t* kb = a.k_cache + (blk0 + i) * bi_kv4::kBlockBytes;
-        const uint8_t* vb = a.v_cache + (blk0 + i) * bi_kv4::kBlockBytes;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) kw[i][t] = *reinterpret_cast<const uint32_t*>(kb + k_at + 16 * t);
-#pragma unroll
-        for (int g = 0; g < 8; ++g) vw[i][g] = *reinterpret_cast<const uint32_t*>(vb + v_at + 64 * g);
-        ks[i] = *reinterpret_cast<const uint16_t*>(kb + s_at);
-        vs[i] = *reinterpret_cast<const uint16_t*>(vb + s_at);
-    }
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        if (h0 + i >= a.Hkv) break;
-        const int64_t out = ((blk0 + i) * BI_PAGE_SIZE + r) * kD + 8 * c;
-        uint32_t ko[4], vo[4];
-        const bi_kv4::ScalePair kp = bi_kv4::scale_pair(ks[i] * 0x10001u);
-        const bi_kv4::ScalePair vp = bi_kv4::scale_pair(vs[i] * 0x10001u);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            ko[t] = bi_kv4::kv4_pair(kw[i][t], c & 3, kp);
-            // dims 8c + 2t, 8c + 2t + 1: code c % 8 of words g = 2t, 2t + 1
-            const uint32_t lo = vw[i][2 * t] >> (4 * (c & 7)), hi = vw[i][2 * t + 1] >> (4 * (c & 7));
-            vo[t] = bi_kv4::kv4_pair(__byte_perm(lo, hi, 0x5410), 0, vp);
+    const int pages = L / BI_PAGE_SIZE + (L % BI_PAGE_SIZE != 0);
+    for (int p = blockIdx.x; p < pages; p += gridDim.x) {
+        const int pg = a.block_table[static_cast<int64_t>(s) * a.max_pages_per_seq + p];
+        if (pg < 0 || pg >= a.num_pages) {
+            if (threadIdx.x == 0 && h0 == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereDecoderOps);
+            continue;
         }
-        *reinterpret_cast<uint4*>(a.k_out + out) = make_uint4(ko[0], ko[1], ko[2], ko[3]);
-        *reinterpret_cast<uint4*>(a.v_out + out) = make_uint4(vo[0], vo[1], vo[2], vo[3]);
+        if (r >= L - p * BI_PAGE_SIZE) continue;  // rows behind the sequence stay as they were
+        const int k_at = 64 * r + 4 * (c >> 2);                                  // word (t = 0, j = c / 4)
+        const int v_at = 512 * (r >> 3) + 8 * (r & 7) + 4 * (c >> 3);            // word (g = 0, w = c / 8)
+        const int s_at = bi_kv4::kScaleOffset + bi_kv4::kScaleRowBytes * r + 2 * (c >> 2);
+        const int64_t blk0 = static_cast<int64_t>(pg) * a.Hkv + h0;
+        uint32_t kw[kHeads][4], vw[kHeads][8], ks[kHeads], vs[kHeads];
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            if (h0 + i >= a.Hkv) break;
+            const uint8_t* kb = a.k_cache + (blk0 + i) * bi_kv4::kBlockBytes;
+            const uint8_t* vb = a.v_cache + (blk0 + i) * bi_kv4::kBlockBytes;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) kw[i][t] = *reinterpret_cast<const uint32_t*>(kb + k_at + 16 * t);
+#pragma unroll
+            for (int g = 0; g < 8; ++g) vw[i][g] = *reinterpret_cast<const uint32_t*>(vb + v_at + 64 * g);
+            ks[i] = *reinterpret_cast<const uint16_t*>(kb + s_at);
+            vs[i] = *reinterpret_cast<const uint16_t*>(vb + s_at);
+        }
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            if (h0 + i >= a.Hkv) break;
+            const int64_t out = ((blk0 + i) * BI_PAGE_SIZE + r) * kD + 8 * c;
+            uint32_t ko[4], vo[4];
+            const bi_kv4::ScalePair kp = bi_kv4::scale_pair(ks[i] * 0x10001u);
+            const bi_kv4::ScalePair vp = bi_kv4::scale_pair(vs[i] * 0x10001u);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                ko[t] = bi_kv4::kv4_pair(kw[i][t], c & 3, kp);
+                // dims 8c + 2t, 8c + 2t + 1: code c % 8 of words g = 2t, 2t + 1
+                const uint32_t lo = vw[i][2 * t] >> (4 * (c & 7)), hi = vw[i][2 * t + 1] >> (4 * (c & 7));
+                vo[t] = bi_kv4::kv4_pair(__byte_perm(lo, hi, 0x5410), 0, vp);
+            }
+            *reinterpret_cast<uint4*>(a.k_out + out) = make_uint4(ko[0], ko[1], ko[2], ko[3]);
+            *reinterpret_cast<uint4*>(a.v_out + out) = make_uint4(vo[0], vo[1], vo[2], vo[3]);
+        }
     }
 }
 
@@ -219,8 +229,10 @@ extern "C" bi_status bi_kv4_read(const void* k_cache, const void* v_cache,
     a.k_out = static_cast<__nv_bfloat16*>(k_out);
     a.v_out = static_cast<__nv_bfloat16*>(v_out);
     a.err = bi::device_error_word();
-    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(max_seq_len) + BI_PAGE_SIZE - 1) / BI_PAGE_SIZE),
-                    static_cast<unsigned>(S), static_cast<unsigned>((Hkv + kHeads - 1) / kHeads));
+    const int64_t pages = (static_cast<int64_t>(max_seq_len) + BI_PAGE_SIZE - 1) / BI_PAGE_SIZE;
+    const int64_t heads = (Hkv + kHeads - 1) / kHeads;
+    const dim3 grid(static_cast<unsigned>(std::min(pages, std::max<int64_t>(1, kMostCtas / (S * heads)))),
+                    static_cast<unsigned>(S), static_cast<unsigned>(heads));
     return bi::launch_pdl(kv4_read_kernel, grid, dim3(kThreads), 0, stream, a) == cudaSuccess
                ? BI_OK
                : BI_ERR_CUDA;

@@ -284,6 +284,62 @@ def test_more_pairs_than_counters():
     assert np.array_equal(bits(got), bits(want))
 
 
+def test_warps_that_take_several_chunks():
+    """4800 (sequence, kv-head) pairs under a bound of 8 chunks: more chunks than
+    warps.  A bad page in one sequence's third chunk, another's first and last."""
+    B, Hkv = 600, 8
+    lens = [1 + (i * 397) % 2000 for i in range(B)]
+    lens[7], lens[300] = 1999, 1300
+    table, P = inputs.paged_layout(torch.tensor(lens), seed=973)
+    g = torch.Generator(device="cuda").manual_seed(974)
+    k = torch.randn(P, Hkv, 16, 128, generator=g, device="cuda").to(torch.bfloat16)
+    v = torch.randn(P, Hkv, 16, 128, generator=g, device="cuda").to(torch.bfloat16)
+    kc, vc = _cache_of(k, v)
+    q = torch.randn(B, 2 * Hkv, 128, generator=g, device="cuda").to(torch.bfloat16)
+    bt, sl = table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got, want, _, _ = _both(q, kc, vc, bt, sl, 2000)
+    assert np.array_equal(bits(got), bits(want))
+    bt = bt.clone()
+    bt[7, 40], bt[300, 0], bt[300, 81] = -1, P, 2 ** 31 - 1
+    out = torch.full_like(q, 9.0)
+    bi.decode_attention_kv4(q, kc, vc, bt, sl, 2000, out=out)
+    with pytest.raises(bi.BiError, match="BAD_INPUT"):
+        bi.get_device_error()
+    assert (out[[7, 300]] == 9).all()
+    keep = torch.ones(B, dtype=torch.bool)
+    keep[[7, 300]] = False
+    assert np.array_equal(bits(out[keep.cuda()]), bits(want[keep.cuda()]))
+
+
+def test_read_back_under_a_bound_far_above_the_lengths():
+    """More pages under the bound than the launch has CTAs."""
+    S, Hkv, bound = 40, 5, 40000
+    lens = [0, 1, 16, 17, 39999, 2500] + [3 * i for i in range(S - 6)]
+    need = [-(-n // 16) for n in lens]
+    P = sum(need) + 1
+    kc = torch.randint(0, 256, (P, Hkv, bi.KV4_BLOCK_BYTES), dtype=torch.uint8, device="cuda")
+    kc[:, :, 1024:] = torch.tensor([0x80, 0x3F], dtype=torch.uint8, device="cuda").repeat(64)  # scales of 1
+    vc = kc.flip(0).contiguous()
+    order = torch.randperm(P, generator=torch.Generator().manual_seed(3)).to(torch.int32)
+    bt = torch.full((S, bound // 16), -1, dtype=torch.int32)
+    used = 0
+    for i, n in enumerate(need):
+        bt[i, :n] = order[used:used + n]
+        used += n
+    sl = torch.tensor(lens, dtype=torch.int32)
+    outs = [torch.full((P, Hkv, 16, 128), 99.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    bi.kv4_read(kc, vc, bt.cuda(), sl.cuda(), bound, *outs)
+    bi.get_device_error()
+    whole = _read_all(kc, vc)  # every page, all 16 rows
+    for got, every in zip(outs, whole):
+        want = torch.full_like(got, 99.0)
+        for i, L in enumerate(lens):
+            for p in range(need[i]):
+                n = min(16, L - 16 * p)
+                want[int(bt[i, p]), :, :n] = every[int(bt[i, p]), :, :n]
+        assert np.array_equal(bits(got), bits(want))
+
+
 def test_row_alone_and_in_a_batch():
     lens = [5, 8000, 256, 1, 4097, 700, 31]
     q, kc, vc, bt, sl = _problem(lens, 32, 8, 980)
