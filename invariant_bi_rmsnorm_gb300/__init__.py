@@ -453,6 +453,17 @@ def _refuse(where: str, *wanted):
     raise ValueError(f"{where}: arguments do not fit together")
 
 
+def _made(stream, make, *args, **kw) -> torch.Tensor:
+    """make(...) on the stream that is to use the tensor first, so that what
+    fills it comes before, and its memory is not handed out again too soon."""
+    if stream is None:
+        return make(*args, **kw)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def kv4_cache(num_pages: int, Hkv: int, device="cuda") -> tuple[torch.Tensor, torch.Tensor]:
     """A pair of empty 4-bit K and V caches, uint8 [num_pages, Hkv, 1152]: pages
     of 16 tokens, heads of 128 dims (include/bi.h gives the layout)."""
@@ -506,7 +517,7 @@ def qk_norm_rope_append_kv4(qkv: torch.Tensor, Hq: int, Hkv: int, positions: tor
     v rows, quantised -> their slots."""
     dev = _current_device()
     if q_out is None:
-        q_out = torch.empty((qkv.shape[0], Hq, 128), dtype=_BF16, device=qkv.device)
+        q_out = _made(stream, torch.empty, (qkv.shape[0], Hq, 128), dtype=_BF16, device=qkv.device)
     shape, cs, rs = qkv.shape, k_cache.shape, rope.shape
     if not (len(shape) == 2 and qkv.dtype is _BF16 and shape[1] >= (Hq + 2 * Hkv) * 128
             and qkv.stride(1) == 1 and positions.dtype is slots.dtype is _I32
@@ -577,7 +588,7 @@ def decode_attention_kv4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     the workspace, as decode_attention."""
     dev = _current_device()
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     qs, cs, bs = q.shape, k_cache.shape, block_table.shape
     if not (q.dtype is out.dtype is _BF16 and len(qs) == 3 and out.shape == qs and q.is_contiguous()
             and out.is_contiguous() and k_cache.dtype is v_cache.dtype is _U8 and len(cs) == 3
@@ -600,7 +611,7 @@ def decode_attention_kv4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
         if need > 0:
             # the leading arrival counters must start at zero (every call leaves
             # them zero, so a caller-kept workspace is cleared only once)
-            workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+            workspace = _made(stream, torch.zeros, need, dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         _refuse("decode_attention_kv4", (workspace, "workspace", workspace.dtype, None))
     ws = workspace is not None
@@ -616,8 +627,8 @@ def decode_attention_kv4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
 def logprobs_top(logits: torch.Tensor, targets: torch.Tensor | None, k: int, stream=None):
     """(logprob of targets [rows] or None, lse [rows], entropy [rows], top_ids
     [rows, k] int32, top_logprobs [rows, k]) of bf16 logits [rows, vocab]: the
-    bits of logprobs(logits, targets), the softmax's entropy in nats, and the k
-    (1 .. 32) largest logits' tokens, largest first, equal ones by ascending id."""
+    bits of logprobs(logits, targets) where logits are -inf or within +-1024, the
+    softmax's entropy in nats, and the k (1 .. 32) largest logits' tokens, largest first, equal ones by ascending id."""
     dev = _current_device()
     shape = logits.shape
     if not (logits.dtype is _BF16 and len(shape) == 2 and logits.stride(1) == 1
@@ -634,11 +645,11 @@ def logprobs_top(logits: torch.Tensor, targets: torch.Tensor | None, k: int, str
                                     and targets.is_contiguous() and targets.get_device() == dev):
         _refuse("logprobs_top", (targets, "targets", _I32, shape[:1]))
     on = logits.device
-    lse = torch.empty(rows, dtype=_F32, device=on)
-    entropy = torch.empty_like(lse)
-    lp = torch.empty_like(lse) if targets is not None else None
-    top = torch.empty((rows, k), dtype=_F32, device=on)
-    ids = torch.empty((rows, k), dtype=_I32, device=on)
+    lse = _made(stream, torch.empty, rows, dtype=_F32, device=on)
+    entropy = _made(stream, torch.empty_like, lse)
+    lp = _made(stream, torch.empty_like, lse) if targets is not None else None
+    top = _made(stream, torch.empty, (rows, k), dtype=_F32, device=on)
+    ids = _made(stream, torch.empty, (rows, k), dtype=_I32, device=on)
     _check(_lib.load().bi_logprobs_top(
         logits.data_ptr(), rows, vocab, logits.stride(0) if rows > 1 else vocab,
         None if targets is None else targets.data_ptr(), None if lp is None else lp.data_ptr(),

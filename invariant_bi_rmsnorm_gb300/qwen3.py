@@ -36,7 +36,7 @@ from . import (add_rmsnorm, decode_attention, decode_attention_kv4,
                prefill_attention_workspace_size, qk_norm_rope_append, qk_norm_rope_append_kv4,
                rmsnorm, silu_mul)
 from . import inputs
-from ._lib import PAGE_SIZE
+from ._lib import MAX_TOP_LOGPROBS, PAGE_SIZE
 
 
 def rope_table(max_pos: int, theta: float, D: int = 128, device=None) -> torch.Tensor:
@@ -485,6 +485,8 @@ class Engine:
         never needs a token's value), its decode rows take their input tokens
         straight from step i's picks on the device, and step i's picks are
         read back only after step i+1 has been queued."""
+        if not 0 <= top <= MAX_TOP_LOGPROBS:
+            raise ValueError(f"top must be 0 .. {MAX_TOP_LOGPROBS}")
         record = record or set()
         rec_rows = {sid: [] for sid in record}  # device rows, copied to the host at the end
         waiting = deque(seqs)

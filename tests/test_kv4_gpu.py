@@ -524,22 +524,23 @@ def test_prompt_then_decode_as_a_server_runs_them():
         assert np.array_equal(bits(got[at]), bits(whole[at])), at
 
 
-def test_captured_steps_replay_beside_eager_ones():
+@pytest.mark.parametrize("bound", [4096, 65536], ids=["few-chunks", "many-chunks"])
+def test_captured_steps_replay_beside_eager_ones(bound):
     """Two captured decode steps with a workspace each, replayed with changed
     inputs while eager calls run on another stream."""
     lens = [700, 30, 4000]
     q, kc, vc, bt, sl = _problem(lens, 32, 8, 1020)
-    size = bi.decode_attention_workspace_size(3, 32, 128, 4096)
-    wide = torch.full((3, 256), -1, dtype=torch.int32, device="cuda")
+    size = bi.decode_attention_workspace_size(3, 32, 128, bound)
+    wide = torch.full((3, bound // 16), -1, dtype=torch.int32, device="cuda")
     wide[:, :bt.shape[1]] = bt
     states = []
     for n in range(2):
         qs, out = q.clone(), torch.empty_like(q)
         ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
-        bi.decode_attention_kv4(qs, kc, vc, wide, sl, 4096, out=out, workspace=ws)
+        bi.decode_attention_kv4(qs, kc, vc, wide, sl, bound, out=out, workspace=ws)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            bi.decode_attention_kv4(qs, kc, vc, wide, sl, 4096, out=out, workspace=ws)
+            bi.decode_attention_kv4(qs, kc, vc, wide, sl, bound, out=out, workspace=ws)
         states.append((g, qs, out))
     side = torch.cuda.Stream()
     ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
@@ -549,12 +550,12 @@ def test_captured_steps_replay_beside_eager_ones():
             qs.copy_(x)
         torch.cuda.synchronize()
         with torch.cuda.stream(side):
-            e = bi.decode_attention_kv4(new[0], kc, vc, wide, sl, 4096, workspace=ws)
+            e = bi.decode_attention_kv4(new[0], kc, vc, wide, sl, bound, workspace=ws)
         for g, _, _ in states:
             g.replay()
         torch.cuda.synchronize()
         for (_, _, out), x in zip(states, new):
-            assert np.array_equal(bits(out), bits(bi.decode_attention_kv4(x, kc, vc, wide, sl, 4096)))
+            assert np.array_equal(bits(out), bits(bi.decode_attention_kv4(x, kc, vc, wide, sl, bound)))
         assert np.array_equal(bits(e), bits(states[0][2]))
 
 
@@ -597,3 +598,24 @@ def test_binding_refusals():
     refused("positions", fused, qkv, 2, 2, idx[:1], idx, rope, None, None, kc, vc)
     refused("k_norm_w", fused, qkv, 2, 2, idx, idx, rope, w, w[:64], kc, vc)
     refused("q_out", fused, qkv, 2, 2, idx, idx, rope, w, w, kc, vc, q_out=qkv)
+
+
+def test_tensors_made_for_another_stream():
+    """Output and workspace of a call on another stream come from that stream:
+    the current one is busy, and the memory it had held is full of ones."""
+    lens = [700, 30, 4000]
+    q, kc, vc, bt, sl = _problem(lens, 32, 8, 1050)
+    want = bi.decode_attention_kv4(q, kc, vc, bt, sl, 4000)
+    size = bi.decode_attention_workspace_size(3, 32, 128, 4000)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    busy = torch.ones(8192, 8192, device="cuda")
+    for stream in (side, side.cuda_stream):
+        dirty = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+        del dirty
+        for _ in range(3):
+            busy @ busy
+        got = bi.decode_attention_kv4(q, kc, vc, bt, sl, 4000, stream=stream)
+        side.synchronize()
+        bi.get_device_error(side)
+        assert np.array_equal(bits(got), bits(want))

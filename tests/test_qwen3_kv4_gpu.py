@@ -83,6 +83,9 @@ def test_bits_alone_batched_graphed_and_reported(two_layer):
     bi.get_device_error()
 
 
-def test_engine_refuses_other_widths(two_layer):
+def test_engine_refuses_other_widths_and_reports(two_layer):
     with pytest.raises(ValueError, match="kv_bits"):
         qwen3.Engine(two_layer[1], num_pages=4, kv_bits=8)
+    for top in (-1, 33):
+        with pytest.raises(ValueError, match="top"):
+            qwen3.Engine(two_layer[1], num_pages=4).generate([], top=top)
