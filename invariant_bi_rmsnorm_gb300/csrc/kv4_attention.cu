@@ -791,13 +791,15 @@ __global__ void __launch_bounds__(32, 14) attn_warp_kv4_kernel(const Kv4Args ka)
 // than arrival counters, and than an arrival counter can count.
 constexpr int64_t kManyChunks = 22;
 
-// Warps of a launch with one chunk each; a launch whose bound on the lengths asks
-// for more has about as many, each with several chunks.  A warp without a chunk
+// Warps of a launch and of a (sequence, kv-head), about; where the bound on the
+// lengths asks for more, a warp takes several chunks.  A warp without a chunk
 // costs 0.7 ns, and a bound may be far above the lengths (captured graphs): 256
-// sequences of 300 tokens under a bound of 131072 take 45 us, and 1060 with a
-// warp a chunk; lengths even over 1 .. 8192, which fill half of the bound,
-// B = 256, 296 against 289 (twice as many warps: 52 and 291).
-constexpr int64_t kMostWarps = 16384;
+// sequences of 300 tokens under a bound of 131072 take 52 us, and 1060 with a
+// warp a chunk, 8 of them 24 and 40.  Lengths even over 1 .. 8192, which fill
+// half of the bound, B = 256, 291 against 289; 1 .. 131072, B = 16, 319 against
+// 317.  Half as many warps: 46, 17, 296 and 330 us.
+constexpr int64_t kMostWarps = 32768;
+constexpr int64_t kMostWarpsOfOne = 256;
 
 // set once per device; any thread may race to set it, the attribute is idempotent
 std::atomic<bool> g_attr_set[64] = {};
@@ -874,7 +876,8 @@ extern "C" bi_status bi_decode_attention_kv4(const void* q, const void* k_cache,
                        cudaSuccess
                    ? BI_OK
                    : BI_ERR_CUDA;
-    const int64_t most = std::max<int64_t>(1, kMostWarps / (static_cast<int64_t>(Hkv) * B));
+    const int64_t most = std::min(
+        kMostWarpsOfOne, std::max<int64_t>(1, kMostWarps / (static_cast<int64_t>(Hkv) * B)));
     const cudaError_t e =
         max_chunks <= most
             ? bi::launch_pdl(attn_warp_kv4_kernel<false>, grid, dim3(32), 0, stream, ka)
