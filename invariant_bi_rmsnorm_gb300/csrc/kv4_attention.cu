@@ -15,11 +15,11 @@
 //
 // The bytes of a chunk are little over a quarter of a bf16 chunk's but its
 // arithmetic is the same, and the codes have to be turned into numbers besides:
-// about 340 instructions a page and kv-head, 24 of them mma.sync, each of which
+// about 350 instructions a page and kv-head, 24 of them mma.sync, each of which
 // keeps a scheduler busy for 8 cycles (measured: 2.04 cycles per SM).  That is
 // about 130 cycles an SM where HBM would deliver the page in 98, so what bounds
 // both kernels below is the instructions they issue.  On GB300, cold, GQA 32/8,
-// lengths even over 1 .. 8192: B = 256 289 us (1.21 GB, 4.2 TB/s, 0.62 of the
+// lengths even over 1 .. 8192: B = 256 292 us (1.21 GB, 4.2 TB/s, 0.61 of the
 // copy rate; the bf16 cache's 4.3 GB take 599 us), B = 64 83 us.
 //
 // Few chunks: one CTA (4 warps) per (sequence, kv-head, chunk), which finishes
@@ -476,11 +476,12 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
 // chunk), so that nothing ever waits for another warp and a finished chunk's
 // place on the SM is taken at once.  Pages come through a ring of kRing
 // stages; while a page's weights and output products are under way the next
-// page's scores are formed (they depend on nothing before them).  366
+// page's scores are formed (they depend on nothing before them).  351
 // instructions a page in all, the chunk's share included; 16 warps per SM (20
-// with fewer registers were no faster).  B = 256 up to 8192 tokens went from 341
-// to 312 us with per-lane copies in the place of bulk copies (see below) and
-// from 524 us with the four-warp CTA of the bf16 kernel.
+// with fewer registers were no faster).  B = 256 up to 8192 tokens took 524 us
+// in the four-warp CTA of the bf16 kernel, 341 in this form with bulk copies,
+// 308 with per-lane copies in their place (see below), 289 with the fold in a
+// launch of its own.
 
 constexpr int kRing = 4;  // pages in flight
 constexpr int kStageBytes = 2 * kBlockBytes;
