@@ -54,7 +54,6 @@ namespace {
 using bi_attn::ceil_div;
 using bi_attn::kChunk;
 using bi_attn::kD;
-using bi_attn::kFoldFloats;
 using bi_attn::kMaxGroup;
 using bi_attn::kPage;
 using bi_attn::kPagesPerChunk;
@@ -69,10 +68,9 @@ using bi_kv4::ScalePair;
 constexpr int kPagesPerWarp = kPagesPerChunk / kWarps;
 constexpr int kMatBytes = kPagesPerChunk * kBlockBytes;  // the chunk's K (or V) blocks
 constexpr int kStagingBytes = 2 * kMatBytes;
-constexpr int kSmemBytes = kStagingBytes + kFoldFloats * 4;
 static_assert(kPagesPerChunk * 32 * 16 <= kMatBytes, "the weights fit over the K blocks");
 
-// Tables of the chunk in the shared memory that the fold uses afterwards.
+// Tables of the chunk, in shared memory.
 struct Tables {
     float pmax[kPagesPerChunk][kMaxGroup];   // a page's largest score (log2 units)
     float ref[kPagesPerChunk][kMaxGroup];    // what the page's scores are taken relative to
@@ -81,9 +79,10 @@ struct Tables {
     float m[kMaxGroup], l[kMaxGroup];        // the chunk's reference and weight sum
     uint32_t moved;                          // pages with an alpha other than 1; kRefPerPage
 };
+constexpr uint32_t kAll = 0xffffffffu;
 constexpr uint32_t kRefPerPage = 1u << 31;  // else ref[0] is every page's and alpha is not set
 static_assert(kPagesPerChunk < 31, "a bit per page");
-static_assert(sizeof(Tables) <= kFoldFloats * 4, "the tables fit where the fold works");
+constexpr int kSmemBytes = kStagingBytes + sizeof(Tables);
 
 struct Kv4Args {
     SplitArgs s;
@@ -240,6 +239,177 @@ __device__ __forceinline__ float reduce_columns(float v0, float v1, int lane, F 
     return f(v, __shfl_xor_sync(0xffffffffu, v, 16));
 }
 
+// A chunk's partial as the warp kernel writes and reads it: O's dims of a row
+// in the order of the accumulators, position 16mt + 2g + i for dim 16mt + g +
+// 8i.
+__device__ __forceinline__ float* partial_o(const SplitArgs& a, int64_t row, int c) {
+    return a.ws_acc + (row * a.max_chunks + c) * kD;
+}
+
+__device__ __forceinline__ float2* partial_ml(const SplitArgs& a, int64_t row, int c) {
+    return reinterpret_cast<float2*>(a.ws_ml) + row * a.max_chunks + c;
+}
+
+// (m, l) of a chunk with a page index out of range: no weight sum is negative.
+constexpr float kNoChunk = -1.f;
+
+// The fold of the warp kernel's partials, a warp per (sequence, query head), in
+// ascending chunk order with bi_attn::attn_merge_kernel's operations.  Lane l
+// has positions 4l .. 4l + 3 of the row.  As in bi_attn::fold_sequence the
+// running maxima are a prefix maximum, taken for 32 chunks at once (lane =
+// chunk), and all factors with them; the partials of kAhead chunks are on their
+// way together.
+//
+// A launch of its own, because the rows are folded side by side here: the warp
+// that arrives last at its (sequence, kv-head) could fold its rows as well, but does
+// it alone while the SMs run dry (32 sequences of 8192 tokens 81 against 72 us,
+// B = 64 up to 8192 92.6 against 83.1, B = 256 308 against 289).  Sixteen
+// partials on their way instead of eight: 78, 89, 296 us.
+constexpr int kMergeWarps = 4;
+
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    merge_rows_kv4_kernel(const SplitArgs a, int64_t rows) {
+    bi::launch_dependents();
+    bi::grid_dependency_wait();  // the partials are there
+    constexpr int kAhead = 8;
+    __shared__ float4 all_factors[kMergeWarps][32];
+    float4* const factors = all_factors[threadIdx.x / 32];
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + threadIdx.x / 32;
+    if (row >= rows) return;
+    const int L = a.seq_lens[row / a.Hq];
+    if (L <= kChunk || L > a.max_seq_len) return;  // written, or reported, by the attention kernel
+    const int nch = (L + kChunk - 1) / kChunk;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f, m = 0.f;
+    for (int cb = 0; cb < nch; cb += 32) {
+        const int nb = min(32, nch - cb);
+        float4 part[kAhead];
+        auto load = [&](int i0) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (i0 + u < nb)
+                    part[u] = __ldcg(reinterpret_cast<const float4*>(partial_o(a, row, cb + i0 + u)) + lane);
+        };
+        const float2 ml = lane < nb ? __ldcg(partial_ml(a, row, cb + lane)) : make_float2(-INFINITY, 0.f);
+        load(0);
+        if (__any_sync(kAll, ml.y == kNoChunk)) return;  // the output stays as it was
+        float v = ml.x;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float u = __shfl_up_sync(kAll, v, off);
+            if (lane >= off) v = fmaxf(v, u);
+        }
+        if (cb > 0) v = fmaxf(m, v);  // running maximum after chunk cb + lane
+        float before = __shfl_up_sync(kAll, v, 1);
+        if (lane == 0) before = cb > 0 ? m : 0.f;
+        m = __shfl_sync(kAll, v, 31);
+        __syncwarp();  // every lane is done with the last factors
+        if (lane < nb)
+            factors[lane] = make_float4(bi_attn::exp2_ftz(before - v), bi_attn::exp2_ftz(ml.x - v), ml.y, 0.f);
+        __syncwarp();
+        for (int i0 = 0; i0 < nb; i0 += kAhead) {
+            if (i0 > 0) load(i0);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (i0 + u >= nb) break;
+                const float4 f = factors[i0 + u];
+                if (cb + i0 + u == 0) {
+                    o = part[u];
+                    l = f.z;
+                } else {
+                    o.x = bi_attn::fold_value(o.x, f.x, part[u].x, f.y);
+                    o.y = bi_attn::fold_value(o.y, f.x, part[u].y, f.y);
+                    o.z = bi_attn::fold_value(o.z, f.x, part[u].z, f.y);
+                    o.w = bi_attn::fold_value(o.w, f.x, part[u].w, f.y);
+                    l = bi_attn::fold_value(l, f.x, f.z, f.y);
+                }
+            }
+        }
+    }
+    // positions 4l .. 4l + 3: dims d, d + 8, d + 1, d + 9
+    const int d = 16 * (lane >> 2) + 2 * (lane & 3);
+    const float il = bi_attn::inv_weight(l);
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * kD + d);
+    out[0] = bi::pack_bf16x2(bi_attn::normalise(o.x, il), bi_attn::normalise(o.z, il));
+    out[4] = bi::pack_bf16x2(bi_attn::normalise(o.y, il), bi_attn::normalise(o.w, il));
+}
+
+// The same fold for few rows: a CTA per row, thread p has position p, and 32
+// chunks' partials are loaded while the 32 before them are folded, the first
+// before the length is known.  One sequence of 300 tokens (the whole call) 6.9
+// against 7.2 us, of 8192 11.3 against 11.6, of 32768 20.0 against 22.5; from
+// 512 rows on it is no faster (B = 24 up to 2048 17.2 against 17.0 us, B = 64 up
+// to 8192 86.4 against 83).
+constexpr int64_t kFewRows = 512;
+
+__global__ void __launch_bounds__(kD) merge_row_kv4_kernel(const SplitArgs a) {
+    bi::launch_dependents();
+    bi::grid_dependency_wait();  // the partials are there
+    __shared__ float4 all_factors[kD / 32][32];
+    const int lane = threadIdx.x & 31;
+    float4* const factors = all_factors[threadIdx.x / 32];
+    const int64_t row = blockIdx.x;
+    const float* const parts = partial_o(a, row, 0) + threadIdx.x;
+    const float2* const mls = partial_ml(a, row, 0);
+    float next[32];
+    float2 next_ml;
+    auto load = [&](int c0, int end) {
+#pragma unroll
+        for (int u = 0; u < 32; ++u)
+            if (c0 + u < end) next[u] = __ldcg(parts + (c0 + u) * kD);
+    };
+    auto load_ml = [&](int c0, int end) {
+        next_ml = c0 + lane < end ? __ldcg(mls + c0 + lane) : make_float2(-INFINITY, 0.f);
+    };
+    // before the length is known: the rows' memory is there, whatever it holds
+    load_ml(0, a.max_chunks);
+    load(0, a.max_chunks);
+    const int L = a.seq_lens[row / a.Hq];
+    if (L <= kChunk || L > a.max_seq_len) return;  // written, or reported, by the attention kernel
+    const int nch = (L + kChunk - 1) / kChunk;
+    float o = 0.f, l = 0.f, m = 0.f;
+    for (int cb = 0; cb < nch; cb += 32) {
+        const int nb = min(32, nch - cb);
+        const float2 ml = lane < nb ? next_ml : make_float2(-INFINITY, 0.f);
+        if (__any_sync(kAll, ml.y == kNoChunk)) return;  // the output stays as it was
+        load_ml(cb + 32, nch);
+        float v = ml.x;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float u = __shfl_up_sync(kAll, v, off);
+            if (lane >= off) v = fmaxf(v, u);
+        }
+        if (cb > 0) v = fmaxf(m, v);  // running maximum after chunk cb + lane
+        float before = __shfl_up_sync(kAll, v, 1);
+        if (lane == 0) before = cb > 0 ? m : 0.f;
+        m = __shfl_sync(kAll, v, 31);
+        __syncwarp();  // every lane is done with the last factors
+        if (lane < nb)
+            factors[lane] = make_float4(bi_attn::exp2_ftz(before - v), bi_attn::exp2_ftz(ml.x - v), ml.y, 0.f);
+        __syncwarp();
+        float part[32];
+#pragma unroll
+        for (int u = 0; u < 32; ++u) part[u] = next[u];
+        load(cb + 32, nch);
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+            if (u >= nb) break;
+            const float4 f = factors[u];
+            if (cb + u == 0) {
+                o = part[u];
+                l = f.z;
+            } else {
+                o = bi_attn::fold_value(o, f.x, part[u], f.y);
+                l = bi_attn::fold_value(l, f.x, f.z, f.y);
+            }
+        }
+    }
+    // position 16mt + 2g + i: dim 16mt + g + 8i
+    const int d = (threadIdx.x & ~15) + ((threadIdx.x & 15) >> 1) + 8 * (threadIdx.x & 1);
+    a.out[row * kD + d] = __float2bfloat16_rn(bi_attn::normalise(o, bi_attn::inv_weight(l)));
+}
+
 __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Args ka) {
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
@@ -260,15 +430,13 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
     if (c >= nch) return;
     const int tokens = min(kChunk, L - c * kChunk);
     const int np = (tokens + kPage - 1) / kPage;
-    // several CTAs share a longer sequence and the last one to arrive folds it
-    uint32_t* const ctr = nch > 1 ? a.counters + static_cast<int64_t>(s) * a.Hkv + g : nullptr;
+    const int64_t row0 = static_cast<int64_t>(s) * a.Hq + g * a.group;
 
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t* const ks = smem;
     uint8_t* const vs = smem + kMatBytes;
     uint4* const weights = reinterpret_cast<uint4*>(ks);  // [page][lane], from phase 3 on
-    float* const small = reinterpret_cast<float*>(smem + kStagingBytes);
-    Tables& tb = *reinterpret_cast<Tables*>(small);
+    Tables& tb = *reinterpret_cast<Tables*>(smem + kStagingBytes);
     __shared__ uint64_t bars[2];  // K landed, V landed
     __shared__ int bad_page;
 
@@ -299,16 +467,12 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
     uint32_t qb0[8], qb1[8];
     {
         const int n = lane >> 2;
-        bi_attn::load_q_frags(
-            n < a.group ? a.q + (static_cast<int64_t>(s) * a.Hq + g * a.group + n) * kD : nullptr,
-            lane, qb0, qb1);
+        bi_attn::load_q_frags(n < a.group ? a.q + (row0 + n) * kD : nullptr, lane, qb0, qb1);
     }
     __syncthreads();  // barriers and bad_page are set
     if (bad_page) {
-        if (tid == 0) {
-            bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
-            if (nch > 1) bi_attn::arrive_bad(ctr, nch);
-        }
+        if (tid == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
+        if (nch > 1 && tid < a.group) *partial_ml(a, row0 + tid, c) = make_float2(-INFINITY, kNoChunk);
         return;
     }
 
@@ -333,8 +497,8 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
             // the copies still write to this CTA's shared memory: one more bounded wait each
             bi::mbar_wait_for(&bars[0], 0, bi::kDrainNs);
             bi::mbar_wait_for(&bars[1], 0, bi::kDrainNs);
-            if (nch > 1) bi_attn::arrive_bad(ctr, nch);
         }
+        if (nch > 1 && tid < a.group) *partial_ml(a, row0 + tid, c) = make_float2(-INFINITY, kNoChunk);
         return;
     }
 
@@ -445,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
     for (int e = 0; e < 2; ++e) {
         const int h = h0 + e;
         if (h >= a.group) continue;
-        const int64_t row = static_cast<int64_t>(s) * a.Hq + g * a.group + h;
+        const int64_t row = row0 + h;
         if (nch == 1) {  // the whole sequence: bf16(O / l)
             const float il = bi_attn::inv_weight(tb.l[h]);
             __nv_bfloat16* o = a.out + row * kD + d0;
@@ -455,20 +619,12 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
                 o[16 * i + 8] = __float2bfloat16_rn(bi_attn::normalise(acc[i][2 + e], il));
             }
         } else {  // the chunk's partial
-            float* o = a.ws_acc + (row * a.max_chunks + c) * kD + d0;
+            float2* o = reinterpret_cast<float2*>(partial_o(a, row, c)) + 16 * warp + (lane >> 2);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                o[16 * i] = acc[i][e];
-                o[16 * i + 8] = acc[i][2 + e];
-            }
-            if (warp == 0 && lane < 4)
-                *reinterpret_cast<float2*>(a.ws_ml + (row * a.max_chunks + c) * 2) =
-                    make_float2(tb.m[h], tb.l[h]);
+            for (int i = 0; i < 2; ++i) o[8 * i] = make_float2(acc[i][e], acc[i][2 + e]);
+            if (warp == 0 && lane < 4) *partial_ml(a, row, c) = make_float2(tb.m[h], tb.l[h]);
         }
     }
-    if (nch == 1) return;
-    // the last CTA of this (sequence, kv-head) to arrive folds it
-    bi_attn::arrive_and_fold<kStagingBytes>(a, ctr, nch, s, g, nch, smem, small, tid);
 }
 
 // ---------------------------------------------------------------------------
@@ -485,7 +641,6 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
 
 constexpr int kRing = 4;  // pages in flight
 constexpr int kStageBytes = 2 * kBlockBytes;
-constexpr uint32_t kAll = 0xffffffffu;
 
 // bi_attn::ColState of two columns, as the fast path of weights_step wants it.
 struct WarpState {
@@ -537,102 +692,6 @@ __device__ __forceinline__ void weights_step(WarpState& st, const float (&x)[4],
     st.l = __fmaf_rn(st.l, al,
                      reduce_columns(__fadd_rn(p[0], p[2]), __fadd_rn(p[1], p[3]), lane,
                                     [](float u, float v) { return __fadd_rn(u, v); }));
-}
-
-// A chunk's partial as the warp kernel writes and reads it: O's dims of a row
-// in the order of the accumulators, position 16mt + 2g + i for dim 16mt + g +
-// 8i.
-__device__ __forceinline__ float* partial_o(const SplitArgs& a, int64_t row, int c) {
-    return a.ws_acc + (row * a.max_chunks + c) * kD;
-}
-
-__device__ __forceinline__ float2* partial_ml(const SplitArgs& a, int64_t row, int c) {
-    return reinterpret_cast<float2*>(a.ws_ml) + row * a.max_chunks + c;
-}
-
-// (m, l) of a chunk with a page index out of range: no weight sum is negative.
-constexpr float kNoChunk = -1.f;
-
-// The fold of the warp kernel's partials, a warp per (sequence, query head), in
-// ascending chunk order with bi_attn::attn_merge_kernel's operations.  Lane l
-// has positions 4l .. 4l + 3 of the row.  As in bi_attn::fold_sequence the
-// running maxima are a prefix maximum, taken for 32 chunks at once (lane =
-// chunk), and all factors with them; the partials of kAhead chunks are on their
-// way together.
-//
-// A launch of its own, because the rows are folded side by side here: the warp
-// that arrives last at its (sequence, kv-head) could fold its rows as well, but does
-// it alone while the SMs run dry (32 sequences of 8192 tokens 81 against 72 us,
-// B = 64 up to 8192 92.6 against 83.1, B = 256 308 against 289).  Sixteen
-// partials on their way instead of eight: 78, 89, 296 us.
-constexpr int kMergeWarps = 4;
-
-__global__ void __launch_bounds__(32 * kMergeWarps)
-    merge_rows_kv4_kernel(const SplitArgs a, int64_t rows) {
-    bi::launch_dependents();
-    bi::grid_dependency_wait();  // the partials are there
-    constexpr int kAhead = 8;
-    __shared__ float4 all_factors[kMergeWarps][32];
-    float4* const factors = all_factors[threadIdx.x / 32];
-    const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + threadIdx.x / 32;
-    if (row >= rows) return;
-    const int L = a.seq_lens[row / a.Hq];
-    if (L <= kChunk || L > a.max_seq_len) return;  // written, or reported, by the warp kernel
-    const int nch = (L + kChunk - 1) / kChunk;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f, m = 0.f;
-    for (int cb = 0; cb < nch; cb += 32) {
-        const int nb = min(32, nch - cb);
-        float4 part[kAhead];
-        auto load = [&](int i0) {
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                if (i0 + u < nb)
-                    part[u] = __ldcg(reinterpret_cast<const float4*>(partial_o(a, row, cb + i0 + u)) + lane);
-        };
-        const float2 ml = lane < nb ? __ldcg(partial_ml(a, row, cb + lane)) : make_float2(-INFINITY, 0.f);
-        load(0);
-        if (__any_sync(kAll, ml.y == kNoChunk)) return;  // the output stays as it was
-        float v = ml.x;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const float u = __shfl_up_sync(kAll, v, off);
-            if (lane >= off) v = fmaxf(v, u);
-        }
-        if (cb > 0) v = fmaxf(m, v);  // running maximum after chunk cb + lane
-        float before = __shfl_up_sync(kAll, v, 1);
-        if (lane == 0) before = cb > 0 ? m : 0.f;
-        m = __shfl_sync(kAll, v, 31);
-        __syncwarp();  // every lane is done with the last factors
-        if (lane < nb)
-            factors[lane] = make_float4(bi_attn::exp2_ftz(before - v), bi_attn::exp2_ftz(ml.x - v), ml.y, 0.f);
-        __syncwarp();
-        for (int i0 = 0; i0 < nb; i0 += kAhead) {
-            if (i0 > 0) load(i0);
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                if (i0 + u >= nb) break;
-                const float4 f = factors[i0 + u];
-                if (cb + i0 + u == 0) {
-                    o = part[u];
-                    l = f.z;
-                } else {
-                    o.x = bi_attn::fold_value(o.x, f.x, part[u].x, f.y);
-                    o.y = bi_attn::fold_value(o.y, f.x, part[u].y, f.y);
-                    o.z = bi_attn::fold_value(o.z, f.x, part[u].z, f.y);
-                    o.w = bi_attn::fold_value(o.w, f.x, part[u].w, f.y);
-                    l = bi_attn::fold_value(l, f.x, f.z, f.y);
-                }
-            }
-        }
-    }
-    // positions 4l .. 4l + 3: dims d, d + 8, d + 1, d + 9
-    const int d = 16 * (lane >> 2) + 2 * (lane & 3);
-    const float il = bi_attn::inv_weight(l);
-    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * kD + d);
-    out[0] = bi::pack_bf16x2(bi_attn::normalise(o.x, il), bi_attn::normalise(o.z, il));
-    out[4] = bi::pack_bf16x2(bi_attn::normalise(o.y, il), bi_attn::normalise(o.w, il));
 }
 
 // kLoop: a warp takes chunks gridDim.x apart, else its one.
@@ -790,7 +849,7 @@ __global__ void __launch_bounds__(32, 14) attn_warp_kv4_kernel(const Kv4Args ka)
 // finish a chunk several times sooner; the warp kernel issues a third fewer
 // instructions and has no barriers.  Below the rule there are far fewer chunks
 // than arrival counters, and than an arrival counter can count.
-constexpr int64_t kManyChunks = 22;
+constexpr int64_t kManyChunks = 28;
 
 // Warps of a launch and of a (sequence, kv-head), about; where the bound on the
 // lengths asks for more, a warp takes several chunks.  A warp without a chunk
@@ -872,23 +931,21 @@ extern "C" bi_status bi_decode_attention_kv4(const void* q, const void* k_cache,
     args.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     args.chunks_per_cta = 1;
     const dim3 grid(max_chunks, Hkv, B);
-    if (static_cast<int64_t>(max_chunks) * Hkv * B < kManyChunks * static_cast<int64_t>(bi::sm_count()))
-        return bi::launch_pdl(attn_chunk_kv4_kernel, grid, dim3(kThreads), kSmemBytes, stream, ka) ==
-                       cudaSuccess
-                   ? BI_OK
-                   : BI_ERR_CUDA;
     const int64_t most = std::min(
         kMostWarpsOfOne, std::max<int64_t>(1, kMostWarps / (static_cast<int64_t>(Hkv) * B)));
     const cudaError_t e =
-        max_chunks <= most
+        static_cast<int64_t>(max_chunks) * Hkv * B < kManyChunks * static_cast<int64_t>(bi::sm_count())
+            ? bi::launch_pdl(attn_chunk_kv4_kernel, grid, dim3(kThreads), kSmemBytes, stream, ka)
+        : max_chunks <= most
             ? bi::launch_pdl(attn_warp_kv4_kernel<false>, grid, dim3(32), 0, stream, ka)
             : bi::launch_pdl(attn_warp_kv4_kernel<true>, dim3(static_cast<unsigned>(most), Hkv, B), dim3(32),
                              0, stream, ka);
     if (e != cudaSuccess) return BI_ERR_CUDA;
     if (max_chunks == 1) return BI_OK;
     const int64_t rows = static_cast<int64_t>(B) * Hq;
-    return bi::launch_pdl(merge_rows_kv4_kernel, dim3(ceil_div(rows, kMergeWarps)),
-                          dim3(32 * kMergeWarps), 0, stream, args, rows) == cudaSuccess
-               ? BI_OK
-               : BI_ERR_CUDA;
+    const cudaError_t f =
+        rows < kFewRows ? bi::launch_pdl(merge_row_kv4_kernel, dim3(static_cast<unsigned>(rows)), dim3(kD), 0, stream, args)
+                        : bi::launch_pdl(merge_rows_kv4_kernel, dim3(ceil_div(rows, kMergeWarps)),
+                                         dim3(32 * kMergeWarps), 0, stream, args, rows);
+    return f == cudaSuccess ? BI_OK : BI_ERR_CUDA;
 }
