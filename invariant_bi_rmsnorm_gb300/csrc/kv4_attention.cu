@@ -25,9 +25,8 @@
 // Few chunks: one CTA (4 warps) per (sequence, kv-head, chunk), which finishes
 // a chunk soonest (one sequence of 8192 tokens 11.4 us, of 300 7.5 us).  The
 // chunk's work is dealt out so that none is done twice:
-//   0  warp 0 copies the chunk's up to 16 pages into shared memory, two bulk
-//      copies (K, V) a lane;
-//   1  scores: warp w takes pages w, w + 4, ..., and their maxima;
+//   0  warp w copies pages w, w + 4, ... into shared memory, asynchronously;
+//   1  scores: warp w takes its own pages, and their maxima;
 //   2  the pages' reference maxima, one after the other (8 columns, one lane
 //      each; a few instructions a page);
 //   3  weights: warp w, its own pages; the split weights go to shared memory in
@@ -89,16 +88,6 @@ struct Kv4Args {
     const uint8_t* k_cache;
     const uint8_t* v_cache;
 };
-
-// `bytes` (a multiple of 16) global -> shared by the bulk-copy engine; both
-// addresses 16-byte aligned; completion counted on `bar`.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            bi::smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(bi::smem_u32(bar))
-        : "memory");
-}
 
 // The low (high) half twice, as moves: the compiler takes them into the operand
 // of the bf16 arithmetic, which it does not with a byte permutation.
@@ -437,31 +426,35 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
     uint8_t* const vs = smem + kMatBytes;
     uint4* const weights = reinterpret_cast<uint4*>(ks);  // [page][lane], from phase 3 on
     Tables& tb = *reinterpret_cast<Tables*>(smem + kStagingBytes);
-    __shared__ uint64_t bars[2];  // K landed, V landed
-    __shared__ int bad_page;
 
-    // ---- 0: copies ----
-    if (warp == 0) {
+    // ---- 0: copies ---- (every warp reads the chunk's pages and copies its own)
+    {
         int pg = 0;
         if (lane < np)
             pg = a.block_table[static_cast<int64_t>(s) * a.max_pages_per_seq + c * kPagesPerChunk + lane];
-        const bool bad = __any_sync(0xffffffffu, pg < 0 || pg >= a.num_pages);
-        if (lane == 0) {
-            bad_page = bad;
-            bi::mbar_init(&bars[0], 1);
-            bi::mbar_init(&bars[1], 1);
-            bi::fence_mbar_init();
-            if (!bad) {
-                bi::mbar_arrive_expect_tx(&bars[0], np * kBlockBytes);
-                bi::mbar_arrive_expect_tx(&bars[1], np * kBlockBytes);
+        if (__any_sync(kAll, pg < 0 || pg >= a.num_pages)) {
+            if (tid == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
+            if (nch > 1 && tid < a.group) *partial_ml(a, row0 + tid, c) = make_float2(-INFINITY, kNoChunk);
+            return;
+        }
+        const int64_t at = (static_cast<int64_t>(pg) * a.Hkv + g) * kBlockBytes;
+        int64_t from[kPagesPerWarp];
+#pragma unroll
+        for (int i = 0; i < kPagesPerWarp; ++i) from[i] = __shfl_sync(kAll, at, warp + kWarps * i) + 16 * lane;
+        auto copy = [&](uint8_t* to, const uint8_t* cache) {
+#pragma unroll
+            for (int i = 0; i < kPagesPerWarp; ++i) {
+                const int p = warp + kWarps * i;
+                if (p >= np) break;
+                uint8_t* dst = to + p * kBlockBytes + 16 * lane;
+                bi::cp_async_16(dst, cache + from[i]);
+                bi::cp_async_16(dst + 512, cache + from[i] + 512);
+                if (lane < kBlockBytes / 16 - 64) bi::cp_async_16(dst + 1024, cache + from[i] + 1024);
             }
-        }
-        __syncwarp();
-        if (!bad && lane < np) {
-            const int64_t at = (static_cast<int64_t>(pg) * a.Hkv + g) * kBlockBytes;
-            bulk_load(ks + lane * kBlockBytes, ka.k_cache + at, kBlockBytes, &bars[0]);
-            bulk_load(vs + lane * kBlockBytes, ka.v_cache + at, kBlockBytes, &bars[1]);
-        }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        copy(ks, ka.k_cache);
+        copy(vs, ka.v_cache);
     }
     // column n of the mma tile = query head g*group + n (n < group)
     uint32_t qb0[8], qb1[8];
@@ -469,38 +462,22 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
         const int n = lane >> 2;
         bi_attn::load_q_frags(n < a.group ? a.q + (row0 + n) * kD : nullptr, lane, qb0, qb1);
     }
-    __syncthreads();  // barriers and bad_page are set
-    if (bad_page) {
-        if (tid == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
-        if (nch > 1 && tid < a.group) *partial_ml(a, row0 + tid, c) = make_float2(-INFINITY, kNoChunk);
-        return;
-    }
 
     // ---- 1: scores of this warp's pages, in log2 units, and their maxima ----
-    const bool k_here = bi::mbar_wait(&bars[0], 0);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();  // K, every lane's copies
     float x[kPagesPerWarp][4];
-    if (k_here) {
 #pragma unroll
-        for (int i = 0; i < kPagesPerWarp; ++i) {
-            const int p = warp + kWarps * i;
-            if (p >= np) break;
-            page_logs(x[i], ks + p * kBlockBytes, qb0, qb1, tokens - p * kPage, a.scale_log2, lane);
-            const float mx = reduce_columns(fmaxf(x[i][0], x[i][2]), fmaxf(x[i][1], x[i][3]), lane,
-                                            [](float u, float v) { return fmaxf(u, v); });
-            if (lane < 8) tb.pmax[p][2 * (lane & 3) + (lane >> 2)] = mx;
-        }
+    for (int i = 0; i < kPagesPerWarp; ++i) {
+        const int p = warp + kWarps * i;
+        if (p >= np) break;
+        page_logs(x[i], ks + p * kBlockBytes, qb0, qb1, tokens - p * kPage, a.scale_log2, lane);
+        const float mx = reduce_columns(fmaxf(x[i][0], x[i][2]), fmaxf(x[i][1], x[i][3]), lane,
+                                        [](float u, float v) { return fmaxf(u, v); });
+        if (lane < 8) tb.pmax[p][2 * (lane & 3) + (lane >> 2)] = mx;
     }
-    const bool v_here = bi::mbar_wait(&bars[1], 0);
-    if (__syncthreads_or(!k_here || !v_here)) {
-        if (tid == 0) {
-            bi::report_error(a.err, bi::kErrTimeout | bi::kWhereAttnSplit);
-            // the copies still write to this CTA's shared memory: one more bounded wait each
-            bi::mbar_wait_for(&bars[0], 0, bi::kDrainNs);
-            bi::mbar_wait_for(&bars[1], 0, bi::kDrainNs);
-        }
-        if (nch > 1 && tid < a.group) *partial_ml(a, row0 + tid, c) = make_float2(-INFINITY, kNoChunk);
-        return;
-    }
+    bi::cp_async_wait_all();
+    __syncthreads();  // the maxima, and V
 
     // ---- 2: the online softmax's reference maxima (bi_attn::softmax_step) ----
     if (warp == 0) {
