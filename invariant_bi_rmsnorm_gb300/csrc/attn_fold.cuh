@@ -311,11 +311,9 @@ __device__ __forceinline__ void arrive_bad(uint32_t* ctr, uint32_t ngroups) {
 }
 
 // Count this CTA in on its (sequence, kv-head)'s counter once its partials
-// are stored; the last of `ngroups` CTAs to arrive folds the sequence.
-template <int kStagingBytes>
-__device__ __forceinline__ void arrive_and_fold(const SplitArgs& a, uint32_t* ctr, uint32_t ngroups,
-                                                int s, int g, int nch, uint8_t* stage, float* small,
-                                                int tid) {
+// are stored.  True in the last of `ngroups` CTAs to arrive, if none found a bad
+// page: it folds the sequence.
+__device__ __forceinline__ bool arrive_last(const SplitArgs& a, uint32_t* ctr, uint32_t ngroups, int tid) {
     __shared__ int fold_here;
     __syncthreads();  // every warp's partial stores precede the arrival
     if (tid == 0) {
@@ -330,8 +328,14 @@ __device__ __forceinline__ void arrive_and_fold(const SplitArgs& a, uint32_t* ct
         fold_here = last && (now >> 16) == 0;
     }
     __syncthreads();
-    if (!fold_here) return;
-    fold_group<kStagingBytes>(a, s, g, nch, stage, small, tid);
+    return fold_here;
+}
+
+template <int kStagingBytes>
+__device__ __forceinline__ void arrive_and_fold(const SplitArgs& a, uint32_t* ctr, uint32_t ngroups,
+                                                int s, int g, int nch, uint8_t* stage, float* small,
+                                                int tid) {
+    if (arrive_last(a, ctr, ngroups, tid)) fold_group<kStagingBytes>(a, s, g, nch, stage, small, tid);
 }
 
 // Fold the chunk partials of one (sequence, query head) in ascending chunk

@@ -23,7 +23,7 @@
 // copy rate; the bf16 cache's 4.3 GB take 599 us), B = 64 83 us.
 //
 // Few chunks: one CTA (4 warps) per (sequence, kv-head, chunk), which finishes
-// a chunk soonest (one sequence of 8192 tokens 11.4 us, of 300 7.5 us).  The
+// a chunk soonest (one sequence of 8192 tokens 11.1 us, of 300 6.7 us).  The
 // chunk's work is dealt out so that none is done twice:
 //   0  warp w copies pages w, w + 4, ... into shared memory, asynchronously;
 //   1  scores: warp w takes its own pages, and their maxima;
@@ -32,7 +32,7 @@
 //   3  weights: warp w, its own pages; the split weights go to shared memory in
 //      the order of mma.sync's B operand, over the K blocks, which are done with;
 //   4  output: warp w takes dims 32w .. 32w + 31 (one group) over all pages.
-// Five CTAs share an SM (41 KB each); four were 12 % slower, seven (V copied
+// Five CTAs share an SM (39 KB each); four were 12 % slower, seven (V copied
 // over K once the scores are there) 3 % faster in the middle and 28 % slower
 // for one sequence.  Many chunks: one warp per chunk, see below.
 #include <cuda_bf16.h>
@@ -81,7 +81,8 @@ struct Tables {
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr uint32_t kRefPerPage = 1u << 31;  // else ref[0] is every page's and alpha is not set
 static_assert(kPagesPerChunk < 31, "a bit per page");
-constexpr int kSmemBytes = kStagingBytes + sizeof(Tables);
+constexpr int kFactorBytes = kWarps * 32 * sizeof(float4);  // fold_row's, where the tables were
+constexpr int kSmemBytes = kStagingBytes + (sizeof(Tables) > kFactorBytes ? sizeof(Tables) : kFactorBytes);
 
 struct Kv4Args {
     SplitArgs s;
@@ -239,6 +240,16 @@ __device__ __forceinline__ float2* partial_ml(const SplitArgs& a, int64_t row, i
     return reinterpret_cast<float2*>(a.ws_ml) + row * a.max_chunks + c;
 }
 
+// bf16(O / l) of a folded row, lane l with positions 4l .. 4l + 3: dims d, d + 8,
+// d + 1, d + 9.
+__device__ __forceinline__ void store_row(const SplitArgs& a, int64_t row, const float4& o, float l, int lane) {
+    const int d = 16 * (lane >> 2) + 2 * (lane & 3);
+    const float il = bi_attn::inv_weight(l);
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * kD + d);
+    out[0] = bi::pack_bf16x2(bi_attn::normalise(o.x, il), bi_attn::normalise(o.z, il));
+    out[4] = bi::pack_bf16x2(bi_attn::normalise(o.y, il), bi_attn::normalise(o.w, il));
+}
+
 // (m, l) of a chunk with a page index out of range: no weight sum is negative.
 constexpr float kNoChunk = -1.f;
 
@@ -249,7 +260,7 @@ constexpr float kNoChunk = -1.f;
 // chunk), and all factors with them; the partials of kAhead chunks are on their
 // way together.
 //
-// A launch of its own, because the rows are folded side by side here: the warp
+// A launch of its own, where the rows are folded side by side: the warp
 // that arrives last at its (sequence, kv-head) could fold its rows as well, but does
 // it alone while the SMs run dry (32 sequences of 8192 tokens 81 against 72 us,
 // B = 64 up to 8192 92.6 against 83.1, B = 256 308 against 289).  Sixteen
@@ -316,20 +327,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
             }
         }
     }
-    // positions 4l .. 4l + 3: dims d, d + 8, d + 1, d + 9
-    const int d = 16 * (lane >> 2) + 2 * (lane & 3);
-    const float il = bi_attn::inv_weight(l);
-    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * kD + d);
-    out[0] = bi::pack_bf16x2(bi_attn::normalise(o.x, il), bi_attn::normalise(o.z, il));
-    out[4] = bi::pack_bf16x2(bi_attn::normalise(o.y, il), bi_attn::normalise(o.w, il));
+    store_row(a, row, o, l, lane);
 }
 
 // The same fold for few rows: a CTA per row, thread p has position p, and 32
 // chunks' partials are loaded while the 32 before them are folded, the first
-// before the length is known.  One sequence of 300 tokens (the whole call) 6.9
-// against 7.2 us, of 8192 11.3 against 11.6, of 32768 20.0 against 22.5; from
-// 512 rows on it is no faster (B = 24 up to 2048 17.2 against 17.0 us, B = 64 up
-// to 8192 86.4 against 83).
+// before the length is known.  One sequence of 32768 tokens (the whole call) 20.0
+// against 22.5 us, of 8192 11.3 against 11.6; from 512 rows on it is no faster (B
+// = 24 up to 2048 17.2 against 17.0 us, B = 64 up to 8192 86.4 against 83).
 constexpr int64_t kFewRows = 512;
 
 __global__ void __launch_bounds__(kD) merge_row_kv4_kernel(const SplitArgs a) {
@@ -399,6 +404,67 @@ __global__ void __launch_bounds__(kD) merge_row_kv4_kernel(const SplitArgs a) {
     a.out[row * kD + d] = __float2bfloat16_rn(bi_attn::normalise(o, bi_attn::inv_weight(l)));
 }
 
+// The fold of a row by a warp of the CTA that arrived last: merge_rows_kv4_kernel
+// with the partials in two halves of shared memory (2 * kFoldHalf rows of 512
+// bytes), the next chunks' on their way while the last are folded.
+constexpr int kFoldHalf = 8;
+static_assert(kWarps * 2 * kFoldHalf * kD * 4 <= kStagingBytes, "a warp's part of the staging memory");
+
+__device__ __forceinline__ void fold_row(const SplitArgs& a, int64_t row, int nch, float4* stage,
+                                         float4* factors, int lane) {
+    const float4* const parts = reinterpret_cast<const float4*>(partial_o(a, row, 0)) + lane;
+    const float2* const mls = partial_ml(a, row, 0);
+    auto copy = [&](int c0, float4* to) {
+#pragma unroll
+        for (int u = 0; u < kFoldHalf; ++u)
+            if (c0 + u < nch) bi::cp_async_16(to + 32 * u + lane, parts + (c0 + u) * (kD / 4));
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float2 ml = lane < nch ? __ldcg(mls + lane) : make_float2(-INFINITY, 0.f);
+    copy(0, stage);
+    copy(kFoldHalf, stage + 32 * kFoldHalf);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f, m = 0.f;
+    for (int cb = 0; cb < nch; cb += kFoldHalf) {
+        if (cb % 32 == 0) {  // the factors of 32 chunks
+            float v = ml.x;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float u = __shfl_up_sync(kAll, v, off);
+                if (lane >= off) v = fmaxf(v, u);
+            }
+            if (cb > 0) v = fmaxf(m, v);  // running maximum after chunk cb + lane
+            float before = __shfl_up_sync(kAll, v, 1);
+            if (lane == 0) before = cb > 0 ? m : 0.f;
+            m = __shfl_sync(kAll, v, 31);
+            factors[lane] = make_float4(bi_attn::exp2_ftz(before - v), bi_attn::exp2_ftz(ml.x - v), ml.y, 0.f);
+            ml = cb + 32 + lane < nch ? __ldcg(mls + cb + 32 + lane) : make_float2(-INFINITY, 0.f);
+        }
+        float4* const half = stage + (cb / kFoldHalf & 1) * 32 * kFoldHalf;
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kFoldHalf; ++u) {
+            if (cb + u >= nch) break;
+            const float4 x = half[32 * u + lane];
+            const float4 f = factors[(cb + u) % 32];
+            if (cb + u == 0) {
+                o = x;
+                l = f.z;
+            } else {
+                o.x = bi_attn::fold_value(o.x, f.x, x.x, f.y);
+                o.y = bi_attn::fold_value(o.y, f.x, x.y, f.y);
+                o.z = bi_attn::fold_value(o.z, f.x, x.z, f.y);
+                o.w = bi_attn::fold_value(o.w, f.x, x.w, f.y);
+                l = bi_attn::fold_value(l, f.x, f.z, f.y);
+            }
+        }
+        __syncwarp();  // every lane is done with the half and the factors
+        copy(cb + 2 * kFoldHalf, half);
+    }
+    store_row(a, row, o, l, lane);
+}
+
 __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Args ka) {
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
@@ -419,6 +485,9 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
     if (c >= nch) return;
     const int tokens = min(kChunk, L - c * kChunk);
     const int np = (tokens + kPage - 1) / kPage;
+    // several CTAs share a longer sequence; the last one to arrive folds it, if a
+    // launch of its own does not
+    uint32_t* const ctr = nch > 1 && a.counters ? a.counters + static_cast<int64_t>(s) * a.Hkv + g : nullptr;
     const int64_t row0 = static_cast<int64_t>(s) * a.Hq + g * a.group;
 
     extern __shared__ __align__(16) uint8_t smem[];
@@ -434,7 +503,11 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
             pg = a.block_table[static_cast<int64_t>(s) * a.max_pages_per_seq + c * kPagesPerChunk + lane];
         if (__any_sync(kAll, pg < 0 || pg >= a.num_pages)) {
             if (tid == 0) bi::report_error(a.err, bi::kErrBadInput | bi::kWhereAttnSplit);
-            if (nch > 1 && tid < a.group) *partial_ml(a, row0 + tid, c) = make_float2(-INFINITY, kNoChunk);
+            if (ctr) {
+                if (tid == 0) bi_attn::arrive_bad(ctr, nch);
+            } else if (nch > 1 && tid < a.group) {
+                *partial_ml(a, row0 + tid, c) = make_float2(-INFINITY, kNoChunk);
+            }
             return;
         }
         const int64_t at = (static_cast<int64_t>(pg) * a.Hkv + g) * kBlockBytes;
@@ -602,6 +675,10 @@ __global__ void __launch_bounds__(kThreads, 5) attn_chunk_kv4_kernel(const Kv4Ar
             if (warp == 0 && lane < 4) *partial_ml(a, row, c) = make_float2(tb.m[h], tb.l[h]);
         }
     }
+    if (!ctr || !bi_attn::arrive_last(a, ctr, nch, tid)) return;
+    float4* const stage = reinterpret_cast<float4*>(smem) + warp * 2 * kFoldHalf * 32;
+    float4* const factors = reinterpret_cast<float4*>(smem + kStagingBytes) + 32 * warp;
+    for (int h = warp; h < a.group; h += kWarps) fold_row(a, row0 + h, nch, stage, factors, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -816,17 +893,23 @@ __global__ void __launch_bounds__(32, 14) attn_warp_kv4_kernel(const Kv4Args ka)
     } while (kLoop && (c += gridDim.x) < nch);
 }
 
+// Chunks of a sequence up to which the chunk kernel's last CTA folds it.  A launch
+// of its own takes the host 3 us (a call for few sequences is bound by the host)
+// and folds faster: one sequence of 4096 tokens 9.5 us, against 8.6 folded in
+// place, 8192 11.7 and 11.2, 16384 13.6 and 16.5, 32768 19.5 and 27.8.
+constexpr int kMaxFolded = 32;
+
 // Chunks per SM (at the launch's bound on the lengths; lengths spread up to the
 // bound fill about half of them) from which on the warp kernel is taken.
-// Measured on GB300 with 8 kv-heads, chunk kernel against warp kernel with its
-// fold: 7 per SM (B = 4 up to 8192 tokens) 14.0 against 20.2 us, 14 (B = 8) 19.6
-// against 23.5, (B = 128 up to 512) 20.5 against 22.1, 27 (B = 16 up to 8192)
-// 32.3 against 30.4, (B = 256 up to 512) 35.9 against 32.4, 40 (B = 24) 46.5
-// against 40.9, 108 (B = 64) 112 against 83.  The chunk kernel's four warps
-// finish a chunk several times sooner; the warp kernel issues a third fewer
-// instructions and has no barriers.  Below the rule there are far fewer chunks
-// than arrival counters, and than an arrival counter can count.
-constexpr int64_t kManyChunks = 28;
+// Measured on GB300 with 8 kv-heads, chunk kernel against warp kernel, folds
+// included: 7 per SM (B = 4 up to 8192 tokens) 14.6 against 20.9 us, 14 (B = 8)
+// 19.4 against 22.7, (B = 128 up to 512) 20.1 against 22.0, 27 (B = 16 up to
+// 8192) 31.9 against 30.5, (B = 256 up to 512) 34.6 against 32.3, 40 (B = 24)
+// 46.2 against 41.0, 108 (B = 64) 109 against 83.  The chunk kernel's four warps finish a chunk several times sooner;
+// the warp kernel issues a third fewer instructions and has no barriers.  Below
+// the rule there are far fewer chunks than arrival counters, and than an arrival
+// counter can count.
+constexpr int64_t kManyChunks = 22;
 
 // Warps of a launch and of a (sequence, kv-head), about; where the bound on the
 // lengths asks for more, a warp takes several chunks.  A warp without a chunk
@@ -910,15 +993,18 @@ extern "C" bi_status bi_decode_attention_kv4(const void* q, const void* k_cache,
     const dim3 grid(max_chunks, Hkv, B);
     const int64_t most = std::min(
         kMostWarpsOfOne, std::max<int64_t>(1, kMostWarps / (static_cast<int64_t>(Hkv) * B)));
+    const bool few =
+        static_cast<int64_t>(max_chunks) * Hkv * B < kManyChunks * static_cast<int64_t>(bi::sm_count());
+    if (max_chunks > kMaxFolded) args.counters = nullptr;
     const cudaError_t e =
-        static_cast<int64_t>(max_chunks) * Hkv * B < kManyChunks * static_cast<int64_t>(bi::sm_count())
+        few
             ? bi::launch_pdl(attn_chunk_kv4_kernel, grid, dim3(kThreads), kSmemBytes, stream, ka)
         : max_chunks <= most
             ? bi::launch_pdl(attn_warp_kv4_kernel<false>, grid, dim3(32), 0, stream, ka)
             : bi::launch_pdl(attn_warp_kv4_kernel<true>, dim3(static_cast<unsigned>(most), Hkv, B), dim3(32),
                              0, stream, ka);
     if (e != cudaSuccess) return BI_ERR_CUDA;
-    if (max_chunks == 1) return BI_OK;
+    if (max_chunks == 1 || (few && args.counters)) return BI_OK;
     const int64_t rows = static_cast<int64_t>(B) * Hq;
     const cudaError_t f =
         rows < kFewRows ? bi::launch_pdl(merge_row_kv4_kernel, dim3(static_cast<unsigned>(rows)), dim3(kD), 0, stream, args)

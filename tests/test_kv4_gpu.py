@@ -219,14 +219,17 @@ def _problem(lens, Hq, Hkv, seed, spare=3):
     return (p["q"].cuda(), kc, vc, p["block_table"].cuda(), p["seq_lens"].cuda())
 
 
-# Launches of many chunks run a kernel of their own; a bound on the lengths far
-# above them makes one of any batch.
-BOTH_KERNELS = pytest.mark.parametrize("many", [False, True], ids=["few-chunks", "many-chunks"])
+# Launches of many chunks run a kernel of their own, and chunks of long sequences
+# are folded by one; a bound on the lengths far above them makes such a launch of
+# any batch.
+BOTH_KERNELS = pytest.mark.parametrize("many", [False, True, "long"], ids=["few-chunks", "many-chunks", "long"])
 
 
 def _bound(many, bt, msl, Hkv):
     """(block table, max_seq_len) of a launch of few or of many chunks."""
-    if many:
+    if many == "long":
+        msl = 256 * 40
+    elif many:
         msl = 256 * -(-42 * 160 // (bt.shape[0] * Hkv))
     wide = torch.full((bt.shape[0], max(bt.shape[1], -(-msl // 16))), -1, dtype=torch.int32, device="cuda")
     wide[:, :bt.shape[1]] = bt
