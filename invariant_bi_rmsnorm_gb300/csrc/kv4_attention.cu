@@ -253,12 +253,28 @@ __device__ __forceinline__ void store_row(const SplitArgs& a, int64_t row, const
 // (m, l) of a chunk with a page index out of range: no weight sum is negative.
 constexpr float kNoChunk = -1.f;
 
+// The factors (2^(M - M'), 2^(m_c - M'), l_c) of 32 chunks of a row, lane = chunk
+// with (m_c, l_c) = ml ((-inf, 0) past the last): the running maxima M' are a
+// prefix maximum, as in bi_attn::fold_sequence.  m: the running maximum before
+// them (unless they are the first), then after them.
+__device__ __forceinline__ float4 fold_factors(const float2& ml, float& m, bool first, int lane) {
+    float v = ml.x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const float u = __shfl_up_sync(kAll, v, off);
+        if (lane >= off) v = fmaxf(v, u);
+    }
+    if (!first) v = fmaxf(m, v);
+    float before = __shfl_up_sync(kAll, v, 1);
+    if (lane == 0) before = first ? 0.f : m;
+    m = __shfl_sync(kAll, v, 31);
+    return make_float4(bi_attn::exp2_ftz(before - v), bi_attn::exp2_ftz(ml.x - v), ml.y, 0.f);
+}
+
 // The fold of the warp kernel's partials, a warp per (sequence, query head), in
 // ascending chunk order with bi_attn::attn_merge_kernel's operations.  Lane l
-// has positions 4l .. 4l + 3 of the row.  As in bi_attn::fold_sequence the
-// running maxima are a prefix maximum, taken for 32 chunks at once (lane =
-// chunk), and all factors with them; the partials of kAhead chunks are on their
-// way together.
+// has positions 4l .. 4l + 3 of the row; the partials of kAhead chunks are on
+// their way together.
 //
 // A launch of its own, where the rows are folded side by side: the warp
 // that arrives last at its (sequence, kv-head) could fold its rows as well, but does
@@ -294,19 +310,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
         const float2 ml = lane < nb ? __ldcg(partial_ml(a, row, cb + lane)) : make_float2(-INFINITY, 0.f);
         load(0);
         if (__any_sync(kAll, ml.y == kNoChunk)) return;  // the output stays as it was
-        float v = ml.x;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const float u = __shfl_up_sync(kAll, v, off);
-            if (lane >= off) v = fmaxf(v, u);
-        }
-        if (cb > 0) v = fmaxf(m, v);  // running maximum after chunk cb + lane
-        float before = __shfl_up_sync(kAll, v, 1);
-        if (lane == 0) before = cb > 0 ? m : 0.f;
-        m = __shfl_sync(kAll, v, 31);
+        const float4 f = fold_factors(ml, m, cb == 0, lane);
         __syncwarp();  // every lane is done with the last factors
-        if (lane < nb)
-            factors[lane] = make_float4(bi_attn::exp2_ftz(before - v), bi_attn::exp2_ftz(ml.x - v), ml.y, 0.f);
+        factors[lane] = f;
         __syncwarp();
         for (int i0 = 0; i0 < nb; i0 += kAhead) {
             if (i0 > 0) load(i0);
@@ -368,19 +374,9 @@ __global__ void __launch_bounds__(kD) merge_row_kv4_kernel(const SplitArgs a) {
         const float2 ml = lane < nb ? next_ml : make_float2(-INFINITY, 0.f);
         if (__any_sync(kAll, ml.y == kNoChunk)) return;  // the output stays as it was
         load_ml(cb + 32, nch);
-        float v = ml.x;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const float u = __shfl_up_sync(kAll, v, off);
-            if (lane >= off) v = fmaxf(v, u);
-        }
-        if (cb > 0) v = fmaxf(m, v);  // running maximum after chunk cb + lane
-        float before = __shfl_up_sync(kAll, v, 1);
-        if (lane == 0) before = cb > 0 ? m : 0.f;
-        m = __shfl_sync(kAll, v, 31);
+        const float4 f = fold_factors(ml, m, cb == 0, lane);
         __syncwarp();  // every lane is done with the last factors
-        if (lane < nb)
-            factors[lane] = make_float4(bi_attn::exp2_ftz(before - v), bi_attn::exp2_ftz(ml.x - v), ml.y, 0.f);
+        factors[lane] = f;
         __syncwarp();
         float part[32];
 #pragma unroll
@@ -427,17 +423,8 @@ __device__ __forceinline__ void fold_row(const SplitArgs& a, int64_t row, int nc
     float l = 0.f, m = 0.f;
     for (int cb = 0; cb < nch; cb += kFoldHalf) {
         if (cb % 32 == 0) {  // the factors of 32 chunks
-            float v = ml.x;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const float u = __shfl_up_sync(kAll, v, off);
-                if (lane >= off) v = fmaxf(v, u);
-            }
-            if (cb > 0) v = fmaxf(m, v);  // running maximum after chunk cb + lane
-            float before = __shfl_up_sync(kAll, v, 1);
-            if (lane == 0) before = cb > 0 ? m : 0.f;
-            m = __shfl_sync(kAll, v, 31);
-            factors[lane] = make_float4(bi_attn::exp2_ftz(before - v), bi_attn::exp2_ftz(ml.x - v), ml.y, 0.f);
+            const float4 f = fold_factors(ml, m, cb == 0, lane);
+            factors[lane] = f;
             ml = cb + 32 + lane < nch ? __ldcg(mls + cb + 32 + lane) : make_float2(-INFINITY, 0.f);
         }
         float4* const half = stage + (cb / kFoldHalf & 1) * 32 * kFoldHalf;
