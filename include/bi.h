@@ -473,7 +473,7 @@ bi_status bi_kv4_read(const void* k_cache, const void* v_cache, const int32_t* b
  * (bi_decode_attention_workspace_size bytes, counters zero at first use),
  * checks and errors as bi_decode_attention; k_cache and v_cache are 4-bit
  * caches, Hkv <= 65535.  One kernel launch, or two (a second one folds the
- * chunks of many long sequences).
+ * chunks of many or of long sequences).
  */
 bi_status bi_decode_attention_kv4(const void* q, const void* k_cache, const void* v_cache,
                                   const int32_t* block_table, int32_t max_pages_per_seq,
@@ -496,7 +496,7 @@ bi_status bi_decode_attention_kv4(const void* q, const void* k_cache, const void
  * Invariance": one row per CTA, reductions in an order that depends only on
  * `vocab`.  -inf logits (a masked vocabulary) add nothing and come last among
  * the k; a row of nothing else has lse -inf, entropy and log-probabilities
- * NaN.  NaN logits make the row's numbers NaN and rank below every number. 
+ * NaN.  NaN logits make the row's numbers NaN and rank below every number.
  * Masks of finite values (-1e9, bf16's lowest) do as well as -inf.
  *   logits       device, bf16 [rows][ld], ld >= vocab, both multiples of 8.
  *   targets      device, int32 [rows], with logprob_out fp32 [rows]; or both null.
