@@ -38,7 +38,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -82,7 +81,9 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr uint32_t kRefPerPage = 1u << 31;  // else ref[0] is every page's and alpha is not set
 static_assert(kPagesPerChunk < 31, "a bit per page");
 constexpr int kFactorBytes = kWarps * 32 * sizeof(float4);  // fold_row's, where the tables were
-constexpr int kSmemBytes = kStagingBytes + (sizeof(Tables) > kFactorBytes ? sizeof(Tables) : kFactorBytes);
+constexpr int kSmemBytes =
+    kStagingBytes + (sizeof(Tables) > kFactorBytes ? sizeof(Tables) : kFactorBytes);
+static_assert(kSmemBytes <= 48 * 1024, "no more than a launch may ask for without an attribute");
 
 struct Kv4Args {
     SplitArgs s;
@@ -229,7 +230,7 @@ __device__ __forceinline__ float reduce_columns(float v0, float v1, int lane, F 
     return f(v, __shfl_xor_sync(0xffffffffu, v, 16));
 }
 
-// A chunk's partial as the warp kernel writes and reads it: O's dims of a row
+// A chunk's partial in the workspace: O's dims of a row
 // in the order of the accumulators, position 16mt + 2g + i for dim 16mt + g +
 // 8i.
 __device__ __forceinline__ float* partial_o(const SplitArgs& a, int64_t row, int c) {
@@ -271,7 +272,7 @@ __device__ __forceinline__ float4 fold_factors(const float2& ml, float& m, bool 
     return make_float4(bi_attn::exp2_ftz(before - v), bi_attn::exp2_ftz(ml.x - v), ml.y, 0.f);
 }
 
-// The fold of the warp kernel's partials, a warp per (sequence, query head), in
+// The fold of a row's chunks, a warp per row (sequence, query head), in
 // ascending chunk order with bi_attn::attn_merge_kernel's operations.  Lane l
 // has positions 4l .. 4l + 3 of the row; the partials of kAhead chunks are on
 // their way together.
@@ -908,9 +909,6 @@ constexpr int64_t kManyChunks = 22;
 constexpr int64_t kMostWarps = 32768;
 constexpr int64_t kMostWarpsOfOne = 256;
 
-// set once per device; any thread may race to set it, the attribute is idempotent
-std::atomic<bool> g_attr_set[64] = {};
-
 }  // namespace
 
 extern "C" bi_status bi_decode_attention_kv4(const void* q, const void* k_cache,
@@ -942,15 +940,6 @@ extern "C" bi_status bi_decode_attention_kv4(const void* q, const void* k_cache,
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return BI_ERR_WORKSPACE_TOO_SMALL;
         if (!bi::aligned16(workspace)) return BI_ERR_MISALIGNED;
-    }
-
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return BI_ERR_CUDA;
-    if (!g_attr_set[dev]) {
-        if (cudaFuncSetAttribute(attn_chunk_kv4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmemBytes) != cudaSuccess)
-            return BI_ERR_CUDA;
-        g_attr_set[dev] = true;
     }
 
     Kv4Args ka;
@@ -994,7 +983,8 @@ extern "C" bi_status bi_decode_attention_kv4(const void* q, const void* k_cache,
     if (max_chunks == 1 || (few && args.counters)) return BI_OK;
     const int64_t rows = static_cast<int64_t>(B) * Hq;
     const cudaError_t f =
-        rows < kFewRows ? bi::launch_pdl(merge_row_kv4_kernel, dim3(static_cast<unsigned>(rows)), dim3(kD), 0, stream, args)
+        rows < kFewRows ? bi::launch_pdl(merge_row_kv4_kernel, dim3(static_cast<unsigned>(rows)), dim3(kD),
+                                         0, stream, args)
                         : bi::launch_pdl(merge_rows_kv4_kernel, dim3(ceil_div(rows, kMergeWarps)),
                                          dim3(32 * kMergeWarps), 0, stream, args, rows);
     return f == cudaSuccess ? BI_OK : BI_ERR_CUDA;
