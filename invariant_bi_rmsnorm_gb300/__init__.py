@@ -46,7 +46,14 @@ __all__ = ["BiError", "rmsnorm", "gemm", "gemm_swiglu", "interleave_gate_up",
            "KV4_BLOCK_BYTES", "MAX_TOP_LOGPROBS"]
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _stream_of(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# The handle of a device's current stream.  Building a torch.cuda.Stream object
+# for it takes 3 us; the function that gives the handle alone exists in CUDA
+# builds of torch only.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
 
 
 def _current_device() -> int:
@@ -79,8 +86,7 @@ def _check(status: int, where: str) -> None:
 
 def _stream(stream) -> int:
     if stream is None:
-        # the handle alone: building a torch.cuda.Stream object takes 3 us
-        return _raw_stream(_current_device())
+        return _raw_stream(torch.cuda.current_device())  # which raises where there is no device
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
