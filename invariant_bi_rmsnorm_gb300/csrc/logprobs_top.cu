@@ -12,9 +12,10 @@
 // One pass over the row (HBM), as bi_logprobs: thread t folds its vectors t,
 // t + 256, ... into (m, s) with the same operations, and beside them
 //     T = sum_j 2^(d_j) d_j,   d_j = (x_j - m) log2(e)          (fp32)
-// (m' = m + D moves d by -D log2(e): T' = (T + (m - m') log2(e) s) 2^(..)), so
+// (m' = m + D moves d by -D log2(e): T' = (T + (m - m') log2(e) S) 2^(..)), so
 //     entropy = -sum p ln p = ln S - ln 2 * T / S,
-// in which nothing cancels: ln S >= 0 and T <= 0.
+// in which nothing cancels: ln S >= 0 and T <= 0.  S is s and a small correction
+// beside it (Run).
 //
 // The k largest: the pass also keeps the maximum of every segment (a few
 // consecutive vectors of one thread) in shared memory.  The k-th largest of
@@ -29,7 +30,7 @@
 // What bounds it is the instructions: 12.6 a logit in all (bi_logprobs 6.9), of
 // which the exponential, its sum in bi_logprobs' order and T take 5, and moving
 // the maximum (in most vectors of a row's first half some lane's does) 2.  1024
-// rows of 151936 logits, k = 20: 69 us, 4.5 TB/s, 0.67 of the copy rate
+// rows of 151936 logits, k = 20: 71 us, 4.4 TB/s, 0.65 of the copy rate
 // (bi_logprobs, without entropy and alternatives, 50 us); one row 18 us.
 #include <cuda_bf16.h>
 
@@ -45,7 +46,7 @@ using bi_lp::kLog2e;
 using bi_lp::kThreads;
 
 // Vectors a thread loads at a time, while it folds as many before them.  1024,
-// 608 rows and one of 151936 logits, k = 20: 4 (four CTAs per SM) 68.8, 44.1 and
+// 608 rows and one of 151936 logits, k = 20 (without Run::c): 4 (four CTAs per SM) 68.8, 44.1 and
 // 17.9 us; nothing loaded ahead: 4 (five CTAs) 70.2, 50.2 and 19.0, 2 (six) 83
 // (1024 rows), 8 (three) 85, 57 and 17.7; 8 loaded ahead (three) 93, 63 and 20.4.
 constexpr int kUnroll = 4;
@@ -55,6 +56,7 @@ constexpr int kMaxCand = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNear = 1024.f;  // maxima up to here: d by one fma
+constexpr float kQuiet = 44.f;   // up to here: 44 log2(e) < 64, so mc is 2^-19 off at most
 constexpr float kLowest = -3.3895313892515355e38f;  // bf16's lowest finite value
 constexpr uint32_t kNegInf2 = 0xFF80FF80u;  // two bf16 -inf
 
@@ -74,16 +76,43 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 // Running reduction of one thread.  m starts at the lowest finite value instead
 // of -inf, so that no difference with it is undefined: s is 0 until a logit
 // reaches m, and what multiplies a zero s changes no bit.
+//
+// d is one fma, x log2(e) - mc, and mc the rounded product m log2(e), so d is
+// mc - m log2(e) too low, up to 2^-14 at |m| = 1024.  That is nothing while the
+// maximum stays: every term, and S with them, has the same factor.  But a
+// rescaling by 2^((m - m') log2(e)) leaves the older terms the old maximum's, and
+// so does joining threads whose maxima differ.  bi_logprobs' s is like that, and
+// lse no worse than its own rounding.  The entropy weighs parts of the row against
+// one another by -ln p: 2047 logits of 1012 below one of 1020 had it 9e-5 off.  So
+// T is moved and rescaled by the difference of these deltas as well, and c = S - s
+// keeps what that makes of s.  While the maxima lie within +-44, as a model's do,
+// it is left out: that is 2.6e-6 of a part at most, and the roundings of a sum of
+// hundreds of terms are allowed more.  1024 rows of 151936: 69.3 us with nothing of
+// this, 71.0 so, 75.5 with it at every move.
 struct Run {
-    float m, mc, s;
+    float m, mc, s, c;
     float2 t;   // T, in two halves (elements 0, 2, .. and 1, 3, .. of the vectors)
-    bool far;   // |m| > kNear in some lane of the warp
+    int mode;   // of the warp: 2 with some lane's |m| > kNear, 1 with some |m| > kQuiet or c, else 0
 };
+
+__device__ __forceinline__ float delta_of(float m) {
+    return fabsf(m) > kQuiet && fabsf(m) <= kNear ? __fmaf_rn(-m, kLog2e, __fmul_rn(m, kLog2e)) : 0.f;
+}
 
 // (a - b) log2(e) for a <= b, by which d falls as the maximum goes from a to
 // b; bounded where 2^.. is 0 anyway, so that 0 times it stays 0
 __device__ __forceinline__ float moved(float a, float b) {
     return fmaxf(__fmul_rn(__fsub_rn(a, b), kLog2e), -1024.f);
+}
+
+// c and T of terms whose d moves by `by` + dd, |dd| at most 2^-13, where f = 2^by
+// rescales s: theirs is 2^(by + dd) = f + f ln 2 dd (to 2^-27), which is returned.
+__device__ __forceinline__ float rescale_ct(float s, float& c, float& t, float f, float by, float dd) {
+    const float extra = __fmul_rn(f, __fmul_rn(kLn2, dd));
+    const float g = __fadd_rn(f, extra);
+    t = __fmul_rn(__fmaf_rn(__fadd_rn(by, dd), __fadd_rn(s, c), t), g);
+    c = __fmaf_rn(c, g, __fmul_rn(s, extra));
+    return g;
 }
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
@@ -108,11 +137,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // in most vectors of a row's first half; the whole warp takes that branch or
 // none of it does.
 //
-// One fma for d leaves it off by the rounding of m log2(e), the same for every
-// term of that maximum (so it cancels in the entropy) and below 2^-14 for |m| <=
-// 1024.  Past that -- logits no model gives, but a thread may see nothing else
-// than a mask's -1e9 or bf16's lowest value, whose m log2(e) is not even finite
-// -- d is taken from the difference, which is exact where it counts.
+// d is one fma for |m| <= 1024.  Past that -- logits no model gives, but a thread may
+// see nothing else than a mask's -1e9 or bf16's lowest value, whose m log2(e) is
+// not even finite -- it is taken from the difference, which is exact where it
+// counts.
 __device__ __forceinline__ float fold_vec_t(Run& r, const uint4& u) {
     const uint32_t h = max_bf16x2(max_bf16x2(u.x, u.y), max_bf16x2(u.z, u.w));
     const float vm = fmaxf(bi_lp::lo16(h), bi_lp::hi16(h));
@@ -120,15 +148,23 @@ __device__ __forceinline__ float fold_vec_t(Run& r, const uint4& u) {
         const float m = fmaxf(r.m, vm);
         const float by = __fmul_rn(__fsub_rn(r.m, m), kLog2e);
         const float f = exp2f(by);  // bi_lp::rescale(r.m, m)
-        r.t.x = __fmul_rn(__fmaf_rn(fmaxf(by, -1024.f), r.s, r.t.x), f);
-        r.t.y = __fmul_rn(r.t.y, f);
+        const float b = fmaxf(by, -1024.f);  // moved(r.m, m)
+        if (!__any_sync(0xffffffffu, fabsf(m) > kQuiet) && r.mode == 0) {
+            r.t.x = __fmul_rn(__fmaf_rn(b, r.s, r.t.x), f);
+            r.t.y = __fmul_rn(r.t.y, f);
+        } else {
+            const float dd = __fsub_rn(delta_of(r.m), delta_of(m));
+            r.t.y = __fmul_rn(r.t.y, rescale_ct(r.s, r.c, r.t.x, f, b, dd));
+            r.mode = __any_sync(0xffffffffu, fabsf(m) > kNear)                   ? 2
+                     : __any_sync(0xffffffffu, fabsf(m) > kQuiet || r.c != 0.f) ? 1
+                                                                                : 0;
+        }
         r.s = __fmul_rn(r.s, f);
         r.m = m;
         r.mc = __fmul_rn(m, kLog2e);
-        r.far = __any_sync(0xffffffffu, fabsf(m) > kNear);
     }
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    if (!r.far) {
+    if (r.mode < 2) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 d = fma2(make_float2(bi_lp::lo16(w[i]), bi_lp::hi16(w[i])),
@@ -153,17 +189,26 @@ __device__ __forceinline__ float fold_vec_t(Run& r, const uint4& u) {
     return vm;
 }
 
-// A thread's part of the row, reduced: combine of logprobs.cu with T beside s.
+// A thread's part of the row, reduced: combine of logprobs.cu with c and T
+// beside s.
 struct Part {
-    float m, s, t;
+    float m, s, c, t;
 };
 
-__device__ __forceinline__ void combine_t(Part& a, float m2, float s2, float t2) {
-    const float M = fmaxf(a.m, m2);
-    const float f1 = bi_lp::rescale(a.m, M), f2 = bi_lp::rescale(m2, M);
-    a.t = __fadd_rn(__fmul_rn(__fmaf_rn(moved(a.m, M), a.s, a.t), f1),
-                    __fmul_rn(__fmaf_rn(moved(m2, M), s2, t2), f2));
-    a.s = __fadd_rn(__fmul_rn(a.s, f1), __fmul_rn(s2, f2));
+__device__ __forceinline__ void combine_t(Part& a, Part b) {
+    const float M = fmaxf(a.m, b.m);
+    const float f1 = bi_lp::rescale(a.m, M), f2 = bi_lp::rescale(b.m, M);
+    if (fmaxf(fabsf(a.m), fabsf(b.m)) <= kQuiet && a.c == 0.f && b.c == 0.f) {
+        a.t = __fadd_rn(__fmul_rn(__fmaf_rn(moved(a.m, M), a.s, a.t), f1),
+                        __fmul_rn(__fmaf_rn(moved(b.m, M), b.s, b.t), f2));
+    } else {
+        const float delta = delta_of(M);
+        rescale_ct(a.s, a.c, a.t, f1, moved(a.m, M), __fsub_rn(delta_of(a.m), delta));
+        rescale_ct(b.s, b.c, b.t, f2, moved(b.m, M), __fsub_rn(delta_of(b.m), delta));
+        a.t = __fadd_rn(a.t, b.t);
+        a.c = __fadd_rn(a.c, b.c);
+    }
+    a.s = __fadd_rn(__fmul_rn(a.s, f1), __fmul_rn(b.s, f2));
     a.m = M;
 }
 
@@ -220,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_top_kernel(const TopArgs
     __shared__ unsigned long long cand[kMaxCand];  // key above, ~id below: larger is better
     __shared__ __align__(16) uint16_t thread_max[kThreads];
     __shared__ uint32_t kth_s;
-    __shared__ float red_m[kWarps], red_s[kWarps], red_t[kWarps];
+    __shared__ Part red_part[kWarps];
     __shared__ int red[kWarps];
     __shared__ float lse_s;
     __shared__ int ncand;
@@ -233,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_top_kernel(const TopArgs
     const int nvec = a.vocab / 8;
 
     // ---- one pass: (m, s, T) and the segments' maxima ----
-    Run run = {kLowest, 0.f, 0.f, make_float2(0.f, 0.f), true};
+    Run run = {kLowest, 0.f, 0.f, 0.f, make_float2(0.f, 0.f), 2};
     uint32_t best = 0;
     auto load = [&](uint4 (&u)[kUnroll], int v0) {
 #pragma unroll
@@ -259,30 +304,23 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_top_kernel(const TopArgs
         best = max(best, key);
     }
     thread_max[tid] = static_cast<uint16_t>(best);
-    Part r = {run.m, run.s, __fadd_rn(run.t.x, run.t.y)};
+    Part r = {run.m, run.s, run.c, __fadd_rn(run.t.x, run.t.y)};
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, r.m, o);
-        const float s2 = __shfl_xor_sync(0xffffffffu, r.s, o);
-        const float t2 = __shfl_xor_sync(0xffffffffu, r.t, o);
-        combine_t(r, m2, s2, t2);
-    }
-    if (lane == 0) {
-        red_m[warp] = r.m;
-        red_s[warp] = r.s;
-        red_t[warp] = r.t;
-    }
+    for (int o = 16; o >= 1; o >>= 1)
+        combine_t(r, Part{__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o),
+                          __shfl_xor_sync(0xffffffffu, r.c, o), __shfl_xor_sync(0xffffffffu, r.t, o)});
+    if (lane == 0) red_part[warp] = r;
     if (tid == 0) ncand = 0;
     __syncthreads();
     if (tid == 0) {
-        Part c = {red_m[0], red_s[0], red_t[0]};
-        for (int i = 1; i < kWarps; ++i) combine_t(c, red_m[i], red_s[i], red_t[i]);
-        const float ls = logf(c.s);
-        const float lse = __fadd_rn(c.m, ls);
+        Part c = red_part[0];
+        for (int i = 1; i < kWarps; ++i) combine_t(c, red_part[i]);
+        const float lse = __fadd_rn(c.m, logf(c.s));
         lse_s = lse;
         if (a.lse_out) a.lse_out[row] = lse;
         if (a.entropy_out) {
-            const float h = __fsub_rn(ls, __fmul_rn(kLn2, __fdiv_rn(c.t, c.s)));
+            const float S = __fadd_rn(c.s, c.c);
+            const float h = __fsub_rn(logf(S), __fmul_rn(kLn2, __fdiv_rn(c.t, S)));
             a.entropy_out[row] = h < 0.f ? 0.f : h;  // the last bit of ln S may differ; NaN stays
         }
         if (a.targets && a.logprob_out) {
