@@ -401,33 +401,37 @@ __global__ void __launch_bounds__(kD) merge_row_kv4_kernel(const SplitArgs a) {
     a.out[row * kD + d] = __float2bfloat16_rn(bi_attn::normalise(o, bi_attn::inv_weight(l)));
 }
 
-// The fold of a row by a warp of the CTA that arrived last: merge_rows_kv4_kernel
-// with the partials in two halves of shared memory (2 * kFoldHalf rows of 512
-// bytes), the next chunks' on their way while the last are folded.
+// Chunks of a sequence up to which the chunk kernel's last CTA folds it.  A launch
+// of its own takes the host 3 us (a call for few sequences is bound by the host)
+// and folds faster: one sequence of 4096 tokens 9.5 us, against 8.6 folded in
+// place, 8192 11.7 and 11.2, 16384 13.6 and 16.5, 32768 19.5 and 27.8.
+constexpr int kMaxFolded = 32;
+
+// The fold of a row of up to kMaxFolded chunks by a warp of the CTA that arrived
+// last: a round of merge_rows_kv4_kernel with the partials in two halves of shared
+// memory (2 * kFoldHalf rows of 512 bytes), the next chunks' on their way while
+// the last are folded.
 constexpr int kFoldHalf = 8;
 static_assert(kWarps * 2 * kFoldHalf * kD * 4 <= kStagingBytes, "a warp's part of the staging memory");
 
 __device__ __forceinline__ void fold_row(const SplitArgs& a, int64_t row, int nch, float4* stage,
                                          float4* factors, int lane) {
     const float4* const parts = reinterpret_cast<const float4*>(partial_o(a, row, 0)) + lane;
-    const float2* const mls = partial_ml(a, row, 0);
     auto copy = [&](int c0, float4* to) {
 #pragma unroll
         for (int u = 0; u < kFoldHalf; ++u)
             if (c0 + u < nch) bi::cp_async_16(to + 32 * u + lane, parts + (c0 + u) * (kD / 4));
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    float2 ml = lane < nch ? __ldcg(mls + lane) : make_float2(-INFINITY, 0.f);
+    const float2 ml = lane < nch ? __ldcg(partial_ml(a, row, lane)) : make_float2(-INFINITY, 0.f);
     copy(0, stage);
     copy(kFoldHalf, stage + 32 * kFoldHalf);
+    float m = 0.f;
+    static_assert(kMaxFolded <= 32, "a factor a lane");
+    factors[lane] = fold_factors(ml, m, true, lane);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f, m = 0.f;
+    float l = 0.f;
     for (int cb = 0; cb < nch; cb += kFoldHalf) {
-        if (cb % 32 == 0) {  // the factors of 32 chunks
-            const float4 f = fold_factors(ml, m, cb == 0, lane);
-            factors[lane] = f;
-            ml = cb + 32 + lane < nch ? __ldcg(mls + cb + 32 + lane) : make_float2(-INFINITY, 0.f);
-        }
         float4* const half = stage + (cb / kFoldHalf & 1) * 32 * kFoldHalf;
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
@@ -435,7 +439,7 @@ __device__ __forceinline__ void fold_row(const SplitArgs& a, int64_t row, int nc
         for (int u = 0; u < kFoldHalf; ++u) {
             if (cb + u >= nch) break;
             const float4 x = half[32 * u + lane];
-            const float4 f = factors[(cb + u) % 32];
+            const float4 f = factors[cb + u];
             if (cb + u == 0) {
                 o = x;
                 l = f.z;
@@ -447,7 +451,7 @@ __device__ __forceinline__ void fold_row(const SplitArgs& a, int64_t row, int nc
                 l = bi_attn::fold_value(l, f.x, f.z, f.y);
             }
         }
-        __syncwarp();  // every lane is done with the half and the factors
+        __syncwarp();  // every lane is done with the half, and in the end with the factors
         copy(cb + 2 * kFoldHalf, half);
     }
     store_row(a, row, o, l, lane);
@@ -880,12 +884,6 @@ __global__ void __launch_bounds__(32, 14) attn_warp_kv4_kernel(const Kv4Args ka)
         if (kLoop) __syncwarp();  // every lane is done with the ring
     } while (kLoop && (c += gridDim.x) < nch);
 }
-
-// Chunks of a sequence up to which the chunk kernel's last CTA folds it.  A launch
-// of its own takes the host 3 us (a call for few sequences is bound by the host)
-// and folds faster: one sequence of 4096 tokens 9.5 us, against 8.6 folded in
-// place, 8192 11.7 and 11.2, 16384 13.6 and 16.5, 32768 19.5 and 27.8.
-constexpr int kMaxFolded = 32;
 
 // Chunks per SM (at the launch's bound on the lengths; lengths spread up to the
 // bound fill about half of them) from which on the warp kernel is taken.
