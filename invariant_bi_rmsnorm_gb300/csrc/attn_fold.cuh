@@ -1,7 +1,10 @@
-// What the decode-attention kernels over a bf16 cache and over a 4-bit cache
-// share after a chunk's pages have been walked: the chunk geometry, the
-// workspace of chunk partials with its arrival counters, and the folds of a
-// sequence's partials in ascending chunk order.
+// What follows once a chunk's pages have been walked.  The decode-attention
+// kernels over a bf16 cache and over a 4-bit cache share the launch's arguments,
+// the workspace of chunk partials and its arrival counters (SplitArgs,
+// arrive_last, arrive_bad).  The chunk geometry of both strategies, the folds of a
+// sequence's partials in ascending chunk order and what stores and reads those
+// partials are the bf16 cache's; the 4-bit kernels keep partials in another order
+// and fold them with the same operations (kv4_attention.cu).
 #pragma once
 #include <cuda_bf16.h>
 

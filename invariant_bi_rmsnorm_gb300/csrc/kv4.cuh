@@ -68,7 +68,10 @@ __device__ __forceinline__ ScalePair scale_pair(uint32_t s2) {
 }
 
 // The values of the codes at bits 4p .. 4p + 3 of both halves of w, as
-// bf16x2.  0x4300 | code is the bf16 number 128 + code; (128 + code) s - 136 s
+// bf16x2.  Putting an integer into the mantissa of a float of fixed exponent is the
+// known way to convert small integers without a conversion instruction; here the
+// subtraction of its exponent's value, of the codes' offset and the scale are one
+// fma.  0x4300 | code is the bf16 number 128 + code; (128 + code) s - 136 s
 // = (code - 8) s has one rounding, of an exact bf16 value.
 __device__ __forceinline__ uint32_t kv4_pair(uint32_t w, int p, const ScalePair& sp) {
     uint32_t c;

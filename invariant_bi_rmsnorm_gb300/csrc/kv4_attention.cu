@@ -15,12 +15,22 @@
 //
 // The bytes of a chunk are little over a quarter of a bf16 chunk's but its
 // arithmetic is the same, and the codes have to be turned into numbers besides:
-// about 350 instructions a page and kv-head, 24 of them mma.sync, each of which
-// keeps a scheduler busy for 8 cycles (measured: 2.04 cycles per SM).  That is
-// about 130 cycles an SM where HBM would deliver the page in 98, so what bounds
-// both kernels below is the instructions they issue.  On GB300, cold, GQA 32/8,
-// lengths even over 1 .. 8192: B = 256 292 us (1.21 GB, 4.2 TB/s, 0.61 of the
-// copy rate; the bf16 cache's 4.3 GB take 599 us), B = 64 83 us.
+// about 350 instructions a page and kv-head, 24 of them mma.sync.  An SM takes 145
+// cycles for a page where HBM would deliver it in 98 (the warp kernel below, every
+// chunk full: 32 sequences of 8192 tokens).  Its four schedulers' instructions
+// would take 88 of them and the tensor pipe 49 (2.04 a mma.sync, measured alone):
+// neither is full, but they hardly overlap, and the two together are within 6 % of
+// what is measured.  Lengths even over 1 .. 8192 cost more, 165 cycles at B = 64 and
+// 152 at B = 256: half of the launch's warps find no chunk, and last pages are not
+// full.  SMs also start late and run out of chunks before the last one does (10 and
+// 6 % of the kernel), and the fold's launch follows (9 and 16 us).  On GB300, cold,
+// GQA 32/8, lengths even over 1 .. 8192: B = 256 292 us (1.21 GB, 4.2 TB/s, 0.61 of
+// the copy rate; the bf16 cache's 4.3 GB take 599 us), B = 64 83 us.
+//
+// mma.sync, not tcgen05, although the two give the same bits: a page is three
+// products too small for tcgen05, each of which takes 44-59 cycles to issue, as much
+// as the whole page takes here, and its operands would have to be written to shared
+// memory as bf16 first.
 //
 // Few chunks: one CTA (4 warps) per (sequence, kv-head, chunk), which finishes
 // a chunk soonest (one sequence of 8192 tokens 11.1 us, of 300 6.7 us).  The
@@ -894,7 +904,9 @@ __global__ void __launch_bounds__(32, 14) attn_warp_kv4_kernel(const Kv4Args ka)
 // 46.2 against 41.0, 108 (B = 64) 109 against 83.  The chunk kernel's four warps finish a chunk several times sooner;
 // the warp kernel issues a third fewer instructions and has no barriers.  Below
 // the rule there are far fewer chunks than arrival counters, and than an arrival
-// counter can count.
+// counter can count.  A call captured under a bound far above its lengths takes the
+// form that the bound asks for: 16 sequences of 300 tokens 16.9 us under a bound of
+// 8192 (warp kernel), 9.1 under 512; 64 of 2000 tokens 54.2, and 40.5 under 2048.
 constexpr int64_t kManyChunks = 22;
 
 // Warps of a launch and of a (sequence, kv-head), about; where the bound on the
