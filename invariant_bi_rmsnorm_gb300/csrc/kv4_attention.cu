@@ -18,19 +18,20 @@
 // about 350 instructions a page and kv-head, 24 of them mma.sync.  An SM takes 145
 // cycles for a page where HBM would deliver it in 98 (the warp kernel below, every
 // chunk full: 32 sequences of 8192 tokens).  Its four schedulers' instructions
-// would take 88 of them and the tensor pipe 49 (2.04 a mma.sync, measured alone):
-// neither is full, but they hardly overlap, and the two together are within 6 % of
-// what is measured.  Lengths even over 1 .. 8192 cost more, 165 cycles at B = 64 and
-// 152 at B = 256: half of the launch's warps find no chunk, and last pages are not
-// full.  SMs also start late and run out of chunks before the last one does (10 and
-// 6 % of the kernel), and the fold's launch follows (9 and 16 us).  On GB300, cold,
-// GQA 32/8, lengths even over 1 .. 8192: B = 256 292 us (1.21 GB, 4.2 TB/s, 0.61 of
-// the copy rate; the bf16 cache's 4.3 GB take 599 us), B = 64 83 us.
+// would take 88 of them and the tensor pipe 49 (2.04 a mma.sync, measured alone).
+// Neither is full, and nor is HBM; that the two together are within 6 % of what is
+// measured suggests that they hardly overlap.  Lengths even over 1 .. 8192 cost
+// more, 165 cycles at B = 64 and 152 at B = 256: half of the launch's warps find no
+// chunk, and last pages are not full.  SMs also start late and run out of chunks
+// before the last one does (10 and 6 % of the kernel), and the fold's launch
+// follows (9 and 16 us).  On GB300, cold, GQA 32/8, lengths even over 1 .. 8192: B =
+// 256 292 us (1.21 GB, 4.2 TB/s, 0.61 of the copy rate; the bf16 cache's 4.3 GB
+// take 599 us), B = 64 83 us.
 //
 // mma.sync, not tcgen05, although the two give the same bits: a page is three
-// products too small for tcgen05, each of which takes 44-59 cycles to issue, as much
-// as the whole page takes here, and its operands would have to be written to shared
-// memory as bf16 first.
+// products too small for tcgen05, each of which takes 44-59 cycles to issue (the
+// three as much as the whole page takes here), and its operands would have to be
+// written to shared memory as bf16 first.
 //
 // Few chunks: one CTA (4 warps) per (sequence, kv-head, chunk), which finishes
 // a chunk soonest (one sequence of 8192 tokens 11.1 us, of 300 6.7 us).  The
