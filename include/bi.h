@@ -24,7 +24,8 @@
  * Data types: all activations, weights, caches and outputs are bf16
  * (IEEE binary32 truncated to its top 16 bits); arithmetic is fp32; every
  * output is rounded once, to nearest-even, to bf16.  Log-probabilities are
- * fp32, and a KV cache can also be held in 4 bits (bi_kv4_append).
+ * fp32, a KV cache can also be held in 4 bits (bi_kv4_append), and weights and
+ * activations of linear layers in 8 (bi_quantize_fp8).
  */
 #ifndef BI_H_
 #define BI_H_
@@ -48,6 +49,10 @@ extern "C" {
 #define BI_DECODE_COUNTER_BYTES 262144
 /* Bytes of one (page, kv-head) block of K or of V in a 4-bit cache. */
 #define BI_KV4_BLOCK_BYTES 1152
+/* Values of a row that share a scale in an 8-bit matrix, and the bytes of one
+ * tile of scales (128 rows x 4 such blocks). */
+#define BI_FP8_BLOCK 128
+#define BI_FP8_TILE_BYTES 512
 /* The most alternatives bi_logprobs_top gives for a row. */
 #define BI_MAX_TOP_LOGPROBS 32
 
@@ -510,6 +515,109 @@ bi_status bi_logprobs_top(const void* logits, int64_t rows, int32_t vocab, int64
                           const int32_t* targets, float* logprob_out, float* lse_out,
                           float* entropy_out, int32_t k, int32_t* top_ids, float* top_logprobs,
                           cudaStream_t stream);
+
+/*
+ * 8-bit matrices.  A matrix of `rows` rows of K values (K a multiple of 16) is
+ * held as e4m3 codes [rows][ld], ld >= K a multiple of 16 bytes, and scales.
+ * A block of BI_FP8_BLOCK = 128 consecutive values of a row, from the row's start
+ * on (the last may be shorter), has one scale 2^(b - 127), b a byte, and stands
+ * for code * 2^(b - 127):
+ *     b = the least number from 8 up with max|x| <= 448 * 2^(b - 127)
+ *     code = x / 2^(b - 127) rounded to nearest even
+ * so that a value is off by at most 2^-4 of itself, or by 2^-10 of its block's
+ * scale where that is more.  The scale being a power of two costs nothing of that
+ * and is what the tensor core multiplies in by itself.  A block with a NaN or an
+ * infinity stands for NaN throughout (b = 255).  Scales lie in tiles of
+ * BI_FP8_TILE_BYTES = 512 bytes, [ceil(rows / 128)][ceil(K / 512)]: block c of row
+ * r has byte 16 (r % 32) + 4 (r % 128 / 32) + c % 4 of tile [r / 128][c / 4].
+ * Bytes of rows past the last, and of blocks past a row's last, are never part of
+ * a result, whatever they hold.  Pointers to codes and scales must be 16-byte
+ * aligned.
+ *
+ * bi_fp8_scales_size -- bytes of the scales of a matrix; 0 for invalid arguments.
+ */
+size_t bi_fp8_scales_size(int64_t rows, int32_t K);
+
+/*
+ * bi_quantize_fp8 -- bf16 rows to an 8-bit matrix: weights once, and activations
+ * that no norm produced (the attention output in front of its projection).  A
+ * row's bytes depend on that row's values only.
+ *   x       device, bf16 [rows][ld_x], ld_x >= K, a multiple of 8.
+ *   q       device, e4m3 [rows][ld_q].   scales  device, bi_fp8_scales_size bytes.
+ *   rows    0 .. 2^31-1;  K  a multiple of 16, >= 16.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA.
+ */
+bi_status bi_quantize_fp8(const void* x, int64_t ld_x, int64_t rows, int32_t K, void* q,
+                          int64_t ld_q, void* scales, cudaStream_t stream);
+
+/*
+ * bi_fp8_read -- an 8-bit matrix back to bf16 [rows][ld_out].  Nothing is rounded
+ * (a code times its scale is a bf16 number; one of 2^128 is an infinity).
+ * Arguments and errors as bi_quantize_fp8.
+ */
+bi_status bi_fp8_read(const void* q, int64_t ld_q, const void* scales, int64_t rows, int32_t K,
+                      void* out, int64_t ld_out, cudaStream_t stream);
+
+/*
+ * bi_rmsnorm_fp8, bi_add_rmsnorm_fp8 -- bi_rmsnorm and bi_add_rmsnorm with an 8-bit
+ * output: x * rsqrt(mean_j x_j^2 + eps) * w, the reduction bi_rmsnorm's in its
+ * order, goes to 8 bits from fp32 (one rounding; not through bf16).  The sum
+ * bf16(residual + x) is written to residual_out, which may be residual itself (as
+ * bi_add_rmsnorm does) or another buffer.
+ *   q, scales   an 8-bit matrix of `rows` rows of `hidden` values.
+ *   hidden      a multiple of 16, 16 .. 32768;  ld_q  a multiple of 16, >= hidden.
+ * Other arguments and errors as bi_rmsnorm and bi_add_rmsnorm; q and scales must
+ * not overlap the inputs.
+ */
+bi_status bi_rmsnorm_fp8(const void* x, const void* w, void* q, void* scales, int64_t rows,
+                         int32_t hidden, int64_t ld_x, int64_t ld_q, float eps,
+                         cudaStream_t stream);
+bi_status bi_add_rmsnorm_fp8(const void* x, const void* residual, void* residual_out,
+                             const void* w, void* q, void* scales, int64_t rows, int32_t hidden,
+                             int64_t ld_x, int64_t ld_res, int64_t ld_res_out, int64_t ld_q,
+                             float eps, cudaStream_t stream);
+
+/*
+ * bi_gemm_fp8 -- y[M][N] = bf16( x[M][K] . W[N][K]^T ) of two 8-bit matrices, fp32
+ * accumulation.
+ *
+ * Operation: "2. Batch-Invariant Matrix Multiplication" of "Defeating
+ * Nondeterminism in LLM Inference: The Core Role of Batch Invariance".  The
+ * order is fixed by K alone: K is cut into P <= 8 parts of L runs of 512 values
+ * (S = ceil(K / 512), L = ceil(S / 8), P = ceil(S / L)); a part is one tensor-core
+ * accumulation over its values ascending, 32 at a time, and the parts' sums are
+ * added ascending in fp32.  Where that is done (one SM after another's tiles for
+ * many rows, the parts on a cluster of SMs for few) follows M and does not show:
+ * a row's bits are the same in any batch.  No workspace, no atomics.
+ *
+ *   x, x_scales  an 8-bit matrix of M rows of K values, leading dimension ld_x.
+ *   W, W_scales  an 8-bit matrix of N rows of K values (nn.Linear layout), ld_w.
+ *   y            device, bf16 [M][ld_y], 16-byte aligned; no overlap with the rest.
+ *   M  0 .. 2^31-257;  N >= 8, a multiple of 8;  K >= 16, a multiple of 16.
+ *   ld_x, ld_w  >= K, multiples of 16;  ld_y  >= N, a multiple of 8.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA.
+ */
+bi_status bi_gemm_fp8(const void* x, const void* x_scales, const void* W, const void* W_scales,
+                      void* y, int32_t M, int32_t N, int32_t K, int64_t ld_x, int64_t ld_w,
+                      int64_t ld_y, cudaStream_t stream);
+
+/*
+ * bi_gemm_fp8_swiglu -- the gate|up projection of a SwiGLU MLP with the product,
+ * 8 bits in and 8 bits out, ready for the down projection:
+ *     h[M][F] = silu(g) * u held in 8 bits,   g = x . W_gate^T,  u = x . W_up^T
+ * with g and u in fp32 as bi_gemm_fp8 sums them (not rounded), silu as bi_silu_mul,
+ * and one rounding, that of h to its codes.  The fused epilogue writes neither
+ * [M][2F] nor a bf16 h.
+ *   W_gu, W_gu_scales   an 8-bit matrix of 2F rows of K values, the gate and up
+ *                       rows interleaved in groups of 8 as bi_gemm_swiglu's.
+ *   h, h_scales         an 8-bit matrix of M rows of F values, leading dimension
+ *                       ld_h >= F, a multiple of 16; no overlap with the rest.
+ *   F  >= 16, a multiple of 16.  Other arguments and errors as bi_gemm_fp8.
+ */
+bi_status bi_gemm_fp8_swiglu(const void* x, const void* x_scales, const void* W_gu,
+                             const void* W_gu_scales, void* h, void* h_scales, int32_t M, int32_t F,
+                             int32_t K, int64_t ld_x, int64_t ld_w, int64_t ld_h,
+                             cudaStream_t stream);
 
 /*
  * bi_decode_attention_fixed_splits -- the same attention with a fixed split

@@ -21,6 +21,13 @@ tensors must live on a CUDA device, and a missing library raises.
     kv4_read(...)                         read sequences back into a bf16 cache (prefill's)
     decode_attention_kv4(...)             decode attention over the 4-bit cache
     logprobs_top(logits, targets, k)      log-probability, lse, entropy, k best tokens
+    quantize_fp8(x), fp8_read(q, scales)  bf16 rows to 8 bits (e4m3, a scale for each 128 values)
+                                          and back
+    rmsnorm_fp8(...), add_rmsnorm_fp8(...)
+                                          the norms with an 8-bit output
+    gemm_fp8(x, x_scales, W, W_scales)    y = x @ W.T of two 8-bit matrices, bf16 out
+    gemm_fp8_swiglu(x, x_scales, W_gu, W_gu_scales)
+                                          silu(x @ W_gate.T) * (x @ W_up.T), 8 bits in and out
 
 Every output row's bits depend only on that row's own inputs (batch
 invariance); see include/bi.h for the exact contract of each call.
@@ -32,8 +39,8 @@ import math
 import torch
 
 from . import _lib
-from ._lib import (DECODE_CHUNK, DECODE_COUNTER_BYTES, KV4_BLOCK_BYTES, MAX_TOP_LOGPROBS,
-                   PAGE_SIZE)
+from ._lib import (DECODE_CHUNK, DECODE_COUNTER_BYTES, FP8_BLOCK, FP8_TILE_BYTES,
+                   KV4_BLOCK_BYTES, MAX_TOP_LOGPROBS, PAGE_SIZE)
 
 __all__ = ["BiError", "rmsnorm", "gemm", "gemm_swiglu", "interleave_gate_up",
            "decode_attention", "decode_attention_fixed_splits",
@@ -43,7 +50,8 @@ __all__ = ["BiError", "rmsnorm", "gemm", "gemm_swiglu", "interleave_gate_up",
            "decode_num_chunks", "decode_chunk_len", "get_device_error", "abi_version",
            "status_string", "PAGE_SIZE", "DECODE_CHUNK", "kv4_cache", "kv4_append",
            "qk_norm_rope_append_kv4", "kv4_read", "decode_attention_kv4", "logprobs_top",
-           "KV4_BLOCK_BYTES", "MAX_TOP_LOGPROBS"]
+           "KV4_BLOCK_BYTES", "MAX_TOP_LOGPROBS", "fp8_scales_shape", "quantize_fp8", "fp8_read",
+           "rmsnorm_fp8", "add_rmsnorm_fp8", "gemm_fp8", "gemm_fp8_swiglu", "FP8_BLOCK"]
 
 
 def _stream_of(device: int) -> int:
@@ -662,3 +670,179 @@ def logprobs_top(logits: torch.Tensor, targets: torch.Tensor | None, k: int, str
         lse.data_ptr(), entropy.data_ptr(), k, ids.data_ptr(), top.data_ptr(),
         _raw_stream(dev) if stream is None else _stream(stream)), "bi_logprobs_top")
     return lp, lse, entropy, ids, top
+
+
+# ------------------------------------------------------ 8-bit linear path ----
+# An 8-bit matrix is a pair: codes [rows, K] float8_e4m3fn (rows may lie apart by a
+# multiple of 16), and scales, uint8 of fp8_scales_shape(rows, K), contiguous.
+_F8 = torch.float8_e4m3fn
+
+
+def fp8_scales_shape(rows: int, K: int) -> tuple[int, int, int]:
+    """Shape of the scales of an 8-bit matrix [rows, K]: tiles of 128 rows by 4
+    blocks of 128 values (include/bi.h gives a scale's place in its tile)."""
+    return (rows + 127) // 128, (K + 511) // 512, FP8_TILE_BYTES
+
+
+def _refuse_rows(where: str, name: str, t: torch.Tensor, dtype, shape=None):
+    """Raise if t is not a 2-D CUDA tensor of that type, and shape, whose rows
+    are each in one run."""
+    if not t.is_cuda:
+        raise ValueError(f"{where}: {name} must be a CUDA tensor (no CPU path exists)")
+    if t.dtype != dtype:
+        raise ValueError(f"{where}: {name} must be {str(dtype).split('.')[-1]}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{where}: {name} must have shape {shape or '[rows, columns]'}, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{where}: {name} must have unit stride along its last dimension")
+    if t.get_device() != _current_device():
+        raise ValueError(f"{where}: {name} must be on the current CUDA device ({_current_device()})")
+
+
+def _rows_of(where: str, name: str, t: torch.Tensor, dtype, rows: int, columns: int, dev: int) -> int:
+    """The leading dimension of t, which has to be rows x columns of dtype on dev."""
+    if not (t.dtype is dtype and t.shape == (rows, columns) and t.get_device() == dev
+            and (t.stride(1) == 1 or columns == 1)):
+        _refuse_rows(where, name, t, dtype, (rows, columns))
+    return t.stride(0) if rows > 1 else -(-columns // 16) * 16
+
+
+def _scales_of(where: str, name: str, t: torch.Tensor, rows: int, K: int, dev: int) -> int:
+    if not (t.dtype is _U8 and t.shape == ((rows + 127) // 128, (K + 511) // 512, FP8_TILE_BYTES)
+            and t.get_device() == dev and t.is_contiguous()):
+        _refuse(where, (t, name, _U8, fp8_scales_shape(rows, K)))
+    return t.data_ptr()
+
+
+def _new_fp8(stream, out, scales, rows: int, K: int, device):
+    if out is None:
+        out = _made(stream, torch.empty, (rows, K), dtype=_F8, device=device)
+    if scales is None:
+        scales = _made(stream, torch.empty, fp8_scales_shape(rows, K), dtype=_U8, device=device)
+    return out, scales
+
+
+def _shape_2d(where: str, name: str, t: torch.Tensor):
+    if t.dim() != 2:
+        raise ValueError(f"{where}: {name} must be 2-D, got {tuple(t.shape)}")
+    return t.shape
+
+
+def quantize_fp8(x: torch.Tensor, out: torch.Tensor | None = None,
+                 scales: torch.Tensor | None = None, stream=None):
+    """bf16 x [rows, K] as an 8-bit matrix (codes, scales): e4m3 and one power of
+    two for each 128 values of a row.  K must be a multiple of 16."""
+    where = "quantize_fp8"
+    dev = _current_device()
+    rows, K = _shape_2d(where, "x", x)
+    ld_x = _rows_of(where, "x", x, _BF16, rows, K, dev)
+    out, scales = _new_fp8(stream, out, scales, rows, K, x.device)
+    _check(_lib.load().bi_quantize_fp8(
+        x.data_ptr(), ld_x, rows, K, out.data_ptr(), _rows_of(where, "out", out, _F8, rows, K, dev),
+        _scales_of(where, "scales", scales, rows, K, dev),
+        _raw_stream(dev) if stream is None else _stream(stream)), "bi_quantize_fp8")
+    return out, scales
+
+
+def fp8_read(q: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor:
+    """What an 8-bit matrix stands for, in bf16 (nothing is rounded)."""
+    where = "fp8_read"
+    dev = _current_device()
+    rows, K = _shape_2d(where, "q", q)
+    ld_q = _rows_of(where, "q", q, _F8, rows, K, dev)
+    if out is None:
+        out = _made(stream, torch.empty, (rows, K), dtype=_BF16, device=q.device)
+    _check(_lib.load().bi_fp8_read(
+        q.data_ptr(), ld_q, _scales_of(where, "scales", scales, rows, K, dev), rows, K, out.data_ptr(),
+        _rows_of(where, "out", out, _BF16, rows, K, dev),
+        _raw_stream(dev) if stream is None else _stream(stream)), "bi_fp8_read")
+    return out
+
+
+def rmsnorm_fp8(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6,
+                out: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """rmsnorm(x, w, eps) as an 8-bit matrix (codes, scales), rounded once."""
+    where = "rmsnorm_fp8"
+    dev = _current_device()
+    rows, hidden = _shape_2d(where, "x", x)
+    ld_x = _rows_of(where, "x", x, _BF16, rows, hidden, dev)
+    if not (w.dtype is _BF16 and w.shape == (hidden,) and w.is_contiguous() and w.get_device() == dev):
+        _refuse(where, (w, "w", _BF16, (hidden,)))
+    out, scales = _new_fp8(stream, out, scales, rows, hidden, x.device)
+    _check(_lib.load().bi_rmsnorm_fp8(
+        x.data_ptr(), w.data_ptr(), out.data_ptr(), _scales_of(where, "scales", scales, rows, hidden, dev),
+        rows, hidden, ld_x, _rows_of(where, "out", out, _F8, rows, hidden, dev), eps,
+        _raw_stream(dev) if stream is None else _stream(stream)), "bi_rmsnorm_fp8")
+    return out, scales
+
+
+def add_rmsnorm_fp8(x: torch.Tensor, residual: torch.Tensor, w: torch.Tensor, eps: float = 1e-6,
+                    residual_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    scales: torch.Tensor | None = None, stream=None):
+    """residual_out = residual + x (bf16; in place of residual by default), and
+    rmsnorm(residual_out, w, eps) as an 8-bit matrix (codes, scales)."""
+    where = "add_rmsnorm_fp8"
+    dev = _current_device()
+    rows, hidden = _shape_2d(where, "x", x)
+    ld_x = _rows_of(where, "x", x, _BF16, rows, hidden, dev)
+    ld_res = _rows_of(where, "residual", residual, _BF16, rows, hidden, dev)
+    if not (w.dtype is _BF16 and w.shape == (hidden,) and w.is_contiguous() and w.get_device() == dev):
+        _refuse(where, (w, "w", _BF16, (hidden,)))
+    if residual_out is None:
+        residual_out, ld_sum = residual, ld_res
+    else:
+        ld_sum = _rows_of(where, "residual_out", residual_out, _BF16, rows, hidden, dev)
+    out, scales = _new_fp8(stream, out, scales, rows, hidden, x.device)
+    _check(_lib.load().bi_add_rmsnorm_fp8(
+        x.data_ptr(), residual.data_ptr(), residual_out.data_ptr(), w.data_ptr(), out.data_ptr(),
+        _scales_of(where, "scales", scales, rows, hidden, dev), rows, hidden, ld_x, ld_res, ld_sum,
+        _rows_of(where, "out", out, _F8, rows, hidden, dev), eps,
+        _raw_stream(dev) if stream is None else _stream(stream)), "bi_add_rmsnorm_fp8")
+    return out, scales
+
+
+def gemm_fp8(x: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor, W_scales: torch.Tensor,
+             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y = x @ W.T in bf16, of 8-bit matrices x [M, K] and W [N, K] (nn.Linear
+    layout), batch-invariant per row.  K must be a multiple of 16, N of 8."""
+    where = "gemm_fp8"
+    dev = _current_device()
+    M, K = _shape_2d(where, "x", x)
+    N = _shape_2d(where, "W", W)[0]
+    ld_x = _rows_of(where, "x", x, _F8, M, K, dev)
+    ld_w = _rows_of(where, "W", W, _F8, N, K, dev)
+    if out is None:
+        out = _made(stream, torch.empty, (M, N), dtype=_BF16, device=x.device)
+    _check(_lib.load().bi_gemm_fp8(
+        x.data_ptr(), _scales_of(where, "x_scales", x_scales, M, K, dev), W.data_ptr(),
+        _scales_of(where, "W_scales", W_scales, N, K, dev), out.data_ptr(), M, N, K, ld_x, ld_w,
+        _rows_of(where, "out", out, _BF16, M, N, dev),
+        _raw_stream(dev) if stream is None else _stream(stream)), "bi_gemm_fp8")
+    return out
+
+
+def gemm_fp8_swiglu(x: torch.Tensor, x_scales: torch.Tensor, W_gu: torch.Tensor,
+                    W_gu_scales: torch.Tensor, out: torch.Tensor | None = None,
+                    scales: torch.Tensor | None = None, stream=None):
+    """h = silu(x @ W_gate.T) * (x @ W_up.T) as an 8-bit matrix [M, F] (codes,
+    scales), from 8-bit x [M, K] and W_gu [2F, K], the gate and up rows interleaved
+    as interleave_gate_up does (quantise the interleaved weight).  F and K must be
+    multiples of 16."""
+    where = "gemm_fp8_swiglu"
+    dev = _current_device()
+    M, K = _shape_2d(where, "x", x)
+    F2 = _shape_2d(where, "W_gu", W_gu)[0]
+    if F2 % 32:
+        raise ValueError(f"{where}: W_gu must have 2F rows, F a multiple of 16")
+    F = F2 // 2
+    ld_x = _rows_of(where, "x", x, _F8, M, K, dev)
+    ld_w = _rows_of(where, "W_gu", W_gu, _F8, F2, K, dev)
+    out, scales = _new_fp8(stream, out, scales, M, F, x.device)
+    _check(_lib.load().bi_gemm_fp8_swiglu(
+        x.data_ptr(), _scales_of(where, "x_scales", x_scales, M, K, dev), W_gu.data_ptr(),
+        _scales_of(where, "W_gu_scales", W_gu_scales, F2, K, dev), out.data_ptr(),
+        _scales_of(where, "scales", scales, M, F, dev), M, F, K, ld_x, ld_w,
+        _rows_of(where, "out", out, _F8, M, F, dev),
+        _raw_stream(dev) if stream is None else _stream(stream)), "bi_gemm_fp8_swiglu")
+    return out, scales

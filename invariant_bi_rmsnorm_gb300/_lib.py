@@ -25,6 +25,8 @@ DECODE_CHUNK = 256
 DECODE_COUNTER_BYTES = 262144  # arrival counters at the start of an attention workspace
 KV4_BLOCK_BYTES = 1152  # one (page, kv-head) block of K or of V in a 4-bit cache
 MAX_TOP_LOGPROBS = 32
+FP8_BLOCK = 128  # values of a row that share a scale in an 8-bit matrix
+FP8_TILE_BYTES = 512  # scales of 128 rows x 4 blocks
 
 # every entry point include/bi.h declares
 EXPORTS = (
@@ -38,6 +40,8 @@ EXPORTS = (
     "bi_gemm_swiglu",
     "bi_kv4_append", "bi_qk_norm_rope_append_kv4", "bi_kv4_read", "bi_decode_attention_kv4",
     "bi_logprobs_top",
+    "bi_fp8_scales_size", "bi_quantize_fp8", "bi_fp8_read", "bi_rmsnorm_fp8", "bi_add_rmsnorm_fp8",
+    "bi_gemm_fp8", "bi_gemm_fp8_swiglu",
 )
 
 _lib = None
@@ -119,6 +123,22 @@ def load() -> ctypes.CDLL:
     lib.bi_decode_attention_kv4.restype = ctypes.c_int
     lib.bi_logprobs_top.argtypes = [_vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp]
     lib.bi_logprobs_top.restype = ctypes.c_int
+    lib.bi_fp8_scales_size.argtypes = [_i64, _i32]
+    lib.bi_fp8_scales_size.restype = ctypes.c_size_t
+    lib.bi_quantize_fp8.argtypes = [_vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp]
+    lib.bi_quantize_fp8.restype = ctypes.c_int
+    lib.bi_fp8_read.argtypes = [_vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp]
+    lib.bi_fp8_read.restype = ctypes.c_int
+    lib.bi_rmsnorm_fp8.argtypes = [_vp, _vp, _vp, _vp, _i64, _i32, _i64, _i64, ctypes.c_float, _vp]
+    lib.bi_rmsnorm_fp8.restype = ctypes.c_int
+    lib.bi_add_rmsnorm_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i64, _i64, _i64,
+                                       _i64, ctypes.c_float, _vp]
+    lib.bi_add_rmsnorm_fp8.restype = ctypes.c_int
+    lib.bi_gemm_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i64, _i64, _i64, _vp]
+    lib.bi_gemm_fp8.restype = ctypes.c_int
+    lib.bi_gemm_fp8_swiglu.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i64, _i64,
+                                       _i64, _vp]
+    lib.bi_gemm_fp8_swiglu.restype = ctypes.c_int
     lib.bi_selftest_wait_timeout.argtypes = [_i32, _vp]
     lib.bi_selftest_wait_timeout.restype = ctypes.c_int
     _lib = lib

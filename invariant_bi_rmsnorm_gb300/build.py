@@ -24,7 +24,7 @@ OBJ_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["api.cu", "rmsnorm.cu", "gemm.cu", "decode_attention.cu", "prefill_attention.cu",
            "decoder_ops.cu", "logprobs.cu", "kv4_cache.cu", "kv4_attention.cu",
-           "logprobs_top.cu"]
+           "logprobs_top.cu", "fp8_quant.cu", "gemm_fp8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]

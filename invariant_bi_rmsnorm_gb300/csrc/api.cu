@@ -71,21 +71,28 @@ int sm_count() {
     return g_sm_count[dev];
 }
 
+namespace {
+
+// cuTensorMapEncodeTiled, looked up at first use.
+bool resolve_encode() {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (g_encode) return true;
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn)
+        return false;
+    g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+    return true;
+}
+
+}  // namespace
+
 CUresult encode_tensor_map_2d(CUtensorMap* map, const void* base, uint64_t inner_elems,
                               uint64_t outer_rows, uint64_t row_stride_bytes, uint32_t box_inner,
                               uint32_t box_outer) {
-    {
-        std::lock_guard<std::mutex> lk(g_mu);
-        if (!g_encode) {
-            void* fn = nullptr;
-            cudaDriverEntryPointQueryResult q{};
-            if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                                 cudaEnableDefault, &q) != cudaSuccess ||
-                q != cudaDriverEntryPointSuccess || !fn)
-                return CUDA_ERROR_NOT_FOUND;
-            g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-        }
-    }
+    if (!resolve_encode()) return CUDA_ERROR_NOT_FOUND;
     cuuint64_t dims[2] = {inner_elems, outer_rows};
     cuuint64_t strides[1] = {row_stride_bytes};
     cuuint32_t box[2] = {box_inner, box_outer};
@@ -126,6 +133,29 @@ CUresult encode_q_map(CUtensorMap* map, const void* base, uint64_t T, uint64_t H
                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+CUresult encode_byte_map_2d(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows,
+                            uint64_t row_stride_bytes, uint32_t box_rows) {
+    if (!resolve_encode()) return CUDA_ERROR_NOT_FOUND;
+    cuuint64_t dims[2] = {row_bytes, rows};
+    cuuint64_t strides[1] = {row_stride_bytes};
+    cuuint32_t box[2] = {128, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+CUresult encode_scale_map(CUtensorMap* map, const void* base, uint64_t tiles) {
+    if (!resolve_encode()) return CUDA_ERROR_NOT_FOUND;
+    cuuint64_t dims[2] = {128, tiles};  // 32-bit words
+    cuuint64_t strides[1] = {512};
+    cuuint32_t box[2] = {128, 1};
+    cuuint32_t estr[2] = {1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 }  // namespace bi

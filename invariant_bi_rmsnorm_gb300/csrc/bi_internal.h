@@ -1,5 +1,6 @@
 // Declarations shared by the library's translation units (not part of the ABI).
 #pragma once
+#include <atomic>
 #include <cstdint>
 
 #include <cuda.h>  // CUtensorMap and its enums only; libcuda is not linked
@@ -33,6 +34,7 @@ enum : uint32_t {
     kWhereAttnMerge = 6u << 8,
     kWhereSelftest = 7u << 8,
     kWhereDecoderOps = 8u << 8,
+    kWhereGemmFp8 = 9u << 8,
 };
 
 // Device address of the current device's error word (nullptr on failure).
@@ -59,7 +61,29 @@ CUresult encode_page_map(CUtensorMap* map, const void* base, uint64_t rows);
 CUresult encode_q_map(CUtensorMap* map, const void* base, uint64_t T, uint64_t Hq,
                       uint32_t box_heads, uint32_t box_rows);
 
+// Rows of bytes, as encode_tensor_map_2d: a box of 128 bytes x box_rows, 128-byte
+// swizzled (8-bit operands: one block of 128 values a row).
+CUresult encode_byte_map_2d(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows,
+                            uint64_t row_stride_bytes, uint32_t box_rows);
+
+// Scale tiles of 512 contiguous bytes each; the box is one tile, as it lies.
+CUresult encode_scale_map(CUtensorMap* map, const void* base, uint64_t tiles);
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Set a kernel's dynamic shared memory limit on the current device once; `set`
+// is one flag per device (any thread may race to set it, the attribute is
+// idempotent).
+template <typename Kernel>
+bool allow_smem(Kernel kernel, int bytes, std::atomic<bool> (&set)[64]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (set[dev]) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return false;
+    set[dev] = true;
+    return true;
+}
 
 // Launch with programmatic stream serialization: the grid may be scheduled
 // while the previous kernel in the stream finishes.  Every kernel launched
@@ -78,6 +102,27 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The same in clusters of `cluster` CTAs along x.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), unsigned cluster, dim3 grid, dim3 block,
+                               size_t smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

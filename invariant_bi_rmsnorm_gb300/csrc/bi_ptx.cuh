@@ -335,6 +335,60 @@ __device__ __forceinline__ void tc_commit_pair_multicast(uint64_t* bar, uint16_t
         : "memory");
 }
 
+// --------------------------------------- tcgen05 with scales per block ----
+// D[tmem] (+)= (A * scales) . (B * scales)^T, kind::mxf8f6f4: 8-bit operands in
+// shared memory, one power-of-two scale byte per row and 32 values of K, taken
+// from tensor memory at sfa / sfb (byte: the descriptor's scale-factor ids).
+__device__ __forceinline__ void tc_mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// The same over a CTA pair, as tc_mma_f16_pair; each CTA's tensor memory holds
+// its own rows' A scales and the scales of all of B's rows.
+__device__ __forceinline__ void tc_mma_mxf8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                                 uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Copy 32 rows of 16 bytes from shared memory to four tensor-memory columns, the
+// same in each quarter of the lanes: a scale tile (128 rows x 4 bytes) to where
+// the MMAs read it.  Executes in order before this thread's later MMAs.  The
+// pair form copies in both CTAs, from the same offsets.
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t s_desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_cp_scales_pair(uint32_t taddr, uint64_t s_desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc)
+                 : "memory");
+}
+
+// 16 bytes of shared memory of a CTA of the cluster (cluster address).
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 // Integer add at device scope with acquire-release semantics; returns the old
 // value.  After a CTA barrier, one thread's release publishes the whole CTA's
 // earlier writes; its acquire, followed by a CTA barrier, lets every thread

@@ -19,6 +19,7 @@
 
 #include "bi_internal.h"
 #include "bi_ptx.cuh"
+#include "fp8.cuh"
 
 namespace {
 
@@ -44,11 +45,22 @@ __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v 
 
 // kAdd: the fused form -- first res = bf16(res + x) (fp32 add, one rounding),
 // stored back, then the RMSNorm of that sum with exactly the reduction below.
-template <int VPT, bool kAdd>
+// kFp8: (x * r) * w goes to 8 bits instead of bf16, rounded once (fp8.cuh): the
+// 16 threads that hold a block of 128 values find its largest magnitude by a
+// butterfly, and the row's scale bytes leave by way of shared memory, a word of
+// four at a time.
+struct Fp8Out {
+    uint8_t* scales;
+    int spans;
+    __nv_bfloat16* res_out;  // where the sum goes: res itself, or another buffer
+    int64_t ld_res_out;
+};
+
+template <int VPT, bool kAdd, bool kFp8>
 __global__ void __launch_bounds__(kMaxThreads)
-    rmsnorm_kernel(const __nv_bfloat16* x, const __nv_bfloat16* __restrict__ w, __nv_bfloat16* y,
+    rmsnorm_kernel(const __nv_bfloat16* x, const __nv_bfloat16* __restrict__ w, void* y,
                    int hidden, int64_t ld_x, int64_t ld_y, float eps, __nv_bfloat16* res,
-                   int64_t ld_res, int64_t rows, int64_t ahead) {
+                   int64_t ld_res, int64_t rows, int64_t ahead, Fp8Out fp8) {
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
     __shared__ float warp_sums[kMaxThreads / 32];
@@ -72,7 +84,9 @@ __global__ void __launch_bounds__(kMaxThreads)
         xv[j] = (v < nvec) ? __ldcs(xr + v) : make_uint4(0, 0, 0, 0);
     }
     if constexpr (kAdd) {
-        uint4* rr = reinterpret_cast<uint4*>(res + row * ld_res);
+        const uint4* rr = reinterpret_cast<const uint4*>(res + row * ld_res);
+        uint4* ro = reinterpret_cast<uint4*>(kFp8 ? fp8.res_out + row * fp8.ld_res_out
+                                                  : res + row * ld_res);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = tid + j * T;
@@ -86,7 +100,7 @@ __global__ void __launch_bounds__(kMaxThreads)
                 o[e] = bi::pack_bf16x2(__fadd_rn(bf16_lo(ru[e]), bf16_lo(xu[e])),
                                        __fadd_rn(bf16_hi(ru[e]), bf16_hi(xu[e])));
             xv[j] = make_uint4(o[0], o[1], o[2], o[3]);
-            rr[v] = xv[j];
+            ro[v] = xv[j];
         }
     }
 
@@ -110,7 +124,48 @@ __global__ void __launch_bounds__(kMaxThreads)
     for (int i = 1; i < nwarps; ++i) total += warp_sums[i];
     const float r = rsqrtf(__fdiv_rn(total, static_cast<float>(hidden)) + eps);
 
-    uint4* yr = reinterpret_cast<uint4*>(y + row * ld_y);
+    if constexpr (kFp8) {
+        __shared__ uint8_t s_byte[32768 / bi_fp8::kBlock];
+        uint2* qr = reinterpret_cast<uint2*>(static_cast<uint8_t*>(y) + row * ld_y);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = tid + j * T;
+            const uint4 wv = (v < nvec) ? __ldg(wr + v) : make_uint4(0, 0, 0, 0);
+            const uint32_t xu[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
+            const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
+            float f[8];
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f[2 * e] = __fmul_rn(__fmul_rn(bf16_lo(xu[e]), r), bf16_lo(wu[e]));
+                f[2 * e + 1] = __fmul_rn(__fmul_rn(bf16_hi(xu[e]), r), bf16_hi(wu[e]));
+                top = max(top, max(__float_as_uint(f[2 * e]) & 0x7fffffffu,
+                                   __float_as_uint(f[2 * e + 1]) & 0x7fffffffu));
+            }
+            // threads past the row's end hold zeros of no row, and must not bring in 0 * r = NaN
+            if (v >= nvec) top = 0;
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const uint32_t b = bi_fp8::scale_byte(top);
+            if (v >= nvec) continue;
+            if ((tid & 15) == 0) s_byte[v >> 4] = static_cast<uint8_t>(b);
+            const float inv = bi_fp8::inverse_scale(b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], inv);
+            qr[v] = make_uint2(bi_fp8::codes4(f[0], f[1], f[2], f[3]),
+                               bi_fp8::codes4(f[4], f[5], f[6], f[7]));
+        }
+        __syncthreads();
+        for (int i = tid; i < fp8.spans; i += T) {
+            uint32_t word = 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (4 * i + c < (nvec + 15) >> 4) word |= static_cast<uint32_t>(s_byte[4 * i + c]) << (8 * c);
+            *reinterpret_cast<uint32_t*>(fp8.scales + bi_fp8::scale_word(row, i, fp8.spans)) = word;
+        }
+        return;
+    }
+    uint4* yr = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(y) + row * ld_y);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int v = tid + j * T;
@@ -133,21 +188,26 @@ __global__ void __launch_bounds__(kMaxThreads)
 
 namespace {
 
-template <bool kAdd>
+template <bool kAdd, bool kFp8>
 bi_status launch_rmsnorm(const void* x, const void* w, void* y, int64_t rows, int32_t hidden,
                          int64_t ld_x, int64_t ld_y, float eps, void* res, int64_t ld_res,
-                         cudaStream_t stream) {
+                         const Fp8Out& fp8, cudaStream_t stream) {
+    constexpr int kMask = kFp8 ? 15 : 7;  // 16-byte rows of y
     if (rows < 0 || rows > 0x7fffffffLL) return BI_ERR_INVALID_ARG;
     if (!(eps >= 0.f) || eps != eps || eps > 3.0e38f) return BI_ERR_INVALID_ARG;
-    if (hidden < 8 || hidden > 32768 || (hidden & 7)) return BI_ERR_UNSUPPORTED_SHAPE;
+    if (hidden < 8 || hidden > 32768 || (hidden & kMask)) return BI_ERR_UNSUPPORTED_SHAPE;
     if (ld_x < hidden || ld_y < hidden) return BI_ERR_INVALID_ARG;
-    if ((ld_x & 7) || (ld_y & 7)) return BI_ERR_MISALIGNED;
+    if ((ld_x & 7) || (ld_y & kMask)) return BI_ERR_MISALIGNED;
     if (kAdd && ld_res < hidden) return BI_ERR_INVALID_ARG;
     if (kAdd && (ld_res & 7)) return BI_ERR_MISALIGNED;
+    if (kAdd && kFp8 && fp8.ld_res_out < hidden) return BI_ERR_INVALID_ARG;
+    if (kAdd && kFp8 && (fp8.ld_res_out & 7)) return BI_ERR_MISALIGNED;
     if (rows == 0) return BI_OK;
-    if (!x || !w || !y || (kAdd && !res)) return BI_ERR_INVALID_ARG;
+    if (!x || !w || !y || (kAdd && !res) || (kFp8 && !fp8.scales) || (kAdd && kFp8 && !fp8.res_out))
+        return BI_ERR_INVALID_ARG;
     if (!bi::aligned16(x) || !bi::aligned16(w) || !bi::aligned16(y) ||
-        (kAdd && !bi::aligned16(res)))
+        (kAdd && !bi::aligned16(res)) || (kFp8 && !bi::aligned16(fp8.scales)) ||
+        (kAdd && kFp8 && !bi::aligned16(fp8.res_out)))
         return BI_ERR_MISALIGNED;
 
     // Thread count and vectors per thread depend on `hidden` alone.
@@ -162,21 +222,24 @@ bi_status launch_rmsnorm(const void* x, const void* w, void* y, int64_t rows, in
     }
     const auto* xb = static_cast<const __nv_bfloat16*>(x);
     const auto* wb = static_cast<const __nv_bfloat16*>(w);
-    auto* yb = static_cast<__nv_bfloat16*>(y);
     auto* rb = static_cast<__nv_bfloat16*>(res);
     const dim3 grid(static_cast<unsigned>(rows));
-    cudaError_t err;
     const int64_t ahead = kPrefetchAheadBytes / (int64_t{hidden} * 2 * (kAdd ? 2 : 1));
+    const auto launch = [&](auto kernel) {
+        return bi::launch_pdl(kernel, grid, dim3(threads), 0, stream, xb, wb, y, hidden, ld_x, ld_y,
+                              eps, rb, ld_res, rows, ahead, fp8);
+    };
+    cudaError_t err;
     if (vpt == 1)
-        err = bi::launch_pdl(rmsnorm_kernel<1, kAdd>, grid, dim3(threads), 0, stream, xb, wb, yb, hidden, ld_x, ld_y, eps, rb, ld_res, rows, ahead);
+        err = launch(rmsnorm_kernel<1, kAdd, kFp8>);
     else if (vpt == 2)
-        err = bi::launch_pdl(rmsnorm_kernel<2, kAdd>, grid, dim3(threads), 0, stream, xb, wb, yb, hidden, ld_x, ld_y, eps, rb, ld_res, rows, ahead);
+        err = launch(rmsnorm_kernel<2, kAdd, kFp8>);
     else if (vpt <= 4)
-        err = bi::launch_pdl(rmsnorm_kernel<4, kAdd>, grid, dim3(threads), 0, stream, xb, wb, yb, hidden, ld_x, ld_y, eps, rb, ld_res, rows, ahead);
+        err = launch(rmsnorm_kernel<4, kAdd, kFp8>);
     else if (vpt <= 8)
-        err = bi::launch_pdl(rmsnorm_kernel<8, kAdd>, grid, dim3(threads), 0, stream, xb, wb, yb, hidden, ld_x, ld_y, eps, rb, ld_res, rows, ahead);
+        err = launch(rmsnorm_kernel<8, kAdd, kFp8>);
     else
-        err = bi::launch_pdl(rmsnorm_kernel<16, kAdd>, grid, dim3(threads), 0, stream, xb, wb, yb, hidden, ld_x, ld_y, eps, rb, ld_res, rows, ahead);
+        err = launch(rmsnorm_kernel<16, kAdd, kFp8>);
     if (err != cudaSuccess) return BI_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? BI_OK : BI_ERR_CUDA;
 }
@@ -186,11 +249,32 @@ bi_status launch_rmsnorm(const void* x, const void* w, void* y, int64_t rows, in
 extern "C" bi_status bi_rmsnorm(const void* x, const void* w, void* y, int64_t rows,
                                 int32_t hidden, int64_t ld_x, int64_t ld_y, float eps,
                                 cudaStream_t stream) {
-    return launch_rmsnorm<false>(x, w, y, rows, hidden, ld_x, ld_y, eps, nullptr, hidden, stream);
+    return launch_rmsnorm<false, false>(x, w, y, rows, hidden, ld_x, ld_y, eps, nullptr, hidden, {},
+                                        stream);
 }
 
 extern "C" bi_status bi_add_rmsnorm(const void* x, void* residual, const void* w, void* y,
                                     int64_t rows, int32_t hidden, int64_t ld_x, int64_t ld_res,
                                     int64_t ld_y, float eps, cudaStream_t stream) {
-    return launch_rmsnorm<true>(x, w, y, rows, hidden, ld_x, ld_y, eps, residual, ld_res, stream);
+    return launch_rmsnorm<true, false>(x, w, y, rows, hidden, ld_x, ld_y, eps, residual, ld_res, {},
+                                       stream);
+}
+
+extern "C" bi_status bi_rmsnorm_fp8(const void* x, const void* w, void* q, void* scales,
+                                    int64_t rows, int32_t hidden, int64_t ld_x, int64_t ld_q,
+                                    float eps, cudaStream_t stream) {
+    const Fp8Out fp8{static_cast<uint8_t*>(scales), bi_fp8::spans_of(hidden), nullptr, 0};
+    return launch_rmsnorm<false, true>(x, w, q, rows, hidden, ld_x, ld_q, eps, nullptr, hidden, fp8,
+                                       stream);
+}
+
+extern "C" bi_status bi_add_rmsnorm_fp8(const void* x, const void* residual, void* residual_out,
+                                        const void* w, void* q, void* scales, int64_t rows,
+                                        int32_t hidden, int64_t ld_x, int64_t ld_res,
+                                        int64_t ld_res_out, int64_t ld_q, float eps,
+                                        cudaStream_t stream) {
+    const Fp8Out fp8{static_cast<uint8_t*>(scales), bi_fp8::spans_of(hidden),
+                     static_cast<__nv_bfloat16*>(residual_out), ld_res_out};
+    return launch_rmsnorm<true, true>(x, w, q, rows, hidden, ld_x, ld_q, eps,
+                                      const_cast<void*>(residual), ld_res, fp8, stream);
 }
