@@ -335,6 +335,21 @@ __device__ __forceinline__ void tc_commit_pair_multicast(uint64_t* bar, uint16_t
         : "memory");
 }
 
+// One lane of a converged warp, always the same one.  A loop that the whole warp
+// runs and only one lane of which issues keeps the addresses and descriptors of
+// tcgen05 instructions in uniform registers: 35 cycles an MMA to issue, against 90
+// to 110 where a branch on the lane index encloses the loop (measured, block-scaled
+// form, its scale copies and commits included).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // --------------------------------------- tcgen05 with scales per block ----
 // D[tmem] (+)= (A * scales) . (B * scales)^T, kind::mxf8f6f4: 8-bit operands in
 // shared memory, one power-of-two scale byte per row and 32 values of K, taken

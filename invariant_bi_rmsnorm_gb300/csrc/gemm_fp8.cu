@@ -134,7 +134,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 
     const uint32_t rank = bi::cluster_ctarank();
     const bool leader = rank == 0;
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int lane = threadIdx.x & 31;
     const int num_m = (M + pair::BMP - 1) / pair::BMP;
     const int num_n = (N + pair::BN - 1) / pair::BN;
@@ -219,86 +219,96 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             s_issued = issued;
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {  // the whole warp runs the loop, one lane issues
+            const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+            const uint32_t ring = bi::smem_u32(smem);
             int stage = 0;
             uint32_t phase = 0;
             int acc = 0;             // accumulators in turn, 0 .. 2
             uint32_t acc_phase = 0;  // flips when the turn comes round
-            uint32_t d[2] = {0, 0}, d_acc[2] = {0, 0};
-            uint32_t sf = 0;  // scale place, 0 .. 7
+            int sf = 0;              // scale place, 0 .. 7
             int consumed = 0;
-            bool issued_any = false, ok = true;
+            bool ok = true;
             for (int tile = pair_id; tile < num_tiles && ok; tile += npairs) {
                 uint32_t sfa = 0;
+                int d[2] = {0, 0};
                 int left = 0;  // k-blocks of the part still to come
                 for (int kb = 0; kb < num_kb; ++kb) {
                     const bool first = left == 0;
                     if (first) left = min(part_blocks, num_kb - kb);
                     --left;
-                    if (!bi::mbar_wait(&full[stage], phase)) {
+                    if (!__all_sync(0xffffffffu, bi::mbar_wait(&full[stage], phase))) {
                         ok = false;
                         break;
                     }
                     ++consumed;
                     bi::tc_fence_after();
+                    const uint32_t sa = ring + stage * kStageBytes;
                     if ((kb & 3) == 0) {
                         // The place was last read by MMAs of 8 tiles of scales ago.
                         // They are done: this stage's load waited for the MMAs of
                         // kStages < 8 k-blocks ago, and tiles are a k-block apart at least.
-                        sfa = tmem_base + pair::kScaleCol + 16 * sf;
+                        sfa = tmem + pair::kScaleCol + 16 * sf;
                         sf = (sf + 1) & 7;
-                        const uint32_t s = bi::smem_u32(smem_scales + stage * pair::kScaleBytes);
-                        bi::tc_cp_scales_pair(sfa, scale_desc(s));
-                        bi::tc_cp_scales_pair(sfa + 4, scale_desc(s + kTile));
-                        bi::tc_cp_scales_pair(sfa + 8, scale_desc(s + 2 * kTile));
-                        issued_any = true;
+                        const uint64_t s = scale_desc(ring + kStages * kStageBytes +
+                                                      stage * pair::kScaleBytes);
+                        if (bi::elect_one()) {
+                            bi::tc_cp_scales_pair(sfa, s);
+                            bi::tc_cp_scales_pair(sfa + 4, s + (kTile >> 4));
+                            bi::tc_cp_scales_pair(sfa + 8, s + (2 * kTile >> 4));
+                        }
+                        __syncwarp();
                     }
                     const uint32_t idesc = with_byte(pair::kIdesc, kb & 3);
-                    const uint32_t sa = bi::smem_u32(smem + stage * kStageBytes);
+                    const uint64_t da = operand_desc(sa), db = operand_desc(sa + kABytes);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (first) {
-                            if (!bi::mbar_wait(&tempty[acc], acc_phase ^ 1)) {
+                            if (!__all_sync(0xffffffffu, bi::mbar_wait(&tempty[acc], acc_phase ^ 1))) {
                                 ok = false;
                                 break;
                             }
                             bi::tc_fence_after();
-                            d_acc[h] = acc;
-                            d[h] = tmem_base + 128 * acc;
+                            d[h] = acc;
                             if (++acc == 3) {
                                 acc = 0;
                                 acc_phase ^= 1;
                             }
                         }
-                        const uint32_t sb = sa + kABytes + h * 64 * BK;
+                        if (bi::elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < BK / 32; ++k)
-                            bi::tc_mma_mxf8_pair(d[h], operand_desc(sa + 32 * k),
-                                                 operand_desc(sb + 32 * k), idesc, sfa,
-                                                 sfa + 4 + 4 * h, (!first || k != 0) ? 1u : 0u);
-                        issued_any = true;
-                        if (left == 0)  // the half's part is complete in both CTAs
-                            bi::tc_commit_pair_multicast(&tfull[d_acc[h]], 0x3);
+                            for (int k = 0; k < BK / 32; ++k)  // 32 bytes of K a step
+                                bi::tc_mma_mxf8_pair(tmem + 128 * d[h], da + 2 * k,
+                                                     db + (h * 64 * BK >> 4) + 2 * k, idesc, sfa,
+                                                     sfa + 4 + 4 * h, (!first || k != 0) ? 1u : 0u);
+                            if (left == 0)  // the half's part is complete in both CTAs
+                                bi::tc_commit_pair_multicast(&tfull[d[h]], 0x3);
+                            if (h == 1)  // the stage is free in both CTAs
+                                bi::tc_commit_pair_multicast(&empty[stage], 0x3);
+                        }
+                        __syncwarp();
                     }
                     if (!ok) break;
-                    bi::tc_commit_pair_multicast(&empty[stage], 0x3);  // stage free in both CTAs
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
             }
-            s_consumed = consumed;
-            if (!ok) {
-                bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
-                s_timeout = 1;
+            if (bi::elect_one()) {
+                s_consumed = consumed;
+                if (!ok) {
+                    bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
+                    s_timeout = 1;
+                }
+                if (s_timeout && consumed > 0) {
+                    // what was issued may still read shared memory and write TMEM: a
+                    // bounded wait for it before both are freed
+                    bi::tc_commit_pair_multicast(drain, 0x1);
+                    bi::mbar_wait_for(drain, 0, bi::kDrainNs);
+                }
             }
-            if (s_timeout && issued_any) {
-                // what was issued may still read shared memory and write TMEM: a
-                // bounded wait for it before both are freed
-                bi::tc_commit_pair_multicast(drain, 0x1);
-                bi::mbar_wait_for(drain, 0, bi::kDrainNs);
-            }
+            __syncwarp();
         }
     } else {
         // epilogue warps 2..9: lane quarter warp % 4 of this CTA's 128 rows, and
@@ -476,7 +486,7 @@ __global__ void __launch_bounds__(192)
     float* partial = reinterpret_cast<float*>(smem);  // [NT][WT * 128], over the ring
     __shared__ int s_timeout, s_issued, s_consumed;
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int lane = threadIdx.x & 31;
     const int rank = blockIdx.x;  // the cluster is the grid's x: one CTA a part
     const int nparts = gridDim.x;
@@ -545,42 +555,50 @@ __global__ void __launch_bounds__(192)
             }
             s_issued = issued;
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t sfw = 0;
-            int i = 0;
-            bool ok = true;
-            for (; i < nkb; ++i) {
-                const int stage = i % kStages;
-                if (!bi::mbar_wait(&full[stage], (i / kStages) & 1)) {
-                    ok = false;
-                    break;
-                }
-                bi::tc_fence_after();
+    } else if (warp == 1) {  // the whole warp runs the loop, one lane issues
+        const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+        const uint32_t ring = bi::smem_u32(smem);
+        uint32_t sfw = 0;
+        int stage = 0;
+        uint32_t phase = 0;
+        int i = 0;
+        bool ok = true;
+        for (; i < nkb; ++i) {
+            if (!__all_sync(0xffffffffu, bi::mbar_wait(&full[stage], phase))) {
+                ok = false;
+                break;
+            }
+            bi::tc_fence_after();
+            const uint32_t idesc = with_byte(mx_idesc(128, NT), i & 3);
+            const uint32_t sw = ring + stage * S::kStageBytes;
+            const uint64_t dw = operand_desc(sw), dx = operand_desc(sw + S::kWBytes);
+            const uint64_t s = scale_desc(ring + kStages * S::kStageBytes + stage * S::kScaleBytes);
+            // a scale place is used again 8 tiles of scales later; by then its MMAs are
+            // done (this stage's load waited for those kStages k-blocks ago)
+            if ((i & 3) == 0) sfw = tmem + S::kScaleCol + 16 * ((i >> 2) & 7);
+            if (bi::elect_one()) {
                 if ((i & 3) == 0) {
-                    // a place is used again 8 tiles of scales later; by then its MMAs are
-                    // done (this stage's load waited for those kStages k-blocks ago)
-                    sfw = tmem_base + S::kScaleCol + 16 * ((i >> 2) & 7);
-                    const uint32_t s = bi::smem_u32(smem_scales + stage * S::kScaleBytes);
 #pragma unroll
-                    for (int t = 0; t <= WT; ++t)
-                        bi::tc_cp_scales(sfw + 4 * t, scale_desc(s + t * kTile));
+                    for (int t = 0; t <= WT; ++t) bi::tc_cp_scales(sfw + 4 * t, s + (t * kTile >> 4));
                 }
-                const uint32_t idesc = with_byte(mx_idesc(128, NT), i & 3);
-                const uint32_t sw = bi::smem_u32(smem + stage * S::kStageBytes);
 #pragma unroll
                 for (int t = 0; t < WT; ++t)
 #pragma unroll
-                    for (int k = 0; k < BK / 32; ++k)
-                        bi::tc_mma_mxf8(tmem_base + t * NT, operand_desc(sw + t * 128 * BK + 32 * k),
-                                        operand_desc(sw + S::kWBytes + 32 * k), idesc, sfw + 4 * t,
-                                        sfw + 4 * WT, (i | k) != 0 ? 1u : 0u);
+                    for (int k = 0; k < BK / 32; ++k)  // 32 bytes of K a step
+                        bi::tc_mma_mxf8(tmem + t * NT, dw + (t * 128 * BK >> 4) + 2 * k, dx + 2 * k,
+                                        idesc, sfw + 4 * t, sfw + 4 * WT, (i | k) != 0 ? 1u : 0u);
                 bi::tc_commit(&empty[stage]);
+                if (i + 1 == nkb) bi::tc_commit(tfull);
             }
+            __syncwarp();
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        if (bi::elect_one()) {
             s_consumed = i;
-            if (ok) {
-                bi::tc_commit(tfull);
-            } else {
+            if (!ok) {
                 bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
                 s_timeout = 1;
                 if (i > 0) {
@@ -589,6 +607,7 @@ __global__ void __launch_bounds__(192)
                 }
             }
         }
+        __syncwarp();
     } else {
         // warps 2..5: W rows quarter * 32 + lane of each W tile, all NT rows of x
         const int quarter = warp & 3;
