@@ -283,6 +283,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                  : "memory");
 }
 
+// The same for an arrival that publishes no ordinary memory, after
+// tcgen05.fence::before_thread_sync: that orders the tensor-memory reads before it.  The
+// release form also waits for the thread's own earlier global stores: 340 cycles with
+// none outstanding, over 1000 behind the stores of a tile.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+                 : "memory");
+}
+
 // TMA 2-D tile load into this CTA's shared memory whose completion is counted
 // on an mbarrier of either CTA of the pair (cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, uint32_t bar_cluster,
@@ -465,6 +474,18 @@ __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint3
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// Hand registers of a warpgroup back to the block's pool, or take some (all four
+// warps of a warpgroup execute it; what all take must fit what the block was
+// launched with).
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // Programmatic dependent launch (PTX griddepcontrol).  launch_dependents lets

@@ -86,7 +86,12 @@ constexpr int kABytes = 128 * BK;
 constexpr int kStageBytes = 2 * kABytes;  // 128 rows of x, 2 x 64 rows of W
 constexpr int kScaleBytes = 3 * kTile;    // 128 rows of x, 256 rows of W
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+// Registers a thread: 168 at launch (three warps share a sub-partition's 16384).  The
+// epilogue holds 128 sums and loads 64 columns at once; the other four warps give
+// theirs up for that.
+constexpr int kFewRegs = 56, kManyRegs = 224;
+static_assert(128 * kFewRegs + 32 * kEpiWarps * kManyRegs <= kThreads * 168, "registers");
 // Tensor memory: three accumulators of 128 columns, and 8 places of 16 columns
 // for scales.  The tile's two column halves are accumulators of their own, taken
 // in turn out of three, so that a half's MMAs of the next part need not wait for
@@ -174,6 +179,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     bi::launch_dependents();
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
 
+    if (warp < 4) {
+        bi::fewer_registers<pair::kFewRegs>();
     if (warp == 0) {
         if (lane == 0) {
             int stage = 0;
@@ -310,20 +317,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             }
             __syncwarp();
         }
+    }
     } else {
-        // epilogue warps 2..9: lane quarter warp % 4 of this CTA's 128 rows, and
+        bi::more_registers<pair::kManyRegs>();
+        // epilogue warps 4..11: lane quarter warp % 4 of this CTA's 128 rows, and
         // 64 of either half's 128 columns
         const int quarter = warp & 3;
-        const int c = (warp - 2) >> 2;
+        const int c = (warp - 4) >> 2;
         const int num_parts = (num_kb + part_blocks - 1) / part_blocks;
         int acc = 0;
         uint32_t acc_phase = 0;
         int turn = 0;
         bool ok = true;  // of the whole warp; a warp that gave up still meets its partner
+        const uint32_t taddr0 =
+            tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 64 * c;
         for (int tile = pair_id; tile < num_tiles; tile += npairs, turn ^= 1) {
-            int mb, nb;
-            tile_coords(tile, num_m, num_n, group_m, mb, nb);
-            float sum[2][64];
+            float sum[2][64];  // from -0 on: -0 + x is x, whatever its sign
+#pragma unroll
+            for (int i = 0; i < 64; ++i) sum[0][i] = sum[1][i] = -0.f;
+#pragma unroll 1
             for (int p = 0; p < num_parts; ++p) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -336,27 +348,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                     }
                     if (ok) {
                         bi::tc_fence_after();
-                        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                               128 * acc + 64 * c;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t r[16];
-                            bi::tmem_ld_32x32b_x16(taddr + 16 * q, r);
-                            bi::tmem_ld_wait();
-                            if (p == 0) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) sum[h][16 * q + i] = __uint_as_float(r[i]);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    sum[h][16 * q + i] =
-                                        __fadd_rn(sum[h][16 * q + i], __uint_as_float(r[i]));
-                            }
-                        }
+                        const uint32_t taddr = taddr0 + 128 * acc;
+                        uint32_t r[2][32];
+                        bi::tmem_ld_32x32b_x32(taddr, r[0]);
+                        bi::tmem_ld_32x32b_x32(taddr + 32, r[1]);
+                        bi::tmem_ld_wait();
                         bi::tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
-                            bi::mbar_arrive_cluster(bi::mapa_shared(bi::smem_u32(&tempty[acc]), 0));
+                            bi::mbar_arrive_cluster_relaxed(bi::mapa_shared(bi::smem_u32(&tempty[acc]), 0));
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            sum[h][i] = __fadd_rn(sum[h][i], __uint_as_float(r[i >> 5][i & 31]));
                     }
                     if (++acc == 3) {
                         acc = 0;
@@ -364,6 +367,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                     }
                 }
             }
+            int mb, nb;  // not before the sums are there: every register counts in that loop
+            tile_coords(tile, num_m, num_n, group_m, mb, nb);
             const int in_tile = quarter * 32 + lane;
             const int row = mb * pair::BMP + static_cast<int>(rank) * 128 + in_tile;
             if constexpr (!kSwiGLU) {
