@@ -147,6 +147,18 @@ CUresult encode_byte_map_2d(CUtensorMap* map, const void* base, uint64_t row_byt
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+CUresult encode_out_map(CUtensorMap* map, const void* base, uint64_t columns, uint64_t rows,
+                        uint64_t row_stride_bytes) {
+    if (!resolve_encode()) return CUDA_ERROR_NOT_FOUND;
+    cuuint64_t dims[2] = {columns, rows};
+    cuuint64_t strides[1] = {row_stride_bytes};
+    cuuint32_t box[2] = {32, 32};
+    cuuint32_t estr[2] = {1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+                    strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 CUresult encode_scale_map(CUtensorMap* map, const void* base, uint64_t tiles) {
     if (!resolve_encode()) return CUDA_ERROR_NOT_FOUND;
     cuuint64_t dims[2] = {128, tiles};  // 32-bit words

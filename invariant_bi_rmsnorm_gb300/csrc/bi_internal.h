@@ -66,6 +66,11 @@ CUresult encode_q_map(CUtensorMap* map, const void* base, uint64_t T, uint64_t H
 CUresult encode_byte_map_2d(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows,
                             uint64_t row_stride_bytes, uint32_t box_rows);
 
+// bf16 rows as encode_tensor_map_2d, the box 32 columns x 32 rows, 64-byte swizzled
+// (output tiles on their way out).
+CUresult encode_out_map(CUtensorMap* map, const void* base, uint64_t columns, uint64_t rows,
+                        uint64_t row_stride_bytes);
+
 // Scale tiles of 512 contiguous bytes each; the box is one tile, as it lies.
 CUresult encode_scale_map(CUtensorMap* map, const void* base, uint64_t tiles);
 

@@ -99,7 +99,10 @@ static_assert(128 * kFewRegs + 32 * kEpiWarps * kManyRegs <= kThreads * 168, "re
 // room for the scales.
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScaleCol = 384;
-constexpr int kSmemBytes = kStages * (kStageBytes + kScaleBytes) + 1024 + 256;
+constexpr int kOutBytes = 32 * 64;  // a warp's 32 rows x 32 bf16 columns on their way out
+static_assert(kStages * (kStageBytes + kScaleBytes) % 1024 == 0, "swizzled output tiles");
+constexpr int kSmemBytes =
+    kStages * (kStageBytes + kScaleBytes) + kEpiWarps * kOutBytes + 1024 + 256;
 constexpr uint32_t kIdesc = mx_idesc(BMP, 128);
 }  // namespace pair
 
@@ -119,14 +122,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
                          const __grid_constant__ CUtensorMap tmap_w,
                          const __grid_constant__ CUtensorMap tmap_xs,
-                         const __grid_constant__ CUtensorMap tmap_ws, Out out, int M, int N, int K,
+                         const __grid_constant__ CUtensorMap tmap_ws,
+                         const __grid_constant__ CUtensorMap tmap_y, Out out, int M, int N, int K,
                          int part_blocks, int group_m, uint32_t* err) {
     constexpr int kStages = pair::kStages, kABytes = pair::kABytes, kStageBytes = pair::kStageBytes;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* smem_scales = smem + kStages * kStageBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem_scales + kStages * pair::kScaleBytes);
+    uint8_t* smem_out = smem_scales + kStages * pair::kScaleBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem_out + pair::kEpiWarps * pair::kOutBytes);
     uint64_t* empty = full + kStages;
     uint64_t* tfull = empty + kStages;
     uint64_t* tempty = tfull + 3;
@@ -372,14 +377,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             const int in_tile = quarter * 32 + lane;
             const int row = mb * pair::BMP + static_cast<int>(rank) * 128 + in_tile;
             if constexpr (!kSwiGLU) {
-                if (!ok || row >= M) continue;
-                __nv_bfloat16* yr = static_cast<__nv_bfloat16*>(out.y) + static_cast<int64_t>(row) * out.ld;
+                // 32 rows x 32 columns at a time through shared memory (64-byte rows,
+                // swizzled: no bank conflicts) and out by TMA, which clips them to y.  A
+                // lane storing its own row's 16 bytes at a time costs a cycle of the
+                // store path for each of a warp's 32 rows: 6900 cycles a tile.
+                if (!ok) continue;
+                uint8_t* buf = smem_out + (warp - 4) * pair::kOutBytes;
+                const int row0 = row - lane;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int col = nb * pair::BN + 128 * h + 64 * c;
+                for (int q = 0; q < 4; ++q) {
+                    const int col = nb * pair::BN + 128 * (q >> 1) + 64 * c + 32 * (q & 1);
+                    if (row0 >= M || col >= N) continue;  // the whole warp
+                    if (lane == 0) bi::tma_store_wait_read<0>();
+                    __syncwarp();
 #pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        if (col + 8 * v < N) *reinterpret_cast<uint4*>(yr + col + 8 * v) = pack8(&sum[h][8 * v]);
+                    for (int v = 0; v < 4; ++v)
+                        *reinterpret_cast<uint4*>(buf + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4)) =
+                            pack8(&sum[q >> 1][32 * (q & 1) + 8 * v]);
+                    bi::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) bi::tma_store_2d(&tmap_y, buf, col, row0);
                 }
             } else {
                 // 16 accumulator columns are 8 gate values and the 8 matching up values;
@@ -432,6 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         }
     }
 
+    if (!kSwiGLU && warp >= 4 && lane == 0) bi::tma_store_wait_all();
     __syncthreads();
     if (s_timeout && leader && threadIdx.x == 0) {
         // loads issued but never seen to land (at most one ring's worth): a bounded
@@ -754,6 +772,9 @@ bi_status launch_pair(const Call& c) {
     if (sms < 2) return BI_ERR_CUDA;
     CUtensorMap t[4];
     if (!encode(c, 128, 64, t)) return BI_ERR_CUDA;
+    CUtensorMap ty = t[0];  // not read where the output is 8 bits
+    if (!kSwiGLU && bi::encode_out_map(&ty, c.out.y, c.N, c.M, c.out.ld * 2) != CUDA_SUCCESS)
+        return BI_ERR_CUDA;
     const int num_m = (c.M + pair::BMP - 1) / pair::BMP;
     const int64_t tiles = static_cast<int64_t>(num_m) * ((c.N + pair::BN - 1) / pair::BN);
     if (tiles > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
@@ -764,7 +785,7 @@ bi_status launch_pair(const Call& c) {
     int group_m = num_m;
     if (slab * num_m > budget) group_m = static_cast<int>(std::max<int64_t>(1, budget / slab));
     return bi::launch_pdl(gemm_fp8_pair_kernel<kSwiGLU>, dim3(2 * pairs), dim3(pair::kThreads),
-                          pair::kSmemBytes, c.stream, t[0], t[1], t[2], t[3], c.out, c.M, c.N, c.K,
+                          pair::kSmemBytes, c.stream, t[0], t[1], t[2], t[3], ty, c.out, c.M, c.N, c.K,
                           parts_of(c.K).blocks, group_m, bi::device_error_word()) == cudaSuccess
                ? BI_OK
                : BI_ERR_CUDA;
