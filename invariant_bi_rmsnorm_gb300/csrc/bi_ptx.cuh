@@ -99,6 +99,15 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_
         : "memory");
 }
 
+// Ask L2 for a 2-D tile: moves data only, so it may come before the grid dependency
+// wait (L2 is where other kernels' writes land too).
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<uint64_t>(tmap)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
 // 2-D tile store from shared memory (what lies outside the tensor is not written),
 // one group per call; the waits are for this thread's groups: until at most N still
 // read shared memory, and until all have been written.
@@ -293,6 +302,12 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t local_addr, uint32_t ra
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
+}
+
+// The same where no memory is handed over (no CTA leaves before the others are done
+// with its shared memory): does not wait for this thread's own stores.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // Arrive once on an mbarrier given by its cluster address (possibly the peer's).

@@ -34,13 +34,14 @@ namespace {
 constexpr int BK = bi_fp8::kBlock;          // bytes and values per k-block
 constexpr int kTile = bi_fp8::kTileBytes;   // scales of 128 rows x 4 k-blocks
 
-// K in parts of `blocks` k-blocks each (the last may be shorter).
+// K in parts of `blocks` k-blocks each (the last may be shorter): 1024 values at
+// least, and 8 parts at most.
 struct Parts {
     int count, blocks;
 };
 inline Parts parts_of(int32_t K) {
     const int spans = bi_fp8::spans_of(K);
-    const int per = (spans + 7) / 8;
+    const int per = std::max(2, (spans + 7) / 8);
     return {(spans + per - 1) / per, 4 * per};
 }
 
@@ -81,7 +82,7 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 namespace pair {
 constexpr int BMP = 256;  // tile rows of the pair; 128 per CTA
 constexpr int BN = 256;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kABytes = 128 * BK;
 constexpr int kStageBytes = 2 * kABytes;  // 128 rows of x, 2 x 64 rows of W
 constexpr int kScaleBytes = 3 * kTile;    // 128 rows of x, 256 rows of W
@@ -100,9 +101,9 @@ static_assert(128 * kFewRegs + 32 * kEpiWarps * kManyRegs <= kThreads * 168, "re
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScaleCol = 384;
 constexpr int kOutBytes = 32 * 64;  // a warp's 32 rows x 32 bf16 columns on their way out
-static_assert(kStages * (kStageBytes + kScaleBytes) % 1024 == 0, "swizzled output tiles");
-constexpr int kSmemBytes =
-    kStages * (kStageBytes + kScaleBytes) + kEpiWarps * kOutBytes + 1024 + 256;
+constexpr int kOutBufs = 3;          // of them in turn
+constexpr int kOutOffset = (kStages * (kStageBytes + kScaleBytes) + 1023) / 1024 * 1024;
+constexpr int kSmemBytes = kOutOffset + kEpiWarps * kOutBufs * kOutBytes + 1024 + 256;
 constexpr uint32_t kIdesc = mx_idesc(BMP, 128);
 }  // namespace pair
 
@@ -130,8 +131,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* smem_scales = smem + kStages * kStageBytes;
-    uint8_t* smem_out = smem_scales + kStages * pair::kScaleBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem_out + pair::kEpiWarps * pair::kOutBytes);
+    uint8_t* smem_out = smem + pair::kOutOffset;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem_out + pair::kEpiWarps * pair::kOutBufs *
+                                                                pair::kOutBytes);
     uint64_t* empty = full + kStages;
     uint64_t* tfull = empty + kStages;
     uint64_t* tempty = tfull + 3;
@@ -186,25 +188,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 
     if (warp < 4) {
         bi::fewer_registers<pair::kFewRegs>();
-    if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int issued = 0;
-            for (int tile = pair_id; tile < num_tiles; tile += npairs) {
-                int mb, nb;
-                tile_coords(tile, num_m, num_n, group_m, mb, nb);
-                const int m_tile = 2 * mb + static_cast<int>(rank);  // of 128 rows
-                const int w_row = nb * pair::BN + static_cast<int>(rank) * 64;
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!bi::mbar_wait(&empty[stage], phase ^ 1)) {
-                        bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
-                        s_timeout = 1;
-                        goto producer_done;
-                    }
-                    const bool scales = (kb & 3) == 0;  // a tile of them serves four k-blocks
-                    uint8_t* sa = smem + stage * kStageBytes;
-                    const uint32_t bar = bi::mapa_shared(bi::smem_u32(&full[stage]), 0);
+    if (warp == 0) {  // the whole warp runs the loop, one lane issues
+        const uint32_t bar0 = bi::mapa_shared(bi::smem_u32(full), 0);  // the leader's
+        int stage = 0;
+        uint32_t phase = 0;
+        int issued = 0;
+        bool ok = true;
+        for (int tile = pair_id; tile < num_tiles && ok; tile += npairs) {
+            int mb, nb;
+            tile_coords(tile, num_m, num_n, group_m, mb, nb);
+            const int m_tile = 2 * mb + static_cast<int>(rank);  // of 128 rows
+            const int w_row = nb * pair::BN + static_cast<int>(rank) * 64;
+            for (int kb = 0; kb < num_kb; ++kb) {
+                if (!__all_sync(0xffffffffu, bi::mbar_wait(&empty[stage], phase ^ 1))) {
+                    ok = false;
+                    break;
+                }
+                const bool scales = (kb & 3) == 0;  // a tile of them serves four k-blocks
+                uint8_t* sa = smem + stage * kStageBytes;
+                const uint32_t bar = bar0 + 8 * stage;
+                if (bi::elect_one()) {
                     if (leader)
                         bi::mbar_arrive_expect_tx(
                             &full[stage], 2 * (kStageBytes + (scales ? pair::kScaleBytes : 0)));
@@ -220,15 +223,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                         bi::tma_load_2d_pair(sf + 2 * kTile, &tmap_ws, bar, 0,
                                              (2 * nb + 1) * spans + (kb >> 2));
                     }
-                    ++issued;
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
-        producer_done:
+        }
+        if (lane == 0) {
             s_issued = issued;
+            if (!ok) {
+                bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
+                s_timeout = 1;
+            }
         }
     } else if (warp == 1) {
         if (leader) {  // the whole warp runs the loop, one lane issues
@@ -332,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         const int num_parts = (num_kb + part_blocks - 1) / part_blocks;
         int acc = 0;
         uint32_t acc_phase = 0;
-        int turn = 0;
+        int turn = 0, out_buf = 0;
         bool ok = true;  // of the whole warp; a warp that gave up still meets its partner
         const uint32_t taddr0 =
             tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 64 * c;
@@ -382,13 +391,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                 // lane storing its own row's 16 bytes at a time costs a cycle of the
                 // store path for each of a warp's 32 rows: 6900 cycles a tile.
                 if (!ok) continue;
-                uint8_t* buf = smem_out + (warp - 4) * pair::kOutBytes;
                 const int row0 = row - lane;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int col = nb * pair::BN + 128 * (q >> 1) + 64 * c + 32 * (q & 1);
                     if (row0 >= M || col >= N) continue;  // the whole warp
-                    if (lane == 0) bi::tma_store_wait_read<0>();
+                    uint8_t* buf = smem_out + ((warp - 4) * pair::kOutBufs + out_buf) * pair::kOutBytes;
+                    if (++out_buf == pair::kOutBufs) out_buf = 0;
+                    if (bi::elect_one()) bi::tma_store_wait_read<pair::kOutBufs - 1>();
                     __syncwarp();
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
@@ -396,7 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                             pack8(&sum[q >> 1][32 * (q & 1) + 8 * v]);
                     bi::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) bi::tma_store_2d(&tmap_y, buf, col, row0);
+                    if (bi::elect_one()) bi::tma_store_2d(&tmap_y, buf, col, row0);
                 }
             } else {
                 // 16 accumulator columns are 8 gate values and the 8 matching up values;
@@ -449,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         }
     }
 
-    if (!kSwiGLU && warp >= 4 && lane == 0) bi::tma_store_wait_all();
+    if (!kSwiGLU && warp >= 4 && bi::elect_one()) bi::tma_store_wait_all();
     __syncthreads();
     if (s_timeout && leader && threadIdx.x == 0) {
         // loads issued but never seen to land (at most one ring's worth): a bounded
@@ -467,35 +477,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 
 // ----------------------------------------------------------- few rows ----
 // NT: rows of x per CTA (the MMA's N); WT: tiles of 128 W rows per CTA (the MMA's
-// M): one, or two where a block of 128 SwiGLU outputs needs 256 W rows.
-template <int NT, int WT>
+// M): one, or two where a block of 128 SwiGLU outputs needs 256 W rows; STAGES: k-blocks
+// in flight per CTA.
+template <int NT, int WT, int STAGES>
 struct PartsShape {
     static constexpr int kWBytes = WT * 128 * BK;
     static constexpr int kStageBytes = kWBytes + NT * BK;
     static constexpr int kScaleBytes = (WT + 1) * kTile;
-    // two CTAs per SM where that leaves a part's loads in flight, else one
-    static constexpr int kStages = WT == 1 ? (NT <= 64 ? 4 : 3) : (NT <= 16 ? 3 : NT <= 64 ? 2 : 4);
-    static constexpr int kSmemBytes = kStages * (kStageBytes + kScaleBytes) + 1024 + 256;
+    static constexpr int kStages = STAGES;
+    static constexpr int kUsedBytes = kStages * (kStageBytes + kScaleBytes) + 1024 + 256;
     static constexpr int kPartialBytes = WT * 128 * NT * 4;
     static_assert(kPartialBytes <= kStages * kStageBytes, "partials lie in the ring");
+    // Tensor memory: the sums, then places for scales.  A place is used again kPlaces
+    // tiles of scales (4 k-blocks each) later, and a stage's load has waited for the MMAs
+    // of kStages k-blocks ago.
     static constexpr uint32_t kScaleCol = WT * NT;
-    static constexpr uint32_t kTmemCols = WT * NT + 128 <= 256 ? 256 : 512;
-    static_assert(kStages < 8, "scale places");
-    // No more CTAs on an SM than its 512 columns of tensor memory serve, with those of
-    // other kernels that allocate some: were a cluster's CTA to wait for columns that
-    // another cluster holds, the two could wait for each other.
-    static_assert((kTmemCols == 512 ? 2 : 3) * (kSmemBytes + 1024) > 228 * 1024, "tensor memory");
+    static constexpr uint32_t kPlaceCols = 4 * (WT + 1);
+    static constexpr uint32_t kPlaces = kStages > 5 ? 4 : 2;
+    static_assert(4 * kPlaces >= kStages + 3, "scale places");
+    static constexpr uint32_t kCols = kScaleCol + kPlaces * kPlaceCols;
+    static constexpr uint32_t kTmemCols =
+        kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+    // An SM must not hold more of this file's CTAs than its 512 columns of tensor
+    // memory serve: were a cluster's CTA to wait for columns that another cluster holds,
+    // the two could wait for each other.  So a CTA takes 1/543 of an SM's shared memory
+    // for each of its columns at least, and the next multiple of 32 above 512 is 544.
+    static constexpr int kShareBytes = (kTmemCols * (228 * 1024) + 542) / 543 - 1024;
+    static constexpr int kSmemBytes = kUsedBytes > kShareBytes ? kUsedBytes : kShareBytes;
 };
 
-template <int NT, bool kSwiGLU>
+template <int NT, bool kSwiGLU, int STAGES>
 __global__ void __launch_bounds__(192)
     gemm_fp8_parts_kernel(const __grid_constant__ CUtensorMap tmap_x,
                           const __grid_constant__ CUtensorMap tmap_w,
                           const __grid_constant__ CUtensorMap tmap_xs,
                           const __grid_constant__ CUtensorMap tmap_ws, Out out, int M, int N, int K,
-                          int part_blocks, uint32_t* err) {
+                          int part_blocks, bool prefetch, uint32_t* err) {
     constexpr int WT = kSwiGLU ? 2 : 1;
-    using S = PartsShape<NT, WT>;
+    using S = PartsShape<NT, WT, STAGES>;
     constexpr int kStages = S::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -540,43 +559,67 @@ __global__ void __launch_bounds__(192)
         bi::tmem_alloc(tmem_slot, S::kTmemCols);
         bi::tmem_relinquish();
     }
+    if (warp == 0) {
+        // the weight may start on its way to L2 while the previous kernel, which as a
+        // rule makes x, still runs (N = K = 4096, one row, after another such call: 6.3 ->
+        // 5.9 us); no use to CTAs that start when others end
+        if (prefetch && bi::elect_one())
+            for (int i = 0; i < nkb; ++i)
+                for (int t = 0; t < WT; ++t)
+                    bi::tma_prefetch_2d(&tmap_w, (kb0 + i) * BK, n0 + 128 * t);
+        __syncwarp();
+    }
     bi::tc_fence_before();
     __syncthreads();
     bi::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     bi::launch_dependents();
-    bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
+    bi::grid_dependency_wait();  // nothing global is read or written before the previous kernel ends
 
-    if (warp == 0) {
-        if (lane == 0) {
-            int issued = 0;
-            for (; issued < nkb; ++issued) {
-                const int stage = issued % kStages;
-                if (issued >= kStages && !bi::mbar_wait(&empty[stage], (issued / kStages - 1) & 1)) {
-                    bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
-                    s_timeout = 1;
-                    break;
-                }
-                const int kb = kb0 + issued;
-                const bool scales = (issued & 3) == 0;  // parts start on whole spans
-                uint8_t* sw = smem + stage * S::kStageBytes;
+    if (warp == 0) {  // the whole warp runs the loop, one lane issues
+        int stage = 0;
+        uint32_t phase = 0;
+        int issued = 0;
+        bool ok = true;
+        for (; issued < nkb; ++issued) {
+            if (!__all_sync(0xffffffffu, bi::mbar_wait(&empty[stage], phase ^ 1))) {
+                ok = false;
+                break;
+            }
+            const int kb = kb0 + issued;
+            const bool scales = (issued & 3) == 0;  // parts start on whole spans
+            uint8_t* sw = smem + stage * S::kStageBytes;
+            if (bi::elect_one()) {
                 bi::mbar_arrive_expect_tx(&full[stage],
                                           S::kStageBytes + (scales ? S::kScaleBytes : 0));
+#pragma unroll
                 for (int t = 0; t < WT; ++t)
                     bi::tma_load_2d(sw + t * 128 * BK, &tmap_w, &full[stage], kb * BK, n0 + 128 * t);
                 bi::tma_load_2d(sw + S::kWBytes, &tmap_x, &full[stage], kb * BK, m0);
                 if (scales) {
                     uint8_t* sf = smem_scales + stage * S::kScaleBytes;
+#pragma unroll
                     for (int t = 0; t < WT; ++t)
                         bi::tma_load_2d(sf + t * kTile, &tmap_ws, &full[stage], 0,
                                         (n0 / 128 + t) * spans + (kb >> 2));
-                    // NT < 128 only where one tile holds all rows, so a tile's rows
-                    // start where its scales do
+                    // NT < 128 only where one tile holds all rows, so a tile's rows start
+                    // where its scales do
                     bi::tma_load_2d(sf + WT * kTile, &tmap_xs, &full[stage], 0,
                                     (m0 / 128) * spans + (kb >> 2));
                 }
             }
+            __syncwarp();
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        if (lane == 0) {
             s_issued = issued;
+            if (!ok) {
+                bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
+                s_timeout = 1;
+            }
         }
     } else if (warp == 1) {  // the whole warp runs the loop, one lane issues
         const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
@@ -596,9 +639,7 @@ __global__ void __launch_bounds__(192)
             const uint32_t sw = ring + stage * S::kStageBytes;
             const uint64_t dw = operand_desc(sw), dx = operand_desc(sw + S::kWBytes);
             const uint64_t s = scale_desc(ring + kStages * S::kStageBytes + stage * S::kScaleBytes);
-            // a scale place is used again 8 tiles of scales later; by then its MMAs are
-            // done (this stage's load waited for those kStages k-blocks ago)
-            if ((i & 3) == 0) sfw = tmem + S::kScaleCol + 16 * ((i >> 2) & 7);
+            if ((i & 3) == 0) sfw = tmem + S::kScaleCol + S::kPlaceCols * ((i >> 2) % S::kPlaces);
             if (bi::elect_one()) {
                 if ((i & 3) == 0) {
 #pragma unroll
@@ -744,7 +785,7 @@ __global__ void __launch_bounds__(192)
         }
     }
     __syncwarp();
-    bi::cluster_sync();  // no CTA leaves while another reads its sums
+    bi::cluster_sync_relaxed();  // no CTA leaves while another reads its sums
 }
 
 // ------------------------------------------------------------- launches ----
@@ -791,31 +832,58 @@ bi_status launch_pair(const Call& c) {
                : BI_ERR_CUDA;
 }
 
-template <int NT, bool kSwiGLU>
-bi_status launch_parts(const Call& c) {
-    using S = PartsShape<NT, kSwiGLU ? 2 : 1>;
+template <int NT, bool kSwiGLU, int STAGES>
+bi_status launch_parts(const Call& c, bool prefetch) {
+    using S = PartsShape<NT, kSwiGLU ? 2 : 1, STAGES>;
     static std::atomic<bool> set[64] = {};
-    if (!bi::allow_smem(gemm_fp8_parts_kernel<NT, kSwiGLU>, S::kSmemBytes, set)) return BI_ERR_CUDA;
+    if (!bi::allow_smem(gemm_fp8_parts_kernel<NT, kSwiGLU, STAGES>, S::kSmemBytes, set))
+        return BI_ERR_CUDA;
     CUtensorMap t[4];
     if (!encode(c, NT, 128, t)) return BI_ERR_CUDA;
     const Parts p = parts_of(c.K);
     const int rows = kSwiGLU ? 256 : 128;
     const dim3 grid(p.count, (c.M + NT - 1) / NT, (c.N + rows - 1) / rows);
-    return bi::launch_pdl_cluster(gemm_fp8_parts_kernel<NT, kSwiGLU>, p.count, grid, dim3(192),
-                                  S::kSmemBytes, c.stream, t[0], t[1], t[2], t[3], c.out, c.M, c.N,
-                                  c.K, p.blocks, bi::device_error_word()) == cudaSuccess
+    return bi::launch_pdl_cluster(gemm_fp8_parts_kernel<NT, kSwiGLU, STAGES>, p.count, grid,
+                                  dim3(192), S::kSmemBytes, c.stream, t[0], t[1], t[2], t[3], c.out,
+                                  c.M, c.N, c.K, p.blocks, prefetch, bi::device_error_word()) ==
+                   cudaSuccess
                ? BI_OK
                : BI_ERR_CUDA;
 }
 
-// Which kernel: a schedule choice, the bits are the same.
+// Stages by the launch's CTAs: one, two or three CTAs an SM, the fewest that hold the
+// launch at once (a CTA then has the most loads in flight), else three.
+template <int NT, bool kSwiGLU, int ONE, int TWO, int THREE>
+bi_status launch_parts(const Call& c) {
+    const int rows = kSwiGLU ? 256 : 128;
+    const int64_t ctas = static_cast<int64_t>(parts_of(c.K).count) * ((c.M + NT - 1) / NT) *
+                         ((c.N + rows - 1) / rows);
+    const int sms = bi::sm_count();
+    if (ctas <= sms) return launch_parts<NT, kSwiGLU, ONE>(c, true);
+    if (ctas <= 2 * sms) return launch_parts<NT, kSwiGLU, TWO>(c, true);
+    return launch_parts<NT, kSwiGLU, THREE>(c, false);
+}
+
+// Which kernel: a schedule choice, the bits are the same.  Up to 32 rows the parts
+// kernel (17 rows, K = 4096: N = 4096 6.3 us against 15, N = 24576 21.4 against 29.7).  Beyond, its
+// time goes with its 128 x 128 tiles, that of the other with its waves of 256 x 256
+// tiles over the CTA pairs, and the two cross at about a pair's worth of tiles a wave:
+// K = 4096, N = 4096 8.6 against 15.5 us at 128 rows and 11.0 against 15.5 at 200 (64
+// tiles), 18.6 against 15.7 at 300 (96); N = 24576 35.6 against 30.1 at 128 rows (192 tiles,
+// two waves); K = 12288, N = 4096 25.6 against 34.1 at 200 rows, 37.1 against 34.3 at 300.
 template <bool kSwiGLU>
 bi_status launch_gemm(const Call& c) {
-    if (c.M <= 512 && (c.N + 127) / 128 <= 65535) {
-        if (c.M <= 16) return launch_parts<16, kSwiGLU>(c);
-        if (c.M <= 32) return launch_parts<32, kSwiGLU>(c);
-        if (c.M <= 64) return launch_parts<64, kSwiGLU>(c);
-        return launch_parts<128, kSwiGLU>(c);
+    const int sms = bi::sm_count();
+    if (sms < 2) return BI_ERR_CUDA;
+    const int64_t small_m = (c.M + 127) / 128, small_n = (c.N + 127) / 128;
+    const int64_t large = static_cast<int64_t>((c.M + 255) / 256) * ((c.N + 255) / 256);
+    const int64_t waves = (large + sms / 2 - 1) / (sms / 2);
+    if ((c.M <= 32 || small_m * small_n <= waves * (sms / 2)) && small_m <= 65535 && small_n <= 65535) {
+        constexpr bool g = kSwiGLU;
+        if (c.M <= 16) return g ? launch_parts<16, g, 6, 3, 2>(c) : launch_parts<16, g, 8, 4, 3>(c);
+        if (c.M <= 32) return g ? launch_parts<32, g, 5, 2, 2>(c) : launch_parts<32, g, 8, 4, 3>(c);
+        if (c.M <= 64) return g ? launch_parts<64, g, 4, 2, 2>(c) : launch_parts<64, g, 8, 4, 4>(c);
+        return g ? launch_parts<128, g, 4, 4, 4>(c) : launch_parts<128, g, 6, 3, 3>(c);
     }
     return launch_pair<kSwiGLU>(c);
 }
