@@ -21,6 +21,13 @@ are appended, decode attends over the codes, and prompt rows attend over the
 step's sequences read back into one bf16 cache that every layer uses in turn.
 Decode and prefill still give a token the same bits, and a request's logits
 still do not depend on the batch.
+
+With linear_bits=8 the layers' four projections run on 8-bit weights and 8-bit
+activations (e4m3, a power-of-two scale for each 128 values): the norms give the
+8-bit input of the projection behind them, attention's output is quantised, and the
+gate|up product hands the down projection its input in 8 bits.  The residual stream,
+the projections' outputs, the final norm and the logits stay bf16.  It goes with
+either cache, and a request's logits still do not depend on the batch.
 """
 from __future__ import annotations
 
@@ -30,11 +37,11 @@ from dataclasses import dataclass, field
 import numpy as np
 import torch
 
-from . import (add_rmsnorm, decode_attention, decode_attention_kv4,
-               decode_attention_workspace_size, gemm, gemm_swiglu, interleave_gate_up, kv4_cache,
-               kv4_read, logprobs, logprobs_top, prefill_attention,
-               prefill_attention_workspace_size, qk_norm_rope_append, qk_norm_rope_append_kv4,
-               rmsnorm, silu_mul)
+from . import (add_rmsnorm, add_rmsnorm_fp8, decode_attention, decode_attention_kv4,
+               decode_attention_workspace_size, fp8_scales_shape, gemm, gemm_fp8, gemm_fp8_swiglu,
+               gemm_swiglu, interleave_gate_up, kv4_cache, kv4_read, logprobs, logprobs_top,
+               prefill_attention, prefill_attention_workspace_size, qk_norm_rope_append,
+               qk_norm_rope_append_kv4, quantize_fp8, rmsnorm, rmsnorm_fp8, silu_mul)
 from . import inputs
 from ._lib import MAX_TOP_LOGPROBS, PAGE_SIZE
 
@@ -128,7 +135,7 @@ class Engine:
 
     def __init__(self, weights: Qwen3Weights, num_pages: int, max_tokens_per_step: int = 8192,
                  n_layers: int | None = None, device="cuda", ops: str = "bi",
-                 cuda_graphs: bool = False, kv_bits: int = 16):
+                 cuda_graphs: bool = False, kv_bits: int = 16, linear_bits: int = 16):
         """ops="bi": every GEMM and RMSNorm through this library (batch-invariant).
         ops="torch": GEMMs through torch.matmul (cuBLAS) and RMSNorms through
         torch.nn.functional.rms_norm instead -- the non-invariant comparison.
@@ -140,11 +147,15 @@ class Engine:
         work of about 300 launches a step.
         kv_bits: 16, a bf16 cache, or 4, a cache of 4-bit codes (1152 bytes a
         page and head where bf16 takes 4096) and one layer's worth of bf16
-        cache for prompts to attend over."""
+        cache for prompts to attend over.
+        linear_bits: 16, or 8: the layers' projections on 8-bit copies of the
+        weights, made here, and 8-bit activations (ops="bi" only)."""
         if ops not in ("bi", "torch"):
             raise ValueError("ops must be 'bi' or 'torch'")
         if kv_bits not in (4, 16):
             raise ValueError("kv_bits must be 4 or 16")
+        if linear_bits not in (8, 16) or (linear_bits == 8 and ops != "bi"):
+            raise ValueError("linear_bits must be 16, or 8 with ops='bi'")
         self.ops = ops
         self.w = weights
         cfg = self.cfg = weights.cfg
@@ -181,8 +192,17 @@ class Engine:
                     "gu": e(T, 2 * F), "h": e(T, F), "d": e(T, H)}
         # the bi path runs gate|up and SwiGLU as one fused GEMM over an
         # interleaved copy of the weight (bit-identical to gemm + silu_mul)
-        self.gate_up_il = ([interleave_gate_up(self.w.layers[l]["gate_up"])
-                            for l in range(self.n_layers)] if ops == "bi" else None)
+        il = lambda l: interleave_gate_up(self.w.layers[l]["gate_up"])  # noqa: E731
+        self.linear_bits = linear_bits
+        self.gate_up_il = self.w8 = None
+        if linear_bits == 8:
+            self.w8 = [{"gate_up": quantize_fp8(il(l)), **{n: quantize_fp8(self.w.layers[l][n]) for n in ("qkv", "o", "down")}}
+                       for l in range(self.n_layers)]
+            for name, cols in (("n", H), ("attn", cfg.heads * D), ("h", F)):
+                self.buf[name + "8"] = torch.empty(T, cols, dtype=torch.float8_e4m3fn, device=self.device)
+                self.buf[name + "8s"] = torch.empty(fp8_scales_shape(T, cols), dtype=torch.uint8, device=self.device)
+        elif ops == "bi":
+            self.gate_up_il = [il(l) for l in range(self.n_layers)]
         self.steps = 0
 
     # ------------------------------------------------------------ pages ----
@@ -274,7 +294,7 @@ class Engine:
                            int(max(nqs)), int(max(lens)))
             meta["pws"] = self._prefill_workspace(len(rows), int(max(lens)))
 
-        b = {k: v[:T] for k, v in self.buf.items()}
+        b = self._rows_of_buffers(T)
         self._layers(b, T, tok_d, pos_d, slot_d, meta)
         samp = [int(offs[k + 1] - 1) for k, want in enumerate(want_logits) if want]
         if not samp:
@@ -283,6 +303,10 @@ class Engine:
         self.steps += 1
         return gemm(nrows, self.w.lm_head, out=torch.empty(len(samp), cfg.vocab,
                                                            dtype=torch.bfloat16, device=dev))
+
+    def _rows_of_buffers(self, T: int):
+        """The step's T rows of every buffer (scales lie in tiles of 128 rows)."""
+        return {k: v[:(T + 127) // 128] if k.endswith("8s") else v[:T] for k, v in self.buf.items()}
 
     def _layers(self, b, T, tok_d, pos_d, slot_d, meta):
         """Embedding, every decoder layer and the final norm for the step's T
@@ -293,6 +317,10 @@ class Engine:
         torch.index_select(self.w.embed, 0, tok_d, out=res)
         Hq, Hkv = cfg.heads, cfg.kv_heads
         append = qk_norm_rope_append_kv4 if self.kv_bits == 4 else qk_norm_rope_append
+        if self.linear_bits == 8:
+            self._layers_8bit(b, T, append, pos_d, slot_d, meta)
+            add_rmsnorm(b["d"], res, self.w.final_norm, cfg.eps, out=b["n"])
+            return
         for l in range(self.n_layers):
             L = self.w.layers[l]
             if l == 0:
@@ -313,6 +341,27 @@ class Engine:
             gemm(b["h"], L["down"], out=b["d"])
         add_rmsnorm(b["d"], res, self.w.final_norm, cfg.eps, out=b["n"])
 
+    def _layers_8bit(self, b, T, append, pos_d, slot_d, meta):
+        """The decoder layers over 8-bit weights (into b["d"], the last layer's share of
+        the residual stream b["res"])."""
+        cfg = self.cfg
+        res, n8 = b["res"], dict(out=b["n8"], scales=b["n8s"])
+        for l in range(self.n_layers):
+            L, W = self.w.layers[l], self.w8[l]
+            if l == 0:
+                n = rmsnorm_fp8(res, L["in_norm"], cfg.eps, **n8)
+            else:
+                n = add_rmsnorm_fp8(b["d"], res, L["in_norm"], cfg.eps, **n8)
+            gemm_fp8(*n, *W["qkv"], out=b["qkv"])
+            append(b["qkv"], cfg.heads, cfg.kv_heads, pos_d, slot_d, self.rope, L["q_norm"], L["k_norm"],
+                   self.k_cache[l], self.v_cache[l], cfg.eps, q_out=b["q"])
+            self._attention(l, b, meta)
+            a = quantize_fp8(b["attn"].view(T, cfg.heads * cfg.head_dim), out=b["attn8"], scales=b["attn8s"])
+            gemm_fp8(*a, *W["o"], out=b["o"])
+            n = add_rmsnorm_fp8(b["o"], res, L["post_norm"], cfg.eps, **n8)
+            h = gemm_fp8_swiglu(*n, *W["gate_up"], out=b["h8"], scales=b["h8s"])
+            gemm_fp8(*h, *W["down"], out=b["d"])
+
     # ----------------------------------------------------------- graphs ----
     def _graph_for(self, Bb: int):
         """The captured decode step for Bb rows, with its static inputs."""
@@ -332,7 +381,7 @@ class Engine:
                                                                 cfg.max_pos),
                                 dtype=torch.uint8, device=dev)}
         meta = {"dec": (slice(0, Bb), st["bt"], st["lens"], cfg.max_pos, W), "ws": st["ws"]}
-        b = {k: v[:Bb] for k, v in self.buf.items()}
+        b = self._rows_of_buffers(Bb)
         gemm_, _, _ = self._ops()
 
         def body():
