@@ -446,6 +446,36 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
+// Four bytes into the shared memory of a CTA of the cluster, counted on an mbarrier there
+// (both by cluster address), and the wait for such bytes: what they wrote is visible.
+__device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(addr),
+        "f"(v), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 0; i < kWaitPollLimit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.b32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((i & 255u) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (i == 0) t0 = now;
+            if (now - t0 > limit_ns) return false;
+        }
+    }
+    return false;
+}
+
 // Integer add at device scope with acquire-release semantics; returns the old
 // value.  After a CTA barrier, one thread's release publishes the whole CTA's
 // earlier writes; its acquire, followed by a CTA barrier, lets every thread

@@ -485,9 +485,24 @@ struct PartsShape {
     static constexpr int kStageBytes = kWBytes + NT * BK;
     static constexpr int kScaleBytes = (WT + 1) * kTile;
     static constexpr int kStages = STAGES;
-    static constexpr int kUsedBytes = kStages * (kStageBytes + kScaleBytes) + 1024 + 256;
-    static constexpr int kPartialBytes = WT * 128 * NT * 4;
-    static_assert(kPartialBytes <= kStages * kStageBytes, "partials lie in the ring");
+    // Scales serve four k-blocks.  Their slot is loaded again for the next four when a
+    // stage is free whose MMAs, kStages k-blocks ago, came after the slot's copy.
+    static constexpr int kSlots = (kStages + 3) / 4;
+    static constexpr int kScaleOffset = kStages * kStageBytes;
+    static constexpr int kBarOffset = kScaleOffset + kSlots * kScaleBytes;
+    static constexpr int kRecvOffset = kBarOffset + 256;
+    // How the parts' sums meet.  Few sums a CTA sends to the CTA that puts the row
+    // together, into memory kept for that: one way, and no barrier (one row, N = K = 4096:
+    // 5.9 -> 5.7 us, K = 12288, 17 rows: 11.0 -> 10.5).  Many would take the place of one more
+    // CTA on the SM (N = 6144, 128 rows: 18.2 us against 11.8; SwiGLU of F = 12288, 17 rows:
+    // 25.0 against 20.0); they are left in the ring, which is done with, for the others to
+    // read.
+    static constexpr bool kSend = WT == 1 ? NT <= 64 : NT <= 16;
+    static int recv_bytes(int rows, int parts) {
+        return kSend ? (rows + parts - 1) / parts * parts * WT * 128 * 4 : 0;
+    }
+    static constexpr int kMostRecv = kSend ? (NT + 7) * WT * 128 * 4 : 0;
+    static_assert(kSend || NT * WT * 128 * 4 <= kScaleOffset, "sums lie in the ring");
     // Tensor memory: the sums, then places for scales.  A place is used again kPlaces
     // tiles of scales (4 k-blocks each) later, and a stage's load has waited for the MMAs
     // of kStages k-blocks ago.
@@ -503,8 +518,56 @@ struct PartsShape {
     // the two could wait for each other.  So a CTA takes 1/543 of an SM's shared memory
     // for each of its columns at least, and the next multiple of 32 above 512 is 544.
     static constexpr int kShareBytes = (kTmemCols * (228 * 1024) + 542) / 543 - 1024;
-    static constexpr int kSmemBytes = kUsedBytes > kShareBytes ? kUsedBytes : kShareBytes;
+    static int smem_bytes(int rows, int parts) {
+        return std::max(kShareBytes, kRecvOffset + recv_bytes(rows, parts) + 1024);
+    }
+    static constexpr int kMostBytes =
+        std::max(kShareBytes, std::min(227 * 1024, kRecvOffset + kMostRecv + 1024));
 };
+
+// Output rows l < rows out of their sums: fold(l, n) gives four neighbouring values of the
+// CTA's WT * 128 columns, row_of(l) the row of the output, n0 the first column's W row.
+template <bool kSwiGLU, int WT, int THREADS, typename Fold, typename RowOf>
+__device__ __forceinline__ void put_rows(const Out& out, const Fold& fold, int rows,
+                                         const RowOf& row_of, int n0, int N) {
+    if constexpr (!kSwiGLU) {
+        constexpr int kFours = WT * 32;
+        for (int i = threadIdx.x; i < rows * kFours; i += THREADS) {
+            const int l = i / kFours, n = 4 * (i % kFours);
+            const float4 s = fold(l, n);
+            if (n0 + n < N)
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out.y) +
+                                          static_cast<int64_t>(row_of(l)) * out.ld + n0 + n) =
+                    make_uint2(bi::pack_bf16x2(s.x, s.y), bi::pack_bf16x2(s.z, s.w));
+        }
+    } else {
+        // a warp takes one row's 256 columns, a block of 128 outputs: lane i the outputs
+        // 4i .. 4i + 3, whose gate and up columns lie 8 apart in a group of 16
+        static_assert(WT == 2, "a whole block of outputs");
+        const int lane = threadIdx.x & 31;
+        const int col = n0 / 2 + 4 * lane;
+        for (int l = threadIdx.x >> 5; l < rows; l += THREADS / 32) {
+            const int at = (lane >> 1) * 16 + (lane & 1) * 4;
+            const float4 g = fold(l, at), u = fold(l, at + 8);
+            const float h0 = bi::swiglu(g.x, u.x), h1 = bi::swiglu(g.y, u.y);
+            const float h2 = bi::swiglu(g.z, u.z), h3 = bi::swiglu(g.w, u.w);
+            uint32_t top = max(max(__float_as_uint(h0) & 0x7fffffffu, __float_as_uint(h1) & 0x7fffffffu),
+                               max(__float_as_uint(h2) & 0x7fffffffu, __float_as_uint(h3) & 0x7fffffffu));
+            if (2 * col >= N) top = 0;  // past F: no W rows, and perhaps NaN for their scales
+            top = __reduce_max_sync(0xffffffffu, top);
+            const uint32_t byte = bi_fp8::scale_byte(top);
+            const float inv = bi_fp8::inverse_scale(byte);
+            const int64_t row = row_of(l);
+            if (2 * col < N)
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(out.y) + row * out.ld + col) =
+                    bi_fp8::codes4(__fmul_rn(h0, inv), __fmul_rn(h1, inv), __fmul_rn(h2, inv),
+                                   __fmul_rn(h3, inv));
+            if (lane == 0)
+                out.scales[bi_fp8::scale_word(row, n0 >> 10, out.spans) + ((n0 >> 8) & 3)] =
+                    static_cast<uint8_t>(byte);
+        }
+    }
+}
 
 template <int NT, bool kSwiGLU, int STAGES>
 __global__ void __launch_bounds__(192)
@@ -519,13 +582,15 @@ __global__ void __launch_bounds__(192)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t* smem_scales = smem + kStages * S::kStageBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem_scales + kStages * S::kScaleBytes);
+    uint8_t* smem_scales = smem + S::kScaleOffset;
+    // sums received [own rows][parts][WT * 128], or left for the others [rows][WT * 128]
+    float* sums = reinterpret_cast<float*>(smem + (S::kSend ? S::kRecvOffset : 0));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBarOffset);
     uint64_t* empty = full + kStages;
     uint64_t* tfull = empty + kStages;
-    uint64_t* drain = tfull + 1;
+    uint64_t* rfull = tfull + 1;  // all sums of this CTA's rows have arrived
+    uint64_t* drain = rfull + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-    float* partial = reinterpret_cast<float*>(smem);  // [NT][WT * 128], over the ring
     __shared__ int s_timeout, s_issued, s_consumed;
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
@@ -538,6 +603,9 @@ __global__ void __launch_bounds__(192)
     const int spans = (num_kb + 3) >> 2;
     const int kb0 = rank * part_blocks;
     const int nkb = min(part_blocks, num_kb - kb0);
+    const int rows = min(NT, M - m0);
+    // row m of the tile is put together by CTA m % nparts, as its row m / nparts
+    const int own_rows = (rows - rank + nparts - 1) / nparts;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -545,8 +613,10 @@ __global__ void __launch_bounds__(192)
             bi::mbar_init(&empty[i], 1);
         }
         bi::mbar_init(tfull, 1);
+        bi::mbar_init(rfull, 1);
         bi::mbar_init(drain, 1);
         bi::fence_mbar_init();
+        if (S::kSend) bi::mbar_arrive_expect_tx(rfull, own_rows * nparts * WT * 512);
         s_timeout = 0;
         s_issued = 0;
         s_consumed = 0;
@@ -570,7 +640,7 @@ __global__ void __launch_bounds__(192)
         __syncwarp();
     }
     bi::tc_fence_before();
-    __syncthreads();
+    bi::cluster_sync();  // every CTA's barriers exist before another's sums arrive
     bi::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     bi::launch_dependents();
@@ -597,7 +667,7 @@ __global__ void __launch_bounds__(192)
                     bi::tma_load_2d(sw + t * 128 * BK, &tmap_w, &full[stage], kb * BK, n0 + 128 * t);
                 bi::tma_load_2d(sw + S::kWBytes, &tmap_x, &full[stage], kb * BK, m0);
                 if (scales) {
-                    uint8_t* sf = smem_scales + stage * S::kScaleBytes;
+                    uint8_t* sf = smem_scales + (issued >> 2) % S::kSlots * S::kScaleBytes;
 #pragma unroll
                     for (int t = 0; t < WT; ++t)
                         bi::tma_load_2d(sf + t * kTile, &tmap_ws, &full[stage], 0,
@@ -638,7 +708,7 @@ __global__ void __launch_bounds__(192)
             const uint32_t idesc = with_byte(mx_idesc(128, NT), i & 3);
             const uint32_t sw = ring + stage * S::kStageBytes;
             const uint64_t dw = operand_desc(sw), dx = operand_desc(sw + S::kWBytes);
-            const uint64_t s = scale_desc(ring + kStages * S::kStageBytes + stage * S::kScaleBytes);
+            const uint64_t s = scale_desc(ring + S::kScaleOffset + (i >> 2) % S::kSlots * S::kScaleBytes);
             if ((i & 3) == 0) sfw = tmem + S::kScaleCol + S::kPlaceCols * ((i >> 2) % S::kPlaces);
             if (bi::elect_one()) {
                 if ((i & 3) == 0) {
@@ -650,7 +720,8 @@ __global__ void __launch_bounds__(192)
 #pragma unroll
                     for (int k = 0; k < BK / 32; ++k)  // 32 bytes of K a step
                         bi::tc_mma_mxf8(tmem + t * NT, dw + (t * 128 * BK >> 4) + 2 * k, dx + 2 * k,
-                                        idesc, sfw + 4 * t, sfw + 4 * WT, (i | k) != 0 ? 1u : 0u);
+                                        idesc, sfw + 4 * t, sfw + 4 * WT,
+                                        (i | k) != 0 ? 1u : 0u);
                 bi::tc_commit(&empty[stage]);
                 if (i + 1 == nkb) bi::tc_commit(tfull);
             }
@@ -681,111 +752,353 @@ __global__ void __launch_bounds__(192)
             s_timeout = 1;
         }
         bi::tc_fence_after();
-        const int rows = min(NT, M - m0);
-        if (ok) {
+        // a part that gave up has NaN: nobody waits in vain, and nothing looks like a sum
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t to = bi::smem_u32(sums + quarter * 32 + lane), bar = bi::smem_u32(rfull);
 #pragma unroll
-            for (int t = 0; t < WT; ++t) {
-                float* to = partial + t * 128 + quarter * 32 + lane;
-                for (int m = 0; m < rows; m += 16) {
-                    uint32_t r[16];
-                    bi::tmem_ld_32x32b_x16(
-                        tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + t * NT + m, r);
+        for (int t = 0; t < WT; ++t) {
+            int owner = 0, local = 0;
+            for (int m = 0; m < rows; m += 16) {
+                uint32_t r[16];
+                if (ok) {
+                    bi::tmem_ld_32x32b_x16(taddr + t * NT + m, r);
                     bi::tmem_ld_wait();
+                }
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) to[(m + e) * (WT * 128)] = __uint_as_float(r[e]);
+                for (int e = 0; e < 16; ++e) {
+                    const float v = __uint_as_float(ok ? r[e] : 0x7FC00000u);
+                    if constexpr (S::kSend) {
+                        if (m + e >= rows) break;
+                        const uint32_t at = to + 4 * ((local * nparts + rank) * (WT * 128) + t * 128);
+                        bi::st_async_f32(bi::mapa_shared(at, owner), v, bi::mapa_shared(bar, owner));
+                        if (++owner == nparts) {
+                            owner = 0;
+                            ++local;
+                        }
+                    } else if (ok) {  // (the ring may still be written where it is not)
+                        sums[(m + e) * (WT * 128) + t * 128 + quarter * 32 + lane] = v;
+                    }
                 }
             }
         }
     }
-    __syncthreads();
-    if (s_timeout) {
-        // copies in flight first (they land in the ring), then NaN where the sums would be
-        if (threadIdx.x == 0)
-            for (int i = s_consumed; i < s_issued; ++i)
-                bi::mbar_wait_for(&full[i % kStages], (i / kStages) & 1, bi::kDrainNs);
+    __syncwarp();
+
+    // the parts' sums of this CTA's rows, ascending
+    bool arrived = true;
+    if constexpr (S::kSend) {  // a peer that gives up does so within kWaitNs and then sends
+        arrived = __all_sync(0xffffffffu, bi::mbar_wait_cluster(rfull, 0, 3 * bi::kWaitNs));
+        if (!arrived && lane == 0) {
+            bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
+            s_timeout = 1;
+        }
+    } else {
         __syncthreads();
-        for (int i = threadIdx.x; i < NT * WT * 128; i += 192) partial[i] = __uint_as_float(0x7FC00000u);
+        if (s_timeout) {
+            if (threadIdx.x == 0)  // copies in flight land in the ring
+                for (int i = s_consumed; i < s_issued; ++i)
+                    bi::mbar_wait_for(&full[i % kStages], (i / kStages) & 1, bi::kDrainNs);
+            __syncthreads();
+            for (int i = threadIdx.x; i < NT * WT * 128; i += 192) sums[i] = __uint_as_float(0x7FC00000u);
+        }
+        bi::cluster_sync();
     }
+    const uint32_t sums_at = bi::smem_u32(sums);
+    const auto fold = [&](int l, int n) {  // four neighbouring values of own row l
+        float4 v[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            if (p >= nparts) continue;
+            if constexpr (S::kSend)
+                v[p] = *reinterpret_cast<const float4*>(sums + (l * nparts + p) * (WT * 128) + n);
+            else
+                v[p] = bi::ld_cluster_f4(
+                    bi::mapa_shared(sums_at + 4 * ((l * nparts + rank) * (WT * 128) + n), p));
+        }
+        float4 s = v[0];
+#pragma unroll
+        for (int p = 1; p < 8; ++p) {
+            if (p >= nparts) continue;
+            s.x = __fadd_rn(s.x, v[p].x);
+            s.y = __fadd_rn(s.y, v[p].y);
+            s.z = __fadd_rn(s.z, v[p].z);
+            s.w = __fadd_rn(s.w, v[p].w);
+        }
+        return s;
+    };
+    if (arrived)
+        put_rows<kSwiGLU, WT, 192>(out, fold, own_rows, [&](int l) { return m0 + l * nparts + rank; },
+                                   n0, N);
     bi::tc_fence_before();
-    bi::cluster_sync();  // all parts' sums are in place
+    __syncthreads();
+    if (S::kSend && s_timeout && threadIdx.x == 0)  // copies in flight
+        for (int i = s_consumed; i < s_issued; ++i)
+            bi::mbar_wait_for(&full[i % kStages], (i / kStages) & 1, bi::kDrainNs);
     if (warp == 1) {
         bi::tc_fence_after();
         bi::tmem_dealloc(tmem_base, S::kTmemCols);
     }
-
-    // the parts' sums, ascending, the outputs dealt out over the cluster's CTAs
-    const int rows = min(NT, M - m0);
-    const uint32_t base = bi::smem_u32(partial);
-    if constexpr (!kSwiGLU) {
-        const int items = rows * 32;  // four outputs each
-        for (int i = rank * 192 + threadIdx.x; i < items; i += nparts * 192) {
-            const int m = i >> 5, n = n0 + 4 * (i & 31);
-            float4 v[8];
-#pragma unroll
-            for (int p = 0; p < 8; ++p)
-                if (p < nparts) v[p] = bi::ld_cluster_f4(bi::mapa_shared(base + 16 * i, p));
-            float4 s = v[0];
-#pragma unroll
-            for (int p = 1; p < 8; ++p)
-                if (p < nparts) {
-                    s.x = __fadd_rn(s.x, v[p].x);
-                    s.y = __fadd_rn(s.y, v[p].y);
-                    s.z = __fadd_rn(s.z, v[p].z);
-                    s.w = __fadd_rn(s.w, v[p].w);
-                }
-            if (n < N)
-                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out.y) +
-                                          static_cast<int64_t>(m0 + m) * out.ld + n) =
-                    make_uint2(bi::pack_bf16x2(s.x, s.y), bi::pack_bf16x2(s.z, s.w));
-        }
-    } else {
-        // a warp folds one row's 256 columns: lane l the outputs 4l .. 4l + 3 of the
-        // block, whose gate and up columns lie 8 apart in a group of 16
-        const int nb = blockIdx.z;
-        for (int m = rank * 6 + warp; m < rows; m += nparts * 6) {
-            const uint32_t at = base + 4 * (m * 256 + (lane >> 1) * 16 + (lane & 1) * 4);
-            float4 v[8], w[8];
-#pragma unroll
-            for (int p = 0; p < 8; ++p)
-                if (p < nparts) {
-                    const uint32_t a = bi::mapa_shared(at, p);
-                    v[p] = bi::ld_cluster_f4(a);
-                    w[p] = bi::ld_cluster_f4(a + 32);
-                }
-            float4 g = v[0], u = w[0];
-#pragma unroll
-            for (int p = 1; p < 8; ++p)
-                if (p < nparts) {
-                    g.x = __fadd_rn(g.x, v[p].x);
-                    g.y = __fadd_rn(g.y, v[p].y);
-                    g.z = __fadd_rn(g.z, v[p].z);
-                    g.w = __fadd_rn(g.w, v[p].w);
-                    u.x = __fadd_rn(u.x, w[p].x);
-                    u.y = __fadd_rn(u.y, w[p].y);
-                    u.z = __fadd_rn(u.z, w[p].z);
-                    u.w = __fadd_rn(u.w, w[p].w);
-                }
-            const float h0 = bi::swiglu(g.x, u.x), h1 = bi::swiglu(g.y, u.y);
-            const float h2 = bi::swiglu(g.z, u.z), h3 = bi::swiglu(g.w, u.w);
-            uint32_t top = max(max(__float_as_uint(h0) & 0x7fffffffu, __float_as_uint(h1) & 0x7fffffffu),
-                               max(__float_as_uint(h2) & 0x7fffffffu, __float_as_uint(h3) & 0x7fffffffu));
-            const int col = nb * 128 + 4 * lane;
-            if (2 * col >= N) top = 0;  // past F: no W rows, and perhaps NaN for their scales
-            top = __reduce_max_sync(0xffffffffu, top);
-            const uint32_t byte = bi_fp8::scale_byte(top);
-            const float inv = bi_fp8::inverse_scale(byte);
-            const int64_t row = m0 + m;
-            if (2 * col < N)
-                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(out.y) + row * out.ld + col) =
-                    bi_fp8::codes4(__fmul_rn(h0, inv), __fmul_rn(h1, inv), __fmul_rn(h2, inv),
-                                   __fmul_rn(h3, inv));
-            if (lane == 0)
-                out.scales[bi_fp8::scale_word(row, nb >> 2, out.spans) + (nb & 3)] =
-                    static_cast<uint8_t>(byte);
-        }
-    }
     __syncwarp();
-    bi::cluster_sync_relaxed();  // no CTA leaves while another reads its sums
+    bi::cluster_sync_relaxed();  // no CTA leaves while sums are on their way to it, or read
+}
+
+// ------------------------------------ few rows, enough W rows for all SMs ----
+// A CTA runs all of K for 256 W rows and NT rows of x, alone on its SM, the parts one
+// after the other: no cluster, and the sums meet in registers as in the pair kernel (whose
+// 256 rows of x would be mostly empty here).
+template <int NT>
+struct WholeShape {
+    static constexpr int kStageBytes = 256 * BK + NT * BK;
+    static constexpr int kScaleBytes = 3 * kTile;
+    static constexpr int kStages = NT <= 32 ? 5 : 4;
+    static constexpr int kScaleOffset = kStages * kStageBytes;
+    static constexpr int kBarOffset = kScaleOffset + kStages * kScaleBytes;
+    static constexpr int kSmemBytes = kBarOffset + 256 + 1024;
+    static_assert(NT * 256 * 4 <= kScaleOffset, "sums lie in the ring at last");
+    // Tensor memory: three accumulators of NT columns, taken in turn by the two W tiles of
+    // every part (one is drained while the other's last k-block still runs), and 8 places
+    // for scales: one is used again at least 8 k-blocks later, kStages < 8.
+    static constexpr uint32_t kScaleCol = 384;
+    static constexpr int kThreads = 320;
+};
+
+template <int NT, bool kSwiGLU>
+__global__ void __launch_bounds__(WholeShape<NT>::kThreads, 1)
+    gemm_fp8_whole_kernel(const __grid_constant__ CUtensorMap tmap_x,
+                          const __grid_constant__ CUtensorMap tmap_w,
+                          const __grid_constant__ CUtensorMap tmap_xs,
+                          const __grid_constant__ CUtensorMap tmap_ws, Out out, int M, int N, int K,
+                          int part_blocks, uint32_t* err) {
+    using S = WholeShape<NT>;
+    constexpr int kStages = S::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* smem_scales = smem + S::kScaleOffset;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBarOffset);
+    uint64_t* empty = full + kStages;
+    uint64_t* tfull = empty + kStages;
+    uint64_t* tempty = tfull + 3;
+    uint64_t* done = tempty + 3;  // every MMA has completed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    __shared__ int s_timeout, s_issued, s_consumed;
+
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int lane = threadIdx.x & 31;
+    const int m0 = blockIdx.x * NT;
+    const int n0 = blockIdx.y * 256;
+    const int num_kb = (K + BK - 1) / BK;
+    const int spans = (num_kb + 3) >> 2;
+    const int rows = min(NT, M - m0);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bi::mbar_init(&full[i], 1);
+            bi::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            bi::mbar_init(&tfull[i], 1);
+            bi::mbar_init(&tempty[i], 4);
+        }
+        bi::mbar_init(done, 1);
+        bi::fence_mbar_init();
+        s_timeout = 0;
+        s_issued = 0;
+        s_consumed = 0;
+        bi::tma_prefetch_desc(&tmap_x);
+        bi::tma_prefetch_desc(&tmap_w);
+        bi::tma_prefetch_desc(&tmap_xs);
+        bi::tma_prefetch_desc(&tmap_ws);
+    }
+    if (warp == 1) {
+        bi::tmem_alloc(tmem_slot, 512);
+        bi::tmem_relinquish();
+    }
+    bi::tc_fence_before();
+    __syncthreads();
+    bi::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    bi::launch_dependents();
+    bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
+
+    float sum[NT];  // epilogue warps; from -0 on: -0 + x is x, whatever its sign
+    if (warp == 0) {  // the whole warp runs the loop, one lane issues
+        int stage = 0;
+        uint32_t phase = 0;
+        int kb = 0;
+        bool ok = true;
+        for (; kb < num_kb; ++kb) {
+            if (!__all_sync(0xffffffffu, bi::mbar_wait(&empty[stage], phase ^ 1))) {
+                ok = false;
+                break;
+            }
+            const bool scales = (kb & 3) == 0;
+            uint8_t* sw = smem + stage * S::kStageBytes;
+            if (bi::elect_one()) {
+                bi::mbar_arrive_expect_tx(&full[stage],
+                                          S::kStageBytes + (scales ? S::kScaleBytes : 0));
+                bi::tma_load_2d(sw, &tmap_w, &full[stage], kb * BK, n0);
+                bi::tma_load_2d(sw + 128 * BK, &tmap_w, &full[stage], kb * BK, n0 + 128);
+                bi::tma_load_2d(sw + 256 * BK, &tmap_x, &full[stage], kb * BK, m0);
+                if (scales) {
+                    uint8_t* sf = smem_scales + stage * S::kScaleBytes;
+                    bi::tma_load_2d(sf, &tmap_ws, &full[stage], 0, (n0 / 128) * spans + (kb >> 2));
+                    bi::tma_load_2d(sf + kTile, &tmap_ws, &full[stage], 0,
+                                    (n0 / 128 + 1) * spans + (kb >> 2));
+                    bi::tma_load_2d(sf + 2 * kTile, &tmap_xs, &full[stage], 0,
+                                    (m0 / 128) * spans + (kb >> 2));
+                }
+            }
+            __syncwarp();
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        if (lane == 0) {
+            s_issued = kb;
+            if (!ok) {
+                bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
+                s_timeout = 1;
+            }
+        }
+    } else if (warp == 1) {  // the whole warp runs the loop, one lane issues
+        const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+        const uint32_t ring = bi::smem_u32(smem);
+        // where in their tile of scales the CTA's rows of x start
+        const uint32_t x_col = 8 + ((m0 & 127) >> 5);
+        uint32_t sf = 0;
+        int stage = 0, acc = 0, left = 0, kb = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        int d[2] = {0, 0};
+        bool ok = true;
+        for (; kb < num_kb && ok; ++kb) {
+            const bool first = left == 0;
+            if (first) left = min(part_blocks, num_kb - kb);
+            --left;
+            if (!__all_sync(0xffffffffu, bi::mbar_wait(&full[stage], phase))) {
+                ok = false;
+                break;
+            }
+            bi::tc_fence_after();
+            const uint32_t sw = ring + stage * S::kStageBytes;
+            const uint64_t dw = operand_desc(sw), dx = operand_desc(sw + 256 * BK);
+            const uint32_t idesc = with_byte(mx_idesc(128, NT), kb & 3);
+            if ((kb & 3) == 0) {
+                sf = tmem + S::kScaleCol + 16 * ((kb >> 2) & 7);
+                const uint64_t s = scale_desc(ring + S::kScaleOffset + stage * S::kScaleBytes);
+                if (bi::elect_one()) {
+#pragma unroll
+                    for (int t = 0; t < 3; ++t) bi::tc_cp_scales(sf + 4 * t, s + (t * kTile >> 4));
+                }
+                __syncwarp();
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (first) {
+                    if (!__all_sync(0xffffffffu, bi::mbar_wait(&tempty[acc], acc_phase ^ 1))) {
+                        ok = false;
+                        break;
+                    }
+                    bi::tc_fence_after();
+                    d[t] = acc;
+                    if (++acc == 3) {
+                        acc = 0;
+                        acc_phase ^= 1;
+                    }
+                }
+                if (bi::elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < BK / 32; ++k)
+                        bi::tc_mma_mxf8(tmem + d[t] * NT, dw + (t * 128 * BK >> 4) + 2 * k, dx + 2 * k,
+                                        idesc, sf + 4 * t, sf + x_col, (!first || k != 0) ? 1u : 0u);
+                    if (left == 0) bi::tc_commit(&tfull[d[t]]);
+                    if (t == 1) bi::tc_commit(&empty[stage]);
+                    if (t == 1 && kb + 1 == num_kb) bi::tc_commit(done);
+                }
+                __syncwarp();
+            }
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        if (bi::elect_one()) {
+            s_consumed = kb;
+            if (!ok) {
+                bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
+                s_timeout = 1;
+                if (kb > 0) {  // a bounded wait for what was issued
+                    bi::tc_commit(done);
+                    bi::mbar_wait_for(done, 0, bi::kDrainNs);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // warps 2..5 tile 0, 6..9 tile 1: W rows quarter * 32 + lane, all rows of x
+        const int quarter = warp & 3;
+        const int t = (warp - 2) >> 2;
+        const int num_parts = (num_kb + part_blocks - 1) / part_blocks;
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+        int acc = t;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) sum[i] = -0.f;
+#pragma unroll 1
+        for (int p = 0; p < num_parts && ok; ++p) {
+            ok = __all_sync(0xffffffffu, bi::mbar_wait(&tfull[acc], acc_phase));
+            if (!ok) break;
+            bi::tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < NT / 16; ++q) {
+                uint32_t r[16];
+                bi::tmem_ld_32x32b_x16(taddr + acc * NT + 16 * q, r);
+                bi::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    sum[16 * q + i] = __fadd_rn(sum[16 * q + i], __uint_as_float(r[i]));
+            }
+            bi::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bi::mbar_arrive(&tempty[acc]);
+            acc += 2;
+            if (acc >= 3) {
+                acc -= 3;
+                acc_phase ^= 1;
+            }
+        }
+        // the ring is free once the other tile's MMAs are done too
+        if (ok) ok = __all_sync(0xffffffffu, bi::mbar_wait(done, 0));
+        if (!ok && lane == 0) {
+            bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
+            s_timeout = 1;
+        }
+        if (ok) {
+            float* to = reinterpret_cast<float*>(smem) + t * 128 + quarter * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                if (i < rows) to[i * 256] = sum[i];
+        }
+        bi::tc_fence_before();
+    }
+    __syncthreads();
+    if (s_timeout) {
+        if (threadIdx.x == 0)  // copies in flight
+            for (int i = s_consumed; i < s_issued; ++i)
+                bi::mbar_wait_for(&full[i % kStages], (i / kStages) & 1, bi::kDrainNs);
+        __syncthreads();
+    } else {
+        const float* sums = reinterpret_cast<const float*>(smem);
+        put_rows<kSwiGLU, 2, S::kThreads>(
+            out, [&](int l, int n) { return *reinterpret_cast<const float4*>(sums + l * 256 + n); },
+            rows, [&](int l) { return m0 + l; }, n0, N);
+    }
+    if (warp == 1) {
+        bi::tc_fence_after();
+        bi::tmem_dealloc(tmem_base, 512);
+    }
 }
 
 // ------------------------------------------------------------- launches ----
@@ -832,58 +1145,103 @@ bi_status launch_pair(const Call& c) {
                : BI_ERR_CUDA;
 }
 
+struct PartsPlan {
+    Parts parts;
+    int64_t ctas;
+    int rows;  // of the largest tile
+};
+
 template <int NT, bool kSwiGLU, int STAGES>
-bi_status launch_parts(const Call& c, bool prefetch) {
+bool at_once(const PartsPlan& p, int sms) {  // whether the SMs hold all CTAs at once
+    using S = PartsShape<NT, kSwiGLU ? 2 : 1, STAGES>;
+    const int bytes = S::smem_bytes(p.rows, p.parts.count);
+    return bytes <= S::kMostBytes && (228 * 1024) / (bytes + 1024 + 128) * int64_t{sms} >= p.ctas;
+}
+
+template <int NT, bool kSwiGLU, int STAGES>
+bi_status launch_parts(const Call& c, const PartsPlan& p, bool prefetch) {
     using S = PartsShape<NT, kSwiGLU ? 2 : 1, STAGES>;
     static std::atomic<bool> set[64] = {};
-    if (!bi::allow_smem(gemm_fp8_parts_kernel<NT, kSwiGLU, STAGES>, S::kSmemBytes, set))
+    if (!bi::allow_smem(gemm_fp8_parts_kernel<NT, kSwiGLU, STAGES>, S::kMostBytes, set))
         return BI_ERR_CUDA;
     CUtensorMap t[4];
     if (!encode(c, NT, 128, t)) return BI_ERR_CUDA;
-    const Parts p = parts_of(c.K);
     const int rows = kSwiGLU ? 256 : 128;
-    const dim3 grid(p.count, (c.M + NT - 1) / NT, (c.N + rows - 1) / rows);
-    return bi::launch_pdl_cluster(gemm_fp8_parts_kernel<NT, kSwiGLU, STAGES>, p.count, grid,
-                                  dim3(192), S::kSmemBytes, c.stream, t[0], t[1], t[2], t[3], c.out,
-                                  c.M, c.N, c.K, p.blocks, prefetch, bi::device_error_word()) ==
-                   cudaSuccess
+    const dim3 grid(p.parts.count, (c.M + NT - 1) / NT, (c.N + rows - 1) / rows);
+    return bi::launch_pdl_cluster(gemm_fp8_parts_kernel<NT, kSwiGLU, STAGES>, p.parts.count, grid,
+                                  dim3(192), S::smem_bytes(p.rows, p.parts.count), c.stream, t[0],
+                                  t[1], t[2], t[3], c.out, c.M, c.N, c.K, p.parts.blocks, prefetch,
+                                  bi::device_error_word()) == cudaSuccess
                ? BI_OK
                : BI_ERR_CUDA;
 }
 
-// Stages by the launch's CTAs: one, two or three CTAs an SM, the fewest that hold the
-// launch at once (a CTA then has the most loads in flight), else three.
-template <int NT, bool kSwiGLU, int ONE, int TWO, int THREE>
-bi_status launch_parts(const Call& c) {
+// The deepest ring (most loads in flight a CTA) with which the SMs hold the launch at
+// once, else the shallowest (most CTAs, whose starts and ends overlap).
+template <int NT, bool kSwiGLU, int DEEP, int MID, int SHALLOW>
+bi_status launch_parts(const Call& c, int sms) {
     const int rows = kSwiGLU ? 256 : 128;
-    const int64_t ctas = static_cast<int64_t>(parts_of(c.K).count) * ((c.M + NT - 1) / NT) *
-                         ((c.N + rows - 1) / rows);
-    const int sms = bi::sm_count();
-    if (ctas <= sms) return launch_parts<NT, kSwiGLU, ONE>(c, true);
-    if (ctas <= 2 * sms) return launch_parts<NT, kSwiGLU, TWO>(c, true);
-    return launch_parts<NT, kSwiGLU, THREE>(c, false);
+    const Parts parts = parts_of(c.K);
+    const PartsPlan p{parts, static_cast<int64_t>(parts.count) * ((c.M + NT - 1) / NT) * ((c.N + rows - 1) / rows),
+                      std::min(NT, c.M)};
+    if (at_once<NT, kSwiGLU, DEEP>(p, sms)) return launch_parts<NT, kSwiGLU, DEEP>(c, p, true);
+    if (at_once<NT, kSwiGLU, MID>(p, sms)) return launch_parts<NT, kSwiGLU, MID>(c, p, true);
+    return launch_parts<NT, kSwiGLU, SHALLOW>(c, p, false);
 }
 
-// Which kernel: a schedule choice, the bits are the same.  Up to 32 rows the parts
-// kernel (17 rows, K = 4096: N = 4096 6.3 us against 15, N = 24576 21.4 against 29.7).  Beyond, its
-// time goes with its 128 x 128 tiles, that of the other with its waves of 256 x 256
-// tiles over the CTA pairs, and the two cross at about a pair's worth of tiles a wave:
-// K = 4096, N = 4096 8.6 against 15.5 us at 128 rows and 11.0 against 15.5 at 200 (64
-// tiles), 18.6 against 15.7 at 300 (96); N = 24576 35.6 against 30.1 at 128 rows (192 tiles,
-// two waves); K = 12288, N = 4096 25.6 against 34.1 at 200 rows, 37.1 against 34.3 at 300.
+template <int NT, bool kSwiGLU>
+bi_status launch_whole(const Call& c) {
+    using S = WholeShape<NT>;
+    static std::atomic<bool> set[64] = {};
+    if (!bi::allow_smem(gemm_fp8_whole_kernel<NT, kSwiGLU>, S::kSmemBytes, set)) return BI_ERR_CUDA;
+    CUtensorMap t[4];
+    if (!encode(c, NT, 128, t)) return BI_ERR_CUDA;
+    const dim3 grid((c.M + NT - 1) / NT, (c.N + 255) / 256);
+    return bi::launch_pdl(gemm_fp8_whole_kernel<NT, kSwiGLU>, grid, dim3(S::kThreads), S::kSmemBytes,
+                          c.stream, t[0], t[1], t[2], t[3], c.out, c.M, c.N, c.K,
+                          parts_of(c.K).blocks, bi::device_error_word()) == cudaSuccess
+               ? BI_OK
+               : BI_ERR_CUDA;
+}
+
+// Which kernel: a schedule choice, the bits are the same.  Measured, us, K = 4096 unless
+// said otherwise, as parts / whole / pair:
+//   up to 32 rows: the parts kernel (N = 4096, 24 rows 6.2 / 14.6 / 15.0; N = 12288 11.6 / 15.2
+//   / 19.8), but the whole kernel where the SMs do not hold the parts' CTAs at once, three
+//   each (N = 24576, one row 19.8 / 19.0 / 34.7, 24 rows 22.1 / 19.7 / 29.4), and for SwiGLU of
+//   more than 16 rows (F = 8192, 24 rows 19.2 / 16.1 / 20.3);
+//   up to 128 rows, where the pair kernel has more than a wave of tiles: the whole kernel
+//   (N = 24576, 64 rows 29.2 / 21.2 / 28.8, 128 rows 35.1 / 24.8 / 29.9; one wave, N = 12288,
+//   128 rows 22.2 / 20.5 / 17.1);
+//   else the parts kernel as long as its 128 x 128 tiles are no more than the pairs of a wave
+//   each (N = 4096, 128 rows 8.8 / 19.7 / 15.6, 256 rows, 64 tiles, 11.6 / 19.3 / 15.7, 384 rows, 96
+//   tiles, 20.3 / 19.2 / 15.8; K = 12288, 256 rows 27.3 / 44.4 / 34.2), for SwiGLU its CTAs no more than
+//   the SMs (F = 4096, 128 rows 14.9 / 21.6 / 16.2; K = 12288 46.6 / 46.4 / 35.6);
+//   else the pair kernel.
 template <bool kSwiGLU>
 bi_status launch_gemm(const Call& c) {
     const int sms = bi::sm_count();
     if (sms < 2) return BI_ERR_CUDA;
+    const int64_t pairs = sms / 2;
     const int64_t small_m = (c.M + 127) / 128, small_n = (c.N + 127) / 128;
-    const int64_t large = static_cast<int64_t>((c.M + 255) / 256) * ((c.N + 255) / 256);
-    const int64_t waves = (large + sms / 2 - 1) / (sms / 2);
-    if ((c.M <= 32 || small_m * small_n <= waves * (sms / 2)) && small_m <= 65535 && small_n <= 65535) {
-        constexpr bool g = kSwiGLU;
-        if (c.M <= 16) return g ? launch_parts<16, g, 6, 3, 2>(c) : launch_parts<16, g, 8, 4, 3>(c);
-        if (c.M <= 32) return g ? launch_parts<32, g, 5, 2, 2>(c) : launch_parts<32, g, 8, 4, 3>(c);
-        if (c.M <= 64) return g ? launch_parts<64, g, 4, 2, 2>(c) : launch_parts<64, g, 8, 4, 4>(c);
-        return g ? launch_parts<128, g, 4, 4, 4>(c) : launch_parts<128, g, 6, 3, 3>(c);
+    const int64_t large_m = (c.M + 255) / 256, large_n = (c.N + 255) / 256;
+    const int64_t waves = (large_m * large_n + pairs - 1) / pairs;
+    const int64_t ctas = parts_of(c.K).count * small_m * (kSwiGLU ? large_n : small_n);
+    constexpr bool g = kSwiGLU;
+    if (c.M <= 128 && large_n * 4 > sms && large_n <= sms &&
+        (c.M > 32 ? large_n > pairs : ctas > 3 * sms || (g && c.M > 16))) {
+        if (c.M <= 16) return launch_whole<16, g>(c);
+        if (c.M <= 32) return launch_whole<32, g>(c);
+        if (c.M <= 64) return launch_whole<64, g>(c);
+        return launch_whole<128, g>(c);
+    }
+    if (small_m <= 65535 && small_n <= 65535 &&
+        (c.M <= 32 || (small_m * small_n <= waves * pairs &&
+                       (!g || (ctas <= sms && parts_of(c.K).count >= 4))))) {
+        if (c.M <= 16) return g ? launch_parts<16, g, 5, 3, 2>(c, sms) : launch_parts<16, g, 8, 4, 3>(c, sms);
+        if (c.M <= 32) return g ? launch_parts<32, g, 4, 2, 2>(c, sms) : launch_parts<32, g, 8, 4, 3>(c, sms);
+        if (c.M <= 64) return g ? launch_parts<64, g, 4, 2, 2>(c, sms) : launch_parts<64, g, 6, 3, 3>(c, sms);
+        return g ? launch_parts<128, g, 4, 4, 4>(c, sms) : launch_parts<128, g, 6, 3, 3>(c, sms);
     }
     return launch_pair<kSwiGLU>(c);
 }
