@@ -79,33 +79,37 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 }
 
 // ---------------------------------------------------------- many rows ----
-namespace pair {
-constexpr int BMP = 256;  // tile rows of the pair; 128 per CTA
-constexpr int BN = 256;
-constexpr int kStages = 5;
-constexpr int kABytes = 128 * BK;
-constexpr int kStageBytes = 2 * kABytes;  // 128 rows of x, 2 x 64 rows of W
-constexpr int kScaleBytes = 3 * kTile;    // 128 rows of x, 256 rows of W
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 128 + 32 * kEpiWarps;
-// Registers a thread: 168 at launch (three warps share a sub-partition's 16384).  The
-// epilogue holds 128 sums and loads 64 columns at once; the other four warps give
-// theirs up for that.
-constexpr int kFewRegs = 56, kManyRegs = 224;
-static_assert(128 * kFewRegs + 32 * kEpiWarps * kManyRegs <= kThreads * 168, "registers");
-// Tensor memory: three accumulators of 128 columns, and 8 places of 16 columns
-// for scales.  The tile's two column halves are accumulators of their own, taken
-// in turn out of three, so that a half's MMAs of the next part need not wait for
-// the other half to be drained; two accumulators of 256 columns would leave no
-// room for the scales.
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kScaleCol = 384;
-constexpr int kOutBytes = 32 * 64;  // a warp's 32 rows x 32 bf16 columns on their way out
-constexpr int kOutBufs = 3;          // of them in turn
-constexpr int kOutOffset = (kStages * (kStageBytes + kScaleBytes) + 1023) / 1024 * 1024;
-constexpr int kSmemBytes = kOutOffset + kEpiWarps * kOutBufs * kOutBytes + 1024 + 256;
-constexpr uint32_t kIdesc = mx_idesc(BMP, 128);
-}  // namespace pair
+// H: halves of 128 columns in a tile.  Two as a rule; one where that keeps more pairs
+// busy, at the price of reading x twice as often (each SM then takes 24 KB in the time of
+// 256 cycles' MMAs, more than the 64 bytes a cycle it can).
+template <int H>
+struct PairShape {
+    static constexpr int BMP = 256;  // tile rows of the pair; 128 per CTA
+    static constexpr int BN = 128 * H;
+    static constexpr int kStages = H == 2 ? 5 : 7;
+    static constexpr int kABytes = 128 * BK;
+    static constexpr int kStageBytes = kABytes + H * 64 * BK;  // 128 rows of x, 64 of each half's W
+    static constexpr int kScaleBytes = (1 + H) * kTile;
+    static constexpr int kEpiWarps = 8;
+    static constexpr int kThreads = 128 + 32 * kEpiWarps;
+    // Registers a thread: 168 at launch (three warps share a sub-partition's 16384).  The
+    // epilogue holds 128 sums and loads 64 columns at once; the other four warps give
+    // theirs up for that.
+    static constexpr int kFewRegs = 56, kManyRegs = 224;
+    static_assert(128 * kFewRegs + 32 * kEpiWarps * kManyRegs <= kThreads * 168, "registers");
+    // Tensor memory: three accumulators of 128 columns, and 8 places of 16 columns
+    // for scales.  The tile's column halves are accumulators of their own, taken in turn out
+    // of three, so that a half's MMAs of the next part need not wait for the other half to
+    // be drained; two accumulators of 256 columns would leave no room for the scales.
+    static constexpr uint32_t kTmemCols = 512;
+    static constexpr uint32_t kScaleCol = 384;
+    static_assert(kStages < 8, "scale places");
+    static constexpr int kOutBytes = 32 * 64;  // a warp's 32 rows x 32 bf16 columns on their way out
+    static constexpr int kOutBufs = 3;         // of them in turn
+    static constexpr int kOutOffset = (kStages * (kStageBytes + kScaleBytes) + 1023) / 1024 * 1024;
+    static constexpr int kSmemBytes = kOutOffset + kEpiWarps * kOutBufs * kOutBytes + 1024 + 256;
+    static constexpr uint32_t kIdesc = mx_idesc(BMP, 128);
+};
 
 // Tile order, as in bi_gemm: groups of M-tiles whose x stays in L2.
 __device__ __forceinline__ void tile_coords(int tile, int num_m, int num_n, int group_m, int& mb,
@@ -118,22 +122,24 @@ __device__ __forceinline__ void tile_coords(int tile, int num_m, int num_n, int 
     nb = r / gm;
 }
 
-template <bool kSwiGLU>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
+template <bool kSwiGLU, int H>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<H>::kThreads, 1)
     gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
                          const __grid_constant__ CUtensorMap tmap_w,
                          const __grid_constant__ CUtensorMap tmap_xs,
                          const __grid_constant__ CUtensorMap tmap_ws,
                          const __grid_constant__ CUtensorMap tmap_y, Out out, int M, int N, int K,
                          int part_blocks, int group_m, uint32_t* err) {
-    constexpr int kStages = pair::kStages, kABytes = pair::kABytes, kStageBytes = pair::kStageBytes;
+    static_assert(!kSwiGLU || H == 2, "a block of 128 outputs takes 256 W rows");
+    using S = PairShape<H>;
+    constexpr int kStages = S::kStages, kABytes = S::kABytes, kStageBytes = S::kStageBytes;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* smem_scales = smem + kStages * kStageBytes;
-    uint8_t* smem_out = smem + pair::kOutOffset;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem_out + pair::kEpiWarps * pair::kOutBufs *
-                                                                pair::kOutBytes);
+    uint8_t* smem_out = smem + S::kOutOffset;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem_out + S::kEpiWarps * S::kOutBufs *
+                                                                S::kOutBytes);
     uint64_t* empty = full + kStages;
     uint64_t* tfull = empty + kStages;
     uint64_t* tempty = tfull + 3;
@@ -148,8 +154,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     const bool leader = rank == 0;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int lane = threadIdx.x & 31;
-    const int num_m = (M + pair::BMP - 1) / pair::BMP;
-    const int num_n = (N + pair::BN - 1) / pair::BN;
+    const int num_m = (M + S::BMP - 1) / S::BMP;
+    const int num_n = (N + S::BN - 1) / S::BN;
     const int num_tiles = num_m * num_n;
     const int num_kb = (K + BK - 1) / BK;
     const int spans = (num_kb + 3) >> 2;
@@ -163,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         }
         for (int i = 0; i < 3; ++i) {
             bi::mbar_init(&tfull[i], 1);
-            bi::mbar_init(&tempty[i], 2 * pair::kEpiWarps);  // both CTAs' (leader's copy used)
+            bi::mbar_init(&tempty[i], 2 * S::kEpiWarps);  // both CTAs' (leader's copy used)
         }
         bi::mbar_init(drain, 1);
         bi::fence_mbar_init();
@@ -176,7 +182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         bi::tma_prefetch_desc(&tmap_ws);
     }
     if (warp == 1) {
-        bi::tmem_alloc_pair(tmem_slot, pair::kTmemCols);
+        bi::tmem_alloc_pair(tmem_slot, S::kTmemCols);
         bi::tmem_relinquish_pair();
     }
     bi::tc_fence_before();
@@ -187,7 +193,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
 
     if (warp < 4) {
-        bi::fewer_registers<pair::kFewRegs>();
+        bi::fewer_registers<S::kFewRegs>();
     if (warp == 0) {  // the whole warp runs the loop, one lane issues
         const uint32_t bar0 = bi::mapa_shared(bi::smem_u32(full), 0);  // the leader's
         int stage = 0;
@@ -198,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             int mb, nb;
             tile_coords(tile, num_m, num_n, group_m, mb, nb);
             const int m_tile = 2 * mb + static_cast<int>(rank);  // of 128 rows
-            const int w_row = nb * pair::BN + static_cast<int>(rank) * 64;
+            const int w_row = nb * S::BN + static_cast<int>(rank) * 64;
             for (int kb = 0; kb < num_kb; ++kb) {
                 if (!__all_sync(0xffffffffu, bi::mbar_wait(&empty[stage], phase ^ 1))) {
                     ok = false;
@@ -210,18 +216,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                 if (bi::elect_one()) {
                     if (leader)
                         bi::mbar_arrive_expect_tx(
-                            &full[stage], 2 * (kStageBytes + (scales ? pair::kScaleBytes : 0)));
+                            &full[stage], 2 * (kStageBytes + (scales ? S::kScaleBytes : 0)));
                     bi::tma_load_2d_pair(sa, &tmap_x, bar, kb * BK, m_tile * 128);
                     // a half's 128 W rows come half from each CTA (its share of B)
-                    bi::tma_load_2d_pair(sa + kABytes, &tmap_w, bar, kb * BK, w_row);
-                    bi::tma_load_2d_pair(sa + kABytes + 64 * BK, &tmap_w, bar, kb * BK, w_row + 128);
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+                        bi::tma_load_2d_pair(sa + kABytes + h * 64 * BK, &tmap_w, bar, kb * BK,
+                                             w_row + 128 * h);
                     if (scales) {
-                        uint8_t* sf = smem_scales + stage * pair::kScaleBytes;
+                        uint8_t* sf = smem_scales + stage * S::kScaleBytes;
                         bi::tma_load_2d_pair(sf, &tmap_xs, bar, 0, m_tile * spans + (kb >> 2));
-                        bi::tma_load_2d_pair(sf + kTile, &tmap_ws, bar, 0,
-                                             2 * nb * spans + (kb >> 2));
-                        bi::tma_load_2d_pair(sf + 2 * kTile, &tmap_ws, bar, 0,
-                                             (2 * nb + 1) * spans + (kb >> 2));
+#pragma unroll
+                        for (int h = 0; h < H; ++h)
+                            bi::tma_load_2d_pair(sf + (1 + h) * kTile, &tmap_ws, bar, 0,
+                                                 (H * nb + h) * spans + (kb >> 2));
                     }
                 }
                 __syncwarp();
@@ -252,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             bool ok = true;
             for (int tile = pair_id; tile < num_tiles && ok; tile += npairs) {
                 uint32_t sfa = 0;
-                int d[2] = {0, 0};
+                int d[H] = {};
                 int left = 0;  // k-blocks of the part still to come
                 for (int kb = 0; kb < num_kb; ++kb) {
                     const bool first = left == 0;
@@ -269,21 +277,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                         // The place was last read by MMAs of 8 tiles of scales ago.
                         // They are done: this stage's load waited for the MMAs of
                         // kStages < 8 k-blocks ago, and tiles are a k-block apart at least.
-                        sfa = tmem + pair::kScaleCol + 16 * sf;
+                        sfa = tmem + S::kScaleCol + 16 * sf;
                         sf = (sf + 1) & 7;
                         const uint64_t s = scale_desc(ring + kStages * kStageBytes +
-                                                      stage * pair::kScaleBytes);
+                                                      stage * S::kScaleBytes);
                         if (bi::elect_one()) {
-                            bi::tc_cp_scales_pair(sfa, s);
-                            bi::tc_cp_scales_pair(sfa + 4, s + (kTile >> 4));
-                            bi::tc_cp_scales_pair(sfa + 8, s + (2 * kTile >> 4));
+#pragma unroll
+                            for (int i = 0; i < 1 + H; ++i)
+                                bi::tc_cp_scales_pair(sfa + 4 * i, s + (i * kTile >> 4));
                         }
                         __syncwarp();
                     }
-                    const uint32_t idesc = with_byte(pair::kIdesc, kb & 3);
+                    const uint32_t idesc = with_byte(S::kIdesc, kb & 3);
                     const uint64_t da = operand_desc(sa), db = operand_desc(sa + kABytes);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < H; ++h) {
                         if (first) {
                             if (!__all_sync(0xffffffffu, bi::mbar_wait(&tempty[acc], acc_phase ^ 1))) {
                                 ok = false;
@@ -304,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                                                      sfa + 4 + 4 * h, (!first || k != 0) ? 1u : 0u);
                             if (left == 0)  // the half's part is complete in both CTAs
                                 bi::tc_commit_pair_multicast(&tfull[d[h]], 0x3);
-                            if (h == 1)  // the stage is free in both CTAs
+                            if (h == H - 1)  // the stage is free in both CTAs
                                 bi::tc_commit_pair_multicast(&empty[stage], 0x3);
                         }
                         __syncwarp();
@@ -333,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         }
     }
     } else {
-        bi::more_registers<pair::kManyRegs>();
+        bi::more_registers<S::kManyRegs>();
         // epilogue warps 4..11: lane quarter warp % 4 of this CTA's 128 rows, and
         // 64 of either half's 128 columns
         const int quarter = warp & 3;
@@ -346,13 +354,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         const uint32_t taddr0 =
             tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 64 * c;
         for (int tile = pair_id; tile < num_tiles; tile += npairs, turn ^= 1) {
-            float sum[2][64];  // from -0 on: -0 + x is x, whatever its sign
+            float sum[H][64];  // from -0 on: -0 + x is x, whatever its sign
 #pragma unroll
-            for (int i = 0; i < 64; ++i) sum[0][i] = sum[1][i] = -0.f;
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int i = 0; i < 64; ++i) sum[h][i] = -0.f;
 #pragma unroll 1
             for (int p = 0; p < num_parts; ++p) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < H; ++h) {
                     if (ok) {
                         ok = __all_sync(0xffffffffu, bi::mbar_wait(&tfull[acc], acc_phase));
                         if (!ok && lane == 0) {
@@ -384,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             int mb, nb;  // not before the sums are there: every register counts in that loop
             tile_coords(tile, num_m, num_n, group_m, mb, nb);
             const int in_tile = quarter * 32 + lane;
-            const int row = mb * pair::BMP + static_cast<int>(rank) * 128 + in_tile;
+            const int row = mb * S::BMP + static_cast<int>(rank) * 128 + in_tile;
             if constexpr (!kSwiGLU) {
                 // 32 rows x 32 columns at a time through shared memory (64-byte rows,
                 // swizzled: no bank conflicts) and out by TMA, which clips them to y.  A
@@ -393,12 +403,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                 if (!ok) continue;
                 const int row0 = row - lane;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int col = nb * pair::BN + 128 * (q >> 1) + 64 * c + 32 * (q & 1);
+                for (int q = 0; q < 2 * H; ++q) {
+                    const int col = nb * S::BN + 128 * (q >> 1) + 64 * c + 32 * (q & 1);
                     if (row0 >= M || col >= N) continue;  // the whole warp
-                    uint8_t* buf = smem_out + ((warp - 4) * pair::kOutBufs + out_buf) * pair::kOutBytes;
-                    if (++out_buf == pair::kOutBufs) out_buf = 0;
-                    if (bi::elect_one()) bi::tma_store_wait_read<pair::kOutBufs - 1>();
+                    uint8_t* buf = smem_out + ((warp - 4) * S::kOutBufs + out_buf) * S::kOutBytes;
+                    if (++out_buf == S::kOutBufs) out_buf = 0;
+                    if (bi::elect_one()) bi::tma_store_wait_read<S::kOutBufs - 1>();
                     __syncwarp();
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
@@ -413,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                 // the tile's 256 columns are one block of 128 outputs of a row
                 uint32_t top = 0;  // outputs take the places of the sums they are made of
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < H; ++h)
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         // past F there are no W rows, and what stands for their scales may
@@ -437,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                 const float inv = bi_fp8::inverse_scale(byte);
                 uint8_t* hr = static_cast<uint8_t*>(out.y) + static_cast<int64_t>(row) * out.ld;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < H; ++h) {
                     const int col = nb * 128 + 64 * h + 32 * c;
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
@@ -471,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     bi::cluster_sync();  // both CTAs past their last TMEM access and remote arrive
     if (warp == 1) {
         bi::tc_fence_after();
-        bi::tmem_dealloc_pair(tmem_base, pair::kTmemCols);
+        bi::tmem_dealloc_pair(tmem_base, S::kTmemCols);
     }
 }
 
@@ -1118,28 +1128,27 @@ bool encode(const Call& c, uint32_t x_rows, uint32_t w_rows, CUtensorMap (&t)[4]
            bi::encode_scale_map(&t[3], c.Ws, (c.N + 127) / 128 * spans) == CUDA_SUCCESS;
 }
 
-template <bool kSwiGLU>
-bi_status launch_pair(const Call& c) {
+template <bool kSwiGLU, int H>
+bi_status launch_pair(const Call& c, int sms) {
+    using S = PairShape<H>;
     static std::atomic<bool> set[64] = {};
-    if (!bi::allow_smem(gemm_fp8_pair_kernel<kSwiGLU>, pair::kSmemBytes, set)) return BI_ERR_CUDA;
-    const int sms = bi::sm_count();
-    if (sms < 2) return BI_ERR_CUDA;
+    if (!bi::allow_smem(gemm_fp8_pair_kernel<kSwiGLU, H>, S::kSmemBytes, set)) return BI_ERR_CUDA;
     CUtensorMap t[4];
     if (!encode(c, 128, 64, t)) return BI_ERR_CUDA;
     CUtensorMap ty = t[0];  // not read where the output is 8 bits
     if (!kSwiGLU && bi::encode_out_map(&ty, c.out.y, c.N, c.M, c.out.ld * 2) != CUDA_SUCCESS)
         return BI_ERR_CUDA;
-    const int num_m = (c.M + pair::BMP - 1) / pair::BMP;
-    const int64_t tiles = static_cast<int64_t>(num_m) * ((c.N + pair::BN - 1) / pair::BN);
+    const int num_m = (c.M + S::BMP - 1) / S::BMP;
+    const int64_t tiles = static_cast<int64_t>(num_m) * ((c.N + S::BN - 1) / S::BN);
     if (tiles > 0x7fffffffLL) return BI_ERR_UNSUPPORTED_SHAPE;
     const int pairs = static_cast<int>(std::min<int64_t>(tiles, sms / 2));
     // at most about 48 MB of x per group of M-tiles, as bi_gemm
-    const int64_t slab = static_cast<int64_t>(pair::BMP) * c.K;
+    const int64_t slab = static_cast<int64_t>(S::BMP) * c.K;
     const int64_t budget = int64_t{48} << 20;
     int group_m = num_m;
     if (slab * num_m > budget) group_m = static_cast<int>(std::max<int64_t>(1, budget / slab));
-    return bi::launch_pdl(gemm_fp8_pair_kernel<kSwiGLU>, dim3(2 * pairs), dim3(pair::kThreads),
-                          pair::kSmemBytes, c.stream, t[0], t[1], t[2], t[3], ty, c.out, c.M, c.N, c.K,
+    return bi::launch_pdl(gemm_fp8_pair_kernel<kSwiGLU, H>, dim3(2 * pairs), dim3(S::kThreads),
+                          S::kSmemBytes, c.stream, t[0], t[1], t[2], t[3], ty, c.out, c.M, c.N, c.K,
                           parts_of(c.K).blocks, group_m, bi::device_error_word()) == cudaSuccess
                ? BI_OK
                : BI_ERR_CUDA;
@@ -1205,19 +1214,26 @@ bi_status launch_whole(const Call& c) {
 }
 
 // Which kernel: a schedule choice, the bits are the same.  Measured, us, K = 4096 unless
-// said otherwise, as parts / whole / pair:
-//   up to 32 rows: the parts kernel (N = 4096, 24 rows 6.2 / 14.6 / 15.0; N = 12288 11.6 / 15.2
-//   / 19.8), but the whole kernel where the SMs do not hold the parts' CTAs at once, three
-//   each (N = 24576, one row 19.8 / 19.0 / 34.7, 24 rows 22.1 / 19.7 / 29.4), and for SwiGLU of
-//   more than 16 rows (F = 8192, 24 rows 19.2 / 16.1 / 20.3);
-//   up to 128 rows, where the pair kernel has more than a wave of tiles: the whole kernel
-//   (N = 24576, 64 rows 29.2 / 21.2 / 28.8, 128 rows 35.1 / 24.8 / 29.9; one wave, N = 12288,
-//   128 rows 22.2 / 20.5 / 17.1);
-//   else the parts kernel as long as its 128 x 128 tiles are no more than the pairs of a wave
-//   each (N = 4096, 128 rows 8.8 / 19.7 / 15.6, 256 rows, 64 tiles, 11.6 / 19.3 / 15.7, 384 rows, 96
-//   tiles, 20.3 / 19.2 / 15.8; K = 12288, 256 rows 27.3 / 44.4 / 34.2), for SwiGLU its CTAs no more than
-//   the SMs (F = 4096, 128 rows 14.9 / 21.6 / 16.2; K = 12288 46.6 / 46.4 / 35.6);
-//   else the pair kernel.
+// said otherwise, as parts / whole / pair with tiles of 128 columns / of 256:
+//   up to 32 rows: the parts kernel (N = 4096, 24 rows 6.2 / 14.6 / 11.0 / 15.0; N = 12288 11.6 /
+//   15.2 / 21.9 / 19.8), but the whole kernel where the SMs do not hold the parts' CTAs at
+//   once, three each (N = 24576, one row 19.8 / 19.0 / - / 34.7, 24 rows 22.1 / 19.7 / - / 29.4), and
+//   for SwiGLU of more than 16 rows (F = 8192, 24 rows 19.2 / 16.1 / - / 20.3);
+//   up to 128 rows, where tiles of 256 columns are more than a wave of the pairs: the whole
+//   kernel (N = 24576, 64 rows 29.2 / 21.2 / - / 28.8, 128 rows 35.1 / 24.8 / - / 29.9; but N = 12288,
+//   128 rows 22.2 / 20.5 / 18.1 / 17.1);
+//   else the parts kernel while its tiles, 64 rows x 256 W rows a piece, keep it below half
+//   the pairs (N = 4096, 128 rows, 32 tiles, 8.8 / 19.7 / 10.6 / 15.6, 256 rows, 64, 11.6 / 19.3 / 10.6 /
+//   15.7; N = 8192, 48 rows, 32, 9.1 / 16.0 / 11.3 / 15.7, 128 rows, 64, 12.3 / 20.1 / 11.7 / 16.1;
+//   K = 12288, N = 4096, 128 rows 15.8 / 44.3 / 22.4 / 34.3) and K has parts to spread (K = 1024, one
+//   part, 48 rows 6.4 / 6.8 / 5.9 / 7.6; K = 2048, two, 48 rows 6.1 / - / 7.5 / -, 96 rows 8.0 / - / 7.5 / -);
+//   for SwiGLU, which has no tiles of 128 columns, while its 128 x 128 tiles are no more than
+//   the pairs of a wave each and its CTAs no more than the SMs (F = 4096, 128 rows 14.9 / 21.6 / -
+//   / 16.2; K = 12288 46.6 / 46.4 / - / 35.6);
+//   else the pair kernel, with tiles of 128 columns where a wave of them, 0.6 of the other's
+//   time, makes up for their number (N = 4096, 400 rows - / - / 11.0 / 15.8, one wave of either; 768
+//   rows 16.9 / 16.4, two and one; N = 6144, 1024 rows 23.6 / 26.7, three and two; N = 8192 29.6 /
+//   27.4, four and two).
 template <bool kSwiGLU>
 bi_status launch_gemm(const Call& c) {
     const int sms = bi::sm_count();
@@ -1226,7 +1242,9 @@ bi_status launch_gemm(const Call& c) {
     const int64_t small_m = (c.M + 127) / 128, small_n = (c.N + 127) / 128;
     const int64_t large_m = (c.M + 255) / 256, large_n = (c.N + 255) / 256;
     const int64_t waves = (large_m * large_n + pairs - 1) / pairs;
-    const int64_t ctas = parts_of(c.K).count * small_m * (kSwiGLU ? large_n : small_n);
+    const int64_t half_waves = (large_m * small_n + pairs - 1) / pairs;
+    const int parts = parts_of(c.K).count;
+    const int64_t ctas = parts * small_m * (kSwiGLU ? large_n : small_n);
     constexpr bool g = kSwiGLU;
     if (c.M <= 128 && large_n * 4 > sms && large_n <= sms &&
         (c.M > 32 ? large_n > pairs : ctas > 3 * sms || (g && c.M > 16))) {
@@ -1236,20 +1254,23 @@ bi_status launch_gemm(const Call& c) {
         return launch_whole<128, g>(c);
     }
     if (small_m <= 65535 && small_n <= 65535 &&
-        (c.M <= 32 || (small_m * small_n <= waves * pairs &&
-                       (!g || (ctas <= sms && parts_of(c.K).count >= 4))))) {
+        (c.M <= 32 || (parts >= (c.M <= 64 ? 2 : 4) &&
+                       (g ? small_m * small_n <= waves * pairs && ctas <= sms
+                          : static_cast<int64_t>((c.M + 63) / 64) * small_n <= pairs)))) {
         if (c.M <= 16) return g ? launch_parts<16, g, 5, 3, 2>(c, sms) : launch_parts<16, g, 8, 4, 3>(c, sms);
         if (c.M <= 32) return g ? launch_parts<32, g, 4, 2, 2>(c, sms) : launch_parts<32, g, 8, 4, 3>(c, sms);
         if (c.M <= 64) return g ? launch_parts<64, g, 4, 2, 2>(c, sms) : launch_parts<64, g, 6, 3, 3>(c, sms);
         return g ? launch_parts<128, g, 4, 4, 4>(c, sms) : launch_parts<128, g, 6, 3, 3>(c, sms);
     }
-    return launch_pair<kSwiGLU>(c);
+    if constexpr (!kSwiGLU)
+        if (5 * half_waves < 8 * waves) return launch_pair<false, 1>(c, sms);
+    return launch_pair<kSwiGLU, 2>(c, sms);
 }
 
 bi_status check(const Call& c, int n_step) {
     if (c.M < 0) return BI_ERR_INVALID_ARG;
     if (c.N < n_step || c.N % n_step || c.K < 16 || (c.K & 15)) return BI_ERR_UNSUPPORTED_SHAPE;
-    if (c.M > 0x7fffffff - pair::BMP || c.N > 0x7fffffff - pair::BN || c.K > 0x7fffffff - 512)
+    if (c.M > 0x7fffffff - 256 || c.N > 0x7fffffff - 256 || c.K > 0x7fffffff - 512)
         return BI_ERR_UNSUPPORTED_SHAPE;  // row, column and byte indices stay in int
     const int64_t spans = bi_fp8::spans_of(c.K);
     if ((c.M + 255) / 128 * spans > 0x7fffffffLL || (c.N + 255) / 128 * spans > 0x7fffffffLL)
