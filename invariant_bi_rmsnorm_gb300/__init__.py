@@ -674,8 +674,13 @@ def logprobs_top(logits: torch.Tensor, targets: torch.Tensor | None, k: int, str
 
 # ------------------------------------------------------ 8-bit linear path ----
 # An 8-bit matrix is a pair: codes [rows, K] float8_e4m3fn (rows may lie apart by a
-# multiple of 16), and scales, uint8 of fp8_scales_shape(rows, K), contiguous.
+# multiple of 16), and scales, uint8 of fp8_scales_shape(rows, K), contiguous.  As with the
+# 4-bit cache each call tests all it has to in one condition, and sorts out what was wrong
+# only when something was.
 _F8 = torch.float8_e4m3fn
+# The current device for a tensor that is on one (CUDA is up then): what
+# torch.cuda.current_device() asks behind its own checks.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def fp8_scales_shape(rows: int, K: int) -> tuple[int, int, int]:
@@ -684,34 +689,22 @@ def fp8_scales_shape(rows: int, K: int) -> tuple[int, int, int]:
     return (rows + 127) // 128, (K + 511) // 512, FP8_TILE_BYTES
 
 
-def _refuse_rows(where: str, name: str, t: torch.Tensor, dtype, shape=None):
-    """Raise if t is not a 2-D CUDA tensor of that type, and shape, whose rows
-    are each in one run."""
-    if not t.is_cuda:
-        raise ValueError(f"{where}: {name} must be a CUDA tensor (no CPU path exists)")
-    if t.dtype != dtype:
-        raise ValueError(f"{where}: {name} must be {str(dtype).split('.')[-1]}, got {t.dtype}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{where}: {name} must have shape {shape or '[rows, columns]'}, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{where}: {name} must have unit stride along its last dimension")
-    if t.get_device() != _current_device():
-        raise ValueError(f"{where}: {name} must be on the current CUDA device ({_current_device()})")
-
-
-def _rows_of(where: str, name: str, t: torch.Tensor, dtype, rows: int, columns: int, dev: int) -> int:
-    """The leading dimension of t, which has to be rows x columns of dtype on dev."""
-    if not (t.dtype is dtype and t.shape == (rows, columns) and t.get_device() == dev
-            and (t.stride(1) == 1 or columns == 1)):
-        _refuse_rows(where, name, t, dtype, (rows, columns))
-    return t.stride(0) if rows > 1 else -(-columns // 16) * 16
-
-
-def _scales_of(where: str, name: str, t: torch.Tensor, rows: int, K: int, dev: int) -> int:
-    if not (t.dtype is _U8 and t.shape == ((rows + 127) // 128, (K + 511) // 512, FP8_TILE_BYTES)
-            and t.get_device() == dev and t.is_contiguous()):
-        _refuse(where, (t, name, _U8, fp8_scales_shape(rows, K)))
-    return t.data_ptr()
+def _refuse_rows(where: str, *wanted):
+    """Raise for the first of (tensor, name, dtype, shape) that is not a 2-D tensor of
+    that type and shape (None: any) on the current CUDA device, each row in one run."""
+    for t, name, dtype, shape in wanted:
+        if t.dim() != 2:
+            raise ValueError(f"{where}: {name} must be 2-D, got {tuple(t.shape)}")
+        if not t.is_cuda:
+            raise ValueError(f"{where}: {name} must be a CUDA tensor (no CPU path exists)")
+        if t.dtype != dtype:
+            raise ValueError(f"{where}: {name} must be {str(dtype).split('.')[-1]}, got {t.dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.stride(1) != 1:
+            raise ValueError(f"{where}: {name} must have unit stride along its last dimension")
+        if t.get_device() != _current_device():
+            raise ValueError(f"{where}: {name} must be on the current CUDA device ({_current_device()})")
 
 
 def _new_fp8(stream, out, scales, rows: int, K: int, device):
@@ -722,24 +715,26 @@ def _new_fp8(stream, out, scales, rows: int, K: int, device):
     return out, scales
 
 
-def _shape_2d(where: str, name: str, t: torch.Tensor):
-    if t.dim() != 2:
-        raise ValueError(f"{where}: {name} must be 2-D, got {tuple(t.shape)}")
-    return t.shape
-
-
 def quantize_fp8(x: torch.Tensor, out: torch.Tensor | None = None,
                  scales: torch.Tensor | None = None, stream=None):
     """bf16 x [rows, K] as an 8-bit matrix (codes, scales): e4m3 and one power of
     two for each 128 values of a row.  K must be a multiple of 16."""
-    where = "quantize_fp8"
-    dev = _current_device()
-    rows, K = _shape_2d(where, "x", x)
-    ld_x = _rows_of(where, "x", x, _BF16, rows, K, dev)
-    out, scales = _new_fp8(stream, out, scales, rows, K, x.device)
+    dev, shape = x.get_device(), x.shape
+    if dev < 0 or len(shape) != 2:
+        _refuse_rows("quantize_fp8", (x, "x", _BF16, None))
+    rows, K = shape
+    if out is None or scales is None:
+        out, scales = _new_fp8(stream, out, scales, rows, K, x.device)
+    xs, qs = x.stride(), out.stride()
+    if not (x.dtype is _BF16 and xs[1] == 1 and out.dtype is _F8 and out.shape == shape and qs[1] == 1
+            and scales.dtype is _U8 and scales.shape == ((rows + 127) // 128, (K + 511) // 512, FP8_TILE_BYTES)
+            and scales.is_contiguous() and dev == out.get_device() == scales.get_device() == _device()):
+        where = "quantize_fp8"
+        _refuse_rows(where, (x, "x", _BF16, None), (out, "out", _F8, shape))
+        _refuse(where, (scales, "scales", _U8, fp8_scales_shape(rows, K)))
     _check(_lib.load().bi_quantize_fp8(
-        x.data_ptr(), ld_x, rows, K, out.data_ptr(), _rows_of(where, "out", out, _F8, rows, K, dev),
-        _scales_of(where, "scales", scales, rows, K, dev),
+        x.data_ptr(), xs[0] if rows > 1 else -(-K // 8) * 8, rows, K, out.data_ptr(),
+        qs[0] if rows > 1 else -(-K // 16) * 16, scales.data_ptr(),
         _raw_stream(dev) if stream is None else _stream(stream)), "bi_quantize_fp8")
     return out, scales
 
@@ -747,32 +742,46 @@ def quantize_fp8(x: torch.Tensor, out: torch.Tensor | None = None,
 def fp8_read(q: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None,
              stream=None) -> torch.Tensor:
     """What an 8-bit matrix stands for, in bf16 (nothing is rounded)."""
-    where = "fp8_read"
-    dev = _current_device()
-    rows, K = _shape_2d(where, "q", q)
-    ld_q = _rows_of(where, "q", q, _F8, rows, K, dev)
+    dev, shape = q.get_device(), q.shape
+    if dev < 0 or len(shape) != 2:
+        _refuse_rows("fp8_read", (q, "q", _F8, None))
+    rows, K = shape
     if out is None:
         out = _made(stream, torch.empty, (rows, K), dtype=_BF16, device=q.device)
+    qs, ys = q.stride(), out.stride()
+    if not (q.dtype is _F8 and qs[1] == 1 and out.dtype is _BF16 and out.shape == shape and ys[1] == 1
+            and scales.dtype is _U8 and scales.shape == ((rows + 127) // 128, (K + 511) // 512, FP8_TILE_BYTES)
+            and scales.is_contiguous() and dev == out.get_device() == scales.get_device() == _device()):
+        where = "fp8_read"
+        _refuse_rows(where, (q, "q", _F8, None), (out, "out", _BF16, shape))
+        _refuse(where, (scales, "scales", _U8, fp8_scales_shape(rows, K)))
     _check(_lib.load().bi_fp8_read(
-        q.data_ptr(), ld_q, _scales_of(where, "scales", scales, rows, K, dev), rows, K, out.data_ptr(),
-        _rows_of(where, "out", out, _BF16, rows, K, dev),
-        _raw_stream(dev) if stream is None else _stream(stream)), "bi_fp8_read")
+        q.data_ptr(), qs[0] if rows > 1 else -(-K // 16) * 16, scales.data_ptr(), rows, K, out.data_ptr(),
+        ys[0] if rows > 1 else -(-K // 8) * 8, _raw_stream(dev) if stream is None else _stream(stream)),
+        "bi_fp8_read")
     return out
 
 
 def rmsnorm_fp8(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6,
                 out: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
     """rmsnorm(x, w, eps) as an 8-bit matrix (codes, scales), rounded once."""
-    where = "rmsnorm_fp8"
-    dev = _current_device()
-    rows, hidden = _shape_2d(where, "x", x)
-    ld_x = _rows_of(where, "x", x, _BF16, rows, hidden, dev)
-    if not (w.dtype is _BF16 and w.shape == (hidden,) and w.is_contiguous() and w.get_device() == dev):
-        _refuse(where, (w, "w", _BF16, (hidden,)))
-    out, scales = _new_fp8(stream, out, scales, rows, hidden, x.device)
+    dev, shape = x.get_device(), x.shape
+    if dev < 0 or len(shape) != 2:
+        _refuse_rows("rmsnorm_fp8", (x, "x", _BF16, None))
+    rows, hidden = shape
+    if out is None or scales is None:
+        out, scales = _new_fp8(stream, out, scales, rows, hidden, x.device)
+    xs, qs = x.stride(), out.stride()
+    if not (x.dtype is w.dtype is _BF16 and xs[1] == 1 and w.shape == (hidden,) and w.is_contiguous()
+            and out.dtype is _F8 and out.shape == shape and qs[1] == 1 and scales.dtype is _U8
+            and scales.shape == ((rows + 127) // 128, (hidden + 511) // 512, FP8_TILE_BYTES) and scales.is_contiguous()
+            and dev == w.get_device() == out.get_device() == scales.get_device() == _device()):
+        where = "rmsnorm_fp8"
+        _refuse_rows(where, (x, "x", _BF16, None), (out, "out", _F8, shape))
+        _refuse(where, (w, "w", _BF16, (hidden,)), (scales, "scales", _U8, fp8_scales_shape(rows, hidden)))
     _check(_lib.load().bi_rmsnorm_fp8(
-        x.data_ptr(), w.data_ptr(), out.data_ptr(), _scales_of(where, "scales", scales, rows, hidden, dev),
-        rows, hidden, ld_x, _rows_of(where, "out", out, _F8, rows, hidden, dev), eps,
+        x.data_ptr(), w.data_ptr(), out.data_ptr(), scales.data_ptr(), rows, hidden,
+        xs[0] if rows > 1 else -(-hidden // 8) * 8, qs[0] if rows > 1 else -(-hidden // 16) * 16, eps,
         _raw_stream(dev) if stream is None else _stream(stream)), "bi_rmsnorm_fp8")
     return out, scales
 
@@ -782,23 +791,31 @@ def add_rmsnorm_fp8(x: torch.Tensor, residual: torch.Tensor, w: torch.Tensor, ep
                     scales: torch.Tensor | None = None, stream=None):
     """residual_out = residual + x (bf16; in place of residual by default), and
     rmsnorm(residual_out, w, eps) as an 8-bit matrix (codes, scales)."""
-    where = "add_rmsnorm_fp8"
-    dev = _current_device()
-    rows, hidden = _shape_2d(where, "x", x)
-    ld_x = _rows_of(where, "x", x, _BF16, rows, hidden, dev)
-    ld_res = _rows_of(where, "residual", residual, _BF16, rows, hidden, dev)
-    if not (w.dtype is _BF16 and w.shape == (hidden,) and w.is_contiguous() and w.get_device() == dev):
-        _refuse(where, (w, "w", _BF16, (hidden,)))
+    dev, shape = x.get_device(), x.shape
+    if dev < 0 or len(shape) != 2:
+        _refuse_rows("add_rmsnorm_fp8", (x, "x", _BF16, None))
+    rows, hidden = shape
     if residual_out is None:
-        residual_out, ld_sum = residual, ld_res
-    else:
-        ld_sum = _rows_of(where, "residual_out", residual_out, _BF16, rows, hidden, dev)
-    out, scales = _new_fp8(stream, out, scales, rows, hidden, x.device)
+        residual_out = residual
+    if out is None or scales is None:
+        out, scales = _new_fp8(stream, out, scales, rows, hidden, x.device)
+    xs, qs, rs, ss = x.stride(), out.stride(), residual.stride(), residual_out.stride()
+    if not (x.dtype is residual.dtype is residual_out.dtype is w.dtype is _BF16 and xs[1] == 1
+            and residual.shape == shape == residual_out.shape and rs[1] == 1 == ss[1] and w.shape == (hidden,)
+            and w.is_contiguous() and out.dtype is _F8 and out.shape == shape and qs[1] == 1 and scales.dtype is _U8
+            and scales.shape == ((rows + 127) // 128, (hidden + 511) // 512, FP8_TILE_BYTES) and scales.is_contiguous()
+            and dev == residual.get_device() == residual_out.get_device() == w.get_device() == out.get_device()
+            == scales.get_device() == _device()):
+        where = "add_rmsnorm_fp8"
+        _refuse_rows(where, (x, "x", _BF16, None), (residual, "residual", _BF16, shape),
+                     (residual_out, "residual_out", _BF16, shape), (out, "out", _F8, shape))
+        _refuse(where, (w, "w", _BF16, (hidden,)), (scales, "scales", _U8, fp8_scales_shape(rows, hidden)))
+    one = -(-hidden // 8) * 8
     _check(_lib.load().bi_add_rmsnorm_fp8(
-        x.data_ptr(), residual.data_ptr(), residual_out.data_ptr(), w.data_ptr(), out.data_ptr(),
-        _scales_of(where, "scales", scales, rows, hidden, dev), rows, hidden, ld_x, ld_res, ld_sum,
-        _rows_of(where, "out", out, _F8, rows, hidden, dev), eps,
-        _raw_stream(dev) if stream is None else _stream(stream)), "bi_add_rmsnorm_fp8")
+        x.data_ptr(), residual.data_ptr(), residual_out.data_ptr(), w.data_ptr(), out.data_ptr(), scales.data_ptr(),
+        rows, hidden, xs[0] if rows > 1 else one, rs[0] if rows > 1 else one, ss[0] if rows > 1 else one,
+        qs[0] if rows > 1 else -(-hidden // 16) * 16, eps, _raw_stream(dev) if stream is None else _stream(stream)),
+        "bi_add_rmsnorm_fp8")
     return out, scales
 
 
@@ -806,18 +823,28 @@ def gemm_fp8(x: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor, W_scales:
              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y = x @ W.T in bf16, of 8-bit matrices x [M, K] and W [N, K] (nn.Linear
     layout), batch-invariant per row.  K must be a multiple of 16, N of 8."""
-    where = "gemm_fp8"
-    dev = _current_device()
-    M, K = _shape_2d(where, "x", x)
-    N = _shape_2d(where, "W", W)[0]
-    ld_x = _rows_of(where, "x", x, _F8, M, K, dev)
-    ld_w = _rows_of(where, "W", W, _F8, N, K, dev)
+    dev, shape, wshape = x.get_device(), x.shape, W.shape
+    if dev < 0 or len(shape) != 2 or len(wshape) != 2:
+        _refuse_rows("gemm_fp8", (x, "x", _F8, None), (W, "W", _F8, None))
+    M, K = shape
+    N = wshape[0]
     if out is None:
         out = _made(stream, torch.empty, (M, N), dtype=_BF16, device=x.device)
+    xs, ws, ys = x.stride(), W.stride(), out.stride()
+    spans = (K + 511) // 512
+    if not (x.dtype is W.dtype is _F8 and wshape[1] == K and xs[1] == 1 == ws[1] and out.dtype is _BF16
+            and out.shape == (M, N) and (ys[1] == 1 or N == 1) and x_scales.dtype is W_scales.dtype is _U8
+            and x_scales.shape == ((M + 127) // 128, spans, FP8_TILE_BYTES)
+            and W_scales.shape == ((N + 127) // 128, spans, FP8_TILE_BYTES) and x_scales.is_contiguous()
+            and W_scales.is_contiguous() and dev == W.get_device() == out.get_device() == x_scales.get_device()
+            == W_scales.get_device() == _device()):
+        where = "gemm_fp8"
+        _refuse_rows(where, (x, "x", _F8, None), (W, "W", _F8, (N, K)), (out, "out", _BF16, (M, N)))
+        _refuse(where, (x_scales, "x_scales", _U8, fp8_scales_shape(M, K)), (W_scales, "W_scales", _U8, fp8_scales_shape(N, K)))
+    one = -(-K // 16) * 16
     _check(_lib.load().bi_gemm_fp8(
-        x.data_ptr(), _scales_of(where, "x_scales", x_scales, M, K, dev), W.data_ptr(),
-        _scales_of(where, "W_scales", W_scales, N, K, dev), out.data_ptr(), M, N, K, ld_x, ld_w,
-        _rows_of(where, "out", out, _BF16, M, N, dev),
+        x.data_ptr(), x_scales.data_ptr(), W.data_ptr(), W_scales.data_ptr(), out.data_ptr(), M, N, K,
+        xs[0] if M > 1 else one, ws[0] if N > 1 else one, ys[0] if M > 1 else -(-N // 8) * 8,
         _raw_stream(dev) if stream is None else _stream(stream)), "bi_gemm_fp8")
     return out
 
@@ -829,20 +856,33 @@ def gemm_fp8_swiglu(x: torch.Tensor, x_scales: torch.Tensor, W_gu: torch.Tensor,
     scales), from 8-bit x [M, K] and W_gu [2F, K], the gate and up rows interleaved
     as interleave_gate_up does (quantise the interleaved weight).  F and K must be
     multiples of 16."""
-    where = "gemm_fp8_swiglu"
-    dev = _current_device()
-    M, K = _shape_2d(where, "x", x)
-    F2 = _shape_2d(where, "W_gu", W_gu)[0]
-    if F2 % 32:
-        raise ValueError(f"{where}: W_gu must have 2F rows, F a multiple of 16")
+    dev, shape, wshape = x.get_device(), x.shape, W_gu.shape
+    if len(wshape) == 2 and wshape[0] % 32:
+        raise ValueError("gemm_fp8_swiglu: W_gu must have 2F rows, F a multiple of 16")
+    if dev < 0 or len(shape) != 2 or len(wshape) != 2:
+        _refuse_rows("gemm_fp8_swiglu", (x, "x", _F8, None), (W_gu, "W_gu", _F8, None))
+    M, K = shape
+    F2 = wshape[0]
     F = F2 // 2
-    ld_x = _rows_of(where, "x", x, _F8, M, K, dev)
-    ld_w = _rows_of(where, "W_gu", W_gu, _F8, F2, K, dev)
-    out, scales = _new_fp8(stream, out, scales, M, F, x.device)
+    if out is None or scales is None:
+        out, scales = _new_fp8(stream, out, scales, M, F, x.device)
+    xs, ws, hs = x.stride(), W_gu.stride(), out.stride()
+    spans = (K + 511) // 512
+    if not (x.dtype is W_gu.dtype is out.dtype is _F8 and wshape[1] == K and xs[1] == 1 == ws[1]
+            and out.shape == (M, F) and (hs[1] == 1 or F == 1)
+            and x_scales.dtype is W_gu_scales.dtype is scales.dtype is _U8
+            and x_scales.shape == ((M + 127) // 128, spans, FP8_TILE_BYTES)
+            and W_gu_scales.shape == ((F2 + 127) // 128, spans, FP8_TILE_BYTES)
+            and scales.shape == ((M + 127) // 128, (F + 511) // 512, FP8_TILE_BYTES) and x_scales.is_contiguous()
+            and W_gu_scales.is_contiguous() and scales.is_contiguous() and dev == W_gu.get_device() == out.get_device()
+            == x_scales.get_device() == W_gu_scales.get_device() == scales.get_device() == _device()):
+        where = "gemm_fp8_swiglu"
+        _refuse_rows(where, (x, "x", _F8, None), (W_gu, "W_gu", _F8, (F2, K)), (out, "out", _F8, (M, F)))
+        _refuse(where, (x_scales, "x_scales", _U8, fp8_scales_shape(M, K)),
+                (W_gu_scales, "W_gu_scales", _U8, fp8_scales_shape(F2, K)), (scales, "scales", _U8, fp8_scales_shape(M, F)))
+    one = -(-K // 16) * 16
     _check(_lib.load().bi_gemm_fp8_swiglu(
-        x.data_ptr(), _scales_of(where, "x_scales", x_scales, M, K, dev), W_gu.data_ptr(),
-        _scales_of(where, "W_gu_scales", W_gu_scales, F2, K, dev), out.data_ptr(),
-        _scales_of(where, "scales", scales, M, F, dev), M, F, K, ld_x, ld_w,
-        _rows_of(where, "out", out, _F8, M, F, dev),
+        x.data_ptr(), x_scales.data_ptr(), W_gu.data_ptr(), W_gu_scales.data_ptr(), out.data_ptr(), scales.data_ptr(),
+        M, F, K, xs[0] if M > 1 else one, ws[0] if F2 > 1 else one, hs[0] if M > 1 else -(-F // 16) * 16,
         _raw_stream(dev) if stream is None else _stream(stream)), "bi_gemm_fp8_swiglu")
     return out, scales

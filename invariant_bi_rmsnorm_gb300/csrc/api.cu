@@ -1,5 +1,6 @@
 // Library-wide pieces of the C ABI: status strings, the device error word and
 // the TMA descriptor encoder shared by the kernels.
+#include <atomic>
 #include <mutex>
 
 #include "bi_internal.h"
@@ -71,11 +72,25 @@ int sm_count() {
     return g_sm_count[dev];
 }
 
+Device current_device_state() {
+    static std::atomic<bool> known[kMaxDevices] = {};
+    const int dev = current_device();
+    if (dev < 0) return {-1, 0, nullptr};
+    if (!known[dev].load(std::memory_order_acquire)) {
+        if (!device_error_word() || sm_count() < 2) return {-1, 0, nullptr};
+        known[dev].store(true, std::memory_order_release);
+    }
+    return {dev, g_sm_count[dev], g_err_ptr[dev]};  // written once, before `known`
+}
+
 namespace {
 
 // cuTensorMapEncodeTiled, looked up at first use.
 bool resolve_encode() {
+    static std::atomic<bool> known{false};
+    if (known.load(std::memory_order_acquire)) return true;
     std::lock_guard<std::mutex> lk(g_mu);
+    known.store(g_encode != nullptr, std::memory_order_release);
     if (g_encode) return true;
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q{};

@@ -43,6 +43,14 @@ uint32_t* device_error_word();
 // Multiprocessor count of the current device (cached per device).
 int sm_count();
 
+// The current device: its index (-1 on failure), multiprocessors and error word, for
+// calls that need all three (one runtime call instead of one each).
+struct Device {
+    int index, sms;
+    uint32_t* err;
+};
+Device current_device_state();
+
 // cuTensorMapEncodeTiled, resolved through the runtime's driver entry point
 // so the library does not link libcuda.  Returns CUDA_SUCCESS or an error.
 CUresult encode_tensor_map_2d(CUtensorMap* map, const void* base, uint64_t inner_elems,
@@ -76,14 +84,11 @@ CUresult encode_scale_map(CUtensorMap* map, const void* base, uint64_t tiles);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Set a kernel's dynamic shared memory limit on the current device once; `set`
-// is one flag per device (any thread may race to set it, the attribute is
-// idempotent).
+// Set a kernel's dynamic shared memory limit on the current device, `dev`, once; `set`
+// is one flag per device (any thread may race to set it, the attribute is idempotent).
 template <typename Kernel>
-bool allow_smem(Kernel kernel, int bytes, std::atomic<bool> (&set)[64]) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-    if (set[dev]) return true;
+bool allow_smem(Kernel kernel, int bytes, std::atomic<bool> (&set)[64], int dev) {
+    if (set[dev].load(std::memory_order_relaxed)) return true;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return false;
     set[dev] = true;

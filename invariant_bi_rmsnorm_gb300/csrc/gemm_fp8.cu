@@ -486,6 +486,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<H>::kThrea
 }
 
 // ----------------------------------------------------------- few rows ----
+// The scales of k-blocks kb .. kb + 3 of 128 rows.  Past the last of a matrix' tiles
+// (where it has no rows, and its codes are zeros) the last one's.
+__device__ __forceinline__ void load_scales(uint8_t* dst, const uint8_t* scales, int tile, int rows,
+                                            int kb, int spans, uint64_t* bar) {
+    tile = min(tile, (rows - 1) >> 7);
+    bi::bulk_load(dst, scales + (static_cast<int64_t>(tile) * spans + (kb >> 2)) * kTile, kTile, bar);
+}
+
 // NT: rows of x per CTA (the MMA's N); WT: tiles of 128 W rows per CTA (the MMA's
 // M): one, or two where a block of 128 SwiGLU outputs needs 256 W rows; STAGES: k-blocks
 // in flight per CTA.
@@ -583,8 +591,8 @@ template <int NT, bool kSwiGLU, int STAGES>
 __global__ void __launch_bounds__(192)
     gemm_fp8_parts_kernel(const __grid_constant__ CUtensorMap tmap_x,
                           const __grid_constant__ CUtensorMap tmap_w,
-                          const __grid_constant__ CUtensorMap tmap_xs,
-                          const __grid_constant__ CUtensorMap tmap_ws, Out out, int M, int N, int K,
+                          const uint8_t* __restrict__ x_scales,
+                          const uint8_t* __restrict__ w_scales, Out out, int M, int N, int K,
                           int part_blocks, bool prefetch, uint32_t* err) {
     constexpr int WT = kSwiGLU ? 2 : 1;
     using S = PartsShape<NT, WT, STAGES>;
@@ -632,8 +640,6 @@ __global__ void __launch_bounds__(192)
         s_consumed = 0;
         bi::tma_prefetch_desc(&tmap_x);
         bi::tma_prefetch_desc(&tmap_w);
-        bi::tma_prefetch_desc(&tmap_xs);
-        bi::tma_prefetch_desc(&tmap_ws);
     }
     if (warp == 1) {
         bi::tmem_alloc(tmem_slot, S::kTmemCols);
@@ -680,12 +686,10 @@ __global__ void __launch_bounds__(192)
                     uint8_t* sf = smem_scales + (issued >> 2) % S::kSlots * S::kScaleBytes;
 #pragma unroll
                     for (int t = 0; t < WT; ++t)
-                        bi::tma_load_2d(sf + t * kTile, &tmap_ws, &full[stage], 0,
-                                        (n0 / 128 + t) * spans + (kb >> 2));
+                        load_scales(sf + t * kTile, w_scales, n0 / 128 + t, N, kb, spans, &full[stage]);
                     // NT < 128 only where one tile holds all rows, so a tile's rows start
                     // where its scales do
-                    bi::tma_load_2d(sf + WT * kTile, &tmap_xs, &full[stage], 0,
-                                    (m0 / 128) * spans + (kb >> 2));
+                    load_scales(sf + WT * kTile, x_scales, m0 / 128, M, kb, spans, &full[stage]);
                 }
             }
             __syncwarp();
@@ -876,8 +880,8 @@ template <int NT, bool kSwiGLU>
 __global__ void __launch_bounds__(WholeShape<NT>::kThreads, 1)
     gemm_fp8_whole_kernel(const __grid_constant__ CUtensorMap tmap_x,
                           const __grid_constant__ CUtensorMap tmap_w,
-                          const __grid_constant__ CUtensorMap tmap_xs,
-                          const __grid_constant__ CUtensorMap tmap_ws, Out out, int M, int N, int K,
+                          const uint8_t* __restrict__ x_scales,
+                          const uint8_t* __restrict__ w_scales, Out out, int M, int N, int K,
                           int part_blocks, uint32_t* err) {
     using S = WholeShape<NT>;
     constexpr int kStages = S::kStages;
@@ -917,8 +921,6 @@ __global__ void __launch_bounds__(WholeShape<NT>::kThreads, 1)
         s_consumed = 0;
         bi::tma_prefetch_desc(&tmap_x);
         bi::tma_prefetch_desc(&tmap_w);
-        bi::tma_prefetch_desc(&tmap_xs);
-        bi::tma_prefetch_desc(&tmap_ws);
     }
     if (warp == 1) {
         bi::tmem_alloc(tmem_slot, 512);
@@ -952,11 +954,9 @@ __global__ void __launch_bounds__(WholeShape<NT>::kThreads, 1)
                 bi::tma_load_2d(sw + 256 * BK, &tmap_x, &full[stage], kb * BK, m0);
                 if (scales) {
                     uint8_t* sf = smem_scales + stage * S::kScaleBytes;
-                    bi::tma_load_2d(sf, &tmap_ws, &full[stage], 0, (n0 / 128) * spans + (kb >> 2));
-                    bi::tma_load_2d(sf + kTile, &tmap_ws, &full[stage], 0,
-                                    (n0 / 128 + 1) * spans + (kb >> 2));
-                    bi::tma_load_2d(sf + 2 * kTile, &tmap_xs, &full[stage], 0,
-                                    (m0 / 128) * spans + (kb >> 2));
+                    load_scales(sf, w_scales, n0 / 128, N, kb, spans, &full[stage]);
+                    load_scales(sf + kTile, w_scales, n0 / 128 + 1, N, kb, spans, &full[stage]);
+                    load_scales(sf + 2 * kTile, x_scales, m0 / 128, M, kb, spans, &full[stage]);
                 }
             }
             __syncwarp();
@@ -1118,12 +1118,17 @@ struct Call {
     int64_t ld_x, ld_w;
     Out out;
     cudaStream_t stream;
+    bi::Device dev;
 };
+
+bool encode(const Call& c, uint32_t x_rows, uint32_t w_rows, CUtensorMap& x, CUtensorMap& w) {
+    return bi::encode_byte_map_2d(&x, c.x, c.K, c.M, c.ld_x, x_rows) == CUDA_SUCCESS &&
+           bi::encode_byte_map_2d(&w, c.W, c.K, c.N, c.ld_w, w_rows) == CUDA_SUCCESS;
+}
 
 bool encode(const Call& c, uint32_t x_rows, uint32_t w_rows, CUtensorMap (&t)[4]) {
     const uint64_t spans = bi_fp8::spans_of(c.K);
-    return bi::encode_byte_map_2d(&t[0], c.x, c.K, c.M, c.ld_x, x_rows) == CUDA_SUCCESS &&
-           bi::encode_byte_map_2d(&t[1], c.W, c.K, c.N, c.ld_w, w_rows) == CUDA_SUCCESS &&
+    return encode(c, x_rows, w_rows, t[0], t[1]) &&
            bi::encode_scale_map(&t[2], c.xs, (c.M + 127) / 128 * spans) == CUDA_SUCCESS &&
            bi::encode_scale_map(&t[3], c.Ws, (c.N + 127) / 128 * spans) == CUDA_SUCCESS;
 }
@@ -1132,7 +1137,7 @@ template <bool kSwiGLU, int H>
 bi_status launch_pair(const Call& c, int sms) {
     using S = PairShape<H>;
     static std::atomic<bool> set[64] = {};
-    if (!bi::allow_smem(gemm_fp8_pair_kernel<kSwiGLU, H>, S::kSmemBytes, set)) return BI_ERR_CUDA;
+    if (!bi::allow_smem(gemm_fp8_pair_kernel<kSwiGLU, H>, S::kSmemBytes, set, c.dev.index)) return BI_ERR_CUDA;
     CUtensorMap t[4];
     if (!encode(c, 128, 64, t)) return BI_ERR_CUDA;
     CUtensorMap ty = t[0];  // not read where the output is 8 bits
@@ -1149,7 +1154,7 @@ bi_status launch_pair(const Call& c, int sms) {
     if (slab * num_m > budget) group_m = static_cast<int>(std::max<int64_t>(1, budget / slab));
     return bi::launch_pdl(gemm_fp8_pair_kernel<kSwiGLU, H>, dim3(2 * pairs), dim3(S::kThreads),
                           S::kSmemBytes, c.stream, t[0], t[1], t[2], t[3], ty, c.out, c.M, c.N, c.K,
-                          parts_of(c.K).blocks, group_m, bi::device_error_word()) == cudaSuccess
+                          parts_of(c.K).blocks, group_m, c.dev.err) == cudaSuccess
                ? BI_OK
                : BI_ERR_CUDA;
 }
@@ -1171,16 +1176,17 @@ template <int NT, bool kSwiGLU, int STAGES>
 bi_status launch_parts(const Call& c, const PartsPlan& p, bool prefetch) {
     using S = PartsShape<NT, kSwiGLU ? 2 : 1, STAGES>;
     static std::atomic<bool> set[64] = {};
-    if (!bi::allow_smem(gemm_fp8_parts_kernel<NT, kSwiGLU, STAGES>, S::kMostBytes, set))
+    if (!bi::allow_smem(gemm_fp8_parts_kernel<NT, kSwiGLU, STAGES>, S::kMostBytes, set, c.dev.index))
         return BI_ERR_CUDA;
-    CUtensorMap t[4];
-    if (!encode(c, NT, 128, t)) return BI_ERR_CUDA;
+    CUtensorMap x, w;
+    if (!encode(c, NT, 128, x, w)) return BI_ERR_CUDA;
     const int rows = kSwiGLU ? 256 : 128;
     const dim3 grid(p.parts.count, (c.M + NT - 1) / NT, (c.N + rows - 1) / rows);
     return bi::launch_pdl_cluster(gemm_fp8_parts_kernel<NT, kSwiGLU, STAGES>, p.parts.count, grid,
-                                  dim3(192), S::smem_bytes(p.rows, p.parts.count), c.stream, t[0],
-                                  t[1], t[2], t[3], c.out, c.M, c.N, c.K, p.parts.blocks, prefetch,
-                                  bi::device_error_word()) == cudaSuccess
+                                  dim3(192), S::smem_bytes(p.rows, p.parts.count), c.stream, x, w,
+                                  static_cast<const uint8_t*>(c.xs),
+                                  static_cast<const uint8_t*>(c.Ws), c.out, c.M, c.N, c.K, p.parts.blocks, prefetch,
+                                  c.dev.err) == cudaSuccess
                ? BI_OK
                : BI_ERR_CUDA;
 }
@@ -1202,13 +1208,14 @@ template <int NT, bool kSwiGLU>
 bi_status launch_whole(const Call& c) {
     using S = WholeShape<NT>;
     static std::atomic<bool> set[64] = {};
-    if (!bi::allow_smem(gemm_fp8_whole_kernel<NT, kSwiGLU>, S::kSmemBytes, set)) return BI_ERR_CUDA;
-    CUtensorMap t[4];
-    if (!encode(c, NT, 128, t)) return BI_ERR_CUDA;
+    if (!bi::allow_smem(gemm_fp8_whole_kernel<NT, kSwiGLU>, S::kSmemBytes, set, c.dev.index)) return BI_ERR_CUDA;
+    CUtensorMap x, w;
+    if (!encode(c, NT, 128, x, w)) return BI_ERR_CUDA;
     const dim3 grid((c.M + NT - 1) / NT, (c.N + 255) / 256);
     return bi::launch_pdl(gemm_fp8_whole_kernel<NT, kSwiGLU>, grid, dim3(S::kThreads), S::kSmemBytes,
-                          c.stream, t[0], t[1], t[2], t[3], c.out, c.M, c.N, c.K,
-                          parts_of(c.K).blocks, bi::device_error_word()) == cudaSuccess
+                          c.stream, x, w, static_cast<const uint8_t*>(c.xs),
+                          static_cast<const uint8_t*>(c.Ws), c.out, c.M, c.N, c.K,
+                          parts_of(c.K).blocks, c.dev.err) == cudaSuccess
                ? BI_OK
                : BI_ERR_CUDA;
 }
@@ -1235,9 +1242,10 @@ bi_status launch_whole(const Call& c) {
 //   rows 16.9 / 16.4, two and one; N = 6144, 1024 rows 23.6 / 26.7, three and two; N = 8192 29.6 /
 //   27.4, four and two).
 template <bool kSwiGLU>
-bi_status launch_gemm(const Call& c) {
-    const int sms = bi::sm_count();
-    if (sms < 2) return BI_ERR_CUDA;
+bi_status launch_gemm(Call& c) {
+    c.dev = bi::current_device_state();
+    if (c.dev.index < 0) return BI_ERR_CUDA;
+    const int sms = c.dev.sms;
     const int64_t pairs = sms / 2;
     const int64_t small_m = (c.M + 127) / 128, small_n = (c.N + 127) / 128;
     const int64_t large_m = (c.M + 255) / 256, large_n = (c.N + 255) / 256;
@@ -1285,7 +1293,7 @@ bi_status check(const Call& c, int n_step) {
 extern "C" bi_status bi_gemm_fp8(const void* x, const void* x_scales, const void* W,
                                  const void* W_scales, void* y, int32_t M, int32_t N, int32_t K,
                                  int64_t ld_x, int64_t ld_w, int64_t ld_y, cudaStream_t stream) {
-    const Call c{x, x_scales, W, W_scales, M, N, K, ld_x, ld_w, {y, ld_y, nullptr, 0}, stream};
+    Call c{x, x_scales, W, W_scales, M, N, K, ld_x, ld_w, {y, ld_y, nullptr, 0}, stream, {}};
     const bi_status st = check(c, 8);
     if (st != BI_OK) return st;
     if (ld_y < N) return BI_ERR_INVALID_ARG;
@@ -1303,8 +1311,8 @@ extern "C" bi_status bi_gemm_fp8_swiglu(const void* x, const void* x_scales, con
                                         int32_t F, int32_t K, int64_t ld_x, int64_t ld_w,
                                         int64_t ld_h, cudaStream_t stream) {
     if (F < 16 || F > (0x7fffffff >> 1)) return BI_ERR_UNSUPPORTED_SHAPE;
-    const Call c{x, x_scales, W_gu, W_gu_scales, M, 2 * F, K, ld_x, ld_w,
-                 {h, ld_h, static_cast<uint8_t*>(h_scales), bi_fp8::spans_of(F)}, stream};
+    Call c{x, x_scales, W_gu, W_gu_scales, M, 2 * F, K, ld_x, ld_w,
+                 {h, ld_h, static_cast<uint8_t*>(h_scales), bi_fp8::spans_of(F)}, stream, {}};
     const bi_status st = check(c, 32);
     if (st != BI_OK) return st;
     if (ld_h < F) return BI_ERR_INVALID_ARG;
