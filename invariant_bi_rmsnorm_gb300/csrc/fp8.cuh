@@ -23,6 +23,23 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
     return max((amax_bits + 0x1FFFFFu) >> 23, 16u) - 8u;
 }
 
+// max(|a|, |b|, |c|), NaN if one is: one instruction.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// {a * b, c * d}, each rounded to nearest, in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
 // 2^(127 - b), by which a block's values are multiplied (exactly, but for
 // results below 2^-126, which become the code 0 either way); NaN for b = 255,
 // which makes every code of the block NaN.

@@ -82,11 +82,12 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 // H: halves of 128 columns in a tile.  Two as a rule; one where that keeps more pairs
 // busy, at the price of reading x twice as often (each SM then takes 24 KB in the time of
 // 256 cycles' MMAs, more than the 64 bytes a cycle it can).
-template <int H>
+// The 8-bit output leaves from registers, so SwiGLU has room for one more stage.
+template <int H, bool kSwiGLU>
 struct PairShape {
     static constexpr int BMP = 256;  // tile rows of the pair; 128 per CTA
     static constexpr int BN = 128 * H;
-    static constexpr int kStages = H == 2 ? 5 : 7;
+    static constexpr int kStages = H == 1 ? 7 : kSwiGLU ? 6 : 5;
     static constexpr int kABytes = 128 * BK;
     static constexpr int kStageBytes = kABytes + H * 64 * BK;  // 128 rows of x, 64 of each half's W
     static constexpr int kScaleBytes = (1 + H) * kTile;
@@ -105,7 +106,7 @@ struct PairShape {
     static constexpr uint32_t kScaleCol = 384;
     static_assert(kStages < 8, "scale places");
     static constexpr int kOutBytes = 32 * 64;  // a warp's 32 rows x 32 bf16 columns on their way out
-    static constexpr int kOutBufs = 3;         // of them in turn
+    static constexpr int kOutBufs = kSwiGLU ? 0 : 3;  // of them in turn
     static constexpr int kOutOffset = (kStages * (kStageBytes + kScaleBytes) + 1023) / 1024 * 1024;
     static constexpr int kSmemBytes = kOutOffset + kEpiWarps * kOutBufs * kOutBytes + 1024 + 256;
     static constexpr uint32_t kIdesc = mx_idesc(BMP, 128);
@@ -123,7 +124,7 @@ __device__ __forceinline__ void tile_coords(int tile, int num_m, int num_n, int 
 }
 
 template <bool kSwiGLU, int H>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<H>::kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<H, kSwiGLU>::kThreads, 1)
     gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_x,
                          const __grid_constant__ CUtensorMap tmap_w,
                          const __grid_constant__ CUtensorMap tmap_xs,
@@ -131,7 +132,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<H>::kThrea
                          const __grid_constant__ CUtensorMap tmap_y, Out out, int M, int N, int K,
                          int part_blocks, int group_m, uint32_t* err) {
     static_assert(!kSwiGLU || H == 2, "a block of 128 outputs takes 256 W rows");
-    using S = PairShape<H>;
+    using S = PairShape<H, kSwiGLU>;
     constexpr int kStages = S::kStages, kABytes = S::kABytes, kStageBytes = S::kStageBytes;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -1135,7 +1136,7 @@ bool encode(const Call& c, uint32_t x_rows, uint32_t w_rows, CUtensorMap (&t)[4]
 
 template <bool kSwiGLU, int H>
 bi_status launch_pair(const Call& c, int sms) {
-    using S = PairShape<H>;
+    using S = PairShape<H, kSwiGLU>;
     static std::atomic<bool> set[64] = {};
     if (!bi::allow_smem(gemm_fp8_pair_kernel<kSwiGLU, H>, S::kSmemBytes, set, c.dev.index)) return BI_ERR_CUDA;
     CUtensorMap t[4];

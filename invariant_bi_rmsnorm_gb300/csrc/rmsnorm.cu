@@ -133,17 +133,19 @@ __global__ void __launch_bounds__(kMaxThreads)
             const uint4 wv = (v < nvec) ? __ldg(wr + v) : make_uint4(0, 0, 0, 0);
             const uint32_t xu[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
             const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
-            float f[8];
-            uint32_t top = 0;
+            float2 f[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                f[2 * e] = __fmul_rn(__fmul_rn(bf16_lo(xu[e]), r), bf16_lo(wu[e]));
-                f[2 * e + 1] = __fmul_rn(__fmul_rn(bf16_hi(xu[e]), r), bf16_hi(wu[e]));
-                top = max(top, max(__float_as_uint(f[2 * e]) & 0x7fffffffu,
-                                   __float_as_uint(f[2 * e + 1]) & 0x7fffffffu));
-            }
-            // threads past the row's end hold zeros of no row, and must not bring in 0 * r = NaN
-            if (v >= nvec) top = 0;
+            for (int e = 0; e < 4; ++e)
+                f[e] = bi_fp8::mul2(bi_fp8::mul2(make_float2(bf16_lo(xu[e]), bf16_hi(xu[e])),
+                                                 make_float2(r, r)),
+                                    make_float2(bf16_lo(wu[e]), bf16_hi(wu[e])));
+            float most = bi_fp8::max3_abs(f[0].x, f[0].y, f[1].x);
+            most = bi_fp8::max3_abs(most, f[1].y, f[2].x);
+            most = bi_fp8::max3_abs(most, f[2].y, f[3].x);
+            most = bi_fp8::max3_abs(most, f[3].y, f[3].y);
+            // threads past the row's end hold zeros of no row, and must not bring in 0 * r = NaN;
+            // as integers NaN comes after infinity and that after the rest
+            uint32_t top = v < nvec ? __float_as_uint(most) : 0u;
 #pragma unroll
             for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
             const uint32_t b = bi_fp8::scale_byte(top);
@@ -151,9 +153,9 @@ __global__ void __launch_bounds__(kMaxThreads)
             if ((tid & 15) == 0) s_byte[v >> 4] = static_cast<uint8_t>(b);
             const float inv = bi_fp8::inverse_scale(b);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], inv);
-            qr[v] = make_uint2(bi_fp8::codes4(f[0], f[1], f[2], f[3]),
-                               bi_fp8::codes4(f[4], f[5], f[6], f[7]));
+            for (int e = 0; e < 4; ++e) f[e] = bi_fp8::mul2(f[e], make_float2(inv, inv));
+            qr[v] = make_uint2(bi_fp8::codes4(f[0].x, f[0].y, f[1].x, f[1].y),
+                               bi_fp8::codes4(f[2].x, f[2].y, f[3].x, f[3].y));
         }
         __syncthreads();
         for (int i = tid; i < fp8.spans; i += T) {
