@@ -73,7 +73,9 @@ def parse_args():
                                        "logprobs", "qk_norm_rope_append", "silu_mul",
                                        "gemm_swiglu", "decode_latency", "attention_kv4",
                                        "kv4_append", "kv4_read", "qk_norm_rope_append_kv4",
-                                       "logprobs_top"],
+                                       "logprobs_top", "gemm_fp8", "gemm_fp8_swiglu",
+                                       "quantize_fp8", "fp8_read", "rmsnorm_fp8",
+                                       "add_rmsnorm_fp8"],
                     help="time one kernel of the path alone (for profiling); prints its own line")
     ap.add_argument("--requests", type=int, default=1000, help="C5 decoder (--case decoder and the default line): requests")
     ap.add_argument("--layers", type=int, default=36, help="--case decoder: decoder layers")
@@ -84,6 +86,10 @@ def parse_args():
                     help="--case decoder: requests re-run alone for the bitwise check")
     ap.add_argument("--batch", type=int, default=ATT_B,
                     help="sequences for --case attention and attention_kv4 (a smaller case for ncu captures)")
+    ap.add_argument("--rows", type=int, default=GEMM_M,
+                    help="rows of x for the 8-bit cases (--case gemm_fp8 and its like)")
+    ap.add_argument("--linear-bits", type=int, choices=[8, 16], default=16,
+                    help="--case decoder and decode_latency: bits of the layers' projections (bi ops)")
     return ap.parse_args()
 
 
@@ -994,6 +1000,35 @@ def build_kv4_case(name: str, batch: int, dev, bi, inputs):
                                                q_out=qo)), float(T * per_tok)
 
 
+FP8_CASES = ("gemm_fp8", "gemm_fp8_swiglu", "quantize_fp8", "fp8_read", "rmsnorm_fp8", "add_rmsnorm_fp8")
+
+
+def build_fp8_case(name: str, rows: int, dev, bi, inputs):
+    """Input of one kernel of the 8-bit linear path as (fn, algorithmic bytes or flops of one
+    launch, unit) for `--case`: the o projection, or the gate|up projection, of `rows` rows, or
+    the norm and quantiser in front of them."""
+    x = inputs.rmsnorm_rows(rows, HIDDEN, seed=640, device=dev)
+    q = bi.quantize_fp8(x)
+    n = float(rows * HIDDEN)
+    if name == "quantize_fp8":
+        return (lambda: bi.quantize_fp8(x, out=q[0], scales=q[1])), 3 * n, "GB/s"
+    if name == "fp8_read":
+        return (lambda: bi.fp8_read(*q, out=x)), 3 * n, "GB/s"
+    w = inputs.rmsnorm_weight(HIDDEN, seed=641, device=dev)
+    if name == "rmsnorm_fp8":
+        return (lambda: bi.rmsnorm_fp8(x, w, EPS, out=q[0], scales=q[1])), 3 * n, "GB/s"
+    if name == "add_rmsnorm_fp8":
+        res, to = torch.zeros_like(x), torch.empty_like(x)
+        return (lambda: bi.add_rmsnorm_fp8(x, res, w, EPS, residual_out=to, out=q[0], scales=q[1])), 7 * n, "GB/s"
+    N, K = LAYERS[1][1:] if name == "gemm_fp8" else LAYERS[2][1:]
+    W = bi.quantize_fp8(inputs.gemm_weight(N, K, seed=642, device=dev))
+    if name == "gemm_fp8":
+        y = torch.empty(rows, N, dtype=torch.bfloat16, device=dev)
+        return (lambda: bi.gemm_fp8(*q, *W, out=y)), 2.0 * rows * N * K, "TFLOP/s"
+    h, hs = bi.gemm_fp8_swiglu(*q, *W)
+    return (lambda: bi.gemm_fp8_swiglu(*q, *W, out=h, scales=hs)), 2.0 * rows * N * K, "TFLOP/s"
+
+
 NEXT_CASES = ("prefill", "add_rmsnorm", "logprobs", "qk_norm_rope_append", "silu_mul",
               "gemm_swiglu")
 
@@ -1039,6 +1074,8 @@ def run_case(args):
         fn, work, unit, _ = build_next_case(args.case, dev, bi, inputs)
     elif args.case in KV4_CASES:
         (fn, work), unit = build_kv4_case(args.case, args.batch, dev, bi, inputs), "GB/s"
+    elif args.case in FP8_CASES:
+        fn, work, unit = build_fp8_case(args.case, args.rows, dev, bi, inputs)
     elif args.case.startswith("gemm"):
         n, N, K = {"gemm_gate_up": LAYERS[2], "gemm_qkv": LAYERS[0]}[args.case]
         x = inputs.gemm_rows(GEMM_M, K, seed=50 + K, device=dev)
@@ -1085,7 +1122,7 @@ TORCH_ARM_SWAPS = ("GEMMs -> torch.matmul (cuBLAS, unfused gate|up then bi_silu_
 
 
 def decoder_c5(requests: int = 1000, layers: int = 36, new_tokens: int = 100,
-               budget: int = 8192, track: int = 16) -> dict:
+               budget: int = 8192, track: int = 16, linear_bits: int = 16) -> dict:
     """The random-init Qwen3-8B-shaped decoder served with continuous batching:
     `requests` prompts of U[32, 512] random tokens, `new_tokens` greedy tokens
     each, at most `budget` tokens per step (prompts split across steps as
@@ -1113,7 +1150,8 @@ def decoder_c5(requests: int = 1000, layers: int = 36, new_tokens: int = 100,
               "prompt_tokens": int(sum(len(r.prompt) for r in reqs)),
               "torch_arm_swaps": TORCH_ARM_SWAPS}
     for ops in ("bi", "torch"):
-        eng = qwen3.Engine(w, num_pages=pages, max_tokens_per_step=budget, ops=ops)
+        eng = qwen3.Engine(w, num_pages=pages, max_tokens_per_step=budget, ops=ops,
+                           linear_bits=linear_bits if ops == "bi" else 16)
         warm = qwen3.random_requests(4, cfg.vocab, 32, 64, 2, seed=99)
         eng.generate(warm)
         eng.reset()
@@ -1150,8 +1188,9 @@ def decoder_c5(requests: int = 1000, layers: int = 36, new_tokens: int = 100,
 def run_decoder(args):
     """`--case decoder`: the C5 decoder run alone, its own JSON line."""
     torch.cuda.set_device(0)
-    res = decoder_c5(args.requests, args.layers, args.new_tokens, args.budget, args.track)
-    print(json.dumps({"case": "decoder", **res}), flush=True)
+    res = decoder_c5(args.requests, args.layers, args.new_tokens, args.budget, args.track,
+                     args.linear_bits)
+    print(json.dumps({"case": "decoder", "linear_bits": args.linear_bits, **res}), flush=True)
 
 
 def run_decode_latency(args):
@@ -1167,12 +1206,12 @@ def run_decode_latency(args):
     cfg = qwen3.Qwen3Config(layers=args.layers)
     w = qwen3.Qwen3Weights(cfg, seed=1000)
     out = {"case": "decode_latency", "layers": args.layers, "prompt_len": 128,
-           "new_tokens": 64, "unit": "ms per step"}
+           "new_tokens": 64, "linear_bits": args.linear_bits, "unit": "ms per step"}
     for B in (1, 8, 64, 256):
         row = {}
         for graphs in (False, True):
             eng = qwen3.Engine(w, num_pages=B * 16 + 64, max_tokens_per_step=8192,
-                               cuda_graphs=graphs)
+                               cuda_graphs=graphs, linear_bits=args.linear_bits)
             eng.generate(qwen3.random_requests(B, cfg.vocab, 128, 128, 4, seed=6))
             eng.reset()
             reqs = qwen3.random_requests(B, cfg.vocab, 128, 128, 64, seed=5)
