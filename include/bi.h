@@ -552,7 +552,7 @@ bi_status bi_quantize_fp8(const void* x, int64_t ld_x, int64_t rows, int32_t K, 
 
 /*
  * bi_fp8_read -- an 8-bit matrix back to bf16 [rows][ld_out].  Nothing is rounded
- * (a code times its scale is a bf16 number; one of 2^128 is an infinity).
+ * (a code times a scale from 2^-119 up is a bf16 number; 2^128 and up an infinity).
  * Arguments and errors as bi_quantize_fp8.
  */
 bi_status bi_fp8_read(const void* q, int64_t ld_q, const void* scales, int64_t rows, int32_t K,
@@ -584,7 +584,7 @@ bi_status bi_add_rmsnorm_fp8(const void* x, const void* residual, void* residual
  * Operation: "2. Batch-Invariant Matrix Multiplication" of "Defeating
  * Nondeterminism in LLM Inference: The Core Role of Batch Invariance".  The
  * order is fixed by K alone: K is cut into P <= 8 parts of L runs of 512 values
- * (S = ceil(K / 512), L = ceil(S / 8), P = ceil(S / L)); a part is one tensor-core
+ * (S = ceil(K / 512), L = max(2, ceil(S / 8)), P = ceil(S / L)); a part is one tensor-core
  * accumulation over its values ascending, 32 at a time, and the parts' sums are
  * added ascending in fp32.  Where that is done (one SM after another's tiles for
  * many rows, the parts on a cluster of SMs for few) follows M and does not show:

@@ -4,7 +4,7 @@
 // Arithmetic, the same for every M ("Defeating Nondeterminism in LLM Inference:
 // The Core Role of Batch Invariance", section "2. Batch-Invariant Matrix
 // Multiplication": the reduction order must not follow the batch size).  K is cut
-// into at most 8 parts of whole runs of 512 values, by K alone (parts_of).  A
+// into at most 8 parts of 1024 values or more, by K alone (parts_of).  A
 // part's sum is one fp32 tensor-memory accumulator: its blocks of 128 ascending,
 // each as four MMAs of depth 32 whose products carry the two scales (powers of
 // two, so scaling rounds nothing).  The parts' sums are then added in ascending
@@ -12,14 +12,21 @@
 // batch changes the order; this one is part of the definition, as the attention's
 // 256-token chunks are, so a call may compute the parts on one SM after another
 // or on several at once:
-//   many rows   gemm_fp8_pair_kernel: 256 x 256 tiles on CTA pairs, a part's
+//   many rows   gemm_fp8_pair_kernel: tiles of 256 rows on CTA pairs, a part's
 //               accumulator drained into registers while the next part runs;
 //   few rows    gemm_fp8_parts_kernel: a cluster of CTAs, one part each, whose sums
 //               meet through distributed shared memory.  The weight is what such
-//               a call has to read, and the parts are what spreads it over all SMs.
-// Both give an output the same bits: the same MMA depth, kind and order, with the
-// operands' roles swapped in the second (tests compare them, adversarial inputs
-// included).
+//               a call has to read, and the parts are what spreads it over all SMs;
+//   few rows, many of W   gemm_fp8_whole_kernel: a CTA an SM, all parts in turn.
+// All give an output the same bits: the same MMA depth, kind and order, with the
+// operands' roles swapped in the last two (tests compare them, adversarial inputs
+// included).  launch_gemm has the rule and what it was measured with.
+//
+// Measured, weights cold: 8192 rows 3.1 to 3.5 PFLOP/s (N = 4096, K = 12288 236 us, N =
+// 24576, K = 4096 475 us), where the board's power holds the clock at 1.7 to 1.8 GHz and L2
+// gives the SMs 16.5 TB/s, 578 cycles a k-block against the MMAs' 512; one row, N = 24576, K =
+// 4096 18.2 us, K = 12288, N = 4096 10.0 us, 5.3 and 5.1 TB/s of weights: what is left
+// are the starts and ends of the CTAs, 2 to 3 us a call that nothing overlaps.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -195,152 +202,152 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<H, kSwiGLU
 
     if (warp < 4) {
         bi::fewer_registers<S::kFewRegs>();
-    if (warp == 0) {  // the whole warp runs the loop, one lane issues
-        const uint32_t bar0 = bi::mapa_shared(bi::smem_u32(full), 0);  // the leader's
-        int stage = 0;
-        uint32_t phase = 0;
-        int issued = 0;
-        bool ok = true;
-        for (int tile = pair_id; tile < num_tiles && ok; tile += npairs) {
-            int mb, nb;
-            tile_coords(tile, num_m, num_n, group_m, mb, nb);
-            const int m_tile = 2 * mb + static_cast<int>(rank);  // of 128 rows
-            const int w_row = nb * S::BN + static_cast<int>(rank) * 64;
-            for (int kb = 0; kb < num_kb; ++kb) {
-                if (!__all_sync(0xffffffffu, bi::mbar_wait(&empty[stage], phase ^ 1))) {
-                    ok = false;
-                    break;
-                }
-                const bool scales = (kb & 3) == 0;  // a tile of them serves four k-blocks
-                uint8_t* sa = smem + stage * kStageBytes;
-                const uint32_t bar = bar0 + 8 * stage;
-                if (bi::elect_one()) {
-                    if (leader)
-                        bi::mbar_arrive_expect_tx(
-                            &full[stage], 2 * (kStageBytes + (scales ? S::kScaleBytes : 0)));
-                    bi::tma_load_2d_pair(sa, &tmap_x, bar, kb * BK, m_tile * 128);
-                    // a half's 128 W rows come half from each CTA (its share of B)
-#pragma unroll
-                    for (int h = 0; h < H; ++h)
-                        bi::tma_load_2d_pair(sa + kABytes + h * 64 * BK, &tmap_w, bar, kb * BK,
-                                             w_row + 128 * h);
-                    if (scales) {
-                        uint8_t* sf = smem_scales + stage * S::kScaleBytes;
-                        bi::tma_load_2d_pair(sf, &tmap_xs, bar, 0, m_tile * spans + (kb >> 2));
-#pragma unroll
-                        for (int h = 0; h < H; ++h)
-                            bi::tma_load_2d_pair(sf + (1 + h) * kTile, &tmap_ws, bar, 0,
-                                                 (H * nb + h) * spans + (kb >> 2));
-                    }
-                }
-                __syncwarp();
-                ++issued;
-                if (++stage == kStages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-        if (lane == 0) {
-            s_issued = issued;
-            if (!ok) {
-                bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
-                s_timeout = 1;
-            }
-        }
-    } else if (warp == 1) {
-        if (leader) {  // the whole warp runs the loop, one lane issues
-            const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
-            const uint32_t ring = bi::smem_u32(smem);
+        if (warp == 0) {  // the whole warp runs the loop, one lane issues
+            const uint32_t bar0 = bi::mapa_shared(bi::smem_u32(full), 0);  // the leader's
             int stage = 0;
             uint32_t phase = 0;
-            int acc = 0;             // accumulators in turn, 0 .. 2
-            uint32_t acc_phase = 0;  // flips when the turn comes round
-            int sf = 0;              // scale place, 0 .. 7
-            int consumed = 0;
+            int issued = 0;
             bool ok = true;
             for (int tile = pair_id; tile < num_tiles && ok; tile += npairs) {
-                uint32_t sfa = 0;
-                int d[H] = {};
-                int left = 0;  // k-blocks of the part still to come
+                int mb, nb;
+                tile_coords(tile, num_m, num_n, group_m, mb, nb);
+                const int m_tile = 2 * mb + static_cast<int>(rank);  // of 128 rows
+                const int w_row = nb * S::BN + static_cast<int>(rank) * 64;
                 for (int kb = 0; kb < num_kb; ++kb) {
-                    const bool first = left == 0;
-                    if (first) left = min(part_blocks, num_kb - kb);
-                    --left;
-                    if (!__all_sync(0xffffffffu, bi::mbar_wait(&full[stage], phase))) {
+                    if (!__all_sync(0xffffffffu, bi::mbar_wait(&empty[stage], phase ^ 1))) {
                         ok = false;
                         break;
                     }
-                    ++consumed;
-                    bi::tc_fence_after();
-                    const uint32_t sa = ring + stage * kStageBytes;
-                    if ((kb & 3) == 0) {
-                        // The place was last read by MMAs of 8 tiles of scales ago.
-                        // They are done: this stage's load waited for the MMAs of
-                        // kStages < 8 k-blocks ago, and tiles are a k-block apart at least.
-                        sfa = tmem + S::kScaleCol + 16 * sf;
-                        sf = (sf + 1) & 7;
-                        const uint64_t s = scale_desc(ring + kStages * kStageBytes +
-                                                      stage * S::kScaleBytes);
-                        if (bi::elect_one()) {
+                    const bool scales = (kb & 3) == 0;  // a tile of them serves four k-blocks
+                    uint8_t* sa = smem + stage * kStageBytes;
+                    const uint32_t bar = bar0 + 8 * stage;
+                    if (bi::elect_one()) {
+                        if (leader)
+                            bi::mbar_arrive_expect_tx(
+                                &full[stage], 2 * (kStageBytes + (scales ? S::kScaleBytes : 0)));
+                        bi::tma_load_2d_pair(sa, &tmap_x, bar, kb * BK, m_tile * 128);
+                        // a half's 128 W rows come half from each CTA (its share of B)
 #pragma unroll
-                            for (int i = 0; i < 1 + H; ++i)
-                                bi::tc_cp_scales_pair(sfa + 4 * i, s + (i * kTile >> 4));
+                        for (int h = 0; h < H; ++h)
+                            bi::tma_load_2d_pair(sa + kABytes + h * 64 * BK, &tmap_w, bar, kb * BK,
+                                                 w_row + 128 * h);
+                        if (scales) {
+                            uint8_t* sf = smem_scales + stage * S::kScaleBytes;
+                            bi::tma_load_2d_pair(sf, &tmap_xs, bar, 0, m_tile * spans + (kb >> 2));
+#pragma unroll
+                            for (int h = 0; h < H; ++h)
+                                bi::tma_load_2d_pair(sf + (1 + h) * kTile, &tmap_ws, bar, 0,
+                                                     (H * nb + h) * spans + (kb >> 2));
                         }
-                        __syncwarp();
                     }
-                    const uint32_t idesc = with_byte(S::kIdesc, kb & 3);
-                    const uint64_t da = operand_desc(sa), db = operand_desc(sa + kABytes);
-#pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        if (first) {
-                            if (!__all_sync(0xffffffffu, bi::mbar_wait(&tempty[acc], acc_phase ^ 1))) {
-                                ok = false;
-                                break;
-                            }
-                            bi::tc_fence_after();
-                            d[h] = acc;
-                            if (++acc == 3) {
-                                acc = 0;
-                                acc_phase ^= 1;
-                            }
-                        }
-                        if (bi::elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < BK / 32; ++k)  // 32 bytes of K a step
-                                bi::tc_mma_mxf8_pair(tmem + 128 * d[h], da + 2 * k,
-                                                     db + (h * 64 * BK >> 4) + 2 * k, idesc, sfa,
-                                                     sfa + 4 + 4 * h, (!first || k != 0) ? 1u : 0u);
-                            if (left == 0)  // the half's part is complete in both CTAs
-                                bi::tc_commit_pair_multicast(&tfull[d[h]], 0x3);
-                            if (h == H - 1)  // the stage is free in both CTAs
-                                bi::tc_commit_pair_multicast(&empty[stage], 0x3);
-                        }
-                        __syncwarp();
-                    }
-                    if (!ok) break;
+                    __syncwarp();
+                    ++issued;
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
             }
-            if (bi::elect_one()) {
-                s_consumed = consumed;
+            if (lane == 0) {
+                s_issued = issued;
                 if (!ok) {
                     bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
                     s_timeout = 1;
                 }
-                if (s_timeout && consumed > 0) {
-                    // what was issued may still read shared memory and write TMEM: a
-                    // bounded wait for it before both are freed
-                    bi::tc_commit_pair_multicast(drain, 0x1);
-                    bi::mbar_wait_for(drain, 0, bi::kDrainNs);
-                }
             }
-            __syncwarp();
+        } else if (warp == 1) {
+            if (leader) {  // the whole warp runs the loop, one lane issues
+                const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+                const uint32_t ring = bi::smem_u32(smem);
+                int stage = 0;
+                uint32_t phase = 0;
+                int acc = 0;             // accumulators in turn, 0 .. 2
+                uint32_t acc_phase = 0;  // flips when the turn comes round
+                int sf = 0;              // scale place, 0 .. 7
+                int consumed = 0;
+                bool ok = true;
+                for (int tile = pair_id; tile < num_tiles && ok; tile += npairs) {
+                    uint32_t sfa = 0;
+                    int d[H] = {};
+                    int left = 0;  // k-blocks of the part still to come
+                    for (int kb = 0; kb < num_kb; ++kb) {
+                        const bool first = left == 0;
+                        if (first) left = min(part_blocks, num_kb - kb);
+                        --left;
+                        if (!__all_sync(0xffffffffu, bi::mbar_wait(&full[stage], phase))) {
+                            ok = false;
+                            break;
+                        }
+                        ++consumed;
+                        bi::tc_fence_after();
+                        const uint32_t sa = ring + stage * kStageBytes;
+                        if ((kb & 3) == 0) {
+                            // The place was last read by MMAs of 8 tiles of scales ago.
+                            // They are done: this stage's load waited for the MMAs of
+                            // kStages < 8 k-blocks ago, and tiles are a k-block apart at least.
+                            sfa = tmem + S::kScaleCol + 16 * sf;
+                            sf = (sf + 1) & 7;
+                            const uint64_t s = scale_desc(ring + kStages * kStageBytes +
+                                                          stage * S::kScaleBytes);
+                            if (bi::elect_one()) {
+#pragma unroll
+                                for (int i = 0; i < 1 + H; ++i)
+                                    bi::tc_cp_scales_pair(sfa + 4 * i, s + (i * kTile >> 4));
+                            }
+                            __syncwarp();
+                        }
+                        const uint32_t idesc = with_byte(S::kIdesc, kb & 3);
+                        const uint64_t da = operand_desc(sa), db = operand_desc(sa + kABytes);
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            if (first) {
+                                if (!__all_sync(0xffffffffu, bi::mbar_wait(&tempty[acc], acc_phase ^ 1))) {
+                                    ok = false;
+                                    break;
+                                }
+                                bi::tc_fence_after();
+                                d[h] = acc;
+                                if (++acc == 3) {
+                                    acc = 0;
+                                    acc_phase ^= 1;
+                                }
+                            }
+                            if (bi::elect_one()) {
+#pragma unroll
+                                for (int k = 0; k < BK / 32; ++k)  // 32 bytes of K a step
+                                    bi::tc_mma_mxf8_pair(tmem + 128 * d[h], da + 2 * k,
+                                                         db + (h * 64 * BK >> 4) + 2 * k, idesc, sfa,
+                                                         sfa + 4 + 4 * h, (!first || k != 0) ? 1u : 0u);
+                                if (left == 0)  // the half's part is complete in both CTAs
+                                    bi::tc_commit_pair_multicast(&tfull[d[h]], 0x3);
+                                if (h == H - 1)  // the stage is free in both CTAs
+                                    bi::tc_commit_pair_multicast(&empty[stage], 0x3);
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+                if (bi::elect_one()) {
+                    s_consumed = consumed;
+                    if (!ok) {
+                        bi::report_error(err, bi::kErrTimeout | bi::kWhereGemmFp8);
+                        s_timeout = 1;
+                    }
+                    if (s_timeout && consumed > 0) {
+                        // what was issued may still read shared memory and write TMEM: a
+                        // bounded wait for it before both are freed
+                        bi::tc_commit_pair_multicast(drain, 0x1);
+                        bi::mbar_wait_for(drain, 0, bi::kDrainNs);
+                    }
+                }
+                __syncwarp();
+            }
         }
-    }
     } else {
         bi::more_registers<S::kManyRegs>();
         // epilogue warps 4..11: lane quarter warp % 4 of this CTA's 128 rows, and
@@ -858,7 +865,7 @@ __global__ void __launch_bounds__(192)
 }
 
 // ------------------------------------ few rows, enough W rows for all SMs ----
-// A CTA runs all of K for 256 W rows and NT rows of x, alone on its SM, the parts one
+// A CTA runs all of K for 256 W rows and the M <= NT rows of x, alone on its SM, the parts one
 // after the other: no cluster, and the sums meet in registers as in the pair kernel (whose
 // 256 rows of x would be mostly empty here).
 template <int NT>
@@ -900,11 +907,9 @@ __global__ void __launch_bounds__(WholeShape<NT>::kThreads, 1)
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int lane = threadIdx.x & 31;
-    const int m0 = blockIdx.x * NT;
-    const int n0 = blockIdx.y * 256;
+    const int n0 = blockIdx.x * 256;
     const int num_kb = (K + BK - 1) / BK;
     const int spans = (num_kb + 3) >> 2;
-    const int rows = min(NT, M - m0);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -952,12 +957,12 @@ __global__ void __launch_bounds__(WholeShape<NT>::kThreads, 1)
                                           S::kStageBytes + (scales ? S::kScaleBytes : 0));
                 bi::tma_load_2d(sw, &tmap_w, &full[stage], kb * BK, n0);
                 bi::tma_load_2d(sw + 128 * BK, &tmap_w, &full[stage], kb * BK, n0 + 128);
-                bi::tma_load_2d(sw + 256 * BK, &tmap_x, &full[stage], kb * BK, m0);
+                bi::tma_load_2d(sw + 256 * BK, &tmap_x, &full[stage], kb * BK, 0);
                 if (scales) {
                     uint8_t* sf = smem_scales + stage * S::kScaleBytes;
                     load_scales(sf, w_scales, n0 / 128, N, kb, spans, &full[stage]);
                     load_scales(sf + kTile, w_scales, n0 / 128 + 1, N, kb, spans, &full[stage]);
-                    load_scales(sf + 2 * kTile, x_scales, m0 / 128, M, kb, spans, &full[stage]);
+                    load_scales(sf + 2 * kTile, x_scales, 0, M, kb, spans, &full[stage]);
                 }
             }
             __syncwarp();
@@ -976,8 +981,6 @@ __global__ void __launch_bounds__(WholeShape<NT>::kThreads, 1)
     } else if (warp == 1) {  // the whole warp runs the loop, one lane issues
         const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
         const uint32_t ring = bi::smem_u32(smem);
-        // where in their tile of scales the CTA's rows of x start
-        const uint32_t x_col = 8 + ((m0 & 127) >> 5);
         uint32_t sf = 0;
         int stage = 0, acc = 0, left = 0, kb = 0;
         uint32_t phase = 0, acc_phase = 0;
@@ -1022,7 +1025,7 @@ __global__ void __launch_bounds__(WholeShape<NT>::kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < BK / 32; ++k)
                         bi::tc_mma_mxf8(tmem + d[t] * NT, dw + (t * 128 * BK >> 4) + 2 * k, dx + 2 * k,
-                                        idesc, sf + 4 * t, sf + x_col, (!first || k != 0) ? 1u : 0u);
+                                        idesc, sf + 4 * t, sf + 8, (!first || k != 0) ? 1u : 0u);
                     if (left == 0) bi::tc_commit(&tfull[d[t]]);
                     if (t == 1) bi::tc_commit(&empty[stage]);
                     if (t == 1 && kb + 1 == num_kb) bi::tc_commit(done);
@@ -1090,7 +1093,7 @@ __global__ void __launch_bounds__(WholeShape<NT>::kThreads, 1)
             float* to = reinterpret_cast<float*>(smem) + t * 128 + quarter * 32 + lane;
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-                if (i < rows) to[i * 256] = sum[i];
+                if (i < M) to[i * 256] = sum[i];
         }
         bi::tc_fence_before();
     }
@@ -1104,7 +1107,7 @@ __global__ void __launch_bounds__(WholeShape<NT>::kThreads, 1)
         const float* sums = reinterpret_cast<const float*>(smem);
         put_rows<kSwiGLU, 2, S::kThreads>(
             out, [&](int l, int n) { return *reinterpret_cast<const float4*>(sums + l * 256 + n); },
-            rows, [&](int l) { return m0 + l; }, n0, N);
+            M, [](int l) { return l; }, n0, N);
     }
     if (warp == 1) {
         bi::tc_fence_after();
@@ -1212,7 +1215,7 @@ bi_status launch_whole(const Call& c) {
     if (!bi::allow_smem(gemm_fp8_whole_kernel<NT, kSwiGLU>, S::kSmemBytes, set, c.dev.index)) return BI_ERR_CUDA;
     CUtensorMap x, w;
     if (!encode(c, NT, 128, x, w)) return BI_ERR_CUDA;
-    const dim3 grid((c.M + NT - 1) / NT, (c.N + 255) / 256);
+    const dim3 grid((c.N + 255) / 256);
     return bi::launch_pdl(gemm_fp8_whole_kernel<NT, kSwiGLU>, grid, dim3(S::kThreads), S::kSmemBytes,
                           c.stream, x, w, static_cast<const uint8_t*>(c.xs),
                           static_cast<const uint8_t*>(c.Ws), c.out, c.M, c.N, c.K,
@@ -1268,7 +1271,7 @@ bi_status launch_gemm(Call& c) {
                           : static_cast<int64_t>((c.M + 63) / 64) * small_n <= pairs)))) {
         if (c.M <= 16) return g ? launch_parts<16, g, 5, 3, 2>(c, sms) : launch_parts<16, g, 8, 4, 3>(c, sms);
         if (c.M <= 32) return g ? launch_parts<32, g, 4, 2, 2>(c, sms) : launch_parts<32, g, 8, 4, 3>(c, sms);
-        if (c.M <= 64) return g ? launch_parts<64, g, 4, 2, 2>(c, sms) : launch_parts<64, g, 6, 3, 3>(c, sms);
+        if (c.M <= 64) return g ? launch_parts<64, g, 4, 4, 4>(c, sms) : launch_parts<64, g, 6, 3, 3>(c, sms);
         return g ? launch_parts<128, g, 4, 4, 4>(c, sms) : launch_parts<128, g, 6, 3, 3>(c, sms);
     }
     if constexpr (!kSwiGLU)
