@@ -193,6 +193,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape<H, kSwiGLU
         bi::tmem_alloc_pair(tmem_slot, S::kTmemCols);
         bi::tmem_relinquish_pair();
     }
+    if (warp == 0) {
+        // the ring's first stages of the weight start on their way to L2 while the previous
+        // kernel still runs, once for all the pairs that share them (a decoder layer's chain
+        // of calls, 300 rows 100.1 -> 99.1 us, 511 rows 102.0 -> 100.9; four rings' worth: 100.2, 102.1)
+        int mb, nb;
+        tile_coords(pair_id, num_m, num_n, group_m, mb, nb);
+        if (mb == 0 && bi::elect_one())
+            for (int i = 0; i < min(num_kb, kStages); ++i)
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+                    bi::tma_prefetch_2d(&tmap_w, i * BK, nb * S::BN + static_cast<int>(rank) * 64 + 128 * h);
+        __syncwarp();
+    }
     bi::tc_fence_before();
     bi::cluster_sync();  // both CTAs' barriers exist before either signals the other
     bi::tc_fence_after();
@@ -932,6 +945,17 @@ __global__ void __launch_bounds__(WholeShape<NT>::kThreads, 1)
         bi::tmem_alloc(tmem_slot, 512);
         bi::tmem_relinquish();
     }
+    if (warp == 0) {
+        // two rings of the weight start on their way to L2 while the previous kernel, which
+        // as a rule makes x, still runs (a decoder layer's chain of calls, 24 rows 52.4 ->
+        // 51.5 us, 128 rows 73.6 -> 71.0; all of the weight at once: 51.7 and 74.5)
+        if (bi::elect_one())
+            for (int i = 0; i < min(num_kb, 2 * kStages); ++i) {
+                bi::tma_prefetch_2d(&tmap_w, i * BK, n0);
+                bi::tma_prefetch_2d(&tmap_w, i * BK, n0 + 128);
+            }
+        __syncwarp();
+    }
     bi::tc_fence_before();
     __syncthreads();
     bi::tc_fence_after();
@@ -1228,8 +1252,10 @@ bi_status launch_whole(const Call& c) {
 // said otherwise, as parts / whole / pair with tiles of 128 columns / of 256:
 //   up to 32 rows: the parts kernel (N = 4096, 24 rows 6.2 / 14.6 / 11.0 / 15.0; N = 12288 11.6 /
 //   15.2 / 21.9 / 19.8), but the whole kernel where the SMs do not hold the parts' CTAs at
-//   once, three each (N = 24576, one row 19.8 / 19.0 / - / 34.7, 24 rows 22.1 / 19.7 / - / 29.4), and
-//   for SwiGLU of more than 16 rows (F = 8192, 24 rows 19.2 / 16.1 / - / 20.3);
+//   once, whose buffers grow with the rows (N = 24576, one row 19.8 / 19.0 / - / 34.7, 24 rows 22.1 /
+//   19.7 / - / 29.4; SwiGLU, F = 12288, 4 rows, at once, 18.4 / 19.7 / - / -, 8 rows, not, 23.5 / 19.6 /
+//   - / -; F = 8192, 16 rows, at once, 14.6 / 16.4 / - / -), and for SwiGLU of more than 16 rows (F =
+//   8192, 24 rows 19.2 / 16.1 / - / 20.3);
 //   up to 128 rows, where tiles of 256 columns are more than a wave of the pairs: the whole
 //   kernel (N = 24576, 64 rows 29.2 / 21.2 / - / 28.8, 128 rows 35.1 / 24.8 / - / 29.9; but N = 12288,
 //   128 rows 22.2 / 20.5 / 18.1 / 17.1);
@@ -1246,6 +1272,13 @@ bi_status launch_whole(const Call& c) {
 //   rows 16.9 / 16.4, two and one; N = 6144, 1024 rows 23.6 / 26.7, three and two; N = 8192 29.6 /
 //   27.4, four and two).
 template <bool kSwiGLU>
+bool few_at_once(const Call& c, int64_t ctas, int sms) {  // of up to 32 rows
+    const PartsPlan p{parts_of(c.K), ctas, c.M};
+    if (c.M <= 16) return at_once<16, kSwiGLU, kSwiGLU ? 2 : 3>(p, sms);
+    return !kSwiGLU && at_once<32, false, 3>(p, sms);
+}
+
+template <bool kSwiGLU>
 bi_status launch_gemm(Call& c) {
     c.dev = bi::current_device_state();
     if (c.dev.index < 0) return BI_ERR_CUDA;
@@ -1259,7 +1292,7 @@ bi_status launch_gemm(Call& c) {
     const int64_t ctas = parts * small_m * (kSwiGLU ? large_n : small_n);
     constexpr bool g = kSwiGLU;
     if (c.M <= 128 && large_n * 4 > sms && large_n <= sms &&
-        (c.M > 32 ? large_n > pairs : ctas > 3 * sms || (g && c.M > 16))) {
+        (c.M > 32 ? large_n > pairs : !few_at_once<g>(c, ctas, sms))) {
         if (c.M <= 16) return launch_whole<16, g>(c);
         if (c.M <= 32) return launch_whole<32, g>(c);
         if (c.M <= 64) return launch_whole<64, g>(c);
