@@ -136,4 +136,24 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), unsigned cluster, dim3 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// How many clusters of `cluster` CTAs the current device holds at once (0 where it cannot say)
+template <typename... KArgs>
+int active_clusters(void (*kernel)(KArgs...), unsigned cluster, dim3 block, size_t smem) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cluster;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) return n;
+    cudaGetLastError();
+    return 0;
+}
+
 }  // namespace bi

@@ -1193,11 +1193,35 @@ struct PartsPlan {
     int rows;  // of the largest tile
 };
 
+// Asked about, never launched: of a kernel that uses tensor memory the runtime says that an
+// SM holds one CTA, as if each took all of it.
+__global__ void no_tensor_memory_kernel() {}
+
+// How many clusters of the parts kernel the device holds at once.  A cluster lies in one of
+// the chip's GPCs, whose SMs are not a multiple of every cluster's size: 8 parts, one CTA an
+// SM, 120 CTAs of 152; two an SM, 288 of 304.
+int clusters_at_once(int dev, int an_sm, int parts, int bytes) {
+    constexpr int kMostAnSm = 16;  // at 32 columns of tensor memory a CTA, the least
+    static std::atomic<int> known[64][kMostAnSm + 1][9] = {};  // the device's answer + 1
+    if (an_sm > kMostAnSm) an_sm = kMostAnSm;
+    std::atomic<int>& slot = known[dev][an_sm][parts];
+    int clusters = slot.load(std::memory_order_relaxed) - 1;
+    if (clusters >= 0) return clusters;
+    static std::atomic<bool> set[64] = {};
+    if (!bi::allow_smem(no_tensor_memory_kernel, 227 * 1024, set, dev)) return 0;
+    clusters = bi::active_clusters(no_tensor_memory_kernel, parts, dim3(192), bytes);
+    slot.store(clusters + 1, std::memory_order_relaxed);
+    return clusters;
+}
+
 template <int NT, bool kSwiGLU, int STAGES>
-bool at_once(const PartsPlan& p, int sms) {  // whether the SMs hold all CTAs at once
+bool at_once(const Call& c, const PartsPlan& p) {  // whether the SMs hold all CTAs at once
     using S = PartsShape<NT, kSwiGLU ? 2 : 1, STAGES>;
     const int bytes = S::smem_bytes(p.rows, p.parts.count);
-    return bytes <= S::kMostBytes && (228 * 1024) / (bytes + 1024 + 128) * int64_t{sms} >= p.ctas;
+    const int an_sm = (228 * 1024) / (bytes + 1024 + 128);
+    if (bytes > S::kMostBytes || int64_t{an_sm} * c.dev.sms < p.ctas) return false;
+    return p.parts.count == 1 ||
+           int64_t{clusters_at_once(c.dev.index, an_sm, p.parts.count, bytes)} * p.parts.count >= p.ctas;
 }
 
 template <int NT, bool kSwiGLU, int STAGES>
@@ -1222,13 +1246,13 @@ bi_status launch_parts(const Call& c, const PartsPlan& p, bool prefetch) {
 // The deepest ring (most loads in flight a CTA) with which the SMs hold the launch at
 // once, else the shallowest (most CTAs, whose starts and ends overlap).
 template <int NT, bool kSwiGLU, int DEEP, int MID, int SHALLOW>
-bi_status launch_parts(const Call& c, int sms) {
+bi_status launch_parts(const Call& c) {
     const int rows = kSwiGLU ? 256 : 128;
     const Parts parts = parts_of(c.K);
     const PartsPlan p{parts, static_cast<int64_t>(parts.count) * ((c.M + NT - 1) / NT) * ((c.N + rows - 1) / rows),
                       std::min(NT, c.M)};
-    if (at_once<NT, kSwiGLU, DEEP>(p, sms)) return launch_parts<NT, kSwiGLU, DEEP>(c, p, true);
-    if (at_once<NT, kSwiGLU, MID>(p, sms)) return launch_parts<NT, kSwiGLU, MID>(c, p, true);
+    if (at_once<NT, kSwiGLU, DEEP>(c, p)) return launch_parts<NT, kSwiGLU, DEEP>(c, p, true);
+    if (at_once<NT, kSwiGLU, MID>(c, p)) return launch_parts<NT, kSwiGLU, MID>(c, p, true);
     return launch_parts<NT, kSwiGLU, SHALLOW>(c, p, false);
 }
 
@@ -1272,10 +1296,10 @@ bi_status launch_whole(const Call& c) {
 //   rows 16.9 / 16.4, two and one; N = 6144, 1024 rows 23.6 / 26.7, three and two; N = 8192 29.6 /
 //   27.4, four and two).
 template <bool kSwiGLU>
-bool few_at_once(const Call& c, int64_t ctas, int sms) {  // of up to 32 rows
+bool few_at_once(const Call& c, int64_t ctas) {  // of up to 32 rows
     const PartsPlan p{parts_of(c.K), ctas, c.M};
-    if (c.M <= 16) return at_once<16, kSwiGLU, kSwiGLU ? 2 : 3>(p, sms);
-    return !kSwiGLU && at_once<32, false, 3>(p, sms);
+    if (c.M <= 16) return at_once<16, kSwiGLU, kSwiGLU ? 2 : 3>(c, p);
+    return !kSwiGLU && at_once<32, false, 3>(c, p);
 }
 
 template <bool kSwiGLU>
@@ -1291,8 +1315,8 @@ bi_status launch_gemm(Call& c) {
     const int parts = parts_of(c.K).count;
     const int64_t ctas = parts * small_m * (kSwiGLU ? large_n : small_n);
     constexpr bool g = kSwiGLU;
-    if (c.M <= 128 && large_n * 4 > sms && large_n <= sms &&
-        (c.M > 32 ? large_n > pairs : !few_at_once<g>(c, ctas, sms))) {
+    if (c.M <= 128 && large_n * 5 > 2 * sms && large_n <= sms &&
+        (c.M > 32 ? large_n > pairs : !few_at_once<g>(c, ctas))) {
         if (c.M <= 16) return launch_whole<16, g>(c);
         if (c.M <= 32) return launch_whole<32, g>(c);
         if (c.M <= 64) return launch_whole<64, g>(c);
@@ -1302,10 +1326,10 @@ bi_status launch_gemm(Call& c) {
         (c.M <= 32 || (parts >= (c.M <= 64 ? 2 : 4) &&
                        (g ? small_m * small_n <= waves * pairs && ctas <= sms
                           : static_cast<int64_t>((c.M + 63) / 64) * small_n <= pairs)))) {
-        if (c.M <= 16) return g ? launch_parts<16, g, 5, 3, 2>(c, sms) : launch_parts<16, g, 8, 4, 3>(c, sms);
-        if (c.M <= 32) return g ? launch_parts<32, g, 4, 2, 2>(c, sms) : launch_parts<32, g, 8, 4, 3>(c, sms);
-        if (c.M <= 64) return g ? launch_parts<64, g, 4, 4, 4>(c, sms) : launch_parts<64, g, 6, 3, 3>(c, sms);
-        return g ? launch_parts<128, g, 4, 4, 4>(c, sms) : launch_parts<128, g, 6, 3, 3>(c, sms);
+        if (c.M <= 16) return g ? launch_parts<16, g, 5, 3, 2>(c) : launch_parts<16, g, 8, 4, 3>(c);
+        if (c.M <= 32) return g ? launch_parts<32, g, 4, 2, 2>(c) : launch_parts<32, g, 8, 4, 3>(c);
+        if (c.M <= 64) return g ? launch_parts<64, g, 4, 2, 2>(c) : launch_parts<64, g, 6, 3, 3>(c);
+        return g ? launch_parts<128, g, 4, 4, 4>(c) : launch_parts<128, g, 6, 3, 3>(c);
     }
     if constexpr (!kSwiGLU)
         if (5 * half_waves < 8 * waves) return launch_pair<false, 1>(c, sms);
