@@ -516,8 +516,8 @@ __device__ __forceinline__ void load_scales(uint8_t* dst, const uint8_t* scales,
 }
 
 // NT: rows of x per CTA (the MMA's N); WT: tiles of 128 W rows per CTA (the MMA's
-// M): one, or two where a block of 128 SwiGLU outputs needs 256 W rows; STAGES: k-blocks
-// in flight per CTA.
+// M): one, or two where a block of 128 SwiGLU outputs needs 256 W rows or half the CTAs
+// are more than the SMs hold at once; STAGES: k-blocks in flight per CTA.
 template <int NT, int WT, int STAGES>
 struct PartsShape {
     static constexpr int kWBytes = WT * 128 * BK;
@@ -608,14 +608,13 @@ __device__ __forceinline__ void put_rows(const Out& out, const Fold& fold, int r
     }
 }
 
-template <int NT, bool kSwiGLU, int STAGES>
+template <int NT, int WT, bool kSwiGLU, int STAGES>
 __global__ void __launch_bounds__(192)
     gemm_fp8_parts_kernel(const __grid_constant__ CUtensorMap tmap_x,
                           const __grid_constant__ CUtensorMap tmap_w,
                           const uint8_t* __restrict__ x_scales,
                           const uint8_t* __restrict__ w_scales, Out out, int M, int N, int K,
                           int part_blocks, bool prefetch, uint32_t* err) {
-    constexpr int WT = kSwiGLU ? 2 : 1;
     using S = PartsShape<NT, WT, STAGES>;
     constexpr int kStages = S::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -1214,9 +1213,9 @@ int clusters_at_once(int dev, int an_sm, int parts, int bytes) {
     return clusters;
 }
 
-template <int NT, bool kSwiGLU, int STAGES>
+template <int NT, int WT, bool kSwiGLU, int STAGES>
 bool at_once(const Call& c, const PartsPlan& p) {  // whether the SMs hold all CTAs at once
-    using S = PartsShape<NT, kSwiGLU ? 2 : 1, STAGES>;
+    using S = PartsShape<NT, WT, STAGES>;
     const int bytes = S::smem_bytes(p.rows, p.parts.count);
     const int an_sm = (228 * 1024) / (bytes + 1024 + 128);
     if (bytes > S::kMostBytes || int64_t{an_sm} * c.dev.sms < p.ctas) return false;
@@ -1224,17 +1223,17 @@ bool at_once(const Call& c, const PartsPlan& p) {  // whether the SMs hold all C
            int64_t{clusters_at_once(c.dev.index, an_sm, p.parts.count, bytes)} * p.parts.count >= p.ctas;
 }
 
-template <int NT, bool kSwiGLU, int STAGES>
+template <int NT, int WT, bool kSwiGLU, int STAGES>
 bi_status launch_parts(const Call& c, const PartsPlan& p, bool prefetch) {
-    using S = PartsShape<NT, kSwiGLU ? 2 : 1, STAGES>;
+    using S = PartsShape<NT, WT, STAGES>;
     static std::atomic<bool> set[64] = {};
-    if (!bi::allow_smem(gemm_fp8_parts_kernel<NT, kSwiGLU, STAGES>, S::kMostBytes, set, c.dev.index))
+    if (!bi::allow_smem(gemm_fp8_parts_kernel<NT, WT, kSwiGLU, STAGES>, S::kMostBytes, set, c.dev.index))
         return BI_ERR_CUDA;
     CUtensorMap x, w;
     if (!encode(c, NT, 128, x, w)) return BI_ERR_CUDA;
-    const int rows = kSwiGLU ? 256 : 128;
+    constexpr int rows = 128 * WT;
     const dim3 grid(p.parts.count, (c.M + NT - 1) / NT, (c.N + rows - 1) / rows);
-    return bi::launch_pdl_cluster(gemm_fp8_parts_kernel<NT, kSwiGLU, STAGES>, p.parts.count, grid,
+    return bi::launch_pdl_cluster(gemm_fp8_parts_kernel<NT, WT, kSwiGLU, STAGES>, p.parts.count, grid,
                                   dim3(192), S::smem_bytes(p.rows, p.parts.count), c.stream, x, w,
                                   static_cast<const uint8_t*>(c.xs),
                                   static_cast<const uint8_t*>(c.Ws), c.out, c.M, c.N, c.K, p.parts.blocks, prefetch,
@@ -1243,17 +1242,24 @@ bi_status launch_parts(const Call& c, const PartsPlan& p, bool prefetch) {
                : BI_ERR_CUDA;
 }
 
-// The deepest ring (most loads in flight a CTA) with which the SMs hold the launch at
-// once, else the shallowest (most CTAs, whose starts and ends overlap).
-template <int NT, bool kSwiGLU, int DEEP, int MID, int SHALLOW>
-bi_status launch_parts(const Call& c) {
-    const int rows = kSwiGLU ? 256 : 128;
+template <int NT, int WT>
+PartsPlan plan_of(const Call& c) {
     const Parts parts = parts_of(c.K);
-    const PartsPlan p{parts, static_cast<int64_t>(parts.count) * ((c.M + NT - 1) / NT) * ((c.N + rows - 1) / rows),
-                      std::min(NT, c.M)};
-    if (at_once<NT, kSwiGLU, DEEP>(c, p)) return launch_parts<NT, kSwiGLU, DEEP>(c, p, true);
-    if (at_once<NT, kSwiGLU, MID>(c, p)) return launch_parts<NT, kSwiGLU, MID>(c, p, true);
-    return launch_parts<NT, kSwiGLU, SHALLOW>(c, p, false);
+    return {parts,
+            static_cast<int64_t>(parts.count) * ((c.M + NT - 1) / NT) * ((c.N + 128 * WT - 1) / (128 * WT)),
+            std::min(NT, c.M)};
+}
+
+// The deepest ring (most loads in flight a CTA) with which the SMs hold the launch at
+// once, else the shallowest (most CTAs, whose starts and ends overlap).  Which of them ask
+// for the weight early was measured: three stages of 128 W rows, at once, N = 12288, one row
+// 10.6 -> 9.8 us; two of 256, N = 24576 18.1 -> 18.6, which therefore do not.
+template <int NT, int WT, bool kSwiGLU, int DEEP, int MID, int SHALLOW>
+bi_status launch_parts(const Call& c) {
+    const PartsPlan p = plan_of<NT, WT>(c);
+    if (at_once<NT, WT, kSwiGLU, DEEP>(c, p)) return launch_parts<NT, WT, kSwiGLU, DEEP>(c, p, true);
+    if (at_once<NT, WT, kSwiGLU, MID>(c, p)) return launch_parts<NT, WT, kSwiGLU, MID>(c, p, true);
+    return launch_parts<NT, WT, kSwiGLU, SHALLOW>(c, p, WT == 1 && at_once<NT, WT, kSwiGLU, SHALLOW>(c, p));
 }
 
 template <int NT, bool kSwiGLU>
@@ -1274,12 +1280,15 @@ bi_status launch_whole(const Call& c) {
 
 // Which kernel: a schedule choice, the bits are the same.  Measured, us, K = 4096 unless
 // said otherwise, as parts / whole / pair with tiles of 128 columns / of 256:
-//   up to 32 rows: the parts kernel (N = 4096, 24 rows 6.2 / 14.6 / 11.0 / 15.0; N = 12288 11.6 /
-//   15.2 / 21.9 / 19.8), but the whole kernel where the SMs do not hold the parts' CTAs at
-//   once, whose buffers grow with the rows (N = 24576, one row 19.8 / 19.0 / - / 34.7, 24 rows 22.1 /
-//   19.7 / - / 29.4; SwiGLU, F = 12288, 4 rows, at once, 18.4 / 19.7 / - / -, 8 rows, not, 23.5 / 19.6 /
-//   - / -; F = 8192, 16 rows, at once, 14.6 / 16.4 / - / -), and for SwiGLU of more than 16 rows (F =
-//   8192, 24 rows 19.2 / 16.1 / - / 20.3);
+//   up to 32 rows: the parts kernel (N = 4096, 24 rows 6.2 / 14.6 / 11.0 / 15.0; N = 12288 10.4 /
+//   15.9 / 21.9 / 19.8), with 128 W rows a CTA while the SMs hold its CTAs at once.  Where they do
+//   not, up to 16 rows take 256 W rows a CTA if that they do (one row, parts of 128 / of 256 /
+//   whole: N = 16384 15.7 / 12.1 / 16.0, N = 24576 19.9 / 18.0 / 19.4, N = K = 8192 15.8 / 11.9 / -; 17
+//   rows, N = 16384 17.1 / 18.2 / 16.5); the rest the whole kernel if it fills two SMs of five (N =
+//   24576, 24 rows 22.1 / - / 20.3; 32 rows, N = 12288, 48 CTAs, 15.3 / 16.4 / 16.1; K = 8192, N = 12288,
+//   one row 20.2 / 22.1 / 25.8), else the parts kernel all the same.  SwiGLU needs 256 W rows a
+//   CTA (F = 12288, 4 rows, at once, 18.4 / whole 19.7, 8 rows, not, 23.5 / 19.6), and above 16 rows,
+//   where the sums are pulled, the whole kernel is faster even so (F = 8192, 24 rows 19.0 / 17.1);
 //   up to 128 rows, where tiles of 256 columns are more than a wave of the pairs: the whole
 //   kernel (N = 24576, 64 rows 29.2 / 21.2 / - / 28.8, 128 rows 35.1 / 24.8 / - / 29.9; but N = 12288,
 //   128 rows 22.2 / 20.5 / 18.1 / 17.1);
@@ -1296,10 +1305,22 @@ bi_status launch_whole(const Call& c) {
 //   rows 16.9 / 16.4, two and one; N = 6144, 1024 rows 23.6 / 26.7, three and two; N = 8192 29.6 /
 //   27.4, four and two).
 template <bool kSwiGLU>
-bool few_at_once(const Call& c, int64_t ctas) {  // of up to 32 rows
-    const PartsPlan p{parts_of(c.K), ctas, c.M};
-    if (c.M <= 16) return at_once<16, kSwiGLU, kSwiGLU ? 2 : 3>(c, p);
-    return !kSwiGLU && at_once<32, false, 3>(c, p);
+bi_status launch_few(const Call& c, bool whole) {  // up to 32 rows
+    if constexpr (kSwiGLU) {
+        if (c.M <= 16)
+            return whole && !at_once<16, 2, true, 2>(c, plan_of<16, 2>(c)) ? launch_whole<16, true>(c)
+                                                                           : launch_parts<16, 2, true, 5, 3, 2>(c);
+        return whole ? launch_whole<32, true>(c) : launch_parts<32, 2, true, 4, 2, 2>(c);
+    } else {
+        if (c.M > 16)
+            return whole && !at_once<32, 1, false, 3>(c, plan_of<32, 1>(c)) ? launch_whole<32, false>(c)
+                                                                            : launch_parts<32, 1, false, 8, 4, 3>(c);
+        if (!at_once<16, 1, false, 3>(c, plan_of<16, 1>(c))) {
+            if (at_once<16, 2, false, 2>(c, plan_of<16, 2>(c))) return launch_parts<16, 2, false, 5, 3, 2>(c);
+            if (whole) return launch_whole<16, false>(c);
+        }
+        return launch_parts<16, 1, false, 8, 4, 3>(c);
+    }
 }
 
 template <bool kSwiGLU>
@@ -1315,21 +1336,19 @@ bi_status launch_gemm(Call& c) {
     const int parts = parts_of(c.K).count;
     const int64_t ctas = parts * small_m * (kSwiGLU ? large_n : small_n);
     constexpr bool g = kSwiGLU;
-    if (c.M <= 128 && large_n * 5 > 2 * sms && large_n <= sms &&
-        (c.M > 32 ? large_n > pairs : !few_at_once<g>(c, ctas))) {
-        if (c.M <= 16) return launch_whole<16, g>(c);
-        if (c.M <= 32) return launch_whole<32, g>(c);
-        if (c.M <= 64) return launch_whole<64, g>(c);
-        return launch_whole<128, g>(c);
+    if (c.M <= 32 && small_n <= 65535) {
+        const bool whole = large_n * 5 > 2 * sms && large_n <= sms;
+        return launch_few<g>(c, whole);
     }
-    if (small_m <= 65535 && small_n <= 65535 &&
-        (c.M <= 32 || (parts >= (c.M <= 64 ? 2 : 4) &&
-                       (g ? small_m * small_n <= waves * pairs && ctas <= sms
-                          : static_cast<int64_t>((c.M + 63) / 64) * small_n <= pairs)))) {
-        if (c.M <= 16) return g ? launch_parts<16, g, 5, 3, 2>(c) : launch_parts<16, g, 8, 4, 3>(c);
-        if (c.M <= 32) return g ? launch_parts<32, g, 4, 2, 2>(c) : launch_parts<32, g, 8, 4, 3>(c);
-        if (c.M <= 64) return g ? launch_parts<64, g, 4, 2, 2>(c) : launch_parts<64, g, 6, 3, 3>(c);
-        return g ? launch_parts<128, g, 4, 4, 4>(c) : launch_parts<128, g, 6, 3, 3>(c);
+    if (c.M > 32 && c.M <= 128 && large_n > pairs && large_n <= sms)
+        return c.M <= 64 ? launch_whole<64, g>(c) : launch_whole<128, g>(c);
+    if (c.M > 32 && small_m <= 65535 && small_n <= 65535 && parts >= (c.M <= 64 ? 2 : 4) &&
+        (g ? small_m * small_n <= waves * pairs && ctas <= sms
+           : static_cast<int64_t>((c.M + 63) / 64) * small_n <= pairs)) {
+        if constexpr (g)
+            return c.M <= 64 ? launch_parts<64, 2, g, 4, 2, 2>(c) : launch_parts<128, 2, g, 4, 4, 4>(c);
+        else
+            return c.M <= 64 ? launch_parts<64, 1, g, 6, 3, 3>(c) : launch_parts<128, 1, g, 6, 3, 3>(c);
     }
     if constexpr (!kSwiGLU)
         if (5 * half_waves < 8 * waves) return launch_pair<false, 1>(c, sms);

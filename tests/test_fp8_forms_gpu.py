@@ -103,3 +103,57 @@ def test_the_same_matrix_on_both_sides_and_rows_given_twice():
     y = bi.gemm_fp8(*x, *W)
     assert torch.equal(y.view(200, 17, 8), y[:, :8].unsqueeze(1).expand(-1, 17, -1))
     bi.get_device_error()
+
+
+# where few rows take 128 W rows a CTA, 256, or every part in one CTA: by how many clusters of 4 and 8
+# parts the SMs hold, which the buffers for the rows change
+@pytest.mark.parametrize("N,K", [(14344, 4096), (16384, 4112), (24584, 2064), (2056, 8208), (8200, 8192), (10248, 8208)])
+def test_few_rows_of_wide_weights(N, K):
+    x, W = random_matrix(300, K, N + 3, spread=8), random_matrix(N, K, N + 4, spread=8)
+    full = bits(bi.gemm_fp8(*x, *W))
+    for M in (1, 2, 5, 8, 15, 16, 17, 24, 32, 33, 64):
+        assert np.array_equal(bits(bi.gemm_fp8(*rows_of(x, M), *W)), full[:M]), f"M = {M}"
+    some = torch.arange(0, N, max(1, N // 61), device="cuda")
+    check_gemm(bi.gemm_fp8(*rows_of(x, 7), *W)[:, some], rows_of(x, 7),
+               bi.quantize_fp8(bi.fp8_read(*W)[some].contiguous()))
+    bi.get_device_error()
+
+
+@pytest.mark.parametrize("F,K", [(2064, 8208), (4112, 8192), (7184, 4112), (12304, 2064)])
+def test_few_rows_of_wide_gate_up_weights(F, K):
+    x = random_matrix(300, K, F + 3, spread=2)
+    W = bi.quantize_fp8(bi.interleave_gate_up(inputs.gemm_weight(2 * F, K, seed=F).cuda()))
+    h, s = bi.gemm_fp8_swiglu(*x, *W)
+    full = bi.fp8_read(h, s)
+    for M in (1, 4, 5, 8, 16, 17, 32, 33, 48, 64, 65):
+        a, b = bi.gemm_fp8_swiglu(*rows_of(x, M), *W)
+        assert torch.equal(a.view(torch.uint8), h[:M].view(torch.uint8)), f"M = {M}"
+        assert torch.equal(bi.fp8_read(a, b), full[:M]), f"M = {M}"
+    bi.get_device_error()
+
+
+FIRST_CALL_OF_SEVERAL_PARTS_CAPTURED = """
+import torch, invariant_bi_rmsnorm_gb300 as bi
+x = torch.ones(3, 4096, dtype=torch.bfloat16, device="cuda")
+q, s = torch.zeros(3, 4096, dtype=torch.float8_e4m3fn, device="cuda"), torch.zeros(bi.fp8_scales_shape(3, 4096), dtype=torch.uint8, device="cuda")
+W, Ws = torch.zeros(136, 4096, dtype=torch.float8_e4m3fn, device="cuda"), torch.zeros(bi.fp8_scales_shape(136, 4096), dtype=torch.uint8, device="cuda")
+y = torch.zeros(3, 136, dtype=torch.bfloat16, device="cuda")
+w = torch.ones(136, 4096, dtype=torch.bfloat16, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    bi.quantize_fp8(x, out=q, scales=s)
+    bi.quantize_fp8(w, out=W, scales=Ws)
+    bi.gemm_fp8(q, s, W, Ws, out=y)
+g.replay()
+torch.cuda.synchronize()
+assert (y == 4096).all(), y
+print("captured")
+"""
+
+
+def test_first_call_of_several_parts_inside_a_capture():
+    """It asks the device how many clusters it holds."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_OF_SEVERAL_PARTS_CAPTURED], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
