@@ -108,7 +108,10 @@ KERNEL_SOURCES = {"bi_gemm": "gemm.cu", "bi_decode_attention": "decode_attention
                   "bi_qk_norm_rope_append": "decoder_ops.cu", "bi_silu_mul": "decoder_ops.cu",
                   "bi_gemm_swiglu": "gemm.cu", "bi_decode_attention_kv4": "kv4_attention.cu",
                   "bi_kv4_append": "kv4_cache.cu", "bi_kv4_read": "kv4_cache.cu",
-                  "bi_qk_norm_rope_append_kv4": "decoder_ops.cu", "bi_logprobs_top": "logprobs_top.cu"}
+                  "bi_qk_norm_rope_append_kv4": "decoder_ops.cu", "bi_logprobs_top": "logprobs_top.cu",
+                  "bi_gemm_fp8": "gemm_fp8.cu", "bi_gemm_fp8_swiglu": "gemm_fp8.cu",
+                  "bi_quantize_fp8": "fp8_quant.cu", "bi_fp8_read": "fp8_quant.cu",
+                  "bi_rmsnorm_fp8": "rmsnorm.cu", "bi_add_rmsnorm_fp8": "rmsnorm.cu"}
 
 
 def kernel_source_sha(src: str) -> str:
