@@ -674,9 +674,11 @@ def logprobs_top(logits: torch.Tensor, targets: torch.Tensor | None, k: int, str
 
 # ------------------------------------------------------ 8-bit linear path ----
 # An 8-bit matrix is a pair: codes [rows, K] float8_e4m3fn (rows may lie apart by a
-# multiple of 16), and scales, uint8 of fp8_scales_shape(rows, K), contiguous.  As with the
-# 4-bit cache each call tests all it has to in one condition, and sorts out what was wrong
-# only when something was.
+# multiple of 16), and scales, uint8 of fp8_scales_shape(rows, K), contiguous.  A call that
+# is given all its outputs and runs on the current stream is tested and made in compiled
+# code (csrc/call_fp8.cpp), which returns -1 for what it does not take as it stands; that
+# and every other call comes to the tests below.  As with the 4-bit cache they are one
+# condition, and sort out what was wrong only when something was.
 _F8 = torch.float8_e4m3fn
 # The current device for a tensor that is on one (CUDA is up then): what
 # torch.cuda.current_device() asks behind its own checks.
@@ -719,6 +721,11 @@ def quantize_fp8(x: torch.Tensor, out: torch.Tensor | None = None,
                  scales: torch.Tensor | None = None, stream=None):
     """bf16 x [rows, K] as an 8-bit matrix (codes, scales): e4m3 and one power of
     two for each 128 values of a row.  K must be a multiple of 16."""
+    if stream is None and out is not None and scales is not None and _lib.fp8_calls is not None:
+        status = _lib.fp8_calls.quantize_fp8(x, out, scales)
+        if status >= 0:
+            _check(status, "bi_quantize_fp8")
+            return out, scales
     dev, shape = x.get_device(), x.shape
     if dev < 0 or len(shape) != 2:
         _refuse_rows("quantize_fp8", (x, "x", _BF16, None))
@@ -742,6 +749,11 @@ def quantize_fp8(x: torch.Tensor, out: torch.Tensor | None = None,
 def fp8_read(q: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None,
              stream=None) -> torch.Tensor:
     """What an 8-bit matrix stands for, in bf16 (nothing is rounded)."""
+    if stream is None and out is not None and _lib.fp8_calls is not None:
+        status = _lib.fp8_calls.fp8_read(q, scales, out)
+        if status >= 0:
+            _check(status, "bi_fp8_read")
+            return out
     dev, shape = q.get_device(), q.shape
     if dev < 0 or len(shape) != 2:
         _refuse_rows("fp8_read", (q, "q", _F8, None))
@@ -765,6 +777,11 @@ def fp8_read(q: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = N
 def rmsnorm_fp8(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6,
                 out: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
     """rmsnorm(x, w, eps) as an 8-bit matrix (codes, scales), rounded once."""
+    if stream is None and out is not None and scales is not None and _lib.fp8_calls is not None:
+        status = _lib.fp8_calls.rmsnorm_fp8(x, w, eps, out, scales)
+        if status >= 0:
+            _check(status, "bi_rmsnorm_fp8")
+            return out, scales
     dev, shape = x.get_device(), x.shape
     if dev < 0 or len(shape) != 2:
         _refuse_rows("rmsnorm_fp8", (x, "x", _BF16, None))
@@ -791,12 +808,17 @@ def add_rmsnorm_fp8(x: torch.Tensor, residual: torch.Tensor, w: torch.Tensor, ep
                     scales: torch.Tensor | None = None, stream=None):
     """residual_out = residual + x (bf16; in place of residual by default), and
     rmsnorm(residual_out, w, eps) as an 8-bit matrix (codes, scales)."""
+    if residual_out is None:
+        residual_out = residual
+    if stream is None and out is not None and scales is not None and _lib.fp8_calls is not None:
+        status = _lib.fp8_calls.add_rmsnorm_fp8(x, residual, w, eps, residual_out, out, scales)
+        if status >= 0:
+            _check(status, "bi_add_rmsnorm_fp8")
+            return out, scales
     dev, shape = x.get_device(), x.shape
     if dev < 0 or len(shape) != 2:
         _refuse_rows("add_rmsnorm_fp8", (x, "x", _BF16, None))
     rows, hidden = shape
-    if residual_out is None:
-        residual_out = residual
     if out is None or scales is None:
         out, scales = _new_fp8(stream, out, scales, rows, hidden, x.device)
     xs, qs, rs, ss = x.stride(), out.stride(), residual.stride(), residual_out.stride()
@@ -823,6 +845,11 @@ def gemm_fp8(x: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor, W_scales:
              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y = x @ W.T in bf16, of 8-bit matrices x [M, K] and W [N, K] (nn.Linear
     layout), batch-invariant per row.  K must be a multiple of 16, N of 8."""
+    if stream is None and out is not None and _lib.fp8_calls is not None:
+        status = _lib.fp8_calls.gemm_fp8(x, x_scales, W, W_scales, out)
+        if status >= 0:
+            _check(status, "bi_gemm_fp8")
+            return out
     dev, shape, wshape = x.get_device(), x.shape, W.shape
     if dev < 0 or len(shape) != 2 or len(wshape) != 2:
         _refuse_rows("gemm_fp8", (x, "x", _F8, None), (W, "W", _F8, None))
@@ -856,6 +883,11 @@ def gemm_fp8_swiglu(x: torch.Tensor, x_scales: torch.Tensor, W_gu: torch.Tensor,
     scales), from 8-bit x [M, K] and W_gu [2F, K], the gate and up rows interleaved
     as interleave_gate_up does (quantise the interleaved weight).  F and K must be
     multiples of 16."""
+    if stream is None and out is not None and scales is not None and _lib.fp8_calls is not None:
+        status = _lib.fp8_calls.gemm_fp8_swiglu(x, x_scales, W_gu, W_gu_scales, out, scales)
+        if status >= 0:
+            _check(status, "bi_gemm_fp8_swiglu")
+            return out, scales
     dev, shape, wshape = x.get_device(), x.shape, W_gu.shape
     if len(wshape) == 2 and wshape[0] % 32:
         raise ValueError("gemm_fp8_swiglu: W_gu must have 2F rows, F a multiple of 16")

@@ -45,6 +45,9 @@ EXPORTS = (
 )
 
 _lib = None
+# The 8-bit linear path's calls, compiled (csrc/call_fp8.cpp), once the library is loaded; None
+# before, and for a torch without CUDA, which has no tensors to call with.
+fp8_calls = None
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -53,7 +56,7 @@ _i64 = ctypes.c_int64
 
 def load() -> ctypes.CDLL:
     """Load libbi.so once; raise if it is missing."""
-    global _lib
+    global _lib, fp8_calls
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -141,5 +144,21 @@ def load() -> ctypes.CDLL:
     lib.bi_gemm_fp8_swiglu.restype = ctypes.c_int
     lib.bi_selftest_wait_timeout.argtypes = [_i32, _vp]
     lib.bi_selftest_wait_timeout.restype = ctypes.c_int
+    fp8_calls = _compiled_calls(lib)
     _lib = lib
     return lib
+
+
+def _compiled_calls(lib):
+    import torch
+    if torch.version.cuda is None:
+        return None
+    try:
+        from . import _call_fp8
+    except ImportError as e:
+        raise RuntimeError("_call_fp8.so is not built for this torch; run `python -m invariant_bi_rmsnorm_gb300.build` "
+                           "first") from e
+    _call_fp8.bind(*(ctypes.cast(getattr(lib, name), _vp).value for name in (
+        "bi_quantize_fp8", "bi_fp8_read", "bi_rmsnorm_fp8", "bi_add_rmsnorm_fp8", "bi_gemm_fp8",
+        "bi_gemm_fp8_swiglu")))
+    return _call_fp8

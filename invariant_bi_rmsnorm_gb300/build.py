@@ -5,6 +5,9 @@ into ``invariant_bi_rmsnorm_gb300/libbi.so``.  nvcc cross-compiles without a
 GPU, so this also runs on a machine with no device.  The library links the
 CUDA runtime statically and resolves the one driver call
 it needs (cuTensorMapEncodeTiled) at run time, so it does not link libcuda.
+
+Beside it, ``_call_fp8.so``: the 8-bit linear path's calls from Python, compiled
+by the host compiler against the torch that is installed.
 """
 from __future__ import annotations
 
@@ -12,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -20,6 +24,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbi.so")
+CALLS = os.path.join(PKG, "_call_fp8.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["api.cu", "rmsnorm.cu", "gemm.cu", "decode_attention.cu", "prefill_attention.cu",
@@ -55,14 +60,44 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _with_calls() -> bool:
+    import torch
+    return torch.version.cuda is not None  # else there are no tensors to call with
+
+
+def _build_calls() -> None:
+    import torch
+    if not _with_calls():
+        return
+    home = os.path.dirname(torch.__file__)
+    fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
+    os.close(fd)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{d}" for d in (os.path.join(home, "include"), os.path.join(cuda, "include"),
+                                      sysconfig.get_paths()["include"])),
+           "-I" + INCLUDE, os.path.join(CSRC, "call_fp8.cpp"), "-o", tmp,
+           "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        os.unlink(tmp)
+        raise RuntimeError(f"call_fp8.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile and link libbi.so unless it is newer than every source."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    """Compile and link libbi.so and _call_fp8.so unless they are newer than every source."""
+    newest = _deps_mtime()
+    made = [LIB, CALLS] if _with_calls() else [LIB]
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in made):
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_build_calls)
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
+        calls.result()
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
     os.close(fd)
     cmd = [nvcc(), *ARCH, "-shared", *objs, "-o", tmp, "-cudart", "static"]
