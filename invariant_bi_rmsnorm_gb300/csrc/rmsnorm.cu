@@ -61,6 +61,60 @@ struct Fp8Out {
     int64_t ld_res_out;
 };
 
+// bf16(a + b) of 8 values: fp32 sums, one rounding
+__device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
+    const uint32_t au[4] = {a.x, a.y, a.z, a.w}, bu[4] = {b.x, b.y, b.z, b.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        o[e] = bi::pack_bf16x2(__fadd_rn(bf16_lo(bu[e]), bf16_lo(au[e])),
+                               __fadd_rn(bf16_hi(bu[e]), bf16_hi(au[e])));
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// s plus the squares of 8 values, left to right
+__device__ __forceinline__ float add_squares(float s, const uint4& x) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float a = bf16_lo(u[e]), b = bf16_hi(u[e]);
+        s = __fmaf_rn(a, a, s);
+        s = __fmaf_rn(b, b, s);
+    }
+    return s;
+}
+
+// The 8 values (x * r) * w as codes at `to`, `in` the row; the scale byte of their block, which
+// 16 neighbouring threads hold.  All of a warp's threads come here.
+__device__ __forceinline__ uint32_t put_block(const uint4& x, const uint4& w, float r, bool in,
+                                              uint2* to) {
+    const uint32_t xu[4] = {x.x, x.y, x.z, x.w}, wu[4] = {w.x, w.y, w.z, w.w};
+    float2 f[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        f[e] = bi_fp8::mul2(bi_fp8::mul2(make_float2(bf16_lo(xu[e]), bf16_hi(xu[e])),
+                                         make_float2(r, r)),
+                            make_float2(bf16_lo(wu[e]), bf16_hi(wu[e])));
+    float most = bi_fp8::max3_abs(f[0].x, f[0].y, f[1].x);
+    most = bi_fp8::max3_abs(most, f[1].y, f[2].x);
+    most = bi_fp8::max3_abs(most, f[2].y, f[3].x);
+    most = bi_fp8::max3_abs(most, f[3].y, f[3].y);
+    // threads past the row's end hold zeros of no row, and must not bring in 0 * r = NaN;
+    // as integers NaN comes after infinity and that after the rest
+    uint32_t top = in ? __float_as_uint(most) : 0u;
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t b = bi_fp8::scale_byte(top);
+    if (in) {
+        const float inv = bi_fp8::inverse_scale(b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = bi_fp8::mul2(f[e], make_float2(inv, inv));
+        *to = make_uint2(bi_fp8::codes4(f[0].x, f[0].y, f[1].x, f[1].y),
+                         bi_fp8::codes4(f[2].x, f[2].y, f[3].x, f[3].y));
+    }
+    return b;
+}
+
 template <int VPT, bool kAdd, bool kFp8>
 __global__ void __launch_bounds__(kMaxThreads)
     rmsnorm_kernel(const __nv_bfloat16* x, const __nv_bfloat16* __restrict__ w, void* y,
@@ -96,30 +150,14 @@ __global__ void __launch_bounds__(kMaxThreads)
         for (int j = 0; j < VPT; ++j) {
             const int v = tid + j * T;
             if (v >= nvec) continue;
-            const uint4 rv = rr[v];
-            const uint32_t xu[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
-            const uint32_t ru[4] = {rv.x, rv.y, rv.z, rv.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[e] = bi::pack_bf16x2(__fadd_rn(bf16_lo(ru[e]), bf16_lo(xu[e])),
-                                       __fadd_rn(bf16_hi(ru[e]), bf16_hi(xu[e])));
-            xv[j] = make_uint4(o[0], o[1], o[2], o[3]);
+            xv[j] = add8(xv[j], rr[v]);
             ro[v] = xv[j];
         }
     }
 
     float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const uint32_t u[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float a = bf16_lo(u[e]), b = bf16_hi(u[e]);
-            s = __fmaf_rn(a, a, s);
-            s = __fmaf_rn(b, b, s);
-        }
-    }
+    for (int j = 0; j < VPT; ++j) s = add_squares(s, xv[j]);
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if ((tid & 31) == 0) warp_sums[tid >> 5] = s;
@@ -135,32 +173,9 @@ __global__ void __launch_bounds__(kMaxThreads)
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = tid + j * T;
-            const uint4 wv = (v < nvec) ? __ldg(wr + v) : make_uint4(0, 0, 0, 0);
-            const uint32_t xu[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
-            const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
-            float2 f[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                f[e] = bi_fp8::mul2(bi_fp8::mul2(make_float2(bf16_lo(xu[e]), bf16_hi(xu[e])),
-                                                 make_float2(r, r)),
-                                    make_float2(bf16_lo(wu[e]), bf16_hi(wu[e])));
-            float most = bi_fp8::max3_abs(f[0].x, f[0].y, f[1].x);
-            most = bi_fp8::max3_abs(most, f[1].y, f[2].x);
-            most = bi_fp8::max3_abs(most, f[2].y, f[3].x);
-            most = bi_fp8::max3_abs(most, f[3].y, f[3].y);
-            // threads past the row's end hold zeros of no row, and must not bring in 0 * r = NaN;
-            // as integers NaN comes after infinity and that after the rest
-            uint32_t top = v < nvec ? __float_as_uint(most) : 0u;
-#pragma unroll
-            for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const uint32_t b = bi_fp8::scale_byte(top);
-            if (v >= nvec) continue;
-            if ((tid & 15) == 0) s_byte[v >> 4] = static_cast<uint8_t>(b);
-            const float inv = bi_fp8::inverse_scale(b);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = bi_fp8::mul2(f[e], make_float2(inv, inv));
-            qr[v] = make_uint2(bi_fp8::codes4(f[0].x, f[0].y, f[1].x, f[1].y),
-                               bi_fp8::codes4(f[2].x, f[2].y, f[3].x, f[3].y));
+            const uint32_t b = put_block(xv[j], v < nvec ? __ldg(wr + v) : make_uint4(0, 0, 0, 0), r,
+                                         v < nvec, qr + v);
+            if (v < nvec && (tid & 15) == 0) s_byte[v >> 4] = static_cast<uint8_t>(b);
         }
         __syncthreads();
         for (int i = tid; i < fp8.spans; i += T) {
@@ -188,6 +203,76 @@ __global__ void __launch_bounds__(kMaxThreads)
             o[e] = bi::pack_bf16x2(a, b);
         }
         yr[v] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// The 8-bit norm of short rows, a warp a row: the grid above starts a CTA a row, and starting
+// them takes 1.03 ns each, whatever a row's length (16384 rows of 16 values 16.9 us).  Lane l
+// holds the vectors l, l + 32, ... that thread l of each of the other kernel's W warps would, and
+// takes each of those warps' sums and its butterfly by itself, so every sum has its order; warps past
+// the row's end add 0.
+template <int W, bool kAdd>
+__global__ void __launch_bounds__(256, 3)
+    rmsnorm_fp8_rows_kernel(const __nv_bfloat16* x, const __nv_bfloat16* __restrict__ w, uint8_t* q,
+                            int hidden, int64_t ld_x, int64_t ld_q, float eps,
+                            const __nv_bfloat16* res, int64_t ld_res, int64_t rows, Fp8Out fp8) {
+    bi::launch_dependents();
+    bi::grid_dependency_wait();  // nothing global is touched before the previous kernel ends
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= rows) return;  // whole warps
+    const int lane = threadIdx.x & 31;
+    const int nvec = hidden >> 3;
+    const uint4* xr = reinterpret_cast<const uint4*>(x + row * ld_x);
+    const uint4* wr = reinterpret_cast<const uint4*>(w);
+    uint2* qr = reinterpret_cast<uint2*>(q + row * ld_q);
+
+    uint4 xv[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const int v = lane + 32 * i;
+        xv[i] = v < nvec ? __ldcs(xr + v) : make_uint4(0, 0, 0, 0);
+    }
+    if constexpr (kAdd) {
+        const uint4* rr = reinterpret_cast<const uint4*>(res + row * ld_res);
+        uint4* ro = reinterpret_cast<uint4*>(fp8.res_out + row * fp8.ld_res_out);
+        uint4 rv[W];  // all read before any is written: res_out may be res
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const int v = lane + 32 * i;
+            rv[i] = v < nvec ? rr[v] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const int v = lane + 32 * i;
+            xv[i] = add8(xv[i], rv[i]);
+            if (v < nvec) ro[v] = xv[i];
+        }
+    }
+
+    float s[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) s[i] = add_squares(0.f, xv[i]);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1)
+#pragma unroll
+        for (int i = 0; i < W; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
+    float total = s[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) total += s[i];
+    const float r = rsqrtf(__fdiv_rn(total, static_cast<float>(hidden)) + eps);
+
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const int v = lane + 32 * i;
+        const uint32_t b = put_block(xv[i], v < nvec ? __ldg(wr + v) : make_uint4(0, 0, 0, 0), r,
+                                     v < nvec, qr + v);
+        word |= ((v & ~15) < nvec ? b : 0u) << (16 * (i & 1));  // lanes 0-15's block, or 16-31's
+        if ((i & 1) == 0 && i + 1 < W) continue;
+        word |= __shfl_xor_sync(0xffffffffu, word, 16) << 8;
+        if (lane == 0 && i / 2 < fp8.spans)
+            *reinterpret_cast<uint32_t*>(fp8.scales + bi_fp8::scale_word(row, i / 2, fp8.spans)) = word;
+        word = 0;
     }
 }
 
@@ -237,6 +322,31 @@ bi_status launch_rmsnorm(const void* x, const void* w, void* y, int64_t rows, in
                               eps, rb, ld_res, rows, ahead, fp8);
     };
     cudaError_t err;
+    if constexpr (kFp8) {
+        // Measured, us, plain / with the sum, a CTA a row against a warp a row: 512 values, 304 rows
+        // 2.1 / 2.2 against 2.0 / 2.3, 16384 rows 16.9 / 17.0 against 5.9 / 7.5; 1024 values, 1216 rows
+        // 2.9 / 3.2 against 2.9 / 3.4, 2432 rows 4.4 / 5.0 against 3.1 / 4.1; 2048 values, 4864 rows
+        // 9.4 / 11.0 against 9.1 / 11.8, 16384 rows 27.8 / 36.7 against 20.7 / 38.2; 4096 values, 16384
+        // rows 41.1 against 56.1.
+        const auto launch_rows = [&](auto kernel) {
+            return bi::launch_pdl(kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, xb,
+                                  wb, static_cast<uint8_t*>(y), hidden, ld_x, ld_y, eps, rb, ld_res, rows, fp8);
+        };
+        const bool a_warp_a_row = hidden <= 512 || (hidden <= 1024 && rows >= 2048) ||
+                                  (!kAdd && hidden <= 2048 && rows >= 8192);
+        if (a_warp_a_row) {
+            if (hidden <= 256)
+                err = launch_rows(rmsnorm_fp8_rows_kernel<1, kAdd>);
+            else if (hidden <= 512)
+                err = launch_rows(rmsnorm_fp8_rows_kernel<2, kAdd>);
+            else if (kAdd || hidden <= 1024)
+                err = launch_rows(rmsnorm_fp8_rows_kernel<4, kAdd>);
+            else
+                err = launch_rows(rmsnorm_fp8_rows_kernel<8, false>);
+            if (err != cudaSuccess) return BI_ERR_CUDA;
+            return cudaGetLastError() == cudaSuccess ? BI_OK : BI_ERR_CUDA;
+        }
+    }
     if (vpt == 1)
         err = launch(rmsnorm_kernel<1, kAdd, kFp8>);
     else if (vpt == 2)

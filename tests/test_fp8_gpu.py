@@ -488,3 +488,40 @@ def test_binding_refusals():
         with pytest.raises(bi.BiError):
             call()
     bi.get_device_error()
+
+
+@pytest.mark.parametrize("hidden,rows", [(16, 9), (128, 8200), (144, 100), (256, 33), (272, 2100), (512, 2500), (528, 2500),
+                                         (768, 2048), (1024, 2051), (1040, 8192), (2048, 8195), (2064, 8192)])
+def test_norms_of_short_rows_one_by_one_and_all_at_once(hidden, rows):
+    """A warp or a CTA a row, by length and number of rows: the same bytes, and the sum in place."""
+    x = inputs.rmsnorm_rows(rows, hidden, seed=hidden).cuda()
+    w, res = inputs.rmsnorm_weight(hidden, seed=hidden + 1).cuda(), inputs.normal_bf16((rows, hidden), hidden + 2, std=4.0).cuda()
+    x[3, 5], x[4, hidden - 1], x[5] = float("nan"), float("inf"), 0
+    some = [0, 3, 4, 5, 7, 8, rows - 1]
+    q, s = bi.rmsnorm_fp8(x, w)
+    full = bi.fp8_read(q, s)
+    total = torch.empty_like(res)
+    q2, s2 = bi.add_rmsnorm_fp8(x, res, w, residual_out=total)
+    full2 = bi.fp8_read(q2, s2)
+    assert np.array_equal(bits(total), bits((res.float() + x.float()).to(torch.bfloat16)))
+    for r in some:
+        a, b = bi.rmsnorm_fp8(x[r:r + 1], w)
+        assert torch.equal(a.view(torch.uint8)[0], q.view(torch.uint8)[r]), r
+        assert np.array_equal(bits(bi.fp8_read(a, b))[0], bits(full[r:r + 1])[0]), r
+        kept = res[r:r + 1].clone()
+        a, b = bi.add_rmsnorm_fp8(x[r:r + 1], kept, w)
+        assert torch.equal(a.view(torch.uint8)[0], q2.view(torch.uint8)[r]), r
+        assert np.array_equal(bits(bi.fp8_read(a, b))[0], bits(full2[r:r + 1])[0]), r
+        assert np.array_equal(bits(kept), bits(total[r:r + 1]))
+    fine = [r for r in range(0, rows, max(1, rows // 50)) if r not in (3, 4)]
+    xd = x[fine].double().cpu().numpy()
+    ref = xd / np.sqrt((xd ** 2).mean(1, keepdims=True) + 1e-6) * w.double().cpu().numpy()
+    check_held(*bi.rmsnorm_fp8(x[fine].contiguous(), w), ref, EPS_NORM)
+    # rows lie apart, the sum in place, bytes between the rows as they were
+    wide = torch.zeros(rows, hidden + 32, dtype=torch.bfloat16, device="cuda")
+    wide[:, 16:16 + hidden] = res
+    codes = torch.full((rows, hidden + 16), 0x55, dtype=torch.uint8, device="cuda")
+    bi.add_rmsnorm_fp8(x, wide[:, 16:16 + hidden], w, out=codes.view(torch.float8_e4m3fn)[:, :hidden])
+    assert np.array_equal(bits(wide[:, 16:16 + hidden].contiguous()), bits(total)) and (wide[:, :16] == 0).all()
+    assert torch.equal(codes[:, :hidden], q2.view(torch.uint8)) and (codes[:, hidden:] == 0x55).all()
+    bi.get_device_error()
