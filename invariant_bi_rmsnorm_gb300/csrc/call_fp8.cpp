@@ -100,6 +100,7 @@ PyObject* call(PyObject* const* a, Py_ssize_t n, const F& f) {
             status = f(a, dev, c10::cuda::getCurrentCUDAStream(dev).stream());
         }
     } catch (...) {  // not plain, or a tensor without storage or strides
+        PyErr_Clear();
         status = -1;
     }
     return PyLong_FromLong(status);
