@@ -7,7 +7,8 @@ CUDA runtime statically and resolves the one driver call
 it needs (cuTensorMapEncodeTiled) at run time, so it does not link libcuda.
 
 Beside it, ``_call_fp8.so``: the 8-bit linear path's calls from Python, compiled
-by the host compiler against the torch that is installed.
+by the host compiler against the torch that is installed.  Where that cannot be
+done the build says so and goes on: the library does not need them.
 """
 from __future__ import annotations
 
@@ -67,8 +68,6 @@ def _with_calls() -> bool:
 
 def _build_calls() -> None:
     import torch
-    if not _with_calls():
-        return
     home = os.path.dirname(torch.__file__)
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
     os.close(fd)
@@ -79,33 +78,52 @@ def _build_calls() -> None:
                                       sysconfig.get_paths()["include"])),
            "-I" + INCLUDE, os.path.join(CSRC, "call_fp8.cpp"), "-o", tmp,
            "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = f"{r.stdout}\n{r.stderr}" if r.returncode else None
+    except OSError as e:  # no such compiler
+        why = str(e)
+    if why is None:
+        os.replace(tmp, CALLS)
+        return
+    os.unlink(tmp)
+    if os.path.exists(CALLS):  # of other sources
+        os.unlink(CALLS)
+    sys.stderr.write(f"call_fp8.cpp did not build, and the 8-bit calls go through Python:\n{why}\n")
+
+
+def _link(cmd: list[str]) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _build_lib(ex: ThreadPoolExecutor, extra: list[str]) -> None:
+    objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
+    fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
+    os.close(fd)
+    try:
+        _link([nvcc(), *ARCH, "-shared", *objs, "-o", tmp, "-cudart", "static"])
+    except RuntimeError:
         os.unlink(tmp)
-        raise RuntimeError(f"call_fp8.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
+        raise
+    os.replace(tmp, LIB)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile and link libbi.so and _call_fp8.so unless they are newer than every source."""
+    """Compile and link libbi.so and _call_fp8.so, each unless it is newer than every source."""
     newest = _deps_mtime()
-    made = [LIB, CALLS] if _with_calls() else [LIB]
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in made):
-        return LIB
+
+    def current(f):
+        return not force and os.path.exists(f) and os.path.getmtime(f) >= newest
+
     os.makedirs(OBJ_DIR, exist_ok=True)
-    extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = ex.submit(_build_calls)
-        objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
-        calls.result()
-    fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
-    os.close(fd)
-    cmd = [nvcc(), *ARCH, "-shared", *objs, "-o", tmp, "-cudart", "static"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        os.unlink(tmp)
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+        calls = ex.submit(_build_calls) if _with_calls() and not current(CALLS) else None
+        if not current(LIB):
+            _build_lib(ex, ["-Xptxas", "-v"] if verbose_ptxas else [])
+        if calls is not None:
+            calls.result()
     return LIB
 
 
