@@ -152,6 +152,12 @@ def load() -> ctypes.CDLL:
     return lib
 
 
+def torch_build() -> str:
+    """Which torch this is: its version and the commit that it was built from."""
+    import torch
+    return f"{torch.__version__} {torch.version.git_version}"
+
+
 def _compiled_calls(lib):
     import torch
     if torch.version.cuda is None:
@@ -159,10 +165,16 @@ def _compiled_calls(lib):
     try:
         from . import _call_fp8
     except ImportError as e:
-        warnings.warn(f"_call_fp8 does not load ({e}): a call of the 8-bit path takes the host 3 us more; "
-                      "`python -m invariant_bi_rmsnorm_gb300.build` builds it", RuntimeWarning, stacklevel=4)
-        return None
-    _call_fp8.bind(*(ctypes.cast(getattr(lib, name), _vp).value for name in (
-        "bi_quantize_fp8", "bi_fp8_read", "bi_rmsnorm_fp8", "bi_add_rmsnorm_fp8", "bi_gemm_fp8",
-        "bi_gemm_fp8_swiglu")))
-    return _call_fp8
+        why = f"does not load ({e})"
+    else:
+        # compiled against the layout of torch's tensors: another torch's may differ
+        built_for = getattr(_call_fp8, "built_for", "an unknown one")
+        if built_for == torch_build():
+            _call_fp8.bind(*(ctypes.cast(getattr(lib, name), _vp).value for name in (
+                "bi_quantize_fp8", "bi_fp8_read", "bi_rmsnorm_fp8", "bi_add_rmsnorm_fp8", "bi_gemm_fp8",
+                "bi_gemm_fp8_swiglu")))
+            return _call_fp8
+        why = f"was built for another torch ({built_for}, this is {torch_build()})"
+    warnings.warn(f"_call_fp8 {why}: a call of the 8-bit path takes the host 3 us more; "
+                  "`python -m invariant_bi_rmsnorm_gb300.build` builds it", RuntimeWarning, stacklevel=4)
+    return None

@@ -6,8 +6,9 @@ GPU, so this also runs on a machine with no device.  The library links the
 CUDA runtime statically and resolves the one driver call
 it needs (cuTensorMapEncodeTiled) at run time, so it does not link libcuda.
 
-Beside it, ``_call_fp8.so``: the 8-bit linear path's calls from Python, compiled
-by the host compiler against the torch that is installed.  Where that cannot be
+Beside it, ``_call_fp8``: the 8-bit linear path's calls from Python, compiled by
+the host compiler against the torch that is installed, and again for another torch
+(an accessor of torch's tensors is compiled in, and with it their layout).  Where that cannot be
 done the build says so and goes on: the library does not need them.
 """
 from __future__ import annotations
@@ -20,13 +21,16 @@ import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
+from . import _lib
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbi.so")
-CALLS = os.path.join(PKG, "_call_fp8.so")
+CALLS = os.path.join(PKG, "_call_fp8" + sysconfig.get_config_var("EXT_SUFFIX"))
 OBJ_DIR = os.path.join(PKG, "_build")
+CALLS_FOR = os.path.join(OBJ_DIR, "call_fp8.torch")  # the torch that CALLS was built for
 
 SOURCES = ["api.cu", "rmsnorm.cu", "gemm.cu", "decode_attention.cu", "prefill_attention.cu",
            "decoder_ops.cu", "logprobs.cu", "kv4_cache.cu", "kv4_attention.cu",
@@ -68,12 +72,12 @@ def _with_calls() -> bool:
 
 def _build_calls() -> None:
     import torch
-    home = os.path.dirname(torch.__file__)
+    home, built_for = os.path.dirname(torch.__file__), _lib.torch_build()
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
     os.close(fd)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBUILT_FOR="{built_for}"',
            *(f"-isystem{d}" for d in (os.path.join(home, "include"), os.path.join(cuda, "include"),
                                       sysconfig.get_paths()["include"])),
            "-I" + INCLUDE, os.path.join(CSRC, "call_fp8.cpp"), "-o", tmp,
@@ -85,11 +89,21 @@ def _build_calls() -> None:
         why = str(e)
     if why is None:
         os.replace(tmp, CALLS)
+        with open(CALLS_FOR, "w") as f:
+            f.write(built_for)
         return
     os.unlink(tmp)
-    if os.path.exists(CALLS):  # of other sources
+    if os.path.exists(CALLS):  # of other sources, or for another torch
         os.unlink(CALLS)
     sys.stderr.write(f"call_fp8.cpp did not build, and the 8-bit calls go through Python:\n{why}\n")
+
+
+def _built_for() -> str | None:
+    try:
+        with open(CALLS_FOR) as f:
+            return f.read()
+    except OSError:
+        return None
 
 
 def _link(cmd: list[str]) -> None:
@@ -111,7 +125,8 @@ def _build_lib(ex: ThreadPoolExecutor, extra: list[str]) -> None:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile and link libbi.so and _call_fp8.so, each unless it is newer than every source."""
+    """Compile and link libbi.so and _call_fp8, each unless it is newer than every source (and
+    the second was built for this torch)."""
     newest = _deps_mtime()
 
     def current(f):
@@ -119,7 +134,9 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
 
     os.makedirs(OBJ_DIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = ex.submit(_build_calls) if _with_calls() and not current(CALLS) else None
+        calls = None
+        if _with_calls() and not (current(CALLS) and _built_for() == _lib.torch_build()):
+            calls = ex.submit(_build_calls)
         if not current(LIB):
             _build_lib(ex, ["-Xptxas", "-v"] if verbose_ptxas else [])
         if calls is not None:

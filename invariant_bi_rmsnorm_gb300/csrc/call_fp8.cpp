@@ -225,4 +225,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_call_fp8", "The 8-bit linear path
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__call_fp8() { return PyModule_Create(&module); }
+// `built_for`: the torch whose objects are read here, by their layout then.
+PyMODINIT_FUNC PyInit__call_fp8() {
+    PyObject* const m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", BUILT_FOR) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
