@@ -680,6 +680,7 @@ def logprobs_top(logits: torch.Tensor, targets: torch.Tensor | None, k: int, str
 # and every other call comes to the tests below.  As with the 4-bit cache they are one
 # condition, and sort out what was wrong only when something was.
 _F8 = torch.float8_e4m3fn
+_MOST = 2 ** 31 - 1  # of what the library takes as int32; more would reach it cut to its low bits
 # The current device for a tensor that is on one (CUDA is up then): what
 # torch.cuda.current_device() asks behind its own checks.
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -705,6 +706,8 @@ def _refuse_rows(where: str, *wanted):
             raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         if t.stride(1) != 1:
             raise ValueError(f"{where}: {name} must have unit stride along its last dimension")
+        if max(t.shape) > _MOST:
+            raise ValueError(f"{where}: {name} must have fewer than 2^31 rows and columns, got {tuple(t.shape)}")
         if t.get_device() != _current_device():
             raise ValueError(f"{where}: {name} must be on the current CUDA device ({_current_device()})")
 
@@ -733,7 +736,7 @@ def quantize_fp8(x: torch.Tensor, out: torch.Tensor | None = None,
     if out is None or scales is None:
         out, scales = _new_fp8(stream, out, scales, rows, K, x.device)
     xs, qs = x.stride(), out.stride()
-    if not (x.dtype is _BF16 and xs[1] == 1 and out.dtype is _F8 and out.shape == shape and qs[1] == 1
+    if not (K <= _MOST and x.dtype is _BF16 and xs[1] == 1 and out.dtype is _F8 and out.shape == shape and qs[1] == 1
             and scales.dtype is _U8 and scales.shape == ((rows + 127) // 128, (K + 511) // 512, FP8_TILE_BYTES)
             and scales.is_contiguous() and dev == out.get_device() == scales.get_device() == _device()):
         where = "quantize_fp8"
@@ -761,7 +764,7 @@ def fp8_read(q: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = N
     if out is None:
         out = _made(stream, torch.empty, (rows, K), dtype=_BF16, device=q.device)
     qs, ys = q.stride(), out.stride()
-    if not (q.dtype is _F8 and qs[1] == 1 and out.dtype is _BF16 and out.shape == shape and ys[1] == 1
+    if not (K <= _MOST and q.dtype is _F8 and qs[1] == 1 and out.dtype is _BF16 and out.shape == shape and ys[1] == 1
             and scales.dtype is _U8 and scales.shape == ((rows + 127) // 128, (K + 511) // 512, FP8_TILE_BYTES)
             and scales.is_contiguous() and dev == out.get_device() == scales.get_device() == _device()):
         where = "fp8_read"
@@ -789,7 +792,7 @@ def rmsnorm_fp8(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6,
     if out is None or scales is None:
         out, scales = _new_fp8(stream, out, scales, rows, hidden, x.device)
     xs, qs = x.stride(), out.stride()
-    if not (x.dtype is w.dtype is _BF16 and xs[1] == 1 and w.shape == (hidden,) and w.is_contiguous()
+    if not (hidden <= _MOST and x.dtype is w.dtype is _BF16 and xs[1] == 1 and w.shape == (hidden,) and w.is_contiguous()
             and out.dtype is _F8 and out.shape == shape and qs[1] == 1 and scales.dtype is _U8
             and scales.shape == ((rows + 127) // 128, (hidden + 511) // 512, FP8_TILE_BYTES) and scales.is_contiguous()
             and dev == w.get_device() == out.get_device() == scales.get_device() == _device()):
@@ -822,7 +825,7 @@ def add_rmsnorm_fp8(x: torch.Tensor, residual: torch.Tensor, w: torch.Tensor, ep
     if out is None or scales is None:
         out, scales = _new_fp8(stream, out, scales, rows, hidden, x.device)
     xs, qs, rs, ss = x.stride(), out.stride(), residual.stride(), residual_out.stride()
-    if not (x.dtype is residual.dtype is residual_out.dtype is w.dtype is _BF16 and xs[1] == 1
+    if not (hidden <= _MOST and x.dtype is residual.dtype is residual_out.dtype is w.dtype is _BF16 and xs[1] == 1
             and residual.shape == shape == residual_out.shape and rs[1] == 1 == ss[1] and w.shape == (hidden,)
             and w.is_contiguous() and out.dtype is _F8 and out.shape == shape and qs[1] == 1 and scales.dtype is _U8
             and scales.shape == ((rows + 127) // 128, (hidden + 511) // 512, FP8_TILE_BYTES) and scales.is_contiguous()
@@ -859,7 +862,7 @@ def gemm_fp8(x: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor, W_scales:
         out = _made(stream, torch.empty, (M, N), dtype=_BF16, device=x.device)
     xs, ws, ys = x.stride(), W.stride(), out.stride()
     spans = (K + 511) // 512
-    if not (x.dtype is W.dtype is _F8 and wshape[1] == K and xs[1] == 1 == ws[1] and out.dtype is _BF16
+    if not (max(M, N, K) <= _MOST and x.dtype is W.dtype is _F8 and wshape[1] == K and xs[1] == 1 == ws[1] and out.dtype is _BF16
             and out.shape == (M, N) and (ys[1] == 1 or N == 1) and x_scales.dtype is W_scales.dtype is _U8
             and x_scales.shape == ((M + 127) // 128, spans, FP8_TILE_BYTES)
             and W_scales.shape == ((N + 127) // 128, spans, FP8_TILE_BYTES) and x_scales.is_contiguous()
@@ -900,7 +903,7 @@ def gemm_fp8_swiglu(x: torch.Tensor, x_scales: torch.Tensor, W_gu: torch.Tensor,
         out, scales = _new_fp8(stream, out, scales, M, F, x.device)
     xs, ws, hs = x.stride(), W_gu.stride(), out.stride()
     spans = (K + 511) // 512
-    if not (x.dtype is W_gu.dtype is out.dtype is _F8 and wshape[1] == K and xs[1] == 1 == ws[1]
+    if not (max(M, F2, K) <= _MOST and x.dtype is W_gu.dtype is out.dtype is _F8 and wshape[1] == K and xs[1] == 1 == ws[1]
             and out.shape == (M, F) and (hs[1] == 1 or F == 1)
             and x_scales.dtype is W_gu_scales.dtype is scales.dtype is _U8
             and x_scales.shape == ((M + 127) // 128, spans, FP8_TILE_BYTES)
