@@ -14,6 +14,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <exception>
+
 #include "bi.h"
 
 namespace {
@@ -99,10 +101,12 @@ PyObject* call(PyObject* const* a, Py_ssize_t n, const F& f) {
             const int dev = c10::cuda::current_device();
             status = f(a, dev, c10::cuda::getCurrentCUDAStream(dev).stream());
         }
-    } catch (...) {  // not plain, or a tensor without storage or strides
+    } catch (const NotPlain&) {
+        status = -1;
+    } catch (const std::exception&) {  // torch's: a tensor without storage or strides
         PyErr_Clear();
         status = -1;
-    }
+    }  // no other: where the interpreter ends meanwhile, the C library unwinds this thread to its end
     return PyLong_FromLong(status);
 }
 
