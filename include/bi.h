@@ -620,6 +620,17 @@ bi_status bi_gemm_fp8_swiglu(const void* x, const void* x_scales, const void* W_
                              cudaStream_t stream);
 
 /*
+ * bi_gemm_fp8_form -- which kernel bi_gemm_fp8 (bi_gemm_fp8_swiglu where `swiglu` is
+ * not 0; N = 2F then) takes for these sizes on the current device.  A schedule's
+ * name: an output's bits are the same in every form.  Launches nothing.
+ *   1CCC00S  CTA pairs, tiles of 256 rows x CCC columns, S stages in the ring;
+ *   2RRR20S  a CTA for 256 rows of W, all parts in turn, up to RRR rows of x;
+ *   3RRRW0S  a cluster of CTAs, a part each, RRR rows of x by W times 128 of W.
+ * 0 for sizes that the call refuses, for M = 0 and where there is no device.
+ */
+int32_t bi_gemm_fp8_form(int32_t M, int32_t N, int32_t K, int32_t swiglu);
+
+/*
  * bi_decode_attention_fixed_splits -- the same attention with a fixed split
  * COUNT instead of a fixed split size: each sequence's pages are cut into
  * num_splits nearly equal runs (ceil(ceil(L/16)/num_splits) pages each), so

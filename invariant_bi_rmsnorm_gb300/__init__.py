@@ -51,7 +51,7 @@ __all__ = ["BiError", "rmsnorm", "gemm", "gemm_swiglu", "interleave_gate_up",
            "status_string", "PAGE_SIZE", "DECODE_CHUNK", "kv4_cache", "kv4_append",
            "qk_norm_rope_append_kv4", "kv4_read", "decode_attention_kv4", "logprobs_top",
            "KV4_BLOCK_BYTES", "MAX_TOP_LOGPROBS", "fp8_scales_shape", "quantize_fp8", "fp8_read",
-           "rmsnorm_fp8", "add_rmsnorm_fp8", "gemm_fp8", "gemm_fp8_swiglu", "FP8_BLOCK"]
+           "rmsnorm_fp8", "add_rmsnorm_fp8", "gemm_fp8", "gemm_fp8_swiglu", "gemm_fp8_form", "FP8_BLOCK"]
 
 
 def _stream_of(device: int) -> int:
@@ -921,3 +921,11 @@ def gemm_fp8_swiglu(x: torch.Tensor, x_scales: torch.Tensor, W_gu: torch.Tensor,
         M, F, K, xs[0] if M > 1 else one, ws[0] if F2 > 1 else one, hs[0] if M > 1 else -(-F // 16) * 16,
         _raw_stream(dev) if stream is None else _stream(stream)), "bi_gemm_fp8_swiglu")
     return out, scales
+
+
+def gemm_fp8_form(M: int, N: int, K: int, swiglu: bool = False) -> int:
+    """The kernel that gemm_fp8 (gemm_fp8_swiglu, N = 2F) takes for these sizes on the current
+    device, as a number (include/bi.h); 0 for sizes it refuses.  The bits do not depend on it."""
+    if max(M, N, K) > _MOST:
+        return 0
+    return int(_lib.load().bi_gemm_fp8_form(int(M), int(N), int(K), int(swiglu)))

@@ -43,7 +43,7 @@ EXPORTS = (
     "bi_kv4_append", "bi_qk_norm_rope_append_kv4", "bi_kv4_read", "bi_decode_attention_kv4",
     "bi_logprobs_top",
     "bi_fp8_scales_size", "bi_quantize_fp8", "bi_fp8_read", "bi_rmsnorm_fp8", "bi_add_rmsnorm_fp8",
-    "bi_gemm_fp8", "bi_gemm_fp8_swiglu",
+    "bi_gemm_fp8", "bi_gemm_fp8_swiglu", "bi_gemm_fp8_form",
 )
 
 _lib = None
@@ -145,6 +145,8 @@ def load() -> ctypes.CDLL:
     lib.bi_gemm_fp8_swiglu.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i64, _i64,
                                        _i64, _vp]
     lib.bi_gemm_fp8_swiglu.restype = ctypes.c_int
+    lib.bi_gemm_fp8_form.argtypes = [_i32, _i32, _i32, _i32]
+    lib.bi_gemm_fp8_form.restype = _i32
     lib.bi_selftest_wait_timeout.argtypes = [_i32, _vp]
     lib.bi_selftest_wait_timeout.restype = ctypes.c_int
     fp8_calls = _compiled_calls(lib)

@@ -1250,18 +1250,6 @@ PartsPlan plan_of(const Call& c) {
             std::min(NT, c.M)};
 }
 
-// The deepest ring (most loads in flight a CTA) with which the SMs hold the launch at
-// once, else the shallowest (most CTAs, whose starts and ends overlap).  Which of them ask
-// for the weight early was measured: three stages of 128 W rows, at once, N = 12288, one row
-// 10.6 -> 9.8 us; two of 256, N = 24576 18.1 -> 18.6, which therefore do not.
-template <int NT, int WT, bool kSwiGLU, int DEEP, int MID, int SHALLOW>
-bi_status launch_parts(const Call& c) {
-    const PartsPlan p = plan_of<NT, WT>(c);
-    if (at_once<NT, WT, kSwiGLU, DEEP>(c, p)) return launch_parts<NT, WT, kSwiGLU, DEEP>(c, p, true);
-    if (at_once<NT, WT, kSwiGLU, MID>(c, p)) return launch_parts<NT, WT, kSwiGLU, MID>(c, p, true);
-    return launch_parts<NT, WT, kSwiGLU, SHALLOW>(c, p, WT == 1 && at_once<NT, WT, kSwiGLU, SHALLOW>(c, p));
-}
-
 template <int NT, bool kSwiGLU>
 bi_status launch_whole(const Call& c) {
     using S = WholeShape<NT>;
@@ -1276,6 +1264,51 @@ bi_status launch_whole(const Call& c) {
                           parts_of(c.K).blocks, c.dev.err) == cudaSuccess
                ? BI_OK
                : BI_ERR_CUDA;
+}
+
+// What becomes of the kernel that a call's sizes choose: it is launched, or named
+// (bi_gemm_fp8_form).
+struct Launch {
+    using Result = bi_status;
+    template <bool g, int H>
+    static bi_status pair(const Call& c) {
+        return launch_pair<g, H>(c, c.dev.sms);
+    }
+    template <bool g, int NT>
+    static bi_status whole(const Call& c) {
+        return launch_whole<NT, g>(c);
+    }
+    template <bool g, int NT, int WT, int STAGES>
+    static bi_status parts(const Call& c, const PartsPlan& p, bool prefetch) {
+        return launch_parts<NT, WT, g, STAGES>(c, p, prefetch);
+    }
+};
+struct Name {
+    using Result = int32_t;
+    template <bool g, int H>
+    static int32_t pair(const Call&) {
+        return 1000000 + 128 * H * 1000 + PairShape<H, g>::kStages;
+    }
+    template <bool g, int NT>
+    static int32_t whole(const Call&) {
+        return 2000000 + NT * 1000 + 200 + WholeShape<NT>::kStages;
+    }
+    template <bool g, int NT, int WT, int STAGES>
+    static int32_t parts(const Call&, const PartsPlan&, bool) {
+        return 3000000 + NT * 1000 + 100 * WT + STAGES;
+    }
+};
+
+// The deepest ring (most loads in flight a CTA) with which the SMs hold the launch at
+// once, else the shallowest (most CTAs, whose starts and ends overlap).  Which of them ask
+// for the weight early was measured: three stages of 128 W rows, at once, N = 12288, one row
+// 10.6 -> 9.8 us; two of 256, N = 24576 18.1 -> 18.6, which therefore do not.
+template <typename Act, bool g, int NT, int WT, int DEEP, int MID, int SHALLOW>
+typename Act::Result choose_ring(const Call& c) {
+    const PartsPlan p = plan_of<NT, WT>(c);
+    if (at_once<NT, WT, g, DEEP>(c, p)) return Act::template parts<g, NT, WT, DEEP>(c, p, true);
+    if (at_once<NT, WT, g, MID>(c, p)) return Act::template parts<g, NT, WT, MID>(c, p, true);
+    return Act::template parts<g, NT, WT, SHALLOW>(c, p, WT == 1 && at_once<NT, WT, g, SHALLOW>(c, p));
 }
 
 // Which kernel: a schedule choice, the bits are the same.  Measured, us, K = 4096 unless
@@ -1304,29 +1337,27 @@ bi_status launch_whole(const Call& c) {
 //   time, makes up for their number (N = 4096, 400 rows - / - / 11.0 / 15.8, one wave of either; 768
 //   rows 16.9 / 16.4, two and one; N = 6144, 1024 rows 23.6 / 26.7, three and two; N = 8192 29.6 /
 //   27.4, four and two).
-template <bool kSwiGLU>
-bi_status launch_few(const Call& c, bool whole) {  // up to 32 rows
-    if constexpr (kSwiGLU) {
+template <typename Act, bool g>
+typename Act::Result choose_few(const Call& c, bool whole) {  // up to 32 rows
+    if constexpr (g) {
         if (c.M <= 16)
-            return whole && !at_once<16, 2, true, 2>(c, plan_of<16, 2>(c)) ? launch_whole<16, true>(c)
-                                                                           : launch_parts<16, 2, true, 5, 3, 2>(c);
-        return whole ? launch_whole<32, true>(c) : launch_parts<32, 2, true, 4, 2, 2>(c);
+            return whole && !at_once<16, 2, true, 2>(c, plan_of<16, 2>(c)) ? Act::template whole<g, 16>(c)
+                                                                           : choose_ring<Act, g, 16, 2, 5, 3, 2>(c);
+        return whole ? Act::template whole<g, 32>(c) : choose_ring<Act, g, 32, 2, 4, 2, 2>(c);
     } else {
         if (c.M > 16)
-            return whole && !at_once<32, 1, false, 3>(c, plan_of<32, 1>(c)) ? launch_whole<32, false>(c)
-                                                                            : launch_parts<32, 1, false, 8, 4, 3>(c);
+            return whole && !at_once<32, 1, false, 3>(c, plan_of<32, 1>(c)) ? Act::template whole<g, 32>(c)
+                                                                            : choose_ring<Act, g, 32, 1, 8, 4, 3>(c);
         if (!at_once<16, 1, false, 3>(c, plan_of<16, 1>(c))) {
-            if (at_once<16, 2, false, 2>(c, plan_of<16, 2>(c))) return launch_parts<16, 2, false, 5, 3, 2>(c);
-            if (whole) return launch_whole<16, false>(c);
+            if (at_once<16, 2, false, 2>(c, plan_of<16, 2>(c))) return choose_ring<Act, g, 16, 2, 5, 3, 2>(c);
+            if (whole) return Act::template whole<g, 16>(c);
         }
-        return launch_parts<16, 1, false, 8, 4, 3>(c);
+        return choose_ring<Act, g, 16, 1, 8, 4, 3>(c);
     }
 }
 
-template <bool kSwiGLU>
-bi_status launch_gemm(Call& c) {
-    c.dev = bi::current_device_state();
-    if (c.dev.index < 0) return BI_ERR_CUDA;
+template <typename Act, bool g>
+typename Act::Result choose(const Call& c) {
     const int sms = c.dev.sms;
     const int64_t pairs = sms / 2;
     const int64_t small_m = (c.M + 127) / 128, small_n = (c.N + 127) / 128;
@@ -1334,25 +1365,31 @@ bi_status launch_gemm(Call& c) {
     const int64_t waves = (large_m * large_n + pairs - 1) / pairs;
     const int64_t half_waves = (large_m * small_n + pairs - 1) / pairs;
     const int parts = parts_of(c.K).count;
-    const int64_t ctas = parts * small_m * (kSwiGLU ? large_n : small_n);
-    constexpr bool g = kSwiGLU;
+    const int64_t ctas = parts * small_m * (g ? large_n : small_n);
     if (c.M <= 32 && small_n <= 65535) {
         const bool whole = large_n * 5 > 2 * sms && large_n <= sms;
-        return launch_few<g>(c, whole);
+        return choose_few<Act, g>(c, whole);
     }
     if (c.M > 32 && c.M <= 128 && large_n > pairs && large_n <= sms)
-        return c.M <= 64 ? launch_whole<64, g>(c) : launch_whole<128, g>(c);
+        return c.M <= 64 ? Act::template whole<g, 64>(c) : Act::template whole<g, 128>(c);
     if (c.M > 32 && small_m <= 65535 && small_n <= 65535 && parts >= (c.M <= 64 ? 2 : 4) &&
         (g ? small_m * small_n <= waves * pairs && ctas <= sms
            : static_cast<int64_t>((c.M + 63) / 64) * small_n <= pairs)) {
         if constexpr (g)
-            return c.M <= 64 ? launch_parts<64, 2, g, 4, 2, 2>(c) : launch_parts<128, 2, g, 4, 4, 4>(c);
+            return c.M <= 64 ? choose_ring<Act, g, 64, 2, 4, 2, 2>(c) : choose_ring<Act, g, 128, 2, 4, 4, 4>(c);
         else
-            return c.M <= 64 ? launch_parts<64, 1, g, 6, 3, 3>(c) : launch_parts<128, 1, g, 6, 3, 3>(c);
+            return c.M <= 64 ? choose_ring<Act, g, 64, 1, 6, 3, 3>(c) : choose_ring<Act, g, 128, 1, 6, 3, 3>(c);
     }
-    if constexpr (!kSwiGLU)
-        if (5 * half_waves < 8 * waves) return launch_pair<false, 1>(c, sms);
-    return launch_pair<kSwiGLU, 2>(c, sms);
+    if constexpr (!g)
+        if (5 * half_waves < 8 * waves) return Act::template pair<g, 1>(c);
+    return Act::template pair<g, 2>(c);
+}
+
+template <bool kSwiGLU>
+bi_status launch_gemm(Call& c) {
+    c.dev = bi::current_device_state();
+    if (c.dev.index < 0) return BI_ERR_CUDA;
+    return choose<Launch, kSwiGLU>(c);
 }
 
 bi_status check(const Call& c, int n_step) {
@@ -1368,7 +1405,21 @@ bi_status check(const Call& c, int n_step) {
     return BI_OK;
 }
 
+template <bool kSwiGLU>
+int32_t form_of(Call& c) {
+    if (check(c, kSwiGLU ? 32 : 8) != BI_OK || c.M == 0) return 0;
+    c.dev = bi::current_device_state();
+    return c.dev.index < 0 ? 0 : choose<Name, kSwiGLU>(c);
+}
+
 }  // namespace
+
+extern "C" int32_t bi_gemm_fp8_form(int32_t M, int32_t N, int32_t K, int32_t swiglu) {
+    Call c{};
+    c.M = M, c.N = N, c.K = K;
+    c.ld_x = c.ld_w = K;
+    return swiglu ? form_of<true>(c) : form_of<false>(c);
+}
 
 extern "C" bi_status bi_gemm_fp8(const void* x, const void* x_scales, const void* W,
                                  const void* W_scales, void* y, int32_t M, int32_t N, int32_t K,
