@@ -1349,7 +1349,9 @@ typename Act::Result choose_few(const Call& c, bool whole) {  // up to 32 rows
             return whole && !at_once<32, 1, false, 3>(c, plan_of<32, 1>(c)) ? Act::template whole<g, 32>(c)
                                                                             : choose_ring<Act, g, 32, 1, 8, 4, 3>(c);
         if (!at_once<16, 1, false, 3>(c, plan_of<16, 1>(c))) {
-            if (at_once<16, 2, false, 2>(c, plan_of<16, 2>(c))) return choose_ring<Act, g, 16, 2, 5, 3, 2>(c);
+            // no ring of five stages: an SM holds one such CTA, and what fits in one of 256 W rows an
+            // SM has fitted above in two of 128
+            if (at_once<16, 2, false, 2>(c, plan_of<16, 2>(c))) return choose_ring<Act, g, 16, 2, 3, 3, 2>(c);
             if (whole) return Act::template whole<g, 16>(c);
         }
         return choose_ring<Act, g, 16, 1, 8, 4, 3>(c);

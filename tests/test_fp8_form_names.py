@@ -1,5 +1,9 @@
-"""Sizes that run on each kernel of the 8-bit products (tests/test_fp8_every_form_gpu.py calls them;
-here without a GPU)."""
+"""The kernels of the 8-bit products that the library holds, and sizes that run on each of them
+(tests/test_fp8_every_form_gpu.py calls them; here without a GPU)."""
+import re
+import shutil
+import subprocess
+
 import pytest
 
 from invariant_bi_rmsnorm_gb300 import _lib
@@ -28,6 +32,26 @@ def lib():
     import __graft_entry__
     __graft_entry__.build()
     return _lib.load()
+
+
+def form_of(kernel, args):
+    """(form without the ring's depth where the name does not say it, SwiGLU)."""
+    if kernel == "parts":
+        rows, tiles, swiglu, stages = args
+        return 3000000 + 1000 * int(rows) + 100 * int(tiles) + int(stages), swiglu == "true"
+    if kernel == "whole":
+        return 2000000 + 1000 * int(args[0]), args[1] == "true"
+    return 1000000 + 128000 * int(args[1]), args[0] == "true"
+
+
+def test_every_kernel_of_the_library_has_its_sizes(lib):
+    """And no kernel is in the library that no size runs on."""
+    if shutil.which("nm") is None:
+        pytest.skip("no nm")
+    names = subprocess.run(["nm", "-C", _lib.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    held = {form_of(k, a.split(", ")) for k, a in re.findall(r"::gemm_fp8_(parts|whole|pair)_kernel<([^>]*)>\(", names)}
+    listed = {(f if f >= 3000000 else f // 1000 * 1000, sw) for forms, sw in ((FORMS, False), (SWIGLU_FORMS, True)) for f in forms}
+    assert held == listed
 
 
 @pytest.mark.parametrize("M,N,K", [(0, 64, 64), (-1, 64, 64), (4, 4, 64), (4, 12, 64), (4, 64, 8), (4, 64, 72), (2 ** 31 - 1, 64, 64)])
