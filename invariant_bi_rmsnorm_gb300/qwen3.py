@@ -189,7 +189,11 @@ class Engine:
         e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device=self.device)  # noqa: E731
         self.buf = {"res": e(T, H), "n": e(T, H), "qkv": e(T, (cfg.heads + 2 * Hkv) * D),
                     "q": e(T, cfg.heads, D), "attn": e(T, cfg.heads, D), "o": e(T, H),
-                    "gu": e(T, 2 * F), "h": e(T, F), "d": e(T, H)}
+                    "d": e(T, H)}
+        if linear_bits == 16:
+            self.buf["h"] = e(T, F)
+        if ops == "torch":  # gate|up before SwiGLU: one call writes h in the others
+            self.buf["gu"] = e(T, 2 * F)
         # the bi path runs gate|up and SwiGLU as one fused GEMM over an
         # interleaved copy of the weight (bit-identical to gemm + silu_mul)
         il = lambda l: interleave_gate_up(self.w.layers[l]["gate_up"])  # noqa: E731
