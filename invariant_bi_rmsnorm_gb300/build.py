@@ -70,22 +70,26 @@ def _with_calls() -> bool:
     return torch.version.cuda is not None  # else there are no tensors to call with
 
 
-def _build_calls() -> None:
+def _calls_command(built_for: str, out: str) -> list[str]:
     import torch
-    home, built_for = os.path.dirname(torch.__file__), _lib.torch_build()
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBUILT_FOR="{built_for}"',
+            *(f"-isystem{d}" for d in (os.path.join(home, "include"), os.path.join(cuda, "include"),
+                                       sysconfig.get_paths()["include"])),
+            "-I" + INCLUDE, os.path.join(CSRC, "call_fp8.cpp"), "-o", out,
+            "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+
+
+def _build_calls() -> None:
+    built_for = _lib.torch_build()
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
     os.close(fd)
-    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBUILT_FOR="{built_for}"',
-           *(f"-isystem{d}" for d in (os.path.join(home, "include"), os.path.join(cuda, "include"),
-                                      sysconfig.get_paths()["include"])),
-           "-I" + INCLUDE, os.path.join(CSRC, "call_fp8.cpp"), "-o", tmp,
-           "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     try:
-        r = subprocess.run(cmd, capture_output=True, text=True)
+        r = subprocess.run(_calls_command(built_for, tmp), capture_output=True, text=True)
         why = f"{r.stdout}\n{r.stderr}" if r.returncode else None
-    except OSError as e:  # no such compiler
+    except (OSError, RuntimeError) as e:  # no such compiler, or no toolkit
         why = str(e)
     if why is None:
         os.replace(tmp, CALLS)

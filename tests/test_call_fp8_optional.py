@@ -80,6 +80,19 @@ def test_the_library_is_built_where_they_cannot_be(tmp_path):
     assert "call_fp8.cpp" in r.stderr
 
 
+@pytest.mark.skipif(torch.version.cuda is None, reason="a torch without CUDA has no such calls")
+def test_a_current_library_needs_no_toolkit(monkeypatch, tmp_path, capfd):
+    import __graft_entry__
+    from invariant_bi_rmsnorm_gb300 import build
+    __graft_entry__.build()
+
+    def nvcc():
+        raise RuntimeError("nvcc not found")
+    monkeypatch.setattr(build, "nvcc", nvcc)
+    monkeypatch.setattr(build, "CALLS", str(tmp_path / "calls.so"))
+    assert build.build() == build.LIB and "nvcc not found" in capfd.readouterr().err
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", ["quantize_fp8", "fp8_read", "rmsnorm_fp8", "add_rmsnorm_fp8", "gemm_fp8", "gemm_fp8_swiglu"])
 def test_the_same_bytes_without_them(name, monkeypatch):
