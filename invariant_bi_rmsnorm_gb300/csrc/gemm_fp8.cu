@@ -23,10 +23,14 @@
 // included).  launch_gemm has the rule and what it was measured with.
 //
 // Measured, weights cold: 8192 rows 3.1 to 3.5 PFLOP/s (N = 4096, K = 12288 236 us, N =
-// 24576, K = 4096 475 us), where the board's power holds the clock at 1.7 to 1.8 GHz and L2
-// gives the SMs 16.5 TB/s, 578 cycles a k-block against the MMAs' 512; one row, N = 24576, K =
-// 4096 18.2 us, K = 12288, N = 4096 10.0 us, 5.3 and 5.1 TB/s of weights: what is left
-// are the starts and ends of the CTAs, 2 to 3 us a call that nothing overlaps.
+// 24576, K = 4096 475 us), where the board's power holds the clock at 1.7 to 1.8 GHz and a k-block
+// takes 578 cycles against the MMAs' 512: its 33152 bytes come into each SM at 57 a cycle.  One
+// row, N = 24576, K = 4096 18.2 us, K = 12288, N = 4096 10.0 us, 5.6 and 5.1 TB/s of weights and
+// scales: what is left are the starts and ends of the CTAs, 2 to 3 us a call that nothing overlaps.
+//
+// Registers spilled (counted by local loads and stores over sizes of K): none in a loop over
+// k-blocks.  Pair with 128 columns, once a tile; with 256, two loads an epilogue warp and part;
+// whole with 128 rows three loads and a store a warp and part, with SwiGLU one load.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -1311,32 +1315,40 @@ typename Act::Result choose_ring(const Call& c) {
     return Act::template parts<g, NT, WT, SHALLOW>(c, p, WT == 1 && at_once<NT, WT, g, SHALLOW>(c, p));
 }
 
-// Which kernel: a schedule choice, the bits are the same.  Measured, us, K = 4096 unless
-// said otherwise, as parts / whole / pair with tiles of 128 columns / of 256:
-//   up to 32 rows: the parts kernel (N = 4096, 24 rows 6.2 / 14.6 / 11.0 / 15.0; N = 12288 10.4 /
-//   15.9 / 21.9 / 19.8), with 128 W rows a CTA while the SMs hold its CTAs at once.  Where they do
-//   not, up to 16 rows take 256 W rows a CTA if that they do (one row, parts of 128 / of 256 /
-//   whole: N = 16384 15.7 / 12.1 / 16.0, N = 24576 19.9 / 18.0 / 19.4, N = K = 8192 15.8 / 11.9 / -; 17
-//   rows, N = 16384 17.1 / 18.2 / 16.5); the rest the whole kernel if it fills two SMs of five (N =
-//   24576, 24 rows 22.1 / - / 20.3; 32 rows, N = 12288, 48 CTAs, 15.3 / 16.4 / 16.1; K = 8192, N = 12288,
-//   one row 20.2 / 22.1 / 25.8), else the parts kernel all the same.  SwiGLU needs 256 W rows a
-//   CTA (F = 12288, 4 rows, at once, 18.4 / whole 19.7, 8 rows, not, 23.5 / 19.6), and above 16 rows,
-//   where the sums are pulled, the whole kernel is faster even so (F = 8192, 24 rows 19.0 / 17.1);
-//   up to 128 rows, where tiles of 256 columns are more than a wave of the pairs: the whole
-//   kernel (N = 24576, 64 rows 29.2 / 21.2 / - / 28.8, 128 rows 35.1 / 24.8 / - / 29.9; but N = 12288,
-//   128 rows 22.2 / 20.5 / 18.1 / 17.1);
-//   else the parts kernel while its tiles, 64 rows x 256 W rows a piece, keep it below half
-//   the pairs (N = 4096, 128 rows, 32 tiles, 8.8 / 19.7 / 10.6 / 15.6, 256 rows, 64, 11.6 / 19.3 / 10.6 /
-//   15.7; N = 8192, 48 rows, 32, 9.1 / 16.0 / 11.3 / 15.7, 128 rows, 64, 12.3 / 20.1 / 11.7 / 16.1;
-//   K = 12288, N = 4096, 128 rows 15.8 / 44.3 / 22.4 / 34.3) and K has parts to spread (K = 1024, one
-//   part, 48 rows 6.4 / 6.8 / 5.9 / 7.6; K = 2048, two, 48 rows 6.1 / - / 7.5 / -, 96 rows 8.0 / - / 7.5 / -);
-//   for SwiGLU, which has no tiles of 128 columns, while its 128 x 128 tiles are no more than
-//   the pairs of a wave each and its CTAs no more than the SMs (F = 4096, 128 rows 14.9 / 21.6 / -
-//   / 16.2; K = 12288 46.6 / 46.4 / - / 35.6);
-//   else the pair kernel, with tiles of 128 columns where a wave of them, 0.6 of the other's
-//   time, makes up for their number (N = 4096, 400 rows - / - / 11.0 / 15.8, one wave of either; 768
-//   rows 16.9 / 16.4, two and one; N = 6144, 1024 rows 23.6 / 26.7, three and two; N = 8192 29.6 /
-//   27.4, four and two).
+// Which kernel: a schedule choice, the bits are the same.  "At once": the SMs hold all CTAs of the
+// launch.  "A CTA an SM": the blocks of 256 W rows are more than two fifths of the SMs, and no more
+// than the SMs.
+//   1 to 32 rows   parts, 128 W rows a CTA, if at once;
+//                  else, up to 16 rows, parts with 256 W rows a CTA, if that is at once;
+//                  else whole, if a CTA an SM;
+//                  else parts, 128 W rows a CTA.
+//     SwiGLU       parts has 256 W rows a CTA.  Up to 16 rows whole if a CTA an SM and parts is not at
+//                  once; above 16 whole if a CTA an SM; else parts.
+//   33 to 128      whole, if the blocks of 256 W rows are more than the pairs and no more than the SMs.
+//   33 and up      parts, if its tiles of 64 rows x 128 W rows are no more than the pairs, and K has two
+//                  parts (up to 64 rows) or four.
+//     SwiGLU       parts, if its tiles of 128 rows x 128 W rows are no more than the pairs in as many
+//                  waves as the pair kernel would take and its CTAs no more than the SMs, K as above.
+//   the rest       pair (as more than 65535 tiles of 128 W rows or rows of x do: a grid's limit); without
+//                  SwiGLU with tiles of 128 columns where a wave of them, 0.6 of the other's time, makes
+//                  up for their number.
+// Measured, us, K = 4096 unless said otherwise, as parts / whole / pair with tiles of 128 columns / of 256:
+//   1 to 32 rows   N = 4096, 24 rows 6.2 / 14.6 / 11.0 / 15.0; N = 12288 10.4 / 15.9 / 21.9 / 19.8.
+//     not at once  one row, parts of 128 / of 256 / whole: N = 16384 15.7 / 12.1 / 16.0, N = 24576 19.9 / 18.0 /
+//                  19.4, N = K = 8192 15.8 / 11.9 / -; 17 rows, N = 16384 17.1 / 18.2 / 16.5.
+//     a CTA an SM  N = 24576, 24 rows 22.1 / - / 20.3; 48 CTAs, N = 12288, 32 rows 15.3 / 16.4 / 16.1, K = 8192, one
+//                  row 20.2 / 22.1 / 25.8.
+//     SwiGLU       F = 12288, 4 rows, at once, 18.4 / whole 19.7, 8 rows, not, 23.5 / 19.6; above 16 rows the
+//                  sums are pulled: F = 8192, 24 rows, at once, 19.0 / 17.1.
+//   whole          N = 24576, 64 rows 29.2 / 21.2 / - / 28.8, 128 rows 35.1 / 24.8 / - / 29.9; but N = 12288, one
+//                  wave of the pairs, 128 rows 22.2 / 20.5 / 18.1 / 17.1.
+//   parts          N = 4096, 128 rows, 64 tiles, 8.8 / 19.7 / 10.6 / 15.6, 256 rows, 128, 11.6 / 19.3 / 10.6 /
+//                  15.7; N = 8192, 48 rows, 64, 9.1 / 16.0 / 11.3 / 15.7, 128 rows, 128, 12.3 / 20.1 / 11.7 / 16.1;
+//                  K = 12288, N = 4096, 128 rows 15.8 / 44.3 / 22.4 / 34.3.  Parts to spread: K = 1024, one, 48
+//                  rows 6.4 / 6.8 / 5.9 / 7.6; K = 2048, two, 48 rows 6.1 / - / 7.5 / -, 96 rows 8.0 / - / 7.5 / -.
+//     SwiGLU       F = 4096, 128 rows 14.9 / 21.6 / - / 16.2; K = 12288 46.6 / 46.4 / - / 35.6.
+//   pair           N = 4096, 400 rows - / - / 11.0 / 15.8, one wave of either; 768 rows 16.9 / 16.4, two and
+//                  one; N = 6144, 1024 rows 23.6 / 26.7, three and two; N = 8192 29.6 / 27.4, four and two.
 template <typename Act, bool g>
 typename Act::Result choose_few(const Call& c, bool whole) {  // up to 32 rows
     if constexpr (g) {

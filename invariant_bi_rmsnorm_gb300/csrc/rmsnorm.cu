@@ -48,9 +48,13 @@ __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v 
 // kFp8: (x * r) * w goes to 8 bits instead of bf16, rounded once (fp8.cuh): the
 // 16 threads that hold a block of 128 values find its largest magnitude by a
 // butterfly, and the row's scale bytes leave by way of shared memory, a word of
-// four at a time.  16384 x 4096: 41.5 us plain (3 bytes a value, 4.85 TB/s: the
-// products, maxima and conversions take the issue slots) and 69.9 us with the sum
-// (7 bytes a value, 6.72 TB/s of HBM's 6.75).  Two products or three maxima an
+// four at a time.  16384 x 4096: 41.5 us plain (3 bytes a value, 4.85 TB/s) and 69.9
+// us with the sum (7 bytes a value, 6.72 TB/s of HBM's 6.75).  The plain form is bound by
+// issue, 83 % of the slots: a thread takes 98 instructions a vector and 120 more that
+// do not depend on how many it has (the sums' folds, the division and the root, two barriers,
+// the scale words, addresses), and at 4096 values it has two.  At 8192 values, four a thread,
+// the instructions are a fifth fewer and the registers (52 for 32) halve the warps: the same
+// time for the same bytes.  Two products or three maxima an
 // instruction (fp8.cuh) took the plain form from 44.6 to 41.0 us; bytes stored without
 // the step through shared memory cost more in long rows (hidden 12288: 82.6 ->
 // 96.6 us for 16384 rows).
