@@ -27,7 +27,10 @@ activations (e4m3, a power-of-two scale for each 128 values): the norms give the
 8-bit input of the projection behind them, attention's output is quantised, and the
 gate|up product hands the down projection its input in 8 bits.  The residual stream,
 the projections' outputs, the final norm and the logits stay bf16.  It goes with
-either cache, and a request's logits still do not depend on the batch.
+either cache, and a request's logits still do not depend on the batch.  With random
+weights the logits lie 0.12 of their norm from the bf16 engine's after one layer and
+0.54 after 36 (kv_bits=4: 0.19 and 0.70).  The 8-bit weights are copies made beside
+the bf16 ones, which stay: what is saved is time, not memory.
 """
 from __future__ import annotations
 
