@@ -136,15 +136,17 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     def current(f):
         return not force and os.path.exists(f) and os.path.getmtime(f) >= newest
 
+    lib = not current(LIB)
+    calls = _with_calls() and not (current(CALLS) and _built_for() == _lib.torch_build())
+    if not lib and not calls:
+        return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = None
-        if _with_calls() and not (current(CALLS) and _built_for() == _lib.torch_build()):
-            calls = ex.submit(_build_calls)
-        if not current(LIB):
+        made = ex.submit(_build_calls) if calls else None
+        if lib:
             _build_lib(ex, ["-Xptxas", "-v"] if verbose_ptxas else [])
-        if calls is not None:
-            calls.result()
+        if made is not None:
+            made.result()
     return LIB
 
 

@@ -93,6 +93,16 @@ def test_a_current_library_needs_no_toolkit(monkeypatch, tmp_path, capfd):
     assert build.build() == build.LIB and "nvcc not found" in capfd.readouterr().err
 
 
+def test_what_is_current_is_left_alone(monkeypatch):
+    """A tree that cannot be written to is no trouble then."""
+    import __graft_entry__
+    from invariant_bi_rmsnorm_gb300 import build
+    __graft_entry__.build()
+    monkeypatch.setattr(build.os, "makedirs", lambda *a, **k: pytest.fail("nothing is to be made"))
+    monkeypatch.setattr(build.tempfile, "mkstemp", lambda *a, **k: pytest.fail("nothing is to be made"))
+    assert build.build() == build.LIB
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", ["quantize_fp8", "fp8_read", "rmsnorm_fp8", "add_rmsnorm_fp8", "gemm_fp8", "gemm_fp8_swiglu"])
 def test_the_same_bytes_without_them(name, monkeypatch):
